@@ -30,6 +30,8 @@ EXPORTS = [
     "moe_dispatch_quant_mx", "moe_quant_weights_mx", "moe_grouped_gemm1_mx", "moe_route_layout_noplan",
     "moe_grouped_gemm1_combine", "moe_send_layout", "moe_dispatch_quant_runs", "moe_grouped_gemm1_gather",
     "moe_grouped_gemm1_pair",
+    "moe_w4_packed_bytes", "moe_quant_weights_w4", "moe_pack_weights_w4", "moe_dequant_weights_w4", "moe_matvec_w4",
+    "moe_layer_few_ws_bytes", "moe_layer_few",
 ]
 
 
@@ -106,6 +108,13 @@ def lib() -> ctypes.CDLL:
         L.moe_dispatch_quant_mx.argtypes = [vp, i32, ctypes.POINTER(LayoutC), vp, vp, vp, vp]
         L.moe_quant_weights_mx.argtypes = [vp, i32, i32, i32, vp, vp, vp]
         L.moe_grouped_gemm1_mx.argtypes = [vp, vp, vp, vp, i32, i32, ctypes.POINTER(LayoutC), vp, vp, vp]
+        L.moe_w4_packed_bytes.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
+        L.moe_quant_weights_w4.argtypes = [vp, i32, i32, i32, i32, vp, vp]
+        L.moe_pack_weights_w4.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp]
+        L.moe_dequant_weights_w4.argtypes = [vp, i32, i32, i32, i32, vp, vp]
+        L.moe_matvec_w4.argtypes = [vp, i32, i32, vp, i32, i32, vp, vp, vp]
+        L.moe_layer_few_ws_bytes.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+        L.moe_layer_few.argtypes = [vp, i32, i32, vp, i32, i32, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, sz, vp, vp]
         for n in EXPORTS:
             if n != "moe_status_string":
                 getattr(L, n).restype = i32
@@ -490,3 +499,106 @@ def moe_grouped_gemm1_gather(A_send: torch.Tensor, A_send_scale: torch.Tensor, W
         _ptr(W, torch.uint8, "W"), _ptr(W_scale, torch.float32, "W_scale"), N, H, ctypes.byref(layout.c),
         _ptr(runs["gather_row"], torch.int32, "gather_row"), runs.max_rows, _ptr(Y, torch.bfloat16, "Y"),
         _ptr(status, torch.int32, "status"), _stream(stream)))
+
+
+# ---------------------------------------------------------------- decoding: few tokens
+
+MOE_FEW_MAX_TOKENS, MOE_FEW_MAX_PAIRS = 64, 1024
+W4_GROUPS = (32, 64, 128)
+
+
+def w4_packed_shape(E: int, N: int, K: int, group: int):
+    """Shape of E laid-out 4-bit matrices [N, K] (u8): tiles of 16 rows x 128
+    columns, each 1024 bytes of codes and 128/group rows of 16 bf16 scales."""
+    if group not in W4_GROUPS:
+        raise ValueError(f"group must be one of {W4_GROUPS}, got {group}")
+    if K % group:
+        raise ValueError(f"K must be a multiple of the group {group}, got {K}")
+    return (E, -(-N // 16), -(-K // 128), 1024 + 32 * (128 // group))
+
+
+def moe_quant_weights_w4(W: torch.Tensor, group: int, Wp: torch.Tensor, stream=None):
+    """bf16 weights [E, N, K] -> 4-bit codes and bf16 group scales, laid out."""
+    E, N, K = _dims(W, 3, "W")
+    _shape(Wp, w4_packed_shape(E, N, K, group), "Wp")
+    _check("moe_quant_weights_w4", lib().moe_quant_weights_w4(
+        _ptr(W, torch.bfloat16, "W"), E, N, K, group, _ptr(Wp, torch.uint8, "Wp"), _stream(stream)))
+
+
+def moe_pack_weights_w4(codes: torch.Tensor, scale: torch.Tensor, group: int, Wp: torch.Tensor, stream=None):
+    """Lay out a checkpoint's codes (u8 [E, N, K/2], column 2i in the low
+    nibble of byte i) and scales (bf16 [E, N, K/group])."""
+    E, N, K2 = _dims(codes, 3, "codes")
+    _shape(Wp, w4_packed_shape(E, N, 2 * K2, group), "Wp")
+    _shape(scale, (E, N, 2 * K2 // group), "scale")
+    _check("moe_pack_weights_w4", lib().moe_pack_weights_w4(
+        _ptr(codes, torch.uint8, "codes"), _ptr(scale, torch.bfloat16, "scale"), E, N, 2 * K2, group,
+        _ptr(Wp, torch.uint8, "Wp"), _stream(stream)))
+
+
+def moe_dequant_weights_w4(Wp: torch.Tensor, group: int, W: torch.Tensor, stream=None):
+    """The values that laid-out codes stand for, f32 [E, N, K] (exact)."""
+    E, N, K = _dims(W, 3, "W")
+    _shape(Wp, w4_packed_shape(E, N, K, group), "Wp")
+    _check("moe_dequant_weights_w4", lib().moe_dequant_weights_w4(
+        _ptr(Wp, torch.uint8, "Wp"), E, N, K, group, _ptr(W, torch.float32, "W"), _stream(stream)))
+
+
+def moe_matvec_w4(x: torch.Tensor, Wp: torch.Tensor, group: int, y: torch.Tensor, status: torch.Tensor, stream=None):
+    """y[t] = W x[t] for up to 64 tokens and one laid-out 4-bit matrix."""
+    T, K = _dims(x, 2, "x")
+    N = _dims(y, 2, "y")[1]
+    _shape(y, (T, N), "y")
+    _shape(Wp, w4_packed_shape(1, N, K, group)[1:], "Wp")
+    _status(status)
+    _check("moe_matvec_w4", lib().moe_matvec_w4(
+        _ptr(x, torch.bfloat16, "x"), T, K, _ptr(Wp, torch.uint8, "Wp"), N, group, _ptr(y, torch.bfloat16, "y"),
+        _ptr(status, torch.int32, "status"), _stream(stream)))
+
+
+def moe_layer_few_ws_bytes(T: int, k: int, E: int, H: int, F: int) -> int:
+    """Workspace of moe_layer_few; zero it (or its first 256 bytes) once."""
+    out = ctypes.c_size_t()
+    _check("moe_layer_few_ws_bytes", lib().moe_layer_few_ws_bytes(T, k, E, H, F, ctypes.byref(out)))
+    return out.value
+
+
+def moe_layer_few(x: torch.Tensor, W1: torch.Tensor, W1_scale: Optional[torch.Tensor], W2: torch.Tensor,
+                  W2_scale: Optional[torch.Tensor], topk_ids: torch.Tensor, topk_w: torch.Tensor, out: torch.Tensor,
+                  ws: torch.Tensor, status: torch.Tensor, router: Optional[torch.Tensor] = None, group: int = 0,
+                  stream=None):
+    """A whole MoE layer for up to 64 tokens: router, gate and up projections,
+    silu(gate) * up, down projection, weighted sum.  group 0: FP8 weights and
+    scales as moe_quant_weights writes them (W1 [E, 2F, H], W2 [E, H, F]);
+    group 32, 64 or 128: laid-out 4-bit weights of those shapes, scales None.
+    router (bf16 [E, H]): topk_ids and topk_w are written; without it they are
+    inputs (a negative id: no route)."""
+    T, H = _dims(x, 2, "x")
+    k = _dims(topk_ids, 2, "topk_ids")[1]
+    if group == 0:
+        E, F2, _ = _dims(W1, 3, "W1")
+        F = F2 // 2
+        _shape(W1, (E, 2 * F, H), "W1")
+        _shape(W2, (E, H, F), "W2")
+        if W1_scale is None or W2_scale is None:
+            raise ValueError("FP8 weights need W1_scale and W2_scale")
+        _shape(W1_scale, (E, F2 // 128, H // 128), "W1_scale")
+        _shape(W2_scale, (E, H // 128, F // 128), "W2_scale")
+    else:
+        E = _dims(W1, 4, "W1")[0]
+        F = 8 * W1.shape[1]
+        _shape(W1, w4_packed_shape(E, 2 * F, H, group), "W1")
+        _shape(W2, w4_packed_shape(E, H, F, group), "W2")
+        if W1_scale is not None or W2_scale is not None:
+            raise ValueError("4-bit weights carry their scales: W1_scale and W2_scale must be None")
+    _shape(topk_ids, (T, k), "topk_ids")
+    _shape(topk_w, (T, k), "topk_w")
+    _shape(out, (T, H), "out")
+    _shape(router, (E, H), "router")
+    _status(status)
+    _check("moe_layer_few", lib().moe_layer_few(
+        _ptr(x, torch.bfloat16, "x"), T, H, _ptr(router, torch.bfloat16, "router"), E, k, _ptr(W1, torch.uint8, "W1"),
+        _ptr(W1_scale, torch.float32, "W1_scale"), _ptr(W2, torch.uint8, "W2"),
+        _ptr(W2_scale, torch.float32, "W2_scale"), F, group, _ptr(topk_ids, torch.int32, "topk_ids"),
+        _ptr(topk_w, torch.float32, "topk_w"), _ptr(out, torch.bfloat16, "out"), _ptr(ws, None, "ws"),
+        ws.numel() * ws.element_size(), _ptr(status, torch.int32, "status"), _stream(stream)))

@@ -401,6 +401,89 @@ int moe_quant_weights(const uint16_t* W, int E, int N, int H, uint8_t* Wq, float
 int moe_dequant_rows(const uint8_t* A, const float* A_scale, int H, const moe_layout_t* L,
                      uint16_t* Y, moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Decoding: few tokens, so the time is that of reading the weights once.
+ *
+ * 4-bit weights with group scales.  A matrix [N, K] has a code c in 0..15 per
+ * value and a bf16 scale per row and group of 32, 64 or 128 columns; a code
+ * stands for (c - 8) * scale.  It is kept laid out in tiles of 16 rows x 128
+ * columns, row-major over the tiles, each one run of 1024 + 32 * (128 / group)
+ * bytes: byte 4 * (4 * (32 * half + 4 * g + t) + j) + b of the codes holds, in
+ * its low and high nibble (i = 0, 1), row 8 * half + g and column
+ * 32 j + 8 t + 4 (b % 2) + 2 i + b / 2 of the tile; then 128 / group rows of 16 bf16
+ * scales, one per matrix row.  What the matrix lacks of a whole tile has
+ * code 8 and scale 0.  E matrices follow one another.
+ * Limits: group 32, 64 or 128; 1 <= N <= MOE_W4_MAX_N; K a multiple of the
+ * group, K <= MOE_W4_MAX_K; E <= 65535.  Laid-out buffers are 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+#define MOE_W4_MAX_N (1 << 20)
+#define MOE_W4_MAX_K 32768
+
+/* Bytes of one laid-out matrix: ceil(N/16) * ceil(K/128) tiles. */
+int moe_w4_packed_bytes(int N, int K, int group, size_t* bytes);
+
+/* moe_quant_weights_w4: bf16 weights [E, N, K] -> laid-out 4-bit codes and
+ * scales.  Per row and group: scale = bf16(max|w| / 7); code = 8 + rint(w /
+ * scale) (fp32 division, ties to even) clamped to [0, 15]; scale 0 gives
+ * code 8.  A group that holds an infinity or a NaN gets a scale that is
+ * not finite. */
+int moe_quant_weights_w4(const uint16_t* W, int E, int N, int K, int group, uint8_t* Wp,
+                         moe_stream_t stream);
+
+/* moe_pack_weights_w4: lay out a checkpoint's codes (u8 [E, N, K/2], column
+ * 2i in the low nibble of byte i) and scales (bf16 [E, N, K/group]). */
+int moe_pack_weights_w4(const uint8_t* codes, const uint16_t* scale, int E, int N, int K, int group,
+                        uint8_t* Wp, moe_stream_t stream);
+
+/* moe_dequant_weights_w4: the values (c - 8) * scale, device f32 [E, N, K]
+ * (exact). */
+int moe_dequant_weights_w4(const uint8_t* Wp, int E, int N, int K, int group, float* W,
+                           moe_stream_t stream);
+
+/* moe_matvec_w4: y[t, n] = bf16( sum_k x[t, k] * (c[n, k] - 8) * scale[n, k / group] ),
+ * fp32 accumulation, one rounding.  For what stands beside the experts: a
+ * shared expert's projections, the vocabulary.
+ *   x  device bf16 [T, K], 1 <= T <= MOE_FEW_MAX_TOKENS, 16-byte aligned.
+ *   Wp one laid-out matrix; y device bf16 [T, N].
+ * A bounded wait that gives up writes MOE_ERR_TIMEOUT to *status. */
+#define MOE_FEW_MAX_TOKENS 64
+#define MOE_FEW_MAX_PAIRS 1024
+int moe_matvec_w4(const uint16_t* x, int T, int K, const uint8_t* Wp, int N, int group, uint16_t* y,
+                  int32_t* status, moe_stream_t stream);
+
+/* moe_layer_few: a whole MoE layer for a few tokens,
+ *   logits[t, e] = sum_h x[t, h] * router[e, h]           (fp32)
+ *   (id, w)[t, j] = the k largest logits, softmax over them (moe_router_topk's rule)
+ *   g, u = rows [0, F) and [F, 2F) of W1[id] times x[t];  a = g / (1 + exp(-g)) * u
+ *   out[t, :] = bf16( sum_j w[t, j] * W2[id[t, j]] * a[t, j] )
+ * with each expert's weights read once however many of the tokens use it.
+ * Products and sums are fp32; w * a is rounded to bf16 once, for the
+ * second product's operands.
+ *   x        device bf16 [T, H].
+ *   router   device bf16 [E, H], or NULL: topk_ids and topk_w are then inputs.
+ *   topk_ids device int32 [T, k], topk_w device f32 [T, k]: written where router
+ *            is given.  As inputs: a negative id means "no route" and is
+ *            skipped; an id >= E is skipped and raises MOE_ERR_EXPERT_ID in
+ *            *status.  A token with no route left gets zeros.  A token may
+ *            name an expert twice.
+ *   W1, W2   group 0: e4m3 codes u8 [E, 2F, H] and [E, H, F] with W1_scale f32
+ *            [E, 2F/128, H/128] and W2_scale [E, H/128, F/128], as
+ *            moe_quant_weights writes them (the buffers that GEMM1 reads).
+ *            group 32, 64, 128: laid-out 4-bit matrices of the same shapes,
+ *            scales NULL.
+ *   out      device bf16 [T, H].
+ *   ws       device workspace of moe_layer_few_ws_bytes, 256-byte aligned.  Its
+ *            first 256 bytes are zero on the first call; every call leaves
+ *            them zero.
+ * Limits: T <= MOE_FEW_MAX_TOKENS, T * k <= MOE_FEW_MAX_PAIRS, k <= 32,
+ * k <= E <= 1024, H and F multiples of 128 up to 32768; x, router, W1, W2, their
+ * scales and out 16-byte aligned. */
+int moe_layer_few_ws_bytes(int T, int k, int E, int H, int F, size_t* bytes);
+int moe_layer_few(const uint16_t* x, int T, int H, const uint16_t* router, int E, int k, const uint8_t* W1,
+                  const float* W1_scale, const uint8_t* W2, const float* W2_scale, int F, int group,
+                  int32_t* topk_ids, float* topk_w, uint16_t* out, void* ws, size_t ws_bytes,
+                  int32_t* status, moe_stream_t stream);
+
 /* Number of SMs of the current device (0 on error): the persistent grids'
  * size. */
 int moe_device_sm_count(void);
