@@ -35,6 +35,7 @@
 // orders like the expert id.
 #include "common.cuh"
 #include "host_util.h"
+#include "router.cuh"
 
 namespace moe {
 
@@ -535,8 +536,7 @@ __global__ void __launch_bounds__(kLayoutThreads) route_layout_kernel(LayoutArgs
 
 // ---------------------------------------------------------------- router helper
 
-// One warp per token: k rounds of a warp-wide arg-max (largest logit, ties to
-// the lower expert id), then softmax weights over the selected logits.
+// One warp per token (warp_topk: the selection and its weights).
 template <int VPL>
 __global__ void __launch_bounds__(256) router_topk_kernel(const float* __restrict__ logits, int T,
                                                           int E, int k, int32_t* __restrict__ ids,
@@ -544,43 +544,11 @@ __global__ void __launch_bounds__(256) router_topk_kernel(const float* __restric
   const int lane = threadIdx.x & 31;
   const int warps = blockDim.x >> 5;
   for (int t = blockIdx.x * warps + (threadIdx.x >> 5); t < T; t += gridDim.x * warps) {
-    float v[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = i * 32 + lane;
-      v[i] = e < E ? logits[(size_t)t * E + e] : -INFINITY;
-    }
-    bool used[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) used[i] = (i * 32 + lane) >= E;
-    float sel_l0 = 0.f, my_l = 0.f;
-    int my_id = 0;
-    for (int j = 0; j < k; ++j) {
-      float best = -INFINITY;
-      int bid = 0x7fffffff;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = i * 32 + lane;
-        if (!used[i] && (v[i] > best || (v[i] == best && e < bid))) { best = v[i]; bid = e; }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float ob = __shfl_xor_sync(0xffffffffu, best, o);
-        const int oi = __shfl_xor_sync(0xffffffffu, bid, o);
-        if (ob > best || (ob == best && oi < bid)) { best = ob; bid = oi; }
-      }
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i * 32 + lane == bid) used[i] = true;
-      if (j == 0) sel_l0 = best;
-      if (lane == j) { my_l = best; my_id = bid; }
-    }
-    const float ex = lane < k ? expf(my_l - sel_l0) : 0.f;
-    float sum = 0.f;
-    for (int j = 0; j < k; ++j) sum += __shfl_sync(0xffffffffu, ex, j);   // slots in order
+    float weight;
+    const int id = warp_topk<VPL>(logits + (size_t)t * E, E, k, lane, &weight);
     if (lane < k) {
-      ids[(size_t)t * k + lane] = my_id;
-      w[(size_t)t * k + lane] = ex / sum;
+      ids[(size_t)t * k + lane] = id;
+      w[(size_t)t * k + lane] = weight;
     }
   }
 }
