@@ -19,8 +19,27 @@ extern "C" int moe_matvec_w4(const uint16_t* x, int T, int K, const uint8_t* Wp,
   return group == 32 ? launch_matvec<32>(a, nsm, s) : group == 64 ? launch_matvec<64>(a, nsm, s) : launch_matvec<128>(a, nsm, s);
 }
 
-// Workspace: 256 bytes of counters, the logits, then the activations.
-static size_t few_logits_bytes(int T, int E) { return ((size_t)T * E * 4 + 255) / 256 * 256; }
+// Workspace: 256 bytes of counters, then what LayerArgs names, each at a multiple of 256 bytes.
+struct FewWorkspace {
+  size_t logits, x8, h8, h, bytes;
+  FewWorkspace(int T, int k, int E, int H, int F) {
+    size_t at = 256;
+    auto take = [&at](size_t n) { const size_t p = at; at += (n + 255) / 256 * 256; return p; };
+    logits = take((size_t)T * E * 4);
+    x8 = take((size_t)T * (H / 128) * kTokenRecord);
+    h8 = take((size_t)T * k * (F / 128) * kTokenRecord);
+    h = take((size_t)T * k * F * 4);
+    bytes = at;
+  }
+};
+
+// The FP8 weights of all experts as {128 bytes, rows, slices of 128 columns}; a box
+// holds 16 rows of up to 8 slices.
+static bool weight_map(CUtensorMap* map, const uint8_t* W, int E, int N, int K) {
+  const uint64_t dims[3] = {128, (uint64_t)E * N, (uint64_t)(K / 128)}, strides[2] = {(uint64_t)K, 128};
+  const uint32_t box[3] = {128, 16, (uint32_t)std::min(8, K / 128)};
+  return encode_u8_map(map, W, 3, dims, strides, box);
+}
 
 static int check_few(int T, int k, int E, int H, int F) {
   if (T < 1 || T > MOE_FEW_MAX_TOKENS || k < 1 || k > 32 || T * k > MOE_FEW_MAX_PAIRS || E < k || E > 1024) return MOE_ERR_INVALID_ARG;
@@ -32,7 +51,7 @@ extern "C" int moe_layer_few_ws_bytes(int T, int k, int E, int H, int F, size_t*
   if (!bytes) return MOE_ERR_INVALID_ARG;
   const int rc = check_few(T, k, E, H, F);
   if (rc) return rc;
-  *bytes = 256 + few_logits_bytes(T, E) + (size_t)T * k * F * 2;
+  *bytes = FewWorkspace(T, k, E, H, F).bytes;
   return MOE_OK;
 }
 
@@ -51,18 +70,24 @@ extern "C" int moe_layer_few(const uint16_t* x, int T, int H, const uint16_t* ro
     return MOE_ERR_INVALID_ARG;
   const int nsm = device_sm_count();
   if (nsm <= 0) return MOE_ERR_CUDA;
-  LayerArgs a;
+  LayerArgs a = {};
   a.x = x; a.router = router;
   a.W1 = W1; a.W2 = W2; a.W1_scale = W1_scale; a.W2_scale = W2_scale;
   a.ids = topk_ids; a.w = topk_w; a.out = out;
   a.counters = reinterpret_cast<int32_t*>(ws);
-  a.logits = reinterpret_cast<float*>((char*)ws + 256);
-  a.h = reinterpret_cast<uint16_t*>((char*)ws + 256 + few_logits_bytes(T, E));
+  const FewWorkspace at(T, k, E, H, F);
+  char* base = reinterpret_cast<char*>(ws);
+  a.logits = reinterpret_cast<float*>(base + at.logits);
+  a.x8 = reinterpret_cast<uint8_t*>(base + at.x8);
+  a.h8 = reinterpret_cast<uint8_t*>(base + at.h8);
+  a.h = reinterpret_cast<float*>(base + at.h);
   a.status = status;
   a.T = T; a.H = H; a.E = E; a.k = k; a.F = F;
   cudaStream_t s = (cudaStream_t)stream;
   switch (group) {
-    case 0: return launch_layer<0>(a, nsm, s);
+    case 0:
+      if (!weight_map(&a.map1, W1, E, 2 * F, H) || !weight_map(&a.map2, W2, E, H, F)) return MOE_ERR_CUDA;
+      return launch_layer<0>(a, nsm, s);
     case 32: return launch_layer<32>(a, nsm, s);
     case 64: return launch_layer<64>(a, nsm, s);
     default: return launch_layer<128>(a, nsm, s);

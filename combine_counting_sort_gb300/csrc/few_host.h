@@ -5,7 +5,7 @@
 
 namespace moe {
 
-constexpr int kFewMinSmem = 200 * 1024;   // what the largest stages and tables need
+constexpr int kFewMinSmem = 227 * 1024;   // room for a ring beside the largest tables
 
 struct MatvecArgs {
   const uint16_t* x;
@@ -17,22 +17,62 @@ struct MatvecArgs {
 };
 
 struct LayerArgs {
+  CUtensorMap map1, map2;   // FP8 weights: 128 bytes x 16 rows x 128-column slices
   const uint16_t *x, *router;
   const uint8_t *W1, *W2;
   const float *W1_scale, *W2_scale;
   int32_t* ids;
   float* w;
   uint16_t* out;
-  int32_t* counters;   // [0] blocks done with the logits, [1] with the activations, [2] with everything
+  int32_t* counters;   // arrivals of the grid's blocks at its meetings, and at the end
   float* logits;       // [T, E]
-  uint16_t* h;         // [rows, F] bf16 activations times their route's weight
+  uint8_t *x8, *h8;    // token records of x [T] and of the activations [T k], K / 128 of 272 bytes each
+  float* h;            // [T k, F] activations times their route's weight
   int32_t* status;
   int T, H, E, k, F;
   uint32_t smem_bytes;
 };
 
+// Bytes of the record that holds 128 values of a token as the layer's MMAs take
+// them: f16 values, the scale, and 12 bytes of alignment.
+constexpr int kTokenRecord = 272;
+
 // GROUP 0: FP8 (the layer only); 32, 64, 128: 4-bit.
 template <int GROUP> int launch_matvec(const MatvecArgs& a, int nsm, cudaStream_t s);
 template <int GROUP> int launch_layer(const LayerArgs& a, int nsm, cudaStream_t s);
+
+// Row tiles per item: the fewest (rounds over the SMs) x (row tiles), and of
+// those the most row tiles, since a stage's tokens are shared by its row tiles.
+inline int few_row_tiles(int tiles, int nsm) {
+  int best = 1, cost = 1 << 30;
+  for (int rt = 1; rt <= 3; ++rt) {
+    const int groups = (tiles + rt - 1) / rt, c = (groups + nsm - 1) / nsm * rt;
+    if (c <= cost) { cost = c; best = rt; }
+  }
+  return best;
+}
+
+// Launch with all the shared memory a block can have.
+template <class Kernel, class Args>
+int few_launch(Kernel kernel, Args& a, int threads, int blocks, bool cooperative, cudaStream_t s) {
+  int dev = 0, smem = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) return MOE_ERR_CUDA;
+  if (smem < kFewMinSmem) return MOE_ERR_UNSUPPORTED;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return MOE_ERR_CUDA;
+  auto args = a;
+  args.smem_bytes = smem;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = cooperative ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
 
 }  // namespace moe

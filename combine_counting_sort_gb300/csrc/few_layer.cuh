@@ -1,0 +1,684 @@
+// few_layer.cuh: a whole MoE layer for a few tokens, in one launch.
+//
+// Both products run on f16 MMAs with fp32 sums.  An e4m3 code is one of the f16
+// values (one conversion per two codes).  A 4-bit code takes one AND: the bits
+// 0x000c and 0x00c0 read as f16 are c * 2^-24 and 16 c * 2^-24 (f16 is linear from its
+// subnormals to the end of the first binade), so the four pairs of a word's
+// eight codes take four ANDs and a shift; token values that meet a code with
+// the 16 are divided by it, and the sums are multiplied by 2^24 at the end.  The 8
+// that every 4-bit code has too much is taken out by the tensor core: -8 times
+// the tokens, once per stage and not per row tile.
+//
+// A token's 128 values share a power of two 2^e that brings their largest magnitude
+// into [2^14, 2^15): a bf16 value is then an f16 value as it is, down to 2^-28 of the
+// block's largest (2^-24 where divided by 16), and smaller ones are within 2^-35 of it,
+// below the rounding of an fp32 sum.  The activations between the products,
+// fp32 values, are rounded to f16's 11 bits this way.
+//
+// What bounds it: memory.  Per tile of 16 x 128 weights a warp spends 40 ANDs and
+// shifts (4-bit) or 32 conversions (FP8), both at 64 lanes a clock, 8 MMAs per 8 tokens
+// and some 30 other instructions.  Widening 4-bit codes by the usual offset and
+// subtraction takes 88, FP8 codes to bf16 128, which is longer than the
+// tile's bytes take from memory.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "few.cuh"
+#include "few_host.h"
+#include "router.cuh"
+
+namespace moe {
+
+template <int GROUP>
+struct LayerForm {
+  static constexpr bool kW4 = GROUP != 0;
+  static constexpr int kTile = w4_tile_bytes(kW4 ? GROUP : 128);
+  // 4-bit: the slices' tiles as they lie in memory.  FP8: per slice 16 rows of
+  // 128 bytes in TMA's 128-byte swizzle, which ldmatrix reads without bank conflicts.
+  static constexpr int kRowTile = kFewWarps * (kW4 ? kTile : 2048);
+  static constexpr int kAlign = kW4 ? 128 : 1024;             // of a stage
+  static constexpr int kScaleBytes = kW4 ? 0 : 4 * kFewWarps; // per row tile
+  // arrivals that complete a stage: weights, tokens, and the lanes' scale copies
+  static constexpr int kArrivals = kW4 ? 2 : 34;
+  static constexpr float kSumScale = kW4 ? 0x1p24f : 1.f;     // what the sums lack
+};
+// A token's records in a stage, 64 mod 128 bytes apart: the 2 tokens x 64 bytes of a
+// quarter-warp's reads fall on distinct banks.
+constexpr int kTokPitch = kFewWarps * kTokenRecord + 64;
+
+// ---------------------------------------------------------------- token records
+
+// Four consecutive values v (columns 4 lane ..) of a warp's 128 into the record at
+// `rec`: the 16 bytes at 64 i + 16 t are the B operands that lane t of a column reads for
+// the MMAs 2i and 2i + 1.  4-bit: columns 32 i + 8 t .., the pairs that meet high nibbles
+// divided by 16.  FP8: columns 32 i + 4 t .. and 32 i + 16 + 4 t .., which ldmatrix gives
+// to lane t.
+template <bool W4>
+MOE_DEV void put_record(const float (&v)[4], uint8_t* rec, int lane) {
+  uint32_t big = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) big = max(big, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  big = __reduce_max_sync(0xffffffffu, big);
+  const int e = max((int)(big >> 23) - 127 - 14, -125);
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23), down2 = W4 ? down * 0.0625f : down;
+  const __half2 a = __floats2half2_rn(v[0] * down, v[1] * down), b = __floats2half2_rn(v[2] * down2, v[3] * down2);
+  const int at = W4 ? 8 * lane : 64 * (lane >> 3) + 16 * (lane & 3) + 8 * ((lane >> 2) & 1);
+  *reinterpret_cast<uint2*>(rec + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  if (lane == 0) *reinterpret_cast<float4*>(rec + 256) = make_float4(__uint_as_float((uint32_t)(127 + e) << 23), 0.f, 0.f, 0.f);
+}
+
+// ---------------------------------------------------------------- products
+
+// The codes of a row tile's slice: 4-bit: the lane's words of row g (0-3) and of row
+// g + 8 (4-7).  FP8: words m and m + 8 are columns 16 m + 4 t .. of row g and of row g + 8.
+template <int GROUP>
+MOE_DEV void load_codes(uint32_t wst, int slice, int lane, uint32_t (&c)[GROUP ? 8 : 16]) {
+  using F = LayerForm<GROUP>;
+  if constexpr (F::kW4) {
+    const uint32_t p = wst + slice * F::kTile + lane * 16;
+    const uint4 l = lds128(p), h = lds128(p + 512);
+    c[0] = l.x; c[1] = l.y; c[2] = l.z; c[3] = l.w;
+    c[4] = h.x; c[5] = h.y; c[6] = h.z; c[7] = h.w;
+  } else {
+    const uint32_t row = wst + slice * 2048 + (lane & 15) * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)   // 16-byte chunks 2j (lanes 0-15 give the rows' addresses) and 2j + 1
+      asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(c[2 * j]), "=r"(c[2 * j + 8]), "=r"(c[2 * j + 1]), "=r"(c[2 * j + 9])
+                   : "r"(row + (((2 * j + (lane >> 4)) ^ (lane & 7)) << 4)) : "memory");
+  }
+}
+
+// Two e4m3 codes as two f16 values.
+MOE_DEV uint32_t widen_e4m3(uint32_t codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+  return (uint32_t)h.x | (uint32_t)h.y << 16;
+}
+
+// The A operand of MMA m of a slice.
+template <int GROUP>
+MOE_DEV void widen(const uint32_t (&c)[GROUP ? 8 : 16], int m, uint32_t (&a)[4]) {
+  if constexpr (GROUP != 0) {
+    const uint32_t l = c[m >> 1] >> (m & 1 ? 8 : 0), h = c[4 + (m >> 1)] >> (m & 1 ? 8 : 0);
+    a[0] = l & 0x000F000Fu;
+    a[1] = h & 0x000F000Fu;
+    a[2] = l & 0x00F000F0u;
+    a[3] = h & 0x00F000F0u;
+  } else {
+    a[0] = widen_e4m3(c[m] & 0xFFFFu);
+    a[1] = widen_e4m3(c[m + 8] & 0xFFFFu);
+    a[2] = widen_e4m3(c[m] >> 16);
+    a[3] = widen_e4m3(c[m + 8] >> 16);
+  }
+}
+
+// The scales of a row tile's slice for rows g and g + 8, per group.
+template <int GROUP>
+MOE_DEV void load_scales(uint32_t wst, uint32_t scales, int rt, int slice, int lane, float (&s)[FewGroups<GROUP>::kCount][2]) {
+  using F = LayerForm<GROUP>;
+#pragma unroll
+  for (int q = 0; q < FewGroups<GROUP>::kCount; ++q) {
+    if (F::kW4) {
+      const uint32_t sc = wst + slice * F::kTile + kW4Codes + 32 * q + 2 * (lane >> 2);
+      s[q][0] = lds_bf16(sc);
+      s[q][1] = lds_bf16(sc + 16);
+    } else {
+      s[q][0] = s[q][1] = lds_f32(scales + 4 * (kFewWarps * rt + slice));
+    }
+  }
+}
+
+// A block of 8 tokens of a stage: the lane's B operands (token 8 j + lane / 4) and the
+// scales of its sums' tokens (8 j + 2 (lane % 4) and the next).  Bit t of `mask` says
+// that token t is there, and the number of bits below it which row of the stage it has.
+MOE_DEV void load_block(uint32_t tokens, uint64_t mask, int j, int lane, uint32_t (&b)[16], float (&xs)[2]) {
+  const int tb = 8 * j + (lane >> 2), tc = 8 * j + 2 * (lane & 3);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) b[i] = 0;
+  if ((mask >> tb) & 1) {
+    const uint32_t p = tokens + __popcll(mask & ((1ull << tb) - 1)) * kTokPitch + (lane & 3) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = lds128(p + 64 * i);
+      b[4 * i] = v.x; b[4 * i + 1] = v.y; b[4 * i + 2] = v.z; b[4 * i + 3] = v.w;
+    }
+  }
+  const uint32_t p = tokens + __popcll(mask & ((1ull << tc) - 1)) * kTokPitch + 256;
+  xs[0] = (mask >> tc) & 1 ? lds_f32(p) : 0.f;
+  xs[1] = (mask >> tc) & 2 ? lds_f32(p + ((mask >> tc) & 1) * kTokPitch) : 0.f;
+  __syncwarp();
+}
+
+// The products of RT row tiles with NT blocks of tokens, added to acc (rows g and g + 8
+// of the lane's two tokens of a block, from block j0).  The MMAs of the row tiles,
+// and those of the eights, are chains of their own: an MMA's result takes some 20
+// cycles, and with two warps to a scheduler nothing else would fill them.
+template <int GROUP, int RT, int NT, int NB>
+MOE_DEV void block_products(const uint32_t (&c)[RT][GROUP ? 8 : 16], const float (&s)[RT][FewGroups<GROUP>::kCount][2],
+                            const uint32_t (&b)[NT][16], const float (&xs)[NT][2], float (&acc)[RT][NB][4], int j0) {
+  constexpr int kCount = FewGroups<GROUP>::kCount, kMmas = 8 / kCount;
+  const uint32_t minus8[4] = {0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u};   // -8, -128 times 2^-24
+  float v[RT][NT][4];
+#pragma unroll
+  for (int q = 0; q < kCount; ++q) {
+    float part[RT][NT][4] = {}, eights[NT][4] = {};
+#pragma unroll
+    for (int m = q * kMmas; m < (q + 1) * kMmas; ++m) {
+      if (GROUP != 0) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mma_f16(eights[j], minus8, b[j][2 * m], b[j][2 * m + 1]);
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        uint32_t a[4];
+        widen<GROUP>(c[rt], m, a);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mma_f16(part[rt][j], a, b[j][2 * m], b[j][2 * m + 1]);
+      }
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = GROUP != 0 ? part[rt][j][i] + eights[j][i] : part[rt][j][i];
+          v[rt][j][i] = q == 0 ? p * s[rt][q][i >> 1] : fmaf(p, s[rt][q][i >> 1], v[rt][j][i]);
+        }
+  }
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[rt][j0 + j][i] = fmaf(v[rt][j][i], xs[j][i & 1], acc[rt][j0 + j][i]);
+}
+
+// One stage's slice of a warp: RT row tiles times the tokens of `mask`, which lie in the
+// first NT of NB blocks of 8.  With many blocks those without a token are passed over.
+// A stage with fewer row tiles holds older ones in their place, whose sums are not used.
+template <int GROUP, int RT, int NT, int NB>
+MOE_DEV void layer_slice(uint32_t st, uint32_t scales, uint32_t tokens, uint64_t mask, int slice, int lane, float (&acc)[RT][NB][4]) {
+  using F = LayerForm<GROUP>;
+  uint32_t c[RT][GROUP ? 8 : 16];
+  float s[RT][FewGroups<GROUP>::kCount][2];
+  tokens += slice * kTokenRecord;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    load_codes<GROUP>(st + rt * F::kRowTile, slice, lane, c[rt]);
+    load_scales<GROUP>(st + rt * F::kRowTile, scales, rt, slice, lane, s[rt]);
+  }
+  if constexpr (NT <= 2) {
+    uint32_t b[NT][16];
+    float xs[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) load_block(tokens, mask, j, lane, b[j], xs[j]);
+    block_products<GROUP, RT, NT, NB>(c, s, b, xs, acc, 0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      if ((mask >> (8 * j)) & 0xFF) {
+        uint32_t b[1][16];
+        float xs[1][2];
+        load_block(tokens, mask, j, lane, b[0], xs[0]);
+        block_products<GROUP, RT, 1, NB>(c, s, b, xs, acc, j);
+      }
+  }
+}
+
+// ---------------------------------------------------------------- copies
+
+struct LayerMatrix {
+  const uint8_t* p;        // 4-bit: the expert's tiles
+  const CUtensorMap* map;  // FP8: all experts' rows
+  const float* scale;
+  int row0, K;             // FP8: the expert's first row
+};
+
+// Copy `tiles` row tiles (the rt-th at row tile tile0 + rt * step) of the 128-column
+// slices [kt0, kt0 + nk) into the stage at `st`; whole warp.
+template <int GROUP>
+MOE_DEV void copy_weights(const LayerMatrix& W, int tile0, int step, int tiles, int kt0, int nk, uint32_t st, uint32_t scales,
+                          uint32_t bar, int lane) {
+  using F = LayerForm<GROUP>;
+  const int KT = W.K / 128;
+  if (F::kW4) {
+    if (lane == 0) mbar_arrive_expect_tx(bar, tiles * nk * F::kTile);
+    __syncwarp();
+    if (lane < tiles) bulk_load(st + lane * F::kRowTile, W.p + ((size_t)(tile0 + lane * step) * KT + kt0) * F::kTile, nk * F::kTile, bar);
+  } else {
+    // a box of min(8, K / 128) slices; slices past K count as bytes and are filled with zeros
+    if (lane == 0) mbar_arrive_expect_tx(bar, tiles * min(kFewWarps, KT) * 2048);
+    __syncwarp();
+    if (lane < tiles) tma_load_3d(st + lane * F::kRowTile, W.map, 0, W.row0 + (tile0 + lane * step) * 16, kt0, bar);
+    for (int i = lane; i < tiles * kFewWarps; i += 32) {
+      const int rt = i / kFewWarps, kt = i % kFewWarps;
+      const bool on = kt < nk;
+      const float* src = W.scale + (size_t)((tile0 + rt * step) >> 3) * KT + (on ? kt0 + kt : kt0);
+      cp_async4(scales + 4 * i, src, on ? 4 : 0);
+    }
+    cp_async_arrive(bar);
+  }
+}
+
+// Copy the records [kt0, kt0 + nk) of `cols` tokens, token c's at record_of(c).
+template <class RecordOf>
+MOE_DEV void copy_tokens(RecordOf record_of, int cols, int kt0, int nk, uint32_t tok, uint32_t bar, int lane) {
+  if (lane == 0) mbar_arrive_expect_tx(bar, cols * nk * kTokenRecord);
+  __syncwarp();
+  if (lane < cols) bulk_load(tok + lane * kTokPitch, record_of(lane) + (size_t)kt0 * kTokenRecord, nk * kTokenRecord, bar);
+}
+
+// ---------------------------------------------------------------- routes
+
+// Tables of the routes in shared memory, sized by the P = T k pairs.  A segment is
+// one expert and up to 16 of the tokens routed to it; row r of the activations
+// belongs to one (token, expert).
+struct FewTables {
+  uint64_t* seg_mask;
+  int *seg_expert, *seg_row;
+  float* row_weight;
+  uint8_t* row_token;
+  MOE_DEV FewTables(unsigned char* p, int P) {
+    seg_mask = reinterpret_cast<uint64_t*>(p);
+    seg_expert = reinterpret_cast<int*>(seg_mask + P);
+    seg_row = seg_expert + P;
+    row_weight = reinterpret_cast<float*>(seg_row + P);
+    row_token = reinterpret_cast<uint8_t*>(row_weight + P);
+  }
+};
+
+// logits[t, e] for the experts of this block: each warp takes every eighth chunk of
+// 256 columns of the expert's row, four tokens at a time; the partial sums meet in
+// shared memory in the warps' order.
+MOE_DEV void few_logits(const LayerArgs& A, float* part, int tid, int warp, int lane) {
+  for (int e = blockIdx.x; e < A.E; e += gridDim.x) {
+    if (warp < kFewWarps) {
+      for (int t0 = 0; t0 < A.T; t0 += 4) {
+        float s[4] = {};
+#pragma unroll 4
+        for (int c = warp * 256 + lane * 8; c < A.H; c += kFewWarps * 256) {
+          const uint4 r = __ldg(reinterpret_cast<const uint4*>(A.router + (size_t)e * A.H + c));
+          const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(A.x + (size_t)min(t0 + j, A.T - 1) * A.H + c));
+            const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[j] = fmaf(bf16_hi(rw[i]), bf16_hi(vw[i]), fmaf(bf16_lo(rw[i]), bf16_lo(vw[i]), s[j]));
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+          if (lane == 0 && t0 + j < A.T) part[warp * A.T + t0 + j] = s[j];
+        }
+      }
+    }
+    __syncthreads();
+    if (tid < A.T) {
+      float s = 0.f;
+      for (int w = 0; w < kFewWarps; ++w) s += part[w * A.T + tid];
+      A.logits[(size_t)tid * A.E + e] = s;
+    }
+    __syncthreads();
+  }
+}
+
+// Bounded wait of one thread for `n` arrivals on a counter of the whole grid.
+MOE_DEV bool grid_wait(const int32_t* ctr, int n, volatile int* abort_flag, int32_t* status) {
+  const uint64_t t0 = globaltimer_ns();
+  while (ld_acquire_gpu(ctr) < n) {
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > kFewTimeoutNs) {
+      *abort_flag = 1;
+      set_status(status, MOE_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// The tables from the pairs' ids and weights (in shared memory).  scratch: E masks,
+// E first rows.
+MOE_DEV void few_tables(const LayerArgs& A, FewShared* sh, const FewTables& tb, const int* ids, const float* w,
+                        unsigned char* scratch, int tid, int warp, int lane) {
+  const int P = A.T * A.k;
+  uint64_t* mask = reinterpret_cast<uint64_t*>(scratch);
+  int* first = reinterpret_cast<int*>(mask + A.E);
+  for (int e = tid; e < A.E; e += kFewThreads) mask[e] = 0;
+  __syncthreads();
+  for (int p = tid; p < P; p += kFewThreads) {
+    const int e = ids[p];
+    if (e >= A.E) {
+      if (blockIdx.x == 0) set_status(A.status, MOE_ERR_EXPERT_ID);
+    } else if (e >= 0) {
+      atomicOr(reinterpret_cast<unsigned long long*>(&mask[e]), 1ull << (p / A.k));   // a set: any order
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int rows = 0, segs = 0, most = 0;
+    for (int e0 = 0; e0 < A.E; e0 += 32) {
+      const int e = e0 + lane;
+      uint64_t m = e < A.E ? mask[e] : 0;
+      const int c = __popcll(m), s = (c + kFewMaxCols - 1) / kFewMaxCols;
+      int incl = c | s << 16;   // at most 1024 rows and 1024 segments
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const int row = rows + (incl & 0xFFFF) - c, seg = segs + (incl >> 16) - s;
+      if (e < A.E) first[e] = row;
+      for (int i = 0; i < s; ++i) {
+        uint64_t take = m;
+        if (__popcll(m) > kFewMaxCols) {
+          take = 0;
+          for (int b = 0; b < kFewMaxCols; ++b) {
+            const uint64_t low = m & (~m + 1);
+            take |= low;
+            m ^= low;
+          }
+        }
+        tb.seg_mask[seg + i] = take;
+        tb.seg_expert[seg + i] = e;
+        tb.seg_row[seg + i] = row + i * kFewMaxCols;
+      }
+      most = max(most, c);
+      const int all = __shfl_sync(0xffffffffu, incl, 31);
+      rows += all & 0xFFFF;
+      segs += all >> 16;
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+      sh->segs = segs;
+      sh->rows = rows;
+      sh->cap = min(most, kFewMaxCols);
+    }
+  }
+  __syncthreads();
+  if (tid < A.T) {   // a token that names an expert again adds to its weight, in slot order
+    for (int j = 0; j < A.k; ++j) {
+      const int e = ids[tid * A.k + j];
+      if (e < 0 || e >= A.E) continue;
+      bool again = false;
+      for (int i = 0; i < j; ++i) again |= ids[tid * A.k + i] == e;
+      const int row = first[e] + __popcll(mask[e] & ((1ull << tid) - 1));
+      tb.row_token[row] = (uint8_t)tid;
+      tb.row_weight[row] = again ? tb.row_weight[row] + w[tid * A.k + j] : w[tid * A.k + j];
+    }
+  }
+}
+
+template <int GROUP>
+MOE_DEV LayerMatrix expert_matrix(const uint8_t* W, const CUtensorMap* map, const float* scale, int e, int N, int K) {
+  if (GROUP != 0) return LayerMatrix{W + (size_t)e * w4_matrix_bytes(N, K, GROUP ? GROUP : 128), nullptr, nullptr, 0, K};
+  return LayerMatrix{nullptr, map, scale + (size_t)e * (N / 128) * (K / 128), e * N, K};
+}
+
+// ---------------------------------------------------------------- the kernel
+
+// One cooperative launch, one block per SM:
+//   tokens to records, and logits; the grid meets; every block selects the
+//   routes for itself and builds the same tables;
+//   gate and up: items (segment, 16 features), the two row tiles of a stage
+//   being the gate's and the up's rows of the same features;
+//   the grid meets, the activations become records, the grid meets again;
+//   meanwhile the ring already fills with the next weights;
+//   down: items (RT2 row tiles of the output), each over all segments with the
+//   sums of every token in registers, so the output is written once, without
+//   atomics, in a fixed order.
+// NB: blocks of 8 tokens that the down sums cover (T <= 8 NB).
+template <int GROUP, int RT2, int NB>
+__global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_constant__ LayerArgs A) {
+  extern __shared__ __align__(1024) unsigned char sm[];
+  using F = LayerForm<GROUP>;
+  constexpr int kRT = RT2 > 2 ? RT2 : 2;
+  FewShared* sh = reinterpret_cast<FewShared*>(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int P = A.T * A.k, HT = A.H / 128, FT = A.F / 128;
+  const FewTables tb(sm + 256, P);
+  const uint32_t after_tables = (256 + P * 21 + 127) & ~127;
+  unsigned char* scratch = sm + after_tables;   // until the ring takes it
+  int* ids = reinterpret_cast<int*>(scratch);
+  float* w = reinterpret_cast<float*>(ids + P);
+  unsigned char* scratch2 = reinterpret_cast<unsigned char*>(w + P);
+
+  if (tid == 0) sh->abort_flag = 0;
+  for (int i = warp * gridDim.x + blockIdx.x; i < A.T * HT; i += (kFewWarps + 1) * gridDim.x) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(A.x + (size_t)i * 128) + lane);   // the tokens' rows are blocks of 128 in a row
+    const float v[4] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)};
+    put_record<F::kW4>(v, A.x8 + (size_t)i * kTokenRecord, lane);
+  }
+  if (A.router) few_logits(A, reinterpret_cast<float*>(scratch), tid, warp, lane);
+  fence_proxy_async_global();   // the records are read by bulk copies
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+    red_release_gpu_add(A.counters, 1);
+    grid_wait(A.counters, gridDim.x, &sh->abort_flag, A.status);
+  }
+  __syncthreads();
+  if (A.router) {
+    for (int t = warp; t < A.T; t += kFewWarps + 1) {
+      float wt;
+      const float* l = A.logits + (size_t)t * A.E;
+      const int id = A.E <= 256 ? warp_topk<8>(l, A.E, A.k, lane, &wt) : warp_topk<32>(l, A.E, A.k, lane, &wt);
+      if (lane < A.k) {
+        ids[t * A.k + lane] = id;
+        w[t * A.k + lane] = wt;
+        if (blockIdx.x == 0) {
+          A.ids[t * A.k + lane] = id;
+          A.w[t * A.k + lane] = wt;
+        }
+      }
+    }
+  } else {
+    for (int p = tid; p < P; p += kFewThreads) {
+      ids[p] = A.ids[p];
+      w[p] = A.w[p];
+    }
+  }
+  __syncthreads();
+  few_tables(A, sh, tb, ids, w, scratch2, tid, warp, lane);
+  fence_proxy_async_shared();   // the ring's copies overwrite the scratch
+  __syncthreads();
+
+  const int segs = sh->segs, cap = max(sh->cap, 1);
+  // the sums' room: two buffers where the columns are few, and 8 columns for the end
+  const int bufs = cap <= 8 ? 2 : 1, red_floats = kFewWarps * 2 * cap * kFewColPitch;
+  float* red = reinterpret_cast<float*>(sm + after_tables);
+  constexpr uint32_t tok = kRT * F::kRowTile;
+  const uint32_t sco = tok + cap * kTokPitch;
+  FewRing ring = few_ring(sm, after_tables + max(bufs * red_floats, kFewWarps * 8 * kFewColPitch) * 4, A.smem_bytes,
+                          (sco + kRT * F::kScaleBytes + F::kAlign - 1) & ~(F::kAlign - 1), F::kArrivals);
+  __syncthreads();
+  const int ftiles = A.F / 16, items1 = segs * ftiles, steps1 = (HT + kFewWarps - 1) / kFewWarps;
+  const int htiles = A.H / 16, items2 = (htiles + RT2 - 1) / RT2, steps2 = (FT + kFewWarps - 1) / kFewWarps;
+
+  if (warp == kFewWarps) {
+    int issued = 0, partial = 0;
+    bool ok = __all_sync(0xffffffffu, !sh->abort_flag);
+    fence_proxy_async_global();
+    for (int item = blockIdx.x; ok && item < items1; item += gridDim.x) {
+      const int seg = item / ftiles, f = item % ftiles;
+      const LayerMatrix W = expert_matrix<GROUP>(A.W1, &A.map1, A.W1_scale, tb.seg_expert[seg], 2 * A.F, A.H);
+      const int cols = __popcll(tb.seg_mask[seg]), row = tb.seg_row[seg];
+      for (int s = 0; s < steps1; ++s) {
+        ok = ring_wait(ring.empty_bar(), ring.phase ^ 1, &sh->abort_flag, A.status);
+        if (!ok) break;
+        const int kt0 = s * kFewWarps, nk = min(kFewWarps, HT - kt0);
+        copy_weights<GROUP>(W, f, ftiles, 2, kt0, nk, ring.stage(), ring.stage() + sco, ring.full_bar(), lane);
+        copy_tokens([&](int c) { return A.x8 + (size_t)tb.row_token[row + c] * HT * kTokenRecord; }, cols, kt0, nk,
+                    ring.stage() + tok, ring.full_bar(), lane);
+        ring.next();
+        ++issued;
+      }
+    }
+    // The down weights do not wait for the activations, only their token copies do.
+    const int mine = items2 > (int)blockIdx.x ? (items2 - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    const int total = mine * segs * steps2;
+    FewRing late = ring;   // the stage whose activations come next
+    int item = blockIdx.x, seg = 0, s = 0, lseg = 0, ls = 0;
+    int begun = 0, filled = 0;
+    bool met = false;
+    while (ok && filled < total) {
+      while (begun < total && (met ? begun == filled : begun < ring.stages)) {
+        ok = ring_wait(ring.empty_bar(), ring.phase ^ 1, &sh->abort_flag, A.status);
+        if (!ok) break;
+        const LayerMatrix W = expert_matrix<GROUP>(A.W2, &A.map2, A.W2_scale, tb.seg_expert[seg], A.H, A.F);
+        const int kt0 = s * kFewWarps, nk = min(kFewWarps, FT - kt0);
+        copy_weights<GROUP>(W, item * RT2, 1, min(RT2, htiles - item * RT2), kt0, nk, ring.stage(), ring.stage() + sco,
+                            ring.full_bar(), lane);
+        ring.next();
+        ++begun;
+        ++issued;
+        ++partial;
+        if (++s == steps2) {
+          s = 0;
+          if (++seg == segs) { seg = 0; item += gridDim.x; }
+        }
+      }
+      if (!ok) break;
+      if (!met) {
+        ok = __all_sync(0xffffffffu, grid_wait(A.counters + 2, gridDim.x, &sh->abort_flag, A.status));
+        if (!ok) break;
+        fence_proxy_async_global();   // the records were written by ordinary stores
+        met = true;
+      }
+      const int kt0 = ls * kFewWarps, nk = min(kFewWarps, FT - kt0);
+      const uint8_t* h8 = A.h8 + (size_t)tb.seg_row[lseg] * FT * kTokenRecord;
+      copy_tokens([&](int c) { return h8 + (size_t)c * FT * kTokenRecord; }, __popcll(tb.seg_mask[lseg]), kt0, nk,
+                  late.stage() + tok, late.full_bar(), lane);
+      late.next();
+      ++filled;
+      --partial;
+      if (++ls == steps2) {
+        ls = 0;
+        if (++lseg == segs) lseg = 0;
+      }
+    }
+    drain(ring, issued, partial, lane);
+  } else {
+    bool ok = consumer_sync_all(!sh->abort_flag);
+    int buf = 0;
+    for (int item = blockIdx.x; ok && item < items1; item += gridDim.x) {
+      const int seg = item / ftiles, f = item % ftiles;
+      const int cols = __popcll(tb.seg_mask[seg]), first = tb.seg_row[seg];
+      float acc[2][2][4] = {};
+      for (int s = 0; s < steps1; ++s, ring.next()) {
+        ok = ring_wait(ring.full_bar(), ring.phase, &sh->abort_flag, A.status);
+        if (!ok) break;
+        if (s * kFewWarps + warp < HT) {
+          const uint32_t st = ring.stage();
+          const uint64_t mask = (1ull << cols) - 1;
+          if (cols <= 8)
+            layer_slice<GROUP, 2, 1>(st, st + sco, st + tok, mask, warp, lane, acc);
+          else
+            layer_slice<GROUP, 2, 2>(st, st + sco, st + tok, mask, warp, lane, acc);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ring.empty_bar());
+      }
+      // with two buffers a warp reaches the next item's meeting only after it has read this one's
+      if (bufs == 1) ok = consumer_sync_all(ok);
+      float* r = red + buf * red_floats;
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = 8 * j + 2 * (lane & 3) + (i & 1);
+            if (c < cols) r[((rt * kFewWarps + warp) * cap + c) * kFewColPitch + (lane >> 2) + 8 * (i >> 1)] = acc[rt][j][i];
+          }
+      ok = consumer_sync_all(ok);
+      if (ok && tid < 16 * cols) {
+        const int i = tid & 15, c = tid >> 4;
+        const float g = get_sum(r, cap, i, c) * F::kSumScale, u = get_sum(r + kFewWarps * cap * kFewColPitch, cap, i, c) * F::kSumScale;
+        A.h[(size_t)(first + c) * A.F + f * 16 + i] = g / (1.f + expf(-g)) * u * tb.row_weight[first + c];
+      }
+      if (bufs == 2) buf ^= 1;
+    }
+    __threadfence();
+    ok = consumer_sync_all(ok);
+    if (tid == 0) {
+      red_release_gpu_add(A.counters + 1, 1);
+      ok = ok && grid_wait(A.counters + 1, gridDim.x, &sh->abort_flag, A.status);
+    }
+    ok = consumer_sync_all(ok);
+    if (ok) {
+      for (int i = warp * gridDim.x + blockIdx.x; i < sh->rows * FT; i += kFewWarps * gridDim.x) {
+        const float4 h = __ldcg(reinterpret_cast<const float4*>(A.h + (size_t)i * 128) + lane);
+        const float v[4] = {h.x, h.y, h.z, h.w};
+        put_record<F::kW4>(v, A.h8 + (size_t)i * kTokenRecord, lane);
+      }
+    }
+    fence_proxy_async_global();   // ordinary stores here, bulk copies there
+    __threadfence();
+    ok = consumer_sync_all(ok);
+    if (tid == 0) red_release_gpu_add(A.counters + 2, 1);
+
+    for (int item = blockIdx.x; ok && item < items2; item += gridDim.x) {
+      const int nrt = min(RT2, htiles - item * RT2);
+      float acc[RT2][NB][4] = {};
+      for (int seg = 0; ok && seg < segs; ++seg) {
+        const uint64_t mask = tb.seg_mask[seg];
+        for (int s = 0; s < steps2; ++s, ring.next()) {
+          ok = ring_wait(ring.full_bar(), ring.phase, &sh->abort_flag, A.status);
+          if (!ok) break;
+          if (s * kFewWarps + warp < FT) {
+            const uint32_t st = ring.stage();
+            layer_slice<GROUP, RT2, NB>(st, st + sco, st + tok, mask, warp, lane, acc);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ring.empty_bar());
+        }
+      }
+      ok = consumer_sync_all(ok);
+      if (!ok) break;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+#pragma unroll
+        for (int rt = 0; rt < RT2; ++rt) {
+          if (8 * j < A.T && rt < nrt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              red[(warp * 8 + 2 * (lane & 3) + (i & 1)) * kFewColPitch + (lane >> 2) + 8 * (i >> 1)] = acc[rt][j][i];
+            consumer_sync();
+            const int t = 8 * j + (tid >> 4), i = tid & 15;
+            if (tid < 128 && t < A.T)
+              A.out[(size_t)t * A.H + (item * RT2 + rt) * 16 + i] = to_bf16(get_sum(red, 8, i, t & 7) * F::kSumScale);
+            consumer_sync();
+          }
+        }
+      }
+    }
+  }
+  // the last block to leave clears the counters for the next call
+  __syncthreads();
+  if (tid == 0 && atomicAdd(A.counters + 3, 1) == (int)gridDim.x - 1) {
+    A.counters[0] = A.counters[1] = A.counters[2] = A.counters[3] = 0;
+    __threadfence();
+  }
+}
+
+template <int GROUP, int RT2>
+int launch_layer_rt(const LayerArgs& a, int nsm, cudaStream_t s) {
+  if (a.T <= 8) return few_launch(layer_few_kernel<GROUP, RT2, 1>, a, kFewThreads, nsm, true, s);
+  if (a.T <= 16) return few_launch(layer_few_kernel<GROUP, RT2, 2>, a, kFewThreads, nsm, true, s);
+  return few_launch(layer_few_kernel<GROUP, RT2, 8>, a, kFewThreads, nsm, true, s);
+}
+template <int GROUP>
+int launch_layer(const LayerArgs& a, int nsm, cudaStream_t s) {
+  switch (few_row_tiles(a.H / 16, nsm)) {
+    case 1: return launch_layer_rt<GROUP, 1>(a, nsm, s);
+    case 2: return launch_layer_rt<GROUP, 2>(a, nsm, s);
+    default: return launch_layer_rt<GROUP, 3>(a, nsm, s);
+  }
+}
+
+}  // namespace moe
