@@ -26,7 +26,7 @@ struct LayerArgs {
   uint16_t* out;
   int32_t* counters;   // arrivals of the grid's blocks at its meetings, and at the end
   float* logits;       // [T, E]
-  uint8_t *x8, *h8;    // token records of x [T] and of the activations [T k], K / 128 of 272 bytes each
+  uint8_t *x8, *h8;    // token records of x [T] and of the activations [T k], K / 128 of kTokenRecord bytes each
   float* h;            // [T k, F] activations times their route's weight
   int32_t* status;
   int T, H, E, k, F;
@@ -34,8 +34,8 @@ struct LayerArgs {
 };
 
 // Bytes of the record that holds 128 values of a token as the layer's MMAs take
-// them: f16 values, the scale, and 12 bytes of alignment.
-constexpr int kTokenRecord = 272;
+// them: f16 values, the scale, the groups' sums, and 12 bytes of alignment.
+constexpr int kTokenRecord = 288;
 
 // GROUP 0: FP8 (the layer only); 32, 64, 128: 4-bit.
 template <int GROUP> int launch_matvec(const MatvecArgs& a, int nsm, cudaStream_t s);

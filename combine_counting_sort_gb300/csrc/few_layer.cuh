@@ -6,8 +6,8 @@
 // subnormals to the end of the first binade), so the four pairs of a word's
 // eight codes take four ANDs and a shift; token values that meet a code with
 // the 16 are divided by it, and the sums are multiplied by 2^24 at the end.  The 8
-// that every 4-bit code has too much is taken out by the tensor core: -8 times
-// the tokens, once per stage and not per row tile.
+// that every 4-bit code has too much is taken out of a group's sum: 8 times the
+// sum of the token's values there, which its record holds.
 //
 // A token's 128 values share a power of two 2^e that brings their largest magnitude
 // into [2^14, 2^15): a bf16 value is then an f16 value as it is, down to 2^-28 of the
@@ -23,6 +23,8 @@
 #pragma once
 
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "few.cuh"
 #include "few_host.h"
@@ -54,18 +56,29 @@ constexpr int kTokPitch = kFewWarps * kTokenRecord + 64;
 // the MMAs 2i and 2i + 1.  4-bit: columns 32 i + 8 t .., the pairs that meet high nibbles
 // divided by 16.  FP8: columns 32 i + 4 t .. and 32 i + 16 + 4 t .., which ldmatrix gives
 // to lane t.
-template <bool W4>
+// Behind the values: the scale, and (4-bit) -8 * 2^-24 times the sum of each group's values.
+template <int GROUP>
 MOE_DEV void put_record(const float (&v)[4], uint8_t* rec, int lane) {
+  constexpr bool kW4 = GROUP != 0;
   uint32_t big = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) big = max(big, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   big = __reduce_max_sync(0xffffffffu, big);
   const int e = max((int)(big >> 23) - 127 - 14, -125);
-  const float down = __uint_as_float((uint32_t)(127 - e) << 23), down2 = W4 ? down * 0.0625f : down;
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23), down2 = kW4 ? down * 0.0625f : down;
   const __half2 a = __floats2half2_rn(v[0] * down, v[1] * down), b = __floats2half2_rn(v[2] * down2, v[3] * down2);
-  const int at = W4 ? 8 * lane : 64 * (lane >> 3) + 16 * (lane & 3) + 8 * ((lane >> 2) & 1);
+  const int at = kW4 ? 8 * lane : 64 * (lane >> 3) + 16 * (lane & 3) + 8 * ((lane >> 2) & 1);
   *reinterpret_cast<uint2*>(rec + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  if (lane == 0) *reinterpret_cast<float4*>(rec + 256) = make_float4(__uint_as_float((uint32_t)(127 + e) << 23), 0.f, 0.f, 0.f);
+  float* tail = reinterpret_cast<float*>(rec + 256);
+  if (lane == 0) tail[0] = __uint_as_float((uint32_t)(127 + e) << 23);
+  if (kW4) {
+    const float2 fa = __half22float2(a), fb = __half22float2(b);
+    float sum = (fa.x + fa.y) + 16.f * (fb.x + fb.y);
+    constexpr int kLanes = (kW4 ? GROUP : 128) / 4;
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane % kLanes == 0) tail[1 + lane / kLanes] = -8.f * 0x1p-24f * sum;
+  }
 }
 
 // ---------------------------------------------------------------- products
@@ -129,46 +142,81 @@ MOE_DEV void load_scales(uint32_t wst, uint32_t scales, int rt, int slice, int l
   }
 }
 
-// A block of 8 tokens of a stage: the lane's B operands (token 8 j + lane / 4) and the
-// scales of its sums' tokens (8 j + 2 (lane % 4) and the next).  Bit t of `mask` says
-// that token t is there, and the number of bits below it which row of the stage it has.
-MOE_DEV void load_block(uint32_t tokens, uint64_t mask, int j, int lane, uint32_t (&b)[16], float (&xs)[2]) {
-  const int tb = 8 * j + (lane >> 2), tc = 8 * j + 2 * (lane & 3);
+// Where a lane finds its columns' tokens in a stage, for NT blocks of 8 columns: its B
+// operand's (column 8 j + lane / 4) and those of its sums (8 j + 2 (lane % 4) and the
+// next); -1 where a column has none.  Bit c of `mask` says that column c has a
+// token, and the number of bits below it which row of the stage is its.
+template <int NT>
+struct LaneTokens {
+  int b[NT], x[NT][2];
+  MOE_DEV LaneTokens(uint32_t mask, uint32_t slice_offset, int lane) {
+    auto at = [&](int c) { return (mask >> c) & 1 ? (int)(slice_offset + __popc(mask & ((1u << c) - 1)) * kTokPitch) : -1; };
 #pragma unroll
-  for (int i = 0; i < 16; ++i) b[i] = 0;
-  if ((mask >> tb) & 1) {
-    const uint32_t p = tokens + __popcll(mask & ((1ull << tb) - 1)) * kTokPitch + (lane & 3) * 16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 v = lds128(p + 64 * i);
-      b[4 * i] = v.x; b[4 * i + 1] = v.y; b[4 * i + 2] = v.z; b[4 * i + 3] = v.w;
+    for (int j = 0; j < NT; ++j) {
+      b[j] = at(8 * j + (lane >> 2));
+      x[j][0] = at(8 * j + 2 * (lane & 3));
+      x[j][1] = at(8 * j + 2 * (lane & 3) + 1);
     }
   }
-  const uint32_t p = tokens + __popcll(mask & ((1ull << tc) - 1)) * kTokPitch + 256;
-  xs[0] = (mask >> tc) & 1 ? lds_f32(p) : 0.f;
-  xs[1] = (mask >> tc) & 2 ? lds_f32(p + ((mask >> tc) & 1) * kTokPitch) : 0.f;
-  __syncwarp();
-}
+};
 
-// The products of RT row tiles with NT blocks of tokens, added to acc (rows g and g + 8
-// of the lane's two tokens of a block, from block j0).  The MMAs of the row tiles,
-// and those of the eights, are chains of their own: an MMA's result takes some 20
-// cycles, and with two warps to a scheduler nothing else would fill them.
-template <int GROUP, int RT, int NT, int NB>
-MOE_DEV void block_products(const uint32_t (&c)[RT][GROUP ? 8 : 16], const float (&s)[RT][FewGroups<GROUP>::kCount][2],
-                            const uint32_t (&b)[NT][16], const float (&xs)[NT][2], float (&acc)[RT][NB][4], int j0) {
+// One stage's slice of a warp: RT row tiles times NT blocks of 8 columns, added to
+// acc (rows g and g + 8 of the lane's two columns of a block).  Columns without a token
+// read the record of zeros at `zero`.  The MMAs of the row tiles are chains of their own:
+// an MMA's result takes some 20 cycles, and with two warps to a scheduler little else
+// fills them.  A stage with fewer row tiles holds older ones in their place, whose
+// sums are not used.
+template <int GROUP, int RT, int NT>
+MOE_DEV void layer_slice(uint32_t st, uint32_t scales, uint32_t zero, const LaneTokens<NT>& lt, int slice, int lane,
+                         float (&acc)[RT][NT][4]) {
+  using F = LayerForm<GROUP>;
   constexpr int kCount = FewGroups<GROUP>::kCount, kMmas = 8 / kCount;
-  const uint32_t minus8[4] = {0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u};   // -8, -128 times 2^-24
+  uint32_t c[RT][GROUP ? 8 : 16], b[NT][16];
+  float s[RT][kCount][2], xs[NT][2], sums[NT][2][kCount];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const uint32_t p = lt.b[j] < 0 ? zero : st + lt.b[j];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = lds128(p + 64 * i + 16 * (lane & 3));
+      b[j][4 * i] = v.x; b[j][4 * i + 1] = v.y; b[j][4 * i + 2] = v.z; b[j][4 * i + 3] = v.w;
+    }
+  }
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    load_codes<GROUP>(st + rt * F::kRowTile, slice, lane, c[rt]);
+    load_scales<GROUP>(st + rt * F::kRowTile, scales, rt, slice, lane, s[rt]);
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t p = (lt.x[j][i] < 0 ? zero : st + lt.x[j][i]) + 256;
+      if (F::kW4) {
+        const uint4 v = lds128(p);
+        xs[j][i] = __uint_as_float(v.x);
+        sums[j][i][0] = __uint_as_float(v.y);
+        if (kCount > 1) sums[j][i][1 % kCount] = __uint_as_float(v.z);
+        if (kCount > 2) {
+          sums[j][i][2 % kCount] = __uint_as_float(v.w);
+          sums[j][i][3 % kCount] = lds_f32(p + 16);
+        }
+      } else {
+        xs[j][i] = lds_f32(p);
+      }
+    }
   float v[RT][NT][4];
 #pragma unroll
   for (int q = 0; q < kCount; ++q) {
-    float part[RT][NT][4] = {}, eights[NT][4] = {};
+    float part[RT][NT][4];
 #pragma unroll
-    for (int m = q * kMmas; m < (q + 1) * kMmas; ++m) {
-      if (GROUP != 0) {
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) mma_f16(eights[j], minus8, b[j][2 * m], b[j][2 * m + 1]);
-      }
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[rt][j][i] = 0.f;
+#pragma unroll
+    for (int m = q * kMmas; m < (q + 1) * kMmas; ++m)
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         uint32_t a[4];
@@ -176,14 +224,13 @@ MOE_DEV void block_products(const uint32_t (&c)[RT][GROUP ? 8 : 16], const float
 #pragma unroll
         for (int j = 0; j < NT; ++j) mma_f16(part[rt][j], a, b[j][2 * m], b[j][2 * m + 1]);
       }
-    }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float p = GROUP != 0 ? part[rt][j][i] + eights[j][i] : part[rt][j][i];
+          const float p = F::kW4 ? part[rt][j][i] + sums[j][i & 1][q] : part[rt][j][i];
           v[rt][j][i] = q == 0 ? p * s[rt][q][i >> 1] : fmaf(p, s[rt][q][i >> 1], v[rt][j][i]);
         }
   }
@@ -192,39 +239,21 @@ MOE_DEV void block_products(const uint32_t (&c)[RT][GROUP ? 8 : 16], const float
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[rt][j0 + j][i] = fmaf(v[rt][j][i], xs[j][i & 1], acc[rt][j0 + j][i]);
+      for (int i = 0; i < 4; ++i) acc[rt][j][i] = fmaf(v[rt][j][i], xs[j][i & 1], acc[rt][j][i]);
 }
 
-// One stage's slice of a warp: RT row tiles times the tokens of `mask`, which lie in the
-// first NT of NB blocks of 8.  With many blocks those without a token are passed over.
-// A stage with fewer row tiles holds older ones in their place, whose sums are not used.
-template <int GROUP, int RT, int NT, int NB>
-MOE_DEV void layer_slice(uint32_t st, uint32_t scales, uint32_t tokens, uint64_t mask, int slice, int lane, float (&acc)[RT][NB][4]) {
-  using F = LayerForm<GROUP>;
-  uint32_t c[RT][GROUP ? 8 : 16];
-  float s[RT][FewGroups<GROUP>::kCount][2];
-  tokens += slice * kTokenRecord;
+// A warp's sums of RT row tiles into the meeting place `red`: [row tile][warp][column].
+template <int RT, int NT>
+MOE_DEV void put_sums(float* red, int pitch, int cols, int warp, int lane, const float (&acc)[RT][NT][4]) {
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    load_codes<GROUP>(st + rt * F::kRowTile, slice, lane, c[rt]);
-    load_scales<GROUP>(st + rt * F::kRowTile, scales, rt, slice, lane, s[rt]);
-  }
-  if constexpr (NT <= 2) {
-    uint32_t b[NT][16];
-    float xs[NT][2];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) load_block(tokens, mask, j, lane, b[j], xs[j]);
-    block_products<GROUP, RT, NT, NB>(c, s, b, xs, acc, 0);
-  } else {
+  for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
     for (int j = 0; j < NT; ++j)
-      if ((mask >> (8 * j)) & 0xFF) {
-        uint32_t b[1][16];
-        float xs[1][2];
-        load_block(tokens, mask, j, lane, b[0], xs[0]);
-        block_products<GROUP, RT, 1, NB>(c, s, b, xs, acc, j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = 8 * j + 2 * (lane & 3) + (i & 1);
+        if (c < cols) red[((rt * kFewWarps + warp) * pitch + c) * kFewColPitch + (lane >> 2) + 8 * (i >> 1)] = acc[rt][j][i];
       }
-  }
 }
 
 // ---------------------------------------------------------------- copies
@@ -289,39 +318,50 @@ struct FewTables {
   }
 };
 
-// logits[t, e] for the experts of this block: each warp takes every eighth chunk of
-// 256 columns of the expert's row, four tokens at a time; the partial sums meet in
+// logits[t, e] for the experts of this block, two at a time: each warp takes every
+// eighth chunk of 256 columns, for four tokens at a time; the partial sums meet in
 // shared memory in the warps' order.
 MOE_DEV void few_logits(const LayerArgs& A, float* part, int tid, int warp, int lane) {
-  for (int e = blockIdx.x; e < A.E; e += gridDim.x) {
+  for (int e0 = blockIdx.x; e0 < A.E; e0 += 2 * gridDim.x) {
+    const int e1 = min(e0 + (int)gridDim.x, A.E - 1);
     if (warp < kFewWarps) {
       for (int t0 = 0; t0 < A.T; t0 += 4) {
-        float s[4] = {};
+        float s[2][4] = {};
 #pragma unroll 4
         for (int c = warp * 256 + lane * 8; c < A.H; c += kFewWarps * 256) {
-          const uint4 r = __ldg(reinterpret_cast<const uint4*>(A.router + (size_t)e * A.H + c));
-          const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
+          const uint4 r0 = __ldg(reinterpret_cast<const uint4*>(A.router + (size_t)e0 * A.H + c));
+          const uint4 r1 = __ldg(reinterpret_cast<const uint4*>(A.router + (size_t)e1 * A.H + c));
+          const uint32_t rw[2][4] = {{r0.x, r0.y, r0.z, r0.w}, {r1.x, r1.y, r1.z, r1.w}};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(A.x + (size_t)min(t0 + j, A.T - 1) * A.H + c));
+            if (t0 + j >= A.T) break;
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(A.x + (size_t)(t0 + j) * A.H + c));
             const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[j] = fmaf(bf16_hi(rw[i]), bf16_hi(vw[i]), fmaf(bf16_lo(rw[i]), bf16_lo(vw[i]), s[j]));
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                s[r][j] = fmaf(bf16_hi(rw[r][i]), bf16_hi(vw[i]), fmaf(bf16_lo(rw[r][i]), bf16_lo(vw[i]), s[r][j]));
           }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          if (t0 + j >= A.T) break;
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
-          if (lane == 0 && t0 + j < A.T) part[warp * A.T + t0 + j] = s[j];
+          for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s[r][j] += __shfl_xor_sync(0xffffffffu, s[r][j], o);
+            if (lane == 0) part[(warp * 2 + r) * A.T + t0 + j] = s[r][j];
+          }
         }
       }
     }
     __syncthreads();
-    if (tid < A.T) {
+    if (tid < 2 * A.T) {
+      const int r = tid >= A.T, t = tid - r * A.T, e = e0 + r * gridDim.x;
       float s = 0.f;
-      for (int w = 0; w < kFewWarps; ++w) s += part[w * A.T + tid];
-      A.logits[(size_t)tid * A.E + e] = s;
+      for (int w = 0; w < kFewWarps; ++w) s += part[(w * 2 + r) * A.T + t];
+      if (e < A.E) A.logits[(size_t)t * A.E + e] = s;
     }
     __syncthreads();
   }
@@ -342,12 +382,14 @@ MOE_DEV bool grid_wait(const int32_t* ctr, int n, volatile int* abort_flag, int3
 }
 
 // The tables from the pairs' ids and weights (in shared memory).  scratch: E masks,
-// E first rows.
+// E first rows, a count per warp.
 MOE_DEV void few_tables(const LayerArgs& A, FewShared* sh, const FewTables& tb, const int* ids, const float* w,
                         unsigned char* scratch, int tid, int warp, int lane) {
   const int P = A.T * A.k;
   uint64_t* mask = reinterpret_cast<uint64_t*>(scratch);
   int* first = reinterpret_cast<int*>(mask + A.E);
+  int* totals = first + A.E;
+  if (tid == 0) sh->cap = 1;
   for (int e = tid; e < A.E; e += kFewThreads) mask[e] = 0;
   __syncthreads();
   for (int p = tid; p < P; p += kFewThreads) {
@@ -359,56 +401,67 @@ MOE_DEV void few_tables(const LayerArgs& A, FewShared* sh, const FewTables& tb, 
     }
   }
   __syncthreads();
-  if (warp == 0) {
-    int rows = 0, segs = 0, most = 0;
-    for (int e0 = 0; e0 < A.E; e0 += 32) {
-      const int e = e0 + lane;
-      uint64_t m = e < A.E ? mask[e] : 0;
-      const int c = __popcll(m), s = (c + kFewMaxCols - 1) / kFewMaxCols;
-      int incl = c | s << 16;   // at most 1024 rows and 1024 segments
+  // thread i: experts 4 i .. 4 i + 3; rows in the low half of a count, segments in the high
+  static_assert(4 * kFewThreads >= 1024, "");
+  int counts = 0, most = 0;
+  uint64_t m4[4];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+  for (int i = 0; i < 4; ++i) {
+    m4[i] = 4 * tid + i < A.E ? mask[4 * tid + i] : 0;
+    const int c = __popcll(m4[i]);
+    counts += c | ((c + kFewMaxCols - 1) / kFewMaxCols) << 16;
+    most = max(most, c);
+  }
+  int incl = counts;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) totals[warp] = incl;
+  if (lane == 0 && most > 1) atomicMax(&sh->cap, min(most, kFewMaxCols));
+  __syncthreads();
+  int at = incl - counts;
+  for (int i = 0; i < warp; ++i) at += totals[i];
+  int row = at & 0xFFFF, seg = at >> 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint64_t m = m4[i];
+    if (4 * tid + i < A.E) first[4 * tid + i] = row;
+    while (m) {
+      uint64_t take = m;
+      if (__popcll(m) > kFewMaxCols) {
+        take = 0;
+        for (int b = 0; b < kFewMaxCols; ++b) take |= (m ^ take) & (~(m ^ take) + 1);   // the lowest bit left
       }
-      const int row = rows + (incl & 0xFFFF) - c, seg = segs + (incl >> 16) - s;
-      if (e < A.E) first[e] = row;
-      for (int i = 0; i < s; ++i) {
-        uint64_t take = m;
-        if (__popcll(m) > kFewMaxCols) {
-          take = 0;
-          for (int b = 0; b < kFewMaxCols; ++b) {
-            const uint64_t low = m & (~m + 1);
-            take |= low;
-            m ^= low;
-          }
-        }
-        tb.seg_mask[seg + i] = take;
-        tb.seg_expert[seg + i] = e;
-        tb.seg_row[seg + i] = row + i * kFewMaxCols;
-      }
-      most = max(most, c);
-      const int all = __shfl_sync(0xffffffffu, incl, 31);
-      rows += all & 0xFFFF;
-      segs += all >> 16;
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) {
-      sh->segs = segs;
-      sh->rows = rows;
-      sh->cap = min(most, kFewMaxCols);
+      m ^= take;
+      tb.seg_mask[seg] = take;
+      tb.seg_expert[seg] = 4 * tid + i;
+      tb.seg_row[seg++] = row;
+      row += __popcll(take);
     }
   }
+  if (tid == kFewThreads - 1) {
+    sh->rows = row;
+    sh->segs = seg;
+  }
   __syncthreads();
-  if (tid < A.T) {   // a token that names an expert again adds to its weight, in slot order
-    for (int j = 0; j < A.k; ++j) {
-      const int e = ids[tid * A.k + j];
-      if (e < 0 || e >= A.E) continue;
-      bool again = false;
-      for (int i = 0; i < j; ++i) again |= ids[tid * A.k + i] == e;
-      const int row = first[e] + __popcll(mask[e] & ((1ull << tid) - 1));
-      tb.row_token[row] = (uint8_t)tid;
-      tb.row_weight[row] = again ? tb.row_weight[row] + w[tid * A.k + j] : w[tid * A.k + j];
+  for (int p = tid; p < P; p += kFewThreads) {   // a token that names an expert again adds to its weight, in slot order
+    const int e = ids[p], t = p / A.k;
+    if (e < 0 || e >= A.E) continue;
+    bool again = false;
+    float sum = 0.f;
+    for (int i = t * A.k; i < (t + 1) * A.k; ++i) {
+      if (ids[i] == e) {
+        again |= i < p;
+        sum += w[i];
+      }
+    }
+    if (!again) {
+      const int r = first[e] + __popcll(mask[e] & ((1ull << t) - 1));
+      tb.row_token[r] = (uint8_t)t;
+      tb.row_weight[r] = sum;
     }
   }
 }
@@ -429,10 +482,12 @@ MOE_DEV LayerMatrix expert_matrix(const uint8_t* W, const CUtensorMap* map, cons
 //   the grid meets, the activations become records, the grid meets again;
 //   meanwhile the ring already fills with the next weights;
 //   down: items (RT2 row tiles of the output), each over all segments with the
-//   sums of every token in registers, so the output is written once, without
-//   atomics, in a fixed order.
-// NB: blocks of 8 tokens that the down sums cover (T <= 8 NB).
-template <int GROUP, int RT2, int NB>
+//   sums of every token on chip, so the output is written once, without atomics,
+//   in a fixed order.
+// DIRECT (T <= 8): a token is a column of the down products, and its sums over all
+// experts stay in registers.  Otherwise the columns are a segment's tokens, and the
+// segments' sums are added up in shared memory.
+template <int GROUP, int RT2, bool DIRECT>
 __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_constant__ LayerArgs A) {
   extern __shared__ __align__(1024) unsigned char sm[];
   using F = LayerForm<GROUP>;
@@ -440,18 +495,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
   FewShared* sh = reinterpret_cast<FewShared*>(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int P = A.T * A.k, HT = A.H / 128, FT = A.F / 128;
-  const FewTables tb(sm + 256, P);
-  const uint32_t after_tables = (256 + P * 21 + 127) & ~127;
+  constexpr uint32_t kZeroAt = 256, kTablesAt = kZeroAt + (kTokenRecord + 15) / 16 * 16;
+  const FewTables tb(sm + kTablesAt, P);
+  const uint32_t after_tables = (kTablesAt + P * 21 + 127) & ~127;
+  const uint32_t zero = smem_u32(sm) + kZeroAt;
   unsigned char* scratch = sm + after_tables;   // until the ring takes it
   int* ids = reinterpret_cast<int*>(scratch);
   float* w = reinterpret_cast<float*>(ids + P);
   unsigned char* scratch2 = reinterpret_cast<unsigned char*>(w + P);
 
   if (tid == 0) sh->abort_flag = 0;
+  if (tid < kTokenRecord / 4) reinterpret_cast<int*>(sm + kZeroAt)[tid] = 0;
   for (int i = warp * gridDim.x + blockIdx.x; i < A.T * HT; i += (kFewWarps + 1) * gridDim.x) {
     const uint2 x = __ldg(reinterpret_cast<const uint2*>(A.x + (size_t)i * 128) + lane);   // the tokens' rows are blocks of 128 in a row
     const float v[4] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)};
-    put_record<F::kW4>(v, A.x8 + (size_t)i * kTokenRecord, lane);
+    put_record<GROUP>(v, A.x8 + (size_t)i * kTokenRecord, lane);
   }
   if (A.router) few_logits(A, reinterpret_cast<float*>(scratch), tid, warp, lane);
   fence_proxy_async_global();   // the records are read by bulk copies
@@ -487,13 +545,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
   fence_proxy_async_shared();   // the ring's copies overwrite the scratch
   __syncthreads();
 
-  const int segs = sh->segs, cap = max(sh->cap, 1);
-  // the sums' room: two buffers where the columns are few, and 8 columns for the end
-  const int bufs = cap <= 8 ? 2 : 1, red_floats = kFewWarps * 2 * cap * kFewColPitch;
+  const int segs = sh->segs, cap = sh->cap;
+  // the sums' meeting place: two buffers where the columns are few; and the output's sums
+  constexpr int kRedTiles = DIRECT ? 2 : kRT;
+  const int red_floats = max(kFewWarps * kRedTiles * cap * kFewColPitch, DIRECT ? kFewWarps * 8 * kFewColPitch / 2 : 0);
+  const int bufs = DIRECT || cap <= 8 ? 2 : 1;
   float* red = reinterpret_cast<float*>(sm + after_tables);
+  float* sums = red + bufs * red_floats;   // [T][16 RT2]
   constexpr uint32_t tok = kRT * F::kRowTile;
   const uint32_t sco = tok + cap * kTokPitch;
-  FewRing ring = few_ring(sm, after_tables + max(bufs * red_floats, kFewWarps * 8 * kFewColPitch) * 4, A.smem_bytes,
+  FewRing ring = few_ring(sm, after_tables + (bufs * red_floats + (DIRECT ? 0 : A.T * 16 * RT2)) * 4, A.smem_bytes,
                           (sco + kRT * F::kScaleBytes + F::kAlign - 1) & ~(F::kAlign - 1), F::kArrivals);
   __syncthreads();
   const int ftiles = A.F / 16, items1 = segs * ftiles, steps1 = (HT + kFewWarps - 1) / kFewWarps;
@@ -568,33 +629,27 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
     for (int item = blockIdx.x; ok && item < items1; item += gridDim.x) {
       const int seg = item / ftiles, f = item % ftiles;
       const int cols = __popcll(tb.seg_mask[seg]), first = tb.seg_row[seg];
-      float acc[2][2][4] = {};
-      for (int s = 0; s < steps1; ++s, ring.next()) {
-        ok = ring_wait(ring.full_bar(), ring.phase, &sh->abort_flag, A.status);
-        if (!ok) break;
-        if (s * kFewWarps + warp < HT) {
-          const uint32_t st = ring.stage();
-          const uint64_t mask = (1ull << cols) - 1;
-          if (cols <= 8)
-            layer_slice<GROUP, 2, 1>(st, st + sco, st + tok, mask, warp, lane, acc);
-          else
-            layer_slice<GROUP, 2, 2>(st, st + sco, st + tok, mask, warp, lane, acc);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ring.empty_bar());
-      }
-      // with two buffers a warp reaches the next item's meeting only after it has read this one's
-      if (bufs == 1) ok = consumer_sync_all(ok);
       float* r = red + buf * red_floats;
-#pragma unroll
-      for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = 8 * j + 2 * (lane & 3) + (i & 1);
-            if (c < cols) r[((rt * kFewWarps + warp) * cap + c) * kFewColPitch + (lane >> 2) + 8 * (i >> 1)] = acc[rt][j][i];
-          }
+      // the stages of an item, and its sums put into r
+      auto item_sums = [&](auto nt) {
+        constexpr int NT = decltype(nt)::value;
+        const LaneTokens<NT> lt((1u << cols) - 1, tok + warp * kTokenRecord, lane);
+        float acc[2][NT][4] = {};
+        for (int s = 0; s < steps1; ++s, ring.next()) {
+          ok = ring_wait(ring.full_bar(), ring.phase, &sh->abort_flag, A.status);
+          if (!ok) break;
+          if (s * kFewWarps + warp < HT) layer_slice<GROUP, 2, NT>(ring.stage(), ring.stage() + sco, zero, lt, warp, lane, acc);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ring.empty_bar());
+        }
+        // with two buffers a warp reaches the next item's meeting only after it has read this one's
+        if (bufs == 1) ok = consumer_sync_all(ok);
+        put_sums<2, NT>(r, cap, cols, warp, lane, acc);
+      };
+      if (DIRECT || cols <= 8)
+        item_sums(std::integral_constant<int, 1>());
+      else
+        item_sums(std::integral_constant<int, 2>());
       ok = consumer_sync_all(ok);
       if (ok && tid < 16 * cols) {
         const int i = tid & 15, c = tid >> 4;
@@ -614,7 +669,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
       for (int i = warp * gridDim.x + blockIdx.x; i < sh->rows * FT; i += kFewWarps * gridDim.x) {
         const float4 h = __ldcg(reinterpret_cast<const float4*>(A.h + (size_t)i * 128) + lane);
         const float v[4] = {h.x, h.y, h.z, h.w};
-        put_record<F::kW4>(v, A.h8 + (size_t)i * kTokenRecord, lane);
+        put_record<GROUP>(v, A.h8 + (size_t)i * kTokenRecord, lane);
       }
     }
     fence_proxy_async_global();   // ordinary stores here, bulk copies there
@@ -624,37 +679,71 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
 
     for (int item = blockIdx.x; ok && item < items2; item += gridDim.x) {
       const int nrt = min(RT2, htiles - item * RT2);
-      float acc[RT2][NB][4] = {};
-      for (int seg = 0; ok && seg < segs; ++seg) {
-        const uint64_t mask = tb.seg_mask[seg];
-        for (int s = 0; s < steps2; ++s, ring.next()) {
-          ok = ring_wait(ring.full_bar(), ring.phase, &sh->abort_flag, A.status);
-          if (!ok) break;
-          if (s * kFewWarps + warp < FT) {
-            const uint32_t st = ring.stage();
-            layer_slice<GROUP, RT2, NB>(st, st + sco, st + tok, mask, warp, lane, acc);
+      if constexpr (DIRECT) {
+        float acc[RT2][1][4] = {};
+        for (int seg = 0; ok && seg < segs; ++seg) {
+          const LaneTokens<1> lt((uint32_t)tb.seg_mask[seg], tok + warp * kTokenRecord, lane);
+          for (int s = 0; s < steps2; ++s, ring.next()) {
+            ok = ring_wait(ring.full_bar(), ring.phase, &sh->abort_flag, A.status);
+            if (!ok) break;
+            if (s * kFewWarps + warp < FT) layer_slice<GROUP, RT2, 1>(ring.stage(), ring.stage() + sco, zero, lt, warp, lane, acc);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ring.empty_bar());
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(ring.empty_bar());
         }
-      }
-      ok = consumer_sync_all(ok);
-      if (!ok) break;
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
+        ok = consumer_sync_all(ok);
+        if (!ok) break;
 #pragma unroll
         for (int rt = 0; rt < RT2; ++rt) {
-          if (8 * j < A.T && rt < nrt) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              red[(warp * 8 + 2 * (lane & 3) + (i & 1)) * kFewColPitch + (lane >> 2) + 8 * (i >> 1)] = acc[rt][j][i];
+          const float one[1][1][4] = {{{acc[rt][0][0], acc[rt][0][1], acc[rt][0][2], acc[rt][0][3]}}};
+          if (rt < nrt) {
+            put_sums<1, 1>(red, 8, A.T, warp, lane, one);
             consumer_sync();
-            const int t = 8 * j + (tid >> 4), i = tid & 15;
-            if (tid < 128 && t < A.T)
-              A.out[(size_t)t * A.H + (item * RT2 + rt) * 16 + i] = to_bf16(get_sum(red, 8, i, t & 7) * F::kSumScale);
+            if (tid < 16 * A.T)
+              A.out[(size_t)(tid >> 4) * A.H + (item * RT2 + rt) * 16 + (tid & 15)] = to_bf16(get_sum(red, 8, tid & 15, tid >> 4) * F::kSumScale);
             consumer_sync();
           }
         }
+      } else {
+        for (int i = tid; i < A.T * 16 * RT2; i += kFewWarps * 32) sums[i] = 0.f;
+        consumer_sync();
+        for (int seg = 0; ok && seg < segs; ++seg) {
+          const int cols = __popcll(tb.seg_mask[seg]), first = tb.seg_row[seg];
+          float* r = red + buf * red_floats;
+          auto segment_sums = [&](auto nt) {
+            constexpr int NT = decltype(nt)::value;
+            const LaneTokens<NT> lt((1u << cols) - 1, tok + warp * kTokenRecord, lane);
+            float acc[RT2][NT][4] = {};
+            for (int s = 0; s < steps2; ++s, ring.next()) {
+              ok = ring_wait(ring.full_bar(), ring.phase, &sh->abort_flag, A.status);
+              if (!ok) break;
+              if (s * kFewWarps + warp < FT) layer_slice<GROUP, RT2, NT>(ring.stage(), ring.stage() + sco, zero, lt, warp, lane, acc);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(ring.empty_bar());
+            }
+            if (bufs == 1) ok = consumer_sync_all(ok);
+            put_sums<RT2, NT>(r, cap, cols, warp, lane, acc);
+          };
+          if (cols <= 8)
+            segment_sums(std::integral_constant<int, 1>());
+          else
+            segment_sums(std::integral_constant<int, 2>());
+          ok = consumer_sync_all(ok);
+          // a row and token of a segment has one thread, and a thread's part of `sums` is its own
+          // from segment to segment only by the meetings between them
+          for (int i = tid; i < 16 * RT2 * cols; i += kFewWarps * 32) {
+            const int c = i / (16 * RT2), row = i % (16 * RT2);
+            sums[tb.row_token[first + c] * 16 * RT2 + row] += get_sum(r + (row >> 4) * kFewWarps * cap * kFewColPitch, cap, row & 15, c);
+          }
+          if (bufs == 2) buf ^= 1;
+        }
+        ok = consumer_sync_all(ok);
+        if (!ok) break;
+        for (int i = tid; i < A.T * 16 * RT2; i += kFewWarps * 32) {
+          const int t = i / (16 * RT2), row = i % (16 * RT2);
+          if (row < 16 * nrt) A.out[(size_t)t * A.H + item * RT2 * 16 + row] = to_bf16(sums[i] * F::kSumScale);
+        }
+        consumer_sync();
       }
     }
   }
@@ -668,9 +757,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
 
 template <int GROUP, int RT2>
 int launch_layer_rt(const LayerArgs& a, int nsm, cudaStream_t s) {
-  if (a.T <= 8) return few_launch(layer_few_kernel<GROUP, RT2, 1>, a, kFewThreads, nsm, true, s);
-  if (a.T <= 16) return few_launch(layer_few_kernel<GROUP, RT2, 2>, a, kFewThreads, nsm, true, s);
-  return few_launch(layer_few_kernel<GROUP, RT2, 8>, a, kFewThreads, nsm, true, s);
+  return a.T <= 8 ? few_launch(layer_few_kernel<GROUP, RT2, true>, a, kFewThreads, nsm, true, s)
+                  : few_launch(layer_few_kernel<GROUP, RT2, false>, a, kFewThreads, nsm, true, s);
 }
 template <int GROUP>
 int launch_layer(const LayerArgs& a, int nsm, cudaStream_t s) {
