@@ -20,12 +20,13 @@ extern "C" int moe_matvec_w4(const uint16_t* x, int T, int K, const uint8_t* Wp,
 }
 
 // Workspace: 256 bytes of counters, then what LayerArgs names, each at a multiple of 256 bytes.
+constexpr int kFewMaxSplits = 4;   // kRouterMaxRuns
 struct FewWorkspace {
   size_t logits, x8, h8, h, bytes;
   FewWorkspace(int T, int k, int E, int H, int F) {
     size_t at = 256;
     auto take = [&at](size_t n) { const size_t p = at; at += (n + 255) / 256 * 256; return p; };
-    logits = take((size_t)T * E * 4);
+    logits = take((size_t)kFewMaxSplits * T * E * 4);
     x8 = take((size_t)T * (H / 128) * kTokenRecord);
     h8 = take((size_t)T * k * (F / 128) * kTokenRecord);
     h = take((size_t)T * k * F * 4);
@@ -83,6 +84,8 @@ extern "C" int moe_layer_few(const uint16_t* x, int T, int H, const uint16_t* ro
   a.h = reinterpret_cast<float*>(base + at.h);
   a.status = status;
   a.T = T; a.H = H; a.E = E; a.k = k; a.F = F;
+  // the logits' units fill the grid once if there are few
+  a.splits = std::max(1, std::min(kFewMaxSplits, nsm / ((E + 15) / 16 * ((T + 7) / 8))));
   cudaStream_t s = (cudaStream_t)stream;
   switch (group) {
     case 0:

@@ -25,11 +25,12 @@ struct LayerArgs {
   float* w;
   uint16_t* out;
   int32_t* counters;   // arrivals of the grid's blocks at its meetings, and at the end
-  float* logits;       // [T, E]
+  float* logits;       // [splits][T, E] sums over runs of columns
   uint8_t *x8, *h8;    // token records of x [T] and of the activations [T k], K / 128 of kTokenRecord bytes each
   float* h;            // [T k, F] activations times their route's weight
   int32_t* status;
   int T, H, E, k, F;
+  int splits;          // runs of columns of the logits
   uint32_t smem_bytes;
 };
 

@@ -48,6 +48,7 @@ struct LayerForm {
 // A token's records in a stage, 64 mod 128 bytes apart: the 2 tokens x 64 bytes of a
 // quarter-warp's reads fall on distinct banks.
 constexpr int kTokPitch = kFewWarps * kTokenRecord + 64;
+constexpr int kFewOwnTopk = 2 * (kFewWarps + 1);   // tokens whose routes every block selects for itself
 
 // ---------------------------------------------------------------- token records
 
@@ -275,12 +276,12 @@ MOE_DEV void copy_weights(const LayerMatrix& W, int tile0, int step, int tiles, 
   if (F::kW4) {
     if (lane == 0) mbar_arrive_expect_tx(bar, tiles * nk * F::kTile);
     __syncwarp();
-    if (lane < tiles) bulk_load(st + lane * F::kRowTile, W.p + ((size_t)(tile0 + lane * step) * KT + kt0) * F::kTile, nk * F::kTile, bar);
+    if (lane < tiles) bulk_load_once(st + lane * F::kRowTile, W.p + ((size_t)(tile0 + lane * step) * KT + kt0) * F::kTile, nk * F::kTile, bar);
   } else {
     // a box of min(8, K / 128) slices; slices past K count as bytes and are filled with zeros
     if (lane == 0) mbar_arrive_expect_tx(bar, tiles * min(kFewWarps, KT) * 2048);
     __syncwarp();
-    if (lane < tiles) tma_load_3d(st + lane * F::kRowTile, W.map, 0, W.row0 + (tile0 + lane * step) * 16, kt0, bar);
+    if (lane < tiles) tma_load_3d_once(st + lane * F::kRowTile, W.map, 0, W.row0 + (tile0 + lane * step) * 16, kt0, bar);
     for (int i = lane; i < tiles * kFewWarps; i += 32) {
       const int rt = i / kFewWarps, kt = i % kFewWarps;
       const bool on = kt < nk;
@@ -318,50 +319,38 @@ struct FewTables {
   }
 };
 
-// logits[t, e] for the experts of this block, two at a time: each warp takes every
-// eighth chunk of 256 columns, for four tokens at a time; the partial sums meet in
-// shared memory in the warps' order.
+// The logits as products of bf16 MMAs: units of 16 experts x 8 tokens x one of `splits`
+// equal runs of columns, one unit to a block.  Each warp takes every eighth chunk of
+// 32 columns, of which lane t of a row (or token) reads columns 8 t .. in one go (the
+// column order inside an MMA is free as long as both operands follow it).  The
+// warps' sums meet in shared memory; the runs' sums go to logits[run][t][e].
 MOE_DEV void few_logits(const LayerArgs& A, float* part, int tid, int warp, int lane) {
-  for (int e0 = blockIdx.x; e0 < A.E; e0 += 2 * gridDim.x) {
-    const int e1 = min(e0 + (int)gridDim.x, A.E - 1);
+  const int rows = (A.E + 15) / 16, blocks = (A.T + 7) / 8, chunks = A.H / 32;
+  for (int unit = blockIdx.x; unit < rows * blocks * A.splits; unit += gridDim.x) {
+    const int e0 = unit % rows * 16, t0 = unit / rows % blocks * 8, run = unit / rows / blocks;
     if (warp < kFewWarps) {
-      for (int t0 = 0; t0 < A.T; t0 += 4) {
-        float s[2][4] = {};
+      const int g = lane >> 2;
+      const uint16_t* r0 = A.router + (size_t)min(e0 + g, A.E - 1) * A.H + 8 * (lane & 3);
+      const uint16_t* r1 = A.router + (size_t)min(e0 + g + 8, A.E - 1) * A.H + 8 * (lane & 3);
+      const uint16_t* x = A.x + (size_t)min(t0 + g, A.T - 1) * A.H + 8 * (lane & 3);
+      float s[2][4] = {};
+      const int end = (run + 1) * chunks / A.splits;
 #pragma unroll 4
-        for (int c = warp * 256 + lane * 8; c < A.H; c += kFewWarps * 256) {
-          const uint4 r0 = __ldg(reinterpret_cast<const uint4*>(A.router + (size_t)e0 * A.H + c));
-          const uint4 r1 = __ldg(reinterpret_cast<const uint4*>(A.router + (size_t)e1 * A.H + c));
-          const uint32_t rw[2][4] = {{r0.x, r0.y, r0.z, r0.w}, {r1.x, r1.y, r1.z, r1.w}};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (t0 + j >= A.T) break;
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(A.x + (size_t)(t0 + j) * A.H + c));
-            const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                s[r][j] = fmaf(bf16_hi(rw[r][i]), bf16_hi(vw[i]), fmaf(bf16_lo(rw[r][i]), bf16_lo(vw[i]), s[r][j]));
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (t0 + j >= A.T) break;
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s[r][j] += __shfl_xor_sync(0xffffffffu, s[r][j], o);
-            if (lane == 0) part[(warp * 2 + r) * A.T + t0 + j] = s[r][j];
-          }
-        }
+      for (int c = run * chunks / A.splits + warp; c < end; c += kFewWarps) {
+        const uint4 a0 = __ldg(reinterpret_cast<const uint4*>(r0 + c * 32)), a1 = __ldg(reinterpret_cast<const uint4*>(r1 + c * 32));
+        const uint4 b = __ldg(reinterpret_cast<const uint4*>(x + c * 32));
+        const uint32_t m0[4] = {a0.x, a1.x, a0.y, a1.y}, m1[4] = {a0.z, a1.z, a0.w, a1.w};
+        mma_bf16(s[0], m0, b.x, b.y);
+        mma_bf16(s[1], m1, b.z, b.w);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        part[(warp * 8 + 2 * (lane & 3) + (i & 1)) * kFewColPitch + g + 8 * (i >> 1)] = s[0][i] + s[1][i];
     }
     __syncthreads();
-    if (tid < 2 * A.T) {
-      const int r = tid >= A.T, t = tid - r * A.T, e = e0 + r * gridDim.x;
-      float s = 0.f;
-      for (int w = 0; w < kFewWarps; ++w) s += part[(w * 2 + r) * A.T + t];
-      if (e < A.E) A.logits[(size_t)t * A.E + e] = s;
+    if (tid < 128) {
+      const int e = e0 + (tid & 15), t = t0 + (tid >> 4);
+      if (e < A.E && t < A.T) A.logits[((size_t)run * A.T + t) * A.E + e] = get_sum(part, 8, tid & 15, tid >> 4);
     }
     __syncthreads();
   }
@@ -379,6 +368,17 @@ MOE_DEV bool grid_wait(const int32_t* ctr, int n, volatile int* abort_flag, int3
     }
   }
   return true;
+}
+
+// The grid's blocks meet: what each wrote before is seen by all after.
+MOE_DEV void few_meet(const LayerArgs& A, int counter, FewShared* sh, int tid) {
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+    red_release_gpu_add(A.counters + counter, 1);
+    grid_wait(A.counters + counter, gridDim.x, &sh->abort_flag, A.status);
+  }
+  __syncthreads();
 }
 
 // The tables from the pairs' ids and weights (in shared memory).  scratch: E masks,
@@ -513,31 +513,34 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
   }
   if (A.router) few_logits(A, reinterpret_cast<float*>(scratch), tid, warp, lane);
   fence_proxy_async_global();   // the records are read by bulk copies
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) {
-    red_release_gpu_add(A.counters, 1);
-    grid_wait(A.counters, gridDim.x, &sh->abort_flag, A.status);
-  }
-  __syncthreads();
+  few_meet(A, 0, sh, tid);
   if (A.router) {
-    for (int t = warp; t < A.T; t += kFewWarps + 1) {
+    // Few tokens: every block selects for all of them.  Many: each block for its own, and the
+    // grid meets once more (1.4 us; a warp takes 2 to 3 us for its first token and 1.5 for each
+    // one more).
+    const bool shared_out = A.T > kFewOwnTopk;
+    for (int t = shared_out ? (int)blockIdx.x + (warp ? A.T : 0) : warp; t < A.T; t += shared_out ? gridDim.x : kFewWarps + 1) {
       float wt;
       const float* l = A.logits + (size_t)t * A.E;
-      const int id = A.E <= 256 ? warp_topk<8>(l, A.E, A.k, lane, &wt) : warp_topk<32>(l, A.E, A.k, lane, &wt);
+      const size_t run = (size_t)A.T * A.E;
+      const int id = A.E <= 256 ? warp_topk<8>(l, run, A.splits, A.E, A.k, lane, &wt) : warp_topk<32>(l, run, A.splits, A.E, A.k, lane, &wt);
       if (lane < A.k) {
-        ids[t * A.k + lane] = id;
-        w[t * A.k + lane] = wt;
-        if (blockIdx.x == 0) {
+        if (!shared_out) {
+          ids[t * A.k + lane] = id;
+          w[t * A.k + lane] = wt;
+        }
+        if (shared_out || blockIdx.x == 0) {
           A.ids[t * A.k + lane] = id;
           A.w[t * A.k + lane] = wt;
         }
       }
     }
-  } else {
+    if (shared_out) few_meet(A, 3, sh, tid);
+  }
+  if (!A.router || A.T > kFewOwnTopk) {
     for (int p = tid; p < P; p += kFewThreads) {
-      ids[p] = A.ids[p];
-      w[p] = A.w[p];
+      ids[p] = __ldcg(A.ids + p);
+      w[p] = __ldcg(A.w + p);
     }
   }
   __syncthreads();
@@ -749,8 +752,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
   }
   // the last block to leave clears the counters for the next call
   __syncthreads();
-  if (tid == 0 && atomicAdd(A.counters + 3, 1) == (int)gridDim.x - 1) {
-    A.counters[0] = A.counters[1] = A.counters[2] = A.counters[3] = 0;
+  if (tid == 0 && atomicAdd(A.counters + 4, 1) == (int)gridDim.x - 1) {
+    for (int i = 0; i < 5; ++i) A.counters[i] = 0;
     __threadfence();
   }
 }

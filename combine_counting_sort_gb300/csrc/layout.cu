@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(256) router_topk_kernel(const float* __restric
   const int warps = blockDim.x >> 5;
   for (int t = blockIdx.x * warps + (threadIdx.x >> 5); t < T; t += gridDim.x * warps) {
     float weight;
-    const int id = warp_topk<VPL>(logits + (size_t)t * E, E, k, lane, &weight);
+    const int id = warp_topk<VPL>(logits + (size_t)t * E, 0, 1, E, k, lane, &weight);
     if (lane < k) {
       ids[(size_t)t * k + lane] = id;
       w[(size_t)t * k + lane] = weight;

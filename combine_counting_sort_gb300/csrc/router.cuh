@@ -5,20 +5,35 @@
 
 namespace moe {
 
+constexpr int kRouterMaxRuns = 4;
+
 // k rounds of a warp-wide arg-max over E <= 32 * VPL logits (largest logit, ties
 // to the lower expert id), then softmax weights over the selected logits, summed
-// in slot order.  Lane j < k returns slot j's id and weight.
+// in slot order.  Lane j < k returns slot j's id and weight.  A logit is the sum of
+// `runs` <= kRouterMaxRuns values, `run` apart, in their order.
 // The logits are compared as unsigned keys of the same order (0: none, a NaN, or
 // taken), so that a round is two warp reductions of one instruction each.
 template <int VPL>
-MOE_DEV int warp_topk(const float* logits, int E, int k, int lane, float* weight) {
+MOE_DEV int warp_topk(const float* logits, size_t run, int runs, int E, int k, int lane, float* weight) {
+  float v[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) v[i] = i * 32 + lane < E ? __ldcg(logits + i * 32 + lane) : NAN;
+  if (runs > 1) {   // all loads in flight together
+    float u[kRouterMaxRuns - 1][VPL];
+#pragma unroll
+    for (int r = 1; r < kRouterMaxRuns; ++r)
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) u[r - 1][i] = r < runs && i * 32 + lane < E ? __ldcg(logits + r * run + i * 32 + lane) : 0.f;
+#pragma unroll
+    for (int r = 1; r < kRouterMaxRuns; ++r)
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) v[i] += u[r - 1][i];
+  }
   uint32_t key[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const int e = i * 32 + lane;
-    const float v = (e < E ? __ldcg(logits + e) : NAN) + 0.f;   // -0 and 0 are the same
-    const uint32_t u = __float_as_uint(v);
-    key[i] = v != v ? 0u : (u >> 31 ? ~u : u | 0x80000000u);
+    const uint32_t b = __float_as_uint(v[i] + 0.f);   // -0 and 0 are the same
+    key[i] = v[i] != v[i] ? 0u : (b >> 31 ? ~b : b | 0x80000000u);
   }
   float sel_l0 = 0.f, my_l = 0.f;
   int my_id = 0;
