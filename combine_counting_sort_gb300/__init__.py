@@ -544,16 +544,36 @@ def moe_dequant_weights_w4(Wp: torch.Tensor, group: int, W: torch.Tensor, stream
         _ptr(Wp, torch.uint8, "Wp"), E, N, K, group, _ptr(W, torch.float32, "W"), _stream(stream)))
 
 
+def _args(*specs):
+    """Addresses of (tensor or None, dtype, shape, name) arguments.  One comparison
+    each where they are as they have to be (these calls take as long as their
+    kernels); otherwise _shape and _ptr say what is wrong, shapes first."""
+    out = []
+    for t, dtype, shape, _ in specs:
+        if t is None:
+            out.append(None)
+        elif t.shape == shape and t.dtype == dtype and t.is_cuda and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            for u, _, want, name in specs:
+                _shape(u, want, name)
+            return [_ptr(u, d, name) for u, d, _, name in specs]
+    return out
+
+
+def _raw_stream(stream) -> int:
+    """_stream, without building a torch.cuda.Stream for the current one."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
+
+
 def moe_matvec_w4(x: torch.Tensor, Wp: torch.Tensor, group: int, y: torch.Tensor, status: torch.Tensor, stream=None):
     """y[t] = W x[t] for up to 64 tokens and one laid-out 4-bit matrix."""
     T, K = _dims(x, 2, "x")
     N = _dims(y, 2, "y")[1]
-    _shape(y, (T, N), "y")
-    _shape(Wp, w4_packed_shape(1, N, K, group)[1:], "Wp")
     _status(status)
-    _check("moe_matvec_w4", lib().moe_matvec_w4(
-        _ptr(x, torch.bfloat16, "x"), T, K, _ptr(Wp, torch.uint8, "Wp"), N, group, _ptr(y, torch.bfloat16, "y"),
-        _ptr(status, torch.int32, "status"), _stream(stream)))
+    px, pw, py, pst = _args((x, torch.bfloat16, (T, K), "x"), (Wp, torch.uint8, w4_packed_shape(1, N, K, group)[1:], "Wp"),
+                            (y, torch.bfloat16, (T, N), "y"), (status, torch.int32, status.shape, "status"))
+    _check("moe_matvec_w4", lib().moe_matvec_w4(px, T, K, pw, N, group, py, pst, _raw_stream(stream)))
 
 
 def moe_layer_few_ws_bytes(T: int, k: int, E: int, H: int, F: int) -> int:
@@ -578,27 +598,21 @@ def moe_layer_few(x: torch.Tensor, W1: torch.Tensor, W1_scale: Optional[torch.Te
     if group == 0:
         E, F2, _ = _dims(W1, 3, "W1")
         F = F2 // 2
-        _shape(W1, (E, 2 * F, H), "W1")
-        _shape(W2, (E, H, F), "W2")
+        W1shape, W2shape = (E, 2 * F, H), (E, H, F)
         if W1_scale is None or W2_scale is None:
             raise ValueError("FP8 weights need W1_scale and W2_scale")
-        _shape(W1_scale, (E, F2 // 128, H // 128), "W1_scale")
-        _shape(W2_scale, (E, H // 128, F // 128), "W2_scale")
     else:
         E = _dims(W1, 4, "W1")[0]
         F = 8 * W1.shape[1]
-        _shape(W1, w4_packed_shape(E, 2 * F, H, group), "W1")
-        _shape(W2, w4_packed_shape(E, H, F, group), "W2")
+        W1shape, W2shape = w4_packed_shape(E, 2 * F, H, group), w4_packed_shape(E, H, F, group)
         if W1_scale is not None or W2_scale is not None:
             raise ValueError("4-bit weights carry their scales: W1_scale and W2_scale must be None")
-    _shape(topk_ids, (T, k), "topk_ids")
-    _shape(topk_w, (T, k), "topk_w")
-    _shape(out, (T, H), "out")
-    _shape(router, (E, H), "router")
     _status(status)
+    px, pr, p1, ps1, p2, ps2, pids, pw, pout, pst = _args(
+        (x, torch.bfloat16, (T, H), "x"), (router, torch.bfloat16, (E, H), "router"), (W1, torch.uint8, W1shape, "W1"),
+        (W1_scale, torch.float32, (E, 2 * F // 128, H // 128), "W1_scale"), (W2, torch.uint8, W2shape, "W2"),
+        (W2_scale, torch.float32, (E, H // 128, F // 128), "W2_scale"), (topk_ids, torch.int32, (T, k), "topk_ids"),
+        (topk_w, torch.float32, (T, k), "topk_w"), (out, torch.bfloat16, (T, H), "out"), (status, torch.int32, status.shape, "status"))
     _check("moe_layer_few", lib().moe_layer_few(
-        _ptr(x, torch.bfloat16, "x"), T, H, _ptr(router, torch.bfloat16, "router"), E, k, _ptr(W1, torch.uint8, "W1"),
-        _ptr(W1_scale, torch.float32, "W1_scale"), _ptr(W2, torch.uint8, "W2"),
-        _ptr(W2_scale, torch.float32, "W2_scale"), F, group, _ptr(topk_ids, torch.int32, "topk_ids"),
-        _ptr(topk_w, torch.float32, "topk_w"), _ptr(out, torch.bfloat16, "out"), _ptr(ws, None, "ws"),
-        ws.numel() * ws.element_size(), _ptr(status, torch.int32, "status"), _stream(stream)))
+        px, T, H, pr, E, k, p1, ps1, p2, ps2, F, group, pids, pw, pout, _ptr(ws, None, "ws"), ws.numel() * ws.element_size(), pst,
+        _raw_stream(stream)))
