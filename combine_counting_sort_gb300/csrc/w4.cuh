@@ -32,13 +32,4 @@ __host__ __device__ __forceinline__ constexpr size_t w4_matrix_bytes(int N, int 
   return (size_t)((N + 15) / 16) * ((K + 127) / 128) * w4_tile_bytes(group);
 }
 
-// Value of column `c` (0..127) of row `r` (0..15) of a tile.
-MOE_DEV float w4_value(const uint8_t* tile, int r, int c, int group) {
-  const int lane = 4 * (r & 7) + ((c & 31) >> 3);
-  const uint8_t b = tile[4 * (4 * (32 * (r >> 3) + lane) + (c >> 5)) + 2 * (c & 1) + ((c & 7) >> 2)];
-  const int code = (c & 2) ? b >> 4 : b & 15;
-  const uint16_t s = *reinterpret_cast<const uint16_t*>(tile + kW4Codes + 2 * (16 * (c / group) + r));
-  return (float)(code - 8) * bf16_lo(s);
-}
-
 }  // namespace moe

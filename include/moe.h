@@ -416,7 +416,7 @@ int moe_dequant_rows(const uint8_t* A, const float* A_scale, int H, const moe_la
  * Limits: group 32, 64 or 128; 1 <= N <= MOE_W4_MAX_N; K a multiple of the
  * group, K <= MOE_W4_MAX_K; E <= 65535.  Laid-out buffers are 16-byte aligned.
  * ------------------------------------------------------------------------- */
-#define MOE_W4_MAX_N (1 << 20)
+#define MOE_W4_MAX_N (65535 * 16)
 #define MOE_W4_MAX_K 32768
 
 /* Bytes of one laid-out matrix: ceil(N/16) * ceil(K/128) tiles. */
@@ -431,7 +431,7 @@ int moe_quant_weights_w4(const uint16_t* W, int E, int N, int K, int group, uint
                          moe_stream_t stream);
 
 /* moe_pack_weights_w4: lay out a checkpoint's codes (u8 [E, N, K/2], column
- * 2i in the low nibble of byte i) and scales (bf16 [E, N, K/group]). */
+ * 2i in the low nibble of byte i; 4-byte aligned) and scales (bf16 [E, N, K/group]). */
 int moe_pack_weights_w4(const uint8_t* codes, const uint16_t* scale, int E, int N, int K, int group,
                         uint8_t* Wp, moe_stream_t stream);
 
