@@ -1,13 +1,14 @@
 // few.cuh: the streaming engine of the decoding kernels (few tokens, all of the
 // time goes into reading weights once).
 //
-// A CTA is eight computing warps and one copying warp.  The copying warp walks
-// the CTA's work and keeps a ring of shared-memory stages full with bulk copies
+// A CTA is eight computing warps, one copying warp and three finishing warps.  The
+// copying warp walks the CTA's work and keeps a ring of shared-memory stages full with bulk copies
 // and TMA loads (counted on an mbarrier per stage): per stage RT row tiles of 16
 // weight rows x 1024 columns, and the same 1024 columns of the tokens that the
 // weights multiply.  Each computing warp takes one 128-column slice of a stage.
-// The eight partial sums of a row meet in shared memory once a row tile is
-// complete, in a fixed order.
+// The eight partial sums of a row go to the finishing warps through shared memory once
+// a row tile is complete; they add them in a fixed order and write the results while
+// the computing warps go on (a block-wide meeting per item had cost a tenth).
 //
 // The products run on mma.sync and not on tcgen05: the tensor work is the
 // weights times 8 columns, far below either's rate, while 4-bit codes have to
@@ -20,7 +21,9 @@
 namespace moe {
 
 constexpr int kFewWarps = 8;                       // computing warps, one per 128-column slice of a stage
-constexpr int kFewThreads = (kFewWarps + 1) * 32;  // and the copying warp
+constexpr int kFewFinish = 3;                      // finishing warps
+constexpr int kFewAllWarps = kFewWarps + 1 + kFewFinish, kFewThreads = kFewAllWarps * 32;
+constexpr int kFewFinishThreads = 32 * kFewFinish;
 constexpr int kFewMaxCols = 16;                    // tokens per pass over a stage
 constexpr int kFewMaxStages = 12;
 constexpr uint64_t kFewTimeoutNs = 1000000000ull;  // bound of every wait
@@ -98,6 +101,7 @@ struct FewGroups {
 // Barriers of the ring and the block's flags at the start of shared memory.
 struct FewShared {
   uint64_t full[kFewMaxStages], empty[kFewMaxStages];
+  uint64_t sums_full[2], sums_empty[2];
   volatile int abort_flag;
   int segs, cap, rows;
 };
@@ -137,9 +141,47 @@ MOE_DEV FewRing few_ring(unsigned char* sm, uint32_t at, uint32_t smem_bytes, ui
   return r;
 }
 
+// The way of the sums from the computing to the finishing warps: one or two buffers of
+// `stage_bytes` at sm + at.
+MOE_DEV FewRing few_sums_ring(unsigned char* sm, uint32_t at, uint32_t bytes, int buffers) {
+  FewShared* sh = reinterpret_cast<FewShared*>(sm);
+  FewRing r;
+  r.base = at;
+  r.stage_bytes = bytes;
+  r.full = smem_u32(sh->sums_full);
+  r.empty = smem_u32(sh->sums_empty);
+  r.stages = buffers;
+  r.slot = r.phase = 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < buffers; ++i) {
+      mbar_init(r.full + 8 * i, kFewWarps);
+      mbar_init(r.empty + 8 * i, kFewFinish);
+    }
+    fence_mbar_init();
+  }
+  return r;
+}
+
 // A warp's bounded wait: one outcome for all lanes.
 MOE_DEV bool ring_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, kFewTimeoutNs));
+}
+
+// The same for a warp with time to spare: it sleeps between looks, since warps that poll
+// take issue slots from those that compute.
+MOE_DEV bool ring_wait_idle(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+    __nanosleep(64);
+    bool over = *abort_flag;
+    if (!over && globaltimer_ns() - t0 > kFewTimeoutNs) {
+      *abort_flag = 1;
+      set_status(status, MOE_ERR_TIMEOUT);
+      over = true;
+    }
+    if (__any_sync(0xffffffffu, over)) return false;
+  }
+  return true;
 }
 
 // The copying warp's end: every stage it has begun is complete before the block
@@ -171,18 +213,18 @@ MOE_DEV float get_sum(const float* red, int pitch, int row, int col) {
   return s;
 }
 
-MOE_DEV void consumer_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-// The computing warps' meeting that also tells all of them whether any gave up, so that
-// they leave together.
+// The meeting of all warps but the copying one, which also tells all of them whether any
+// gave up, so that they leave together.
 MOE_DEV bool consumer_sync_all(bool ok) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 1, 256, p;\n\t"
+      "bar.red.and.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(all) : "r"((uint32_t)ok) : "memory");
+      : "=r"(all) : "r"((uint32_t)ok), "n"(kFewThreads - 32) : "memory");
   return all != 0;
 }
+MOE_DEV void finish_sync() { asm volatile("bar.sync 2, %0;" :: "n"(kFewFinishThreads) : "memory"); }
 
 }  // namespace moe

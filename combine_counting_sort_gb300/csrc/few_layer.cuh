@@ -32,23 +32,25 @@
 
 namespace moe {
 
-template <int GROUP>
+// SP: 128-column slices of a stage per warp.
+template <int GROUP, int SP>
 struct LayerForm {
   static constexpr bool kW4 = GROUP != 0;
   static constexpr int kTile = w4_tile_bytes(kW4 ? GROUP : 128);
+  static constexpr int kSlices = kFewWarps * SP;
   // 4-bit: the slices' tiles as they lie in memory.  FP8: per slice 16 rows of
   // 128 bytes in TMA's 128-byte swizzle, which ldmatrix reads without bank conflicts.
-  static constexpr int kRowTile = kFewWarps * (kW4 ? kTile : 2048);
-  static constexpr int kAlign = kW4 ? 128 : 1024;             // of a stage
-  static constexpr int kScaleBytes = kW4 ? 0 : 4 * kFewWarps; // per row tile
+  static constexpr int kRowTile = kSlices * (kW4 ? kTile : 2048);
+  static constexpr int kAlign = kW4 ? 128 : 1024;           // of a stage
+  static constexpr int kScaleBytes = kW4 ? 0 : 4 * kSlices; // per row tile
+  // A token's records in a stage, 64 mod 128 bytes apart: the 2 tokens x 64 bytes of a
+  // quarter-warp's reads fall on distinct banks.
+  static constexpr int kTokPitch = kSlices * kTokenRecord + 64;
   // arrivals that complete a stage: weights, tokens, and the lanes' scale copies
   static constexpr int kArrivals = kW4 ? 2 : 34;
-  static constexpr float kSumScale = kW4 ? 0x1p24f : 1.f;     // what the sums lack
+  static constexpr float kSumScale = kW4 ? 0x1p24f : 1.f;   // what the sums lack
 };
-// A token's records in a stage, 64 mod 128 bytes apart: the 2 tokens x 64 bytes of a
-// quarter-warp's reads fall on distinct banks.
-constexpr int kTokPitch = kFewWarps * kTokenRecord + 64;
-constexpr int kFewOwnTopk = 2 * (kFewWarps + 1);   // tokens whose routes every block selects for itself
+constexpr int kFewOwnTopk = 2 * kFewAllWarps;   // tokens whose routes every block selects for itself
 
 // ---------------------------------------------------------------- token records
 
@@ -88,7 +90,7 @@ MOE_DEV void put_record(const float (&v)[4], uint8_t* rec, int lane) {
 // g + 8 (4-7).  FP8: words m and m + 8 are columns 16 m + 4 t .. of row g and of row g + 8.
 template <int GROUP>
 MOE_DEV void load_codes(uint32_t wst, int slice, int lane, uint32_t (&c)[GROUP ? 8 : 16]) {
-  using F = LayerForm<GROUP>;
+  using F = LayerForm<GROUP, 1>;
   if constexpr (F::kW4) {
     const uint32_t p = wst + slice * F::kTile + lane * 16;
     const uint4 l = lds128(p), h = lds128(p + 512);
@@ -128,9 +130,9 @@ MOE_DEV void widen(const uint32_t (&c)[GROUP ? 8 : 16], int m, uint32_t (&a)[4])
 }
 
 // The scales of a row tile's slice for rows g and g + 8, per group.
-template <int GROUP>
+template <int GROUP, int SP>
 MOE_DEV void load_scales(uint32_t wst, uint32_t scales, int rt, int slice, int lane, float (&s)[FewGroups<GROUP>::kCount][2]) {
-  using F = LayerForm<GROUP>;
+  using F = LayerForm<GROUP, SP>;
 #pragma unroll
   for (int q = 0; q < FewGroups<GROUP>::kCount; ++q) {
     if (F::kW4) {
@@ -138,7 +140,7 @@ MOE_DEV void load_scales(uint32_t wst, uint32_t scales, int rt, int slice, int l
       s[q][0] = lds_bf16(sc);
       s[q][1] = lds_bf16(sc + 16);
     } else {
-      s[q][0] = s[q][1] = lds_f32(scales + 4 * (kFewWarps * rt + slice));
+      s[q][0] = s[q][1] = lds_f32(scales + 4 * (F::kSlices * rt + slice));
     }
   }
 }
@@ -147,11 +149,11 @@ MOE_DEV void load_scales(uint32_t wst, uint32_t scales, int rt, int slice, int l
 // operand's (column 8 j + lane / 4) and those of its sums (8 j + 2 (lane % 4) and the
 // next); -1 where a column has none.  Bit c of `mask` says that column c has a
 // token, and the number of bits below it which row of the stage is its.
-template <int NT>
+template <int NT, int PITCH>
 struct LaneTokens {
   int b[NT], x[NT][2];
   MOE_DEV LaneTokens(uint32_t mask, uint32_t slice_offset, int lane) {
-    auto at = [&](int c) { return (mask >> c) & 1 ? (int)(slice_offset + __popc(mask & ((1u << c) - 1)) * kTokPitch) : -1; };
+    auto at = [&](int c) { return (mask >> c) & 1 ? (int)(slice_offset + __popc(mask & ((1u << c) - 1)) * PITCH) : -1; };
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       b[j] = at(8 * j + (lane >> 2));
@@ -167,16 +169,16 @@ struct LaneTokens {
 // an MMA's result takes some 20 cycles, and with two warps to a scheduler little else
 // fills them.  A stage with fewer row tiles holds older ones in their place, whose
 // sums are not used.
-template <int GROUP, int RT, int NT>
-MOE_DEV void layer_slice(uint32_t st, uint32_t scales, uint32_t zero, const LaneTokens<NT>& lt, int slice, int lane,
-                         float (&acc)[RT][NT][4]) {
-  using F = LayerForm<GROUP>;
+template <int GROUP, int SP, int RT, int NT>
+MOE_DEV void layer_slice(uint32_t st, uint32_t scales, uint32_t zero, const LaneTokens<NT, LayerForm<GROUP, SP>::kTokPitch>& lt, int slice,
+                         int lane, float (&acc)[RT][NT][4]) {
+  using F = LayerForm<GROUP, SP>;
   constexpr int kCount = FewGroups<GROUP>::kCount, kMmas = 8 / kCount;
   uint32_t c[RT][GROUP ? 8 : 16], b[NT][16];
   float s[RT][kCount][2], xs[NT][2], sums[NT][2][kCount];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const uint32_t p = lt.b[j] < 0 ? zero : st + lt.b[j];
+    const uint32_t p = lt.b[j] < 0 ? zero : st + lt.b[j] + slice * kTokenRecord;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint4 v = lds128(p + 64 * i + 16 * (lane & 3));
@@ -186,13 +188,13 @@ MOE_DEV void layer_slice(uint32_t st, uint32_t scales, uint32_t zero, const Lane
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     load_codes<GROUP>(st + rt * F::kRowTile, slice, lane, c[rt]);
-    load_scales<GROUP>(st + rt * F::kRowTile, scales, rt, slice, lane, s[rt]);
+    load_scales<GROUP, SP>(st + rt * F::kRowTile, scales, rt, slice, lane, s[rt]);
   }
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t p = (lt.x[j][i] < 0 ? zero : st + lt.x[j][i]) + 256;
+      const uint32_t p = (lt.x[j][i] < 0 ? zero : st + lt.x[j][i] + slice * kTokenRecord) + 256;
       if (F::kW4) {
         const uint4 v = lds128(p);
         xs[j][i] = __uint_as_float(v.x);
@@ -268,10 +270,11 @@ struct LayerMatrix {
 
 // Copy `tiles` row tiles (the rt-th at row tile tile0 + rt * step) of the 128-column
 // slices [kt0, kt0 + nk) into the stage at `st`; whole warp.
-template <int GROUP>
+template <int GROUP, int SP>
 MOE_DEV void copy_weights(const LayerMatrix& W, int tile0, int step, int tiles, int kt0, int nk, uint32_t st, uint32_t scales,
                           uint32_t bar, int lane) {
-  using F = LayerForm<GROUP>;
+  using F = LayerForm<GROUP, SP>;
+  static_assert(F::kW4 || SP == 1, "a box has 8 slices");
   const int KT = W.K / 128;
   if (F::kW4) {
     if (lane == 0) mbar_arrive_expect_tx(bar, tiles * nk * F::kTile);
@@ -293,11 +296,11 @@ MOE_DEV void copy_weights(const LayerMatrix& W, int tile0, int step, int tiles, 
 }
 
 // Copy the records [kt0, kt0 + nk) of `cols` tokens, token c's at record_of(c).
-template <class RecordOf>
+template <int PITCH, class RecordOf>
 MOE_DEV void copy_tokens(RecordOf record_of, int cols, int kt0, int nk, uint32_t tok, uint32_t bar, int lane) {
   if (lane == 0) mbar_arrive_expect_tx(bar, cols * nk * kTokenRecord);
   __syncwarp();
-  if (lane < cols) bulk_load(tok + lane * kTokPitch, record_of(lane) + (size_t)kt0 * kTokenRecord, nk * kTokenRecord, bar);
+  if (lane < cols) bulk_load(tok + lane * PITCH, record_of(lane) + (size_t)kt0 * kTokenRecord, nk * kTokenRecord, bar);
 }
 
 // ---------------------------------------------------------------- routes
@@ -490,7 +493,10 @@ MOE_DEV LayerMatrix expert_matrix(const uint8_t* W, const CUtensorMap* map, cons
 template <int GROUP, int RT2, bool DIRECT>
 __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_constant__ LayerArgs A) {
   extern __shared__ __align__(1024) unsigned char sm[];
-  using F = LayerForm<GROUP>;
+  // 4-bit stages are short of work: handing one over takes some 300 cycles of a warp's 900.
+  // Two slices per warp halve that where the tokens leave room for it.
+  constexpr int kSP = GROUP != 0 && DIRECT ? 2 : 1;
+  using F = LayerForm<GROUP, kSP>;
   constexpr int kRT = RT2 > 2 ? RT2 : 2;
   FewShared* sh = reinterpret_cast<FewShared*>(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -506,7 +512,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
 
   if (tid == 0) sh->abort_flag = 0;
   if (tid < kTokenRecord / 4) reinterpret_cast<int*>(sm + kZeroAt)[tid] = 0;
-  for (int i = warp * gridDim.x + blockIdx.x; i < A.T * HT; i += (kFewWarps + 1) * gridDim.x) {
+  for (int i = warp * gridDim.x + blockIdx.x; i < A.T * HT; i += kFewAllWarps * gridDim.x) {
     const uint2 x = __ldg(reinterpret_cast<const uint2*>(A.x + (size_t)i * 128) + lane);   // the tokens' rows are blocks of 128 in a row
     const float v[4] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)};
     put_record<GROUP>(v, A.x8 + (size_t)i * kTokenRecord, lane);
@@ -519,7 +525,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
     // grid meets once more (1.4 us; a warp takes 2 to 3 us for its first token and 1.5 for each
     // one more).
     const bool shared_out = A.T > kFewOwnTopk;
-    for (int t = shared_out ? (int)blockIdx.x + (warp ? A.T : 0) : warp; t < A.T; t += shared_out ? gridDim.x : kFewWarps + 1) {
+    for (int t = shared_out ? (int)blockIdx.x + (warp ? A.T : 0) : warp; t < A.T; t += shared_out ? gridDim.x : kFewAllWarps) {
       float wt;
       const float* l = A.logits + (size_t)t * A.E;
       const size_t run = (size_t)A.T * A.E;
@@ -549,19 +555,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
   __syncthreads();
 
   const int segs = sh->segs, cap = sh->cap;
-  // the sums' meeting place: two buffers where the columns are few; and the output's sums
-  constexpr int kRedTiles = DIRECT ? 2 : kRT;
-  const int red_floats = max(kFewWarps * kRedTiles * cap * kFewColPitch, DIRECT ? kFewWarps * 8 * kFewColPitch / 2 : 0);
+  // The sums on their way to the finishing warps: gate and up two buffers where the columns
+  // are few.  Down: DIRECT one, [row tile][warp][token]; else those, and the output's
+  // sums [T][16 RT2].
+  constexpr int kSumTiles = DIRECT ? 2 : kRT;
   const int bufs = DIRECT || cap <= 8 ? 2 : 1;
-  float* red = reinterpret_cast<float*>(sm + after_tables);
-  float* sums = red + bufs * red_floats;   // [T][16 RT2]
+  const uint32_t buf_bytes = kFewWarps * kSumTiles * cap * kFewColPitch * 4;
+  const uint32_t sums_bytes = DIRECT ? max(bufs * buf_bytes, kFewWarps * RT2 * A.T * kFewColPitch * 4) : bufs * buf_bytes;
+  FewRing way = few_sums_ring(sm, after_tables, buf_bytes, bufs);
+  float* sums = reinterpret_cast<float*>(sm + after_tables + sums_bytes);
   constexpr uint32_t tok = kRT * F::kRowTile;
-  const uint32_t sco = tok + cap * kTokPitch;
-  FewRing ring = few_ring(sm, after_tables + (bufs * red_floats + (DIRECT ? 0 : A.T * 16 * RT2)) * 4, A.smem_bytes,
+  const uint32_t sco = tok + cap * F::kTokPitch;
+  FewRing ring = few_ring(sm, after_tables + sums_bytes + (DIRECT ? 0 : A.T * 16 * RT2 * 4), A.smem_bytes,
                           (sco + kRT * F::kScaleBytes + F::kAlign - 1) & ~(F::kAlign - 1), F::kArrivals);
   __syncthreads();
-  const int ftiles = A.F / 16, items1 = segs * ftiles, steps1 = (HT + kFewWarps - 1) / kFewWarps;
-  const int htiles = A.H / 16, items2 = (htiles + RT2 - 1) / RT2, steps2 = (FT + kFewWarps - 1) / kFewWarps;
+  const int ftiles = A.F / 16, items1 = segs * ftiles, steps1 = (HT + F::kSlices - 1) / F::kSlices;
+  const int htiles = A.H / 16, items2 = (htiles + RT2 - 1) / RT2, steps2 = (FT + F::kSlices - 1) / F::kSlices;
 
   if (warp == kFewWarps) {
     int issued = 0, partial = 0;
@@ -574,9 +583,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
       for (int s = 0; s < steps1; ++s) {
         ok = ring_wait(ring.empty_bar(), ring.phase ^ 1, &sh->abort_flag, A.status);
         if (!ok) break;
-        const int kt0 = s * kFewWarps, nk = min(kFewWarps, HT - kt0);
-        copy_weights<GROUP>(W, f, ftiles, 2, kt0, nk, ring.stage(), ring.stage() + sco, ring.full_bar(), lane);
-        copy_tokens([&](int c) { return A.x8 + (size_t)tb.row_token[row + c] * HT * kTokenRecord; }, cols, kt0, nk,
+        const int kt0 = s * F::kSlices, nk = min(F::kSlices, HT - kt0);
+        copy_weights<GROUP, kSP>(W, f, ftiles, 2, kt0, nk, ring.stage(), ring.stage() + sco, ring.full_bar(), lane);
+        copy_tokens<F::kTokPitch>([&](int c) { return A.x8 + (size_t)tb.row_token[row + c] * HT * kTokenRecord; }, cols, kt0, nk,
                     ring.stage() + tok, ring.full_bar(), lane);
         ring.next();
         ++issued;
@@ -594,8 +603,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
         ok = ring_wait(ring.empty_bar(), ring.phase ^ 1, &sh->abort_flag, A.status);
         if (!ok) break;
         const LayerMatrix W = expert_matrix<GROUP>(A.W2, &A.map2, A.W2_scale, tb.seg_expert[seg], A.H, A.F);
-        const int kt0 = s * kFewWarps, nk = min(kFewWarps, FT - kt0);
-        copy_weights<GROUP>(W, item * RT2, 1, min(RT2, htiles - item * RT2), kt0, nk, ring.stage(), ring.stage() + sco,
+        const int kt0 = s * F::kSlices, nk = min(F::kSlices, FT - kt0);
+        copy_weights<GROUP, kSP>(W, item * RT2, 1, min(RT2, htiles - item * RT2), kt0, nk, ring.stage(), ring.stage() + sco,
                             ring.full_bar(), lane);
         ring.next();
         ++begun;
@@ -613,9 +622,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
         fence_proxy_async_global();   // the records were written by ordinary stores
         met = true;
       }
-      const int kt0 = ls * kFewWarps, nk = min(kFewWarps, FT - kt0);
+      const int kt0 = ls * F::kSlices, nk = min(F::kSlices, FT - kt0);
       const uint8_t* h8 = A.h8 + (size_t)tb.seg_row[lseg] * FT * kTokenRecord;
-      copy_tokens([&](int c) { return h8 + (size_t)c * FT * kTokenRecord; }, __popcll(tb.seg_mask[lseg]), kt0, nk,
+      copy_tokens<F::kTokPitch>([&](int c) { return h8 + (size_t)c * FT * kTokenRecord; }, __popcll(tb.seg_mask[lseg]), kt0, nk,
                   late.stage() + tok, late.full_bar(), lane);
       late.next();
       ++filled;
@@ -627,49 +636,62 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
     }
     drain(ring, issued, partial, lane);
   } else {
+    const bool finisher = warp > kFewWarps;
+    const int fid = tid - 32 * (kFewWarps + 1);   // of a finishing thread
     bool ok = consumer_sync_all(!sh->abort_flag);
-    int buf = 0;
-    for (int item = blockIdx.x; ok && item < items1; item += gridDim.x) {
-      const int seg = item / ftiles, f = item % ftiles;
-      const int cols = __popcll(tb.seg_mask[seg]), first = tb.seg_row[seg];
-      float* r = red + buf * red_floats;
-      // the stages of an item, and its sums put into r
-      auto item_sums = [&](auto nt) {
-        constexpr int NT = decltype(nt)::value;
-        const LaneTokens<NT> lt((1u << cols) - 1, tok + warp * kTokenRecord, lane);
-        float acc[2][NT][4] = {};
-        for (int s = 0; s < steps1; ++s, ring.next()) {
-          ok = ring_wait(ring.full_bar(), ring.phase, &sh->abort_flag, A.status);
-          if (!ok) break;
-          if (s * kFewWarps + warp < HT) layer_slice<GROUP, 2, NT>(ring.stage(), ring.stage() + sco, zero, lt, warp, lane, acc);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(ring.empty_bar());
+    auto wait = [&](uint32_t bar, uint32_t parity) { return ok = ring_wait(bar, parity, &sh->abort_flag, A.status); };
+    auto arrive = [&](uint32_t bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+
+    if (finisher) {
+      for (int item = blockIdx.x; item < items1; item += gridDim.x, way.next()) {
+        if (!(ok = ring_wait_idle(way.full_bar(), way.phase, &sh->abort_flag, A.status))) break;
+        const int seg = item / ftiles, f = item % ftiles;
+        const int cols = __popcll(tb.seg_mask[seg]), first = tb.seg_row[seg];
+        const float* r = reinterpret_cast<const float*>(sm + way.stage());
+        for (int i = fid; i < 16 * cols; i += kFewFinishThreads) {
+          const int row = i & 15, c = i >> 4;
+          const float g = get_sum(r, cap, row, c) * F::kSumScale, u = get_sum(r + kFewWarps * cap * kFewColPitch, cap, row, c) * F::kSumScale;
+          A.h[(size_t)(first + c) * A.F + f * 16 + row] = g / (1.f + expf(-g)) * u * tb.row_weight[first + c];
         }
-        // with two buffers a warp reaches the next item's meeting only after it has read this one's
-        if (bufs == 1) ok = consumer_sync_all(ok);
-        put_sums<2, NT>(r, cap, cols, warp, lane, acc);
-      };
-      if (DIRECT || cols <= 8)
-        item_sums(std::integral_constant<int, 1>());
-      else
-        item_sums(std::integral_constant<int, 2>());
-      ok = consumer_sync_all(ok);
-      if (ok && tid < 16 * cols) {
-        const int i = tid & 15, c = tid >> 4;
-        const float g = get_sum(r, cap, i, c) * F::kSumScale, u = get_sum(r + kFewWarps * cap * kFewColPitch, cap, i, c) * F::kSumScale;
-        A.h[(size_t)(first + c) * A.F + f * 16 + i] = g / (1.f + expf(-g)) * u * tb.row_weight[first + c];
+        arrive(way.empty_bar());
       }
-      if (bufs == 2) buf ^= 1;
-    }
-    __threadfence();
-    ok = consumer_sync_all(ok);
-    if (tid == 0) {
-      red_release_gpu_add(A.counters + 1, 1);
-      ok = ok && grid_wait(A.counters + 1, gridDim.x, &sh->abort_flag, A.status);
+      __threadfence();
+      finish_sync();
+      if (fid == 0) {
+        red_release_gpu_add(A.counters + 1, 1);
+        ok = ok && grid_wait(A.counters + 1, gridDim.x, &sh->abort_flag, A.status);
+      }
+    } else {
+      for (int item = blockIdx.x; ok && item < items1; item += gridDim.x) {
+        const int cols = __popcll(tb.seg_mask[item / ftiles]);
+        auto item_sums = [&](auto nt) {
+          constexpr int NT = decltype(nt)::value;
+          const LaneTokens<NT, F::kTokPitch> lt((1u << cols) - 1, tok, lane);
+          float acc[2][NT][4] = {};
+          for (int s = 0; s < steps1; ++s, ring.next()) {
+            if (!wait(ring.full_bar(), ring.phase)) return;
+#pragma unroll
+            for (int i = warp; i < F::kSlices; i += kFewWarps)
+              if (s * F::kSlices + i < HT) layer_slice<GROUP, kSP, 2, NT>(ring.stage(), ring.stage() + sco, zero, lt, i, lane, acc);
+            arrive(ring.empty_bar());
+          }
+          if (!wait(way.empty_bar(), way.phase ^ 1)) return;
+          put_sums<2, NT>(reinterpret_cast<float*>(sm + way.stage()), cap, cols, warp, lane, acc);
+          arrive(way.full_bar());
+          way.next();
+        };
+        if (DIRECT || cols <= 8)
+          item_sums(std::integral_constant<int, 1>());
+        else
+          item_sums(std::integral_constant<int, 2>());
+      }
     }
     ok = consumer_sync_all(ok);
     if (ok) {
-      for (int i = warp * gridDim.x + blockIdx.x; i < sh->rows * FT; i += kFewWarps * gridDim.x) {
+      for (int i = (finisher ? warp - 1 : warp) * gridDim.x + blockIdx.x; i < sh->rows * FT; i += (kFewAllWarps - 1) * gridDim.x) {
         const float4 h = __ldcg(reinterpret_cast<const float4*>(A.h + (size_t)i * 128) + lane);
         const float v[4] = {h.x, h.y, h.z, h.w};
         put_record<GROUP>(v, A.h8 + (size_t)i * kTokenRecord, lane);
@@ -680,73 +702,89 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
     ok = consumer_sync_all(ok);
     if (tid == 0) red_release_gpu_add(A.counters + 2, 1);
 
-    for (int item = blockIdx.x; ok && item < items2; item += gridDim.x) {
-      const int nrt = min(RT2, htiles - item * RT2);
-      if constexpr (DIRECT) {
-        float acc[RT2][1][4] = {};
-        for (int seg = 0; ok && seg < segs; ++seg) {
-          const LaneTokens<1> lt((uint32_t)tb.seg_mask[seg], tok + warp * kTokenRecord, lane);
-          for (int s = 0; s < steps2; ++s, ring.next()) {
-            ok = ring_wait(ring.full_bar(), ring.phase, &sh->abort_flag, A.status);
-            if (!ok) break;
-            if (s * kFewWarps + warp < FT) layer_slice<GROUP, RT2, 1>(ring.stage(), ring.stage() + sco, zero, lt, warp, lane, acc);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ring.empty_bar());
+    // Down.  DIRECT: one item's sums at a time, in one buffer; its barriers are those of
+    // buffer 0, of which all fillings so far are over.
+    if (DIRECT) {
+      const int filled = (items1 > (int)blockIdx.x ? (items1 - 1 - blockIdx.x) / gridDim.x + 1 : 0) + 1 >> 1;   // of buffer 0
+      way.slot = 0;
+      way.phase = filled & 1;
+      way.stages = 1;
+    }
+    if (finisher) {
+      constexpr int kParts = kFewFinishThreads / (16 * RT2);   // threads to a row: a token's is t % kParts
+      const int row = fid % (16 * RT2), part = fid / (16 * RT2);
+      for (int item = blockIdx.x; ok && item < items2; item += gridDim.x) {
+        const int nrt = min(RT2, htiles - item * RT2);
+        if constexpr (DIRECT) {
+          if (!(ok = ring_wait_idle(way.full_bar(), way.phase, &sh->abort_flag, A.status))) break;
+          const float* r = reinterpret_cast<const float*>(sm + way.stage());
+          for (int i = fid; i < 16 * nrt * A.T; i += kFewFinishThreads) {
+            const int t = i / (16 * nrt), o = i % (16 * nrt);
+            A.out[(size_t)t * A.H + item * RT2 * 16 + o] =
+                to_bf16(get_sum(r + (o >> 4) * kFewWarps * A.T * kFewColPitch, A.T, o & 15, t) * F::kSumScale);
           }
-        }
-        ok = consumer_sync_all(ok);
-        if (!ok) break;
-#pragma unroll
-        for (int rt = 0; rt < RT2; ++rt) {
-          const float one[1][1][4] = {{{acc[rt][0][0], acc[rt][0][1], acc[rt][0][2], acc[rt][0][3]}}};
-          if (rt < nrt) {
-            put_sums<1, 1>(red, 8, A.T, warp, lane, one);
-            consumer_sync();
-            if (tid < 16 * A.T)
-              A.out[(size_t)(tid >> 4) * A.H + (item * RT2 + rt) * 16 + (tid & 15)] = to_bf16(get_sum(red, 8, tid & 15, tid >> 4) * F::kSumScale);
-            consumer_sync();
-          }
-        }
-      } else {
-        for (int i = tid; i < A.T * 16 * RT2; i += kFewWarps * 32) sums[i] = 0.f;
-        consumer_sync();
-        for (int seg = 0; ok && seg < segs; ++seg) {
-          const int cols = __popcll(tb.seg_mask[seg]), first = tb.seg_row[seg];
-          float* r = red + buf * red_floats;
-          auto segment_sums = [&](auto nt) {
-            constexpr int NT = decltype(nt)::value;
-            const LaneTokens<NT> lt((1u << cols) - 1, tok + warp * kTokenRecord, lane);
-            float acc[RT2][NT][4] = {};
-            for (int s = 0; s < steps2; ++s, ring.next()) {
-              ok = ring_wait(ring.full_bar(), ring.phase, &sh->abort_flag, A.status);
-              if (!ok) break;
-              if (s * kFewWarps + warp < FT) layer_slice<GROUP, RT2, NT>(ring.stage(), ring.stage() + sco, zero, lt, warp, lane, acc);
-              __syncwarp();
-              if (lane == 0) mbar_arrive(ring.empty_bar());
+          arrive(way.empty_bar());
+          way.next();
+        } else {
+          for (int t = part; t < A.T; t += kParts) sums[t * 16 * RT2 + row] = 0.f;
+          for (int seg = 0; seg < segs; ++seg, way.next()) {
+            if (!(ok = ring_wait_idle(way.full_bar(), way.phase, &sh->abort_flag, A.status))) break;
+            const int cols = __popcll(tb.seg_mask[seg]), first = tb.seg_row[seg];
+            const float* r = reinterpret_cast<const float*>(sm + way.stage()) + (row >> 4) * kFewWarps * cap * kFewColPitch;
+            for (int c = 0; c < cols; ++c) {
+              const int t = tb.row_token[first + c];
+              if (t % kParts == part) sums[t * 16 * RT2 + row] += get_sum(r, cap, row & 15, c);
             }
-            if (bufs == 1) ok = consumer_sync_all(ok);
-            put_sums<RT2, NT>(r, cap, cols, warp, lane, acc);
-          };
-          if (cols <= 8)
-            segment_sums(std::integral_constant<int, 1>());
-          else
-            segment_sums(std::integral_constant<int, 2>());
-          ok = consumer_sync_all(ok);
-          // a row and token of a segment has one thread, and a thread's part of `sums` is its own
-          // from segment to segment only by the meetings between them
-          for (int i = tid; i < 16 * RT2 * cols; i += kFewWarps * 32) {
-            const int c = i / (16 * RT2), row = i % (16 * RT2);
-            sums[tb.row_token[first + c] * 16 * RT2 + row] += get_sum(r + (row >> 4) * kFewWarps * cap * kFewColPitch, cap, row & 15, c);
+            arrive(way.empty_bar());
           }
-          if (bufs == 2) buf ^= 1;
+          if (!ok) break;
+          if (row < 16 * nrt)
+            for (int t = part; t < A.T; t += kParts) A.out[(size_t)t * A.H + item * RT2 * 16 + row] = to_bf16(sums[t * 16 * RT2 + row] * F::kSumScale);
         }
-        ok = consumer_sync_all(ok);
-        if (!ok) break;
-        for (int i = tid; i < A.T * 16 * RT2; i += kFewWarps * 32) {
-          const int t = i / (16 * RT2), row = i % (16 * RT2);
-          if (row < 16 * nrt) A.out[(size_t)t * A.H + item * RT2 * 16 + row] = to_bf16(sums[i] * F::kSumScale);
+      }
+    } else {
+      for (int item = blockIdx.x; ok && item < items2; item += gridDim.x) {
+        if constexpr (DIRECT) {
+          float acc[RT2][1][4] = {};
+          for (int seg = 0; ok && seg < segs; ++seg) {
+            const LaneTokens<1, F::kTokPitch> lt((uint32_t)tb.seg_mask[seg], tok, lane);
+            for (int s = 0; s < steps2; ++s, ring.next()) {
+              if (!wait(ring.full_bar(), ring.phase)) break;
+#pragma unroll
+              for (int i = warp; i < F::kSlices; i += kFewWarps)
+                if (s * F::kSlices + i < FT) layer_slice<GROUP, kSP, RT2, 1>(ring.stage(), ring.stage() + sco, zero, lt, i, lane, acc);
+              arrive(ring.empty_bar());
+            }
+          }
+          if (!ok || !wait(way.empty_bar(), way.phase ^ 1)) break;
+          put_sums<RT2, 1>(reinterpret_cast<float*>(sm + way.stage()), A.T, A.T, warp, lane, acc);
+          arrive(way.full_bar());
+          way.next();
+        } else {
+          for (int seg = 0; ok && seg < segs; ++seg) {
+            const int cols = __popcll(tb.seg_mask[seg]);
+            auto segment_sums = [&](auto nt) {
+              constexpr int NT = decltype(nt)::value;
+              const LaneTokens<NT, F::kTokPitch> lt((1u << cols) - 1, tok, lane);
+              float acc[RT2][NT][4] = {};
+              for (int s = 0; s < steps2; ++s, ring.next()) {
+                if (!wait(ring.full_bar(), ring.phase)) return;
+#pragma unroll
+                for (int i = warp; i < F::kSlices; i += kFewWarps)
+                  if (s * F::kSlices + i < FT) layer_slice<GROUP, kSP, RT2, NT>(ring.stage(), ring.stage() + sco, zero, lt, i, lane, acc);
+                arrive(ring.empty_bar());
+              }
+              if (!wait(way.empty_bar(), way.phase ^ 1)) return;
+              put_sums<RT2, NT>(reinterpret_cast<float*>(sm + way.stage()), cap, cols, warp, lane, acc);
+              arrive(way.full_bar());
+              way.next();
+            };
+            if (cols <= 8)
+              segment_sums(std::integral_constant<int, 1>());
+            else
+              segment_sums(std::integral_constant<int, 2>());
+          }
         }
-        consumer_sync();
       }
     }
   }

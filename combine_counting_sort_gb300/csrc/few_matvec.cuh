@@ -104,10 +104,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) matvec_kernel(const MatvecArgs
   const int tiles = (A.N + 15) / 16, groups = (tiles + RT - 1) / RT;
   const int passes = (A.T + kFewMaxCols - 1) / kFewMaxCols, per = (A.T + passes - 1) / passes;
   const int items = groups * passes, KT = (A.K + 127) / 128, steps = (KT + kFewWarps - 1) / kFewWarps;
-  float* red = reinterpret_cast<float*>(sm + 256);
-  const int tile_floats = kFewWarps * per * kFewColPitch;
+  const int tile_floats = kFewWarps * per * kFewColPitch, bufs = per <= 8 ? 2 : 1;
   constexpr uint32_t tok = RT * F::kRowTile;
-  FewRing ring = few_ring(sm, 256 + RT * tile_floats * 4, A.smem_bytes, (tok + per * F::kTokPitch + 127) & ~127u, 2);
+  FewRing way = few_sums_ring(sm, 256, RT * tile_floats * 4, bufs);
+  FewRing ring = few_ring(sm, 256 + bufs * RT * tile_floats * 4, A.smem_bytes, (tok + per * F::kTokPitch + 127) & ~127u, 2);
   if (tid == 0) sh->abort_flag = 0;
   __syncthreads();
 
@@ -144,19 +144,33 @@ __global__ void __launch_bounds__(kFewThreads, 1) matvec_kernel(const MatvecArgs
     return;
   }
 
-  bool ok = true;
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int group = item / passes, t0 = item % passes * per, cols = min(per, A.T - t0), nrt = min(RT, tiles - group * RT);
+  if (warp > kFewWarps) {
+    const int fid = tid - 32 * (kFewWarps + 1);
+    for (int item = blockIdx.x; item < items; item += gridDim.x, way.next()) {
+      if (!ring_wait_idle(way.full_bar(), way.phase, &sh->abort_flag, A.status)) return;
+      const int group = item / passes, t0 = item % passes * per, cols = min(per, A.T - t0), nrt = min(RT, tiles - group * RT);
+      const float* r = reinterpret_cast<const float*>(sm + way.stage());
+      for (int i = fid; i < nrt * 16 * cols; i += kFewFinishThreads) {
+        const int row = i % (nrt * 16), c = i / (nrt * 16), n = group * RT * 16 + row;
+        if (n < A.N)
+          A.y[(size_t)(t0 + c) * A.N + n] = to_bf16(get_sum(r + (row >> 4) * tile_floats, per, row & 15, c) * 0x1p69f);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(way.empty_bar());
+    }
+    return;
+  }
+
+  for (int item = blockIdx.x; item < items; item += gridDim.x, way.next()) {
+    const int t0 = item % passes * per, cols = min(per, A.T - t0);
     float acc[RT][2][4] = {};
     uint32_t b[2][16] = {};
     for (int s = 0; s < steps; ++s, ring.next()) {
-      ok = ring_wait(ring.full_bar(), ring.phase, &sh->abort_flag, A.status);
-      if (!ok) break;
+      if (!ring_wait(ring.full_bar(), ring.phase, &sh->abort_flag, A.status)) return;
       if (s * kFewWarps + warp < KT) {
         const uint32_t st = ring.stage();
         const int c = lane >> 2;
-        const uint32_t row[2] = {c < cols ? st + tok + c * F::kTokPitch : 0,
-                                       c + 8 < cols ? st + tok + (c + 8) * F::kTokPitch : 0};
+        const uint32_t row[2] = {c < cols ? st + tok + c * F::kTokPitch : 0, c + 8 < cols ? st + tok + (c + 8) * F::kTokPitch : 0};
         if (cols <= 8)
           matvec_slice<GROUP, RT, 1>(st, row, warp, lane, b, acc);
         else
@@ -165,7 +179,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) matvec_kernel(const MatvecArgs
       __syncwarp();
       if (lane == 0) mbar_arrive(ring.empty_bar());
     }
-    if (!consumer_sync_all(ok)) return;   // everyone has read the last item's sums
+    if (!ring_wait(way.empty_bar(), way.phase ^ 1, &sh->abort_flag, A.status)) return;
+    float* red = reinterpret_cast<float*>(sm + way.stage());
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -175,12 +190,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) matvec_kernel(const MatvecArgs
           const int col = 8 * j + 2 * (lane & 3) + (i & 1);
           if (col < cols) red[rt * tile_floats + (warp * per + col) * kFewColPitch + (lane >> 2) + 8 * (i >> 1)] = acc[rt][j][i];
         }
-    consumer_sync();
-    for (int i = tid; i < nrt * 16 * cols; i += kFewWarps * 32) {
-      const int row = i % (nrt * 16), c = i / (nrt * 16), n = group * RT * 16 + row;
-      if (n < A.N)
-        A.y[(size_t)(t0 + c) * A.N + n] = to_bf16(get_sum(red + (row >> 4) * tile_floats, per, row & 15, c) * 0x1p69f);
-    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(way.full_bar());
   }
 }
 
