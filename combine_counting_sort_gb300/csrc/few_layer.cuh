@@ -106,10 +106,13 @@ MOE_DEV void load_codes(uint32_t wst, int slice, int lane, uint32_t (&c)[GROUP ?
   }
 }
 
-// Two e4m3 codes as two f16 values.
-MOE_DEV uint32_t widen_e4m3(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
-  return (uint32_t)h.x | (uint32_t)h.y << 16;
+// Four e4m3 codes as f16 values: the first two, and the others.
+MOE_DEV void widen_e4m3(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(codes));
 }
 
 // The A operand of MMA m of a slice.
@@ -122,10 +125,8 @@ MOE_DEV void widen(const uint32_t (&c)[GROUP ? 8 : 16], int m, uint32_t (&a)[4])
     a[2] = l & 0x00F000F0u;
     a[3] = h & 0x00F000F0u;
   } else {
-    a[0] = widen_e4m3(c[m] & 0xFFFFu);
-    a[1] = widen_e4m3(c[m + 8] & 0xFFFFu);
-    a[2] = widen_e4m3(c[m] >> 16);
-    a[3] = widen_e4m3(c[m + 8] >> 16);
+    widen_e4m3(c[m], a[0], a[2]);
+    widen_e4m3(c[m + 8], a[1], a[3]);
   }
 }
 
