@@ -24,7 +24,6 @@ constexpr int kFewWarps = 8;                       // computing warps, one per 1
 constexpr int kFewFinish = 3;                      // finishing warps
 constexpr int kFewAllWarps = kFewWarps + 1 + kFewFinish, kFewThreads = kFewAllWarps * 32;
 constexpr int kFewFinishThreads = 32 * kFewFinish;
-constexpr int kFewMaxCols = 16;                    // tokens per pass over a stage
 constexpr int kFewMaxStages = 12;
 constexpr uint64_t kFewTimeoutNs = 1000000000ull;  // bound of every wait
 
@@ -119,9 +118,24 @@ struct FewRing {
   }
 };
 
-// A ring in the shared memory [at, smem_bytes); the calling thread 0 initialises
-// the barriers, and the caller synchronises the block.
-MOE_DEV FewRing few_ring(unsigned char* sm, uint32_t at, uint32_t smem_bytes, uint32_t stage_bytes, int arrivals) {
+// All barriers and the abort flag, by the block's first threads; the caller
+// synchronises the block.  `arrivals` complete a stage.
+MOE_DEV void few_barriers(unsigned char* sm, int tid, int arrivals) {
+  FewShared* sh = reinterpret_cast<FewShared*>(sm);
+  if (tid < kFewMaxStages) {
+    mbar_init(smem_u32(sh->full + tid), arrivals);
+    mbar_init(smem_u32(sh->empty + tid), kFewWarps);
+    if (tid < 2) {
+      mbar_init(smem_u32(sh->sums_full + tid), kFewWarps);
+      mbar_init(smem_u32(sh->sums_empty + tid), kFewFinish);
+    }
+    fence_mbar_init();
+  }
+  if (tid == 0) sh->abort_flag = 0;
+}
+
+// A ring in the shared memory [at, smem_bytes).
+MOE_DEV FewRing few_ring(unsigned char* sm, uint32_t at, uint32_t smem_bytes, uint32_t stage_bytes) {
   FewShared* sh = reinterpret_cast<FewShared*>(sm);
   FewRing r;
   at = (at + 1023) & ~1023u;
@@ -131,13 +145,6 @@ MOE_DEV FewRing few_ring(unsigned char* sm, uint32_t at, uint32_t smem_bytes, ui
   r.empty = smem_u32(sh->empty);
   r.stages = min((int)((smem_bytes - at) / stage_bytes), kFewMaxStages);
   r.slot = r.phase = 0;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < r.stages; ++i) {
-      mbar_init(r.full + 8 * i, arrivals);
-      mbar_init(r.empty + 8 * i, kFewWarps);
-    }
-    fence_mbar_init();
-  }
   return r;
 }
 
@@ -152,13 +159,6 @@ MOE_DEV FewRing few_sums_ring(unsigned char* sm, uint32_t at, uint32_t bytes, in
   r.empty = smem_u32(sh->sums_empty);
   r.stages = buffers;
   r.slot = r.phase = 0;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < buffers; ++i) {
-      mbar_init(r.full + 8 * i, kFewWarps);
-      mbar_init(r.empty + 8 * i, kFewFinish);
-    }
-    fence_mbar_init();
-  }
   return r;
 }
 

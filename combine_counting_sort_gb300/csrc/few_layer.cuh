@@ -50,6 +50,7 @@ struct LayerForm {
   static constexpr int kArrivals = kW4 ? 2 : 34;
   static constexpr float kSumScale = kW4 ? 0x1p24f : 1.f;   // what the sums lack
 };
+constexpr int kLayerCols = 16;                  // tokens per pass over a stage
 constexpr int kFewOwnTopk = 2 * kFewAllWarps;   // tokens whose routes every block selects for itself
 
 // ---------------------------------------------------------------- token records
@@ -307,7 +308,7 @@ MOE_DEV void copy_tokens(RecordOf record_of, int cols, int kt0, int nk, uint32_t
 // ---------------------------------------------------------------- routes
 
 // Tables of the routes in shared memory, sized by the P = T k pairs.  A segment is
-// one expert and up to 16 of the tokens routed to it; row r of the activations
+// one expert and as many of the tokens routed to it as a stage has room for; row r of the activations
 // belongs to one (token, expert).
 struct FewTables {
   uint64_t* seg_mask;
@@ -385,11 +386,75 @@ MOE_DEV void few_meet(const LayerArgs& A, int counter, FewShared* sh, int tid) {
   __syncthreads();
 }
 
+// The tables of at most 32 pairs, by one warp: lane p is pair p, the lowest lane of those
+// with the same expert makes its segment.
+template <int MAXCOLS>
+MOE_DEV void few_tables_small(const LayerArgs& A, FewShared* sh, const FewTables& tb, const int* ids, const float* w, int lane) {
+  const int P = A.T * A.k, t = lane / A.k;
+  const int e = lane < P ? ids[lane] : -1;
+  if (e >= A.E && blockIdx.x == 0) set_status(A.status, MOE_ERR_EXPERT_ID);
+  const bool on = e >= 0 && e < A.E;
+  const uint32_t same = __match_any_sync(0xffffffffu, on ? e : -1 - lane);
+  uint32_t tokens = 0;
+  float sum = 0.f;
+  bool again = false;   // the token names the expert in an earlier slot too
+  for (int p = 0; p < P; ++p) {
+    const float wp = __shfl_sync(0xffffffffu, lane < P ? w[lane] : 0.f, p);
+    if ((same >> p) & 1) {
+      tokens |= 1u << (p / A.k);
+      if (p / A.k == t) {
+        again |= p < lane;
+        sum += wp;   // in slot order
+      }
+    }
+  }
+  const bool leads = on && lane == __ffs(same) - 1;
+  const int c = leads ? __popc(tokens) : 0, s = (c + MAXCOLS - 1) / MAXCOLS;
+  int incl = c | s << 16;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  int row = (incl & 0xFFFF) - c, seg = (incl >> 16) - s;
+  const int first = __shfl_sync(0xffffffffu, row, __ffs(same) - 1);
+  const int most = __reduce_max_sync(0xffffffffu, c), all = __shfl_sync(0xffffffffu, incl, 31);
+  if (leads) {
+    for (uint32_t m = tokens; m;) {
+      uint32_t take = m;
+      if (__popc(m) > MAXCOLS) {
+        take = 0;
+        for (int b = 0; b < MAXCOLS; ++b) take |= (m ^ take) & (~(m ^ take) + 1);   // the lowest bit left
+      }
+      m ^= take;
+      tb.seg_mask[seg] = take;
+      tb.seg_expert[seg] = e;
+      tb.seg_row[seg++] = row;
+      row += __popc(take);
+    }
+  }
+  if (on && !again) {
+    const int r = first + __popc(tokens & ((1u << t) - 1));
+    tb.row_token[r] = (uint8_t)t;
+    tb.row_weight[r] = sum;
+  }
+  if (lane == 0) {
+    sh->rows = all & 0xFFFF;
+    sh->segs = all >> 16;
+    sh->cap = max(1, min(most, MAXCOLS));
+  }
+}
+
 // The tables from the pairs' ids and weights (in shared memory).  scratch: E masks,
 // E first rows, a count per warp.
+template <int MAXCOLS>
 MOE_DEV void few_tables(const LayerArgs& A, FewShared* sh, const FewTables& tb, const int* ids, const float* w,
                         unsigned char* scratch, int tid, int warp, int lane) {
   const int P = A.T * A.k;
+  if (P <= 32) {   // 0.4 us, and 1.7 us the other way
+    if (warp == 0) few_tables_small<MAXCOLS>(A, sh, tb, ids, w, lane);
+    return;
+  }
   uint64_t* mask = reinterpret_cast<uint64_t*>(scratch);
   int* first = reinterpret_cast<int*>(mask + A.E);
   int* totals = first + A.E;
@@ -413,7 +478,7 @@ MOE_DEV void few_tables(const LayerArgs& A, FewShared* sh, const FewTables& tb, 
   for (int i = 0; i < 4; ++i) {
     m4[i] = 4 * tid + i < A.E ? mask[4 * tid + i] : 0;
     const int c = __popcll(m4[i]);
-    counts += c | ((c + kFewMaxCols - 1) / kFewMaxCols) << 16;
+    counts += c | ((c + MAXCOLS - 1) / MAXCOLS) << 16;
     most = max(most, c);
   }
   int incl = counts;
@@ -424,7 +489,7 @@ MOE_DEV void few_tables(const LayerArgs& A, FewShared* sh, const FewTables& tb, 
   }
   most = __reduce_max_sync(0xffffffffu, most);
   if (lane == 31) totals[warp] = incl;
-  if (lane == 0 && most > 1) atomicMax(&sh->cap, min(most, kFewMaxCols));
+  if (lane == 0 && most > 1) atomicMax(&sh->cap, min(most, MAXCOLS));
   __syncthreads();
   int at = incl - counts;
   for (int i = 0; i < warp; ++i) at += totals[i];
@@ -435,9 +500,9 @@ MOE_DEV void few_tables(const LayerArgs& A, FewShared* sh, const FewTables& tb, 
     if (4 * tid + i < A.E) first[4 * tid + i] = row;
     while (m) {
       uint64_t take = m;
-      if (__popcll(m) > kFewMaxCols) {
+      if (__popcll(m) > MAXCOLS) {
         take = 0;
-        for (int b = 0; b < kFewMaxCols; ++b) take |= (m ^ take) & (~(m ^ take) + 1);   // the lowest bit left
+        for (int b = 0; b < MAXCOLS; ++b) take |= (m ^ take) & (~(m ^ take) + 1);   // the lowest bit left
       }
       m ^= take;
       tb.seg_mask[seg] = take;
@@ -476,85 +541,15 @@ MOE_DEV LayerMatrix expert_matrix(const uint8_t* W, const CUtensorMap* map, cons
   return LayerMatrix{nullptr, map, scale + (size_t)e * (N / 128) * (K / 128), e * N, K};
 }
 
-// ---------------------------------------------------------------- the kernel
+// ---------------------------------------------------------------- gate and up, down
 
-// One cooperative launch, one block per SM:
-//   tokens to records, and logits; the grid meets; every block selects the
-//   routes for itself and builds the same tables;
-//   gate and up: items (segment, 16 features), the two row tiles of a stage
-//   being the gate's and the up's rows of the same features;
-//   the grid meets, the activations become records, the grid meets again;
-//   meanwhile the ring already fills with the next weights;
-//   down: items (RT2 row tiles of the output), each over all segments with the
-//   sums of every token on chip, so the output is written once, without atomics,
-//   in a fixed order.
-// DIRECT (T <= 8): a token is a column of the down products, and its sums over all
-// experts stay in registers.  Otherwise the columns are a segment's tokens, and the
-// segments' sums are added up in shared memory.
-template <int GROUP, int RT2, bool DIRECT>
-__global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_constant__ LayerArgs A) {
-  extern __shared__ __align__(1024) unsigned char sm[];
-  // 4-bit stages are short of work: handing one over takes some 300 cycles of a warp's 900.
-  // Two slices per warp halve that where the tokens leave room for it.
-  constexpr int kSP = GROUP != 0 && DIRECT ? 2 : 1;
-  using F = LayerForm<GROUP, kSP>;
+template <int GROUP, int RT2, bool DIRECT, int SP>
+MOE_DEV void layer_products(const LayerArgs& A, unsigned char* sm, const FewTables& tb, uint32_t after_tables, uint32_t zero, int tid,
+                            int warp, int lane) {
+  using F = LayerForm<GROUP, SP>;
   constexpr int kRT = RT2 > 2 ? RT2 : 2;
   FewShared* sh = reinterpret_cast<FewShared*>(sm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int P = A.T * A.k, HT = A.H / 128, FT = A.F / 128;
-  constexpr uint32_t kZeroAt = 256, kTablesAt = kZeroAt + (kTokenRecord + 15) / 16 * 16;
-  const FewTables tb(sm + kTablesAt, P);
-  const uint32_t after_tables = (kTablesAt + P * 21 + 127) & ~127;
-  const uint32_t zero = smem_u32(sm) + kZeroAt;
-  unsigned char* scratch = sm + after_tables;   // until the ring takes it
-  int* ids = reinterpret_cast<int*>(scratch);
-  float* w = reinterpret_cast<float*>(ids + P);
-  unsigned char* scratch2 = reinterpret_cast<unsigned char*>(w + P);
-
-  if (tid == 0) sh->abort_flag = 0;
-  if (tid < kTokenRecord / 4) reinterpret_cast<int*>(sm + kZeroAt)[tid] = 0;
-  for (int i = warp * gridDim.x + blockIdx.x; i < A.T * HT; i += kFewAllWarps * gridDim.x) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(A.x + (size_t)i * 128) + lane);   // the tokens' rows are blocks of 128 in a row
-    const float v[4] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)};
-    put_record<GROUP>(v, A.x8 + (size_t)i * kTokenRecord, lane);
-  }
-  if (A.router) few_logits(A, reinterpret_cast<float*>(scratch), tid, warp, lane);
-  fence_proxy_async_global();   // the records are read by bulk copies
-  few_meet(A, 0, sh, tid);
-  if (A.router) {
-    // Few tokens: every block selects for all of them.  Many: each block for its own, and the
-    // grid meets once more (1.4 us; a warp takes 2 to 3 us for its first token and 1.5 for each
-    // one more).
-    const bool shared_out = A.T > kFewOwnTopk;
-    for (int t = shared_out ? (int)blockIdx.x + (warp ? A.T : 0) : warp; t < A.T; t += shared_out ? gridDim.x : kFewAllWarps) {
-      float wt;
-      const float* l = A.logits + (size_t)t * A.E;
-      const size_t run = (size_t)A.T * A.E;
-      const int id = A.E <= 256 ? warp_topk<8>(l, run, A.splits, A.E, A.k, lane, &wt) : warp_topk<32>(l, run, A.splits, A.E, A.k, lane, &wt);
-      if (lane < A.k) {
-        if (!shared_out) {
-          ids[t * A.k + lane] = id;
-          w[t * A.k + lane] = wt;
-        }
-        if (shared_out || blockIdx.x == 0) {
-          A.ids[t * A.k + lane] = id;
-          A.w[t * A.k + lane] = wt;
-        }
-      }
-    }
-    if (shared_out) few_meet(A, 3, sh, tid);
-  }
-  if (!A.router || A.T > kFewOwnTopk) {
-    for (int p = tid; p < P; p += kFewThreads) {
-      ids[p] = __ldcg(A.ids + p);
-      w[p] = __ldcg(A.w + p);
-    }
-  }
-  __syncthreads();
-  few_tables(A, sh, tb, ids, w, scratch2, tid, warp, lane);
-  fence_proxy_async_shared();   // the ring's copies overwrite the scratch
-  __syncthreads();
-
+  const int HT = A.H / 128, FT = A.F / 128;
   const int segs = sh->segs, cap = sh->cap;
   // The sums on their way to the finishing warps: gate and up two buffers where the columns
   // are few.  Down: DIRECT one, [row tile][warp][token]; else those, and the output's
@@ -568,8 +563,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
   constexpr uint32_t tok = kRT * F::kRowTile;
   const uint32_t sco = tok + cap * F::kTokPitch;
   FewRing ring = few_ring(sm, after_tables + sums_bytes + (DIRECT ? 0 : A.T * 16 * RT2 * 4), A.smem_bytes,
-                          (sco + kRT * F::kScaleBytes + F::kAlign - 1) & ~(F::kAlign - 1), F::kArrivals);
-  __syncthreads();
+                          (sco + kRT * F::kScaleBytes + F::kAlign - 1) & ~(F::kAlign - 1));
   const int ftiles = A.F / 16, items1 = segs * ftiles, steps1 = (HT + F::kSlices - 1) / F::kSlices;
   const int htiles = A.H / 16, items2 = (htiles + RT2 - 1) / RT2, steps2 = (FT + F::kSlices - 1) / F::kSlices;
 
@@ -585,7 +579,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
         ok = ring_wait(ring.empty_bar(), ring.phase ^ 1, &sh->abort_flag, A.status);
         if (!ok) break;
         const int kt0 = s * F::kSlices, nk = min(F::kSlices, HT - kt0);
-        copy_weights<GROUP, kSP>(W, f, ftiles, 2, kt0, nk, ring.stage(), ring.stage() + sco, ring.full_bar(), lane);
+        copy_weights<GROUP, SP>(W, f, ftiles, 2, kt0, nk, ring.stage(), ring.stage() + sco, ring.full_bar(), lane);
         copy_tokens<F::kTokPitch>([&](int c) { return A.x8 + (size_t)tb.row_token[row + c] * HT * kTokenRecord; }, cols, kt0, nk,
                     ring.stage() + tok, ring.full_bar(), lane);
         ring.next();
@@ -605,7 +599,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
         if (!ok) break;
         const LayerMatrix W = expert_matrix<GROUP>(A.W2, &A.map2, A.W2_scale, tb.seg_expert[seg], A.H, A.F);
         const int kt0 = s * F::kSlices, nk = min(F::kSlices, FT - kt0);
-        copy_weights<GROUP, kSP>(W, item * RT2, 1, min(RT2, htiles - item * RT2), kt0, nk, ring.stage(), ring.stage() + sco,
+        copy_weights<GROUP, SP>(W, item * RT2, 1, min(RT2, htiles - item * RT2), kt0, nk, ring.stage(), ring.stage() + sco,
                             ring.full_bar(), lane);
         ring.next();
         ++begun;
@@ -676,7 +670,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
             if (!wait(ring.full_bar(), ring.phase)) return;
 #pragma unroll
             for (int i = warp; i < F::kSlices; i += kFewWarps)
-              if (s * F::kSlices + i < HT) layer_slice<GROUP, kSP, 2, NT>(ring.stage(), ring.stage() + sco, zero, lt, i, lane, acc);
+              if (s * F::kSlices + i < HT) layer_slice<GROUP, SP, 2, NT>(ring.stage(), ring.stage() + sco, zero, lt, i, lane, acc);
             arrive(ring.empty_bar());
           }
           if (!wait(way.empty_bar(), way.phase ^ 1)) return;
@@ -684,7 +678,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
           arrive(way.full_bar());
           way.next();
         };
-        if (DIRECT || cols <= 8)
+        if (SP == 2 || DIRECT || cols <= 8)
           item_sums(std::integral_constant<int, 1>());
         else
           item_sums(std::integral_constant<int, 2>());
@@ -753,7 +747,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
               if (!wait(ring.full_bar(), ring.phase)) break;
 #pragma unroll
               for (int i = warp; i < F::kSlices; i += kFewWarps)
-                if (s * F::kSlices + i < FT) layer_slice<GROUP, kSP, RT2, 1>(ring.stage(), ring.stage() + sco, zero, lt, i, lane, acc);
+                if (s * F::kSlices + i < FT) layer_slice<GROUP, SP, RT2, 1>(ring.stage(), ring.stage() + sco, zero, lt, i, lane, acc);
               arrive(ring.empty_bar());
             }
           }
@@ -772,7 +766,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
                 if (!wait(ring.full_bar(), ring.phase)) return;
 #pragma unroll
                 for (int i = warp; i < F::kSlices; i += kFewWarps)
-                  if (s * F::kSlices + i < FT) layer_slice<GROUP, kSP, RT2, NT>(ring.stage(), ring.stage() + sco, zero, lt, i, lane, acc);
+                  if (s * F::kSlices + i < FT) layer_slice<GROUP, SP, RT2, NT>(ring.stage(), ring.stage() + sco, zero, lt, i, lane, acc);
                 arrive(ring.empty_bar());
               }
               if (!wait(way.empty_bar(), way.phase ^ 1)) return;
@@ -780,7 +774,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
               arrive(way.full_bar());
               way.next();
             };
-            if (cols <= 8)
+            if (SP == 2 || cols <= 8)
               segment_sums(std::integral_constant<int, 1>());
             else
               segment_sums(std::integral_constant<int, 2>());
@@ -789,6 +783,89 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
       }
     }
   }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+// One cooperative launch, one block per SM:
+//   tokens to records, and logits; the grid meets; every block selects the
+//   routes for itself and builds the same tables;
+//   gate and up: items (segment, 16 features), the two row tiles of a stage
+//   being the gate's and the up's rows of the same features;
+//   the grid meets, the activations become records, the grid meets again;
+//   meanwhile the ring already fills with the next weights;
+//   down: items (RT2 row tiles of the output), each over all segments with the
+//   sums of every token on chip, so the output is written once, without atomics,
+//   in a fixed order.
+// DIRECT (T <= 8): a token is a column of the down products, and its sums over all
+// experts stay in registers.  Otherwise the columns are a segment's tokens, and the
+// segments' sums are added up in shared memory.
+template <int GROUP, int RT2, bool DIRECT>
+__global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_constant__ LayerArgs A) {
+  extern __shared__ __align__(1024) unsigned char sm[];
+  FewShared* sh = reinterpret_cast<FewShared*>(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int P = A.T * A.k, HT = A.H / 128;
+  constexpr uint32_t kZeroAt = 256, kTablesAt = kZeroAt + (kTokenRecord + 15) / 16 * 16;
+  const FewTables tb(sm + kTablesAt, P);
+  const uint32_t after_tables = (kTablesAt + P * 21 + 127) & ~127;
+  const uint32_t zero = smem_u32(sm) + kZeroAt;
+  unsigned char* scratch = sm + after_tables;   // until the ring takes it
+  int* ids = reinterpret_cast<int*>(scratch);
+  float* w = reinterpret_cast<float*>(ids + P);
+  unsigned char* scratch2 = reinterpret_cast<unsigned char*>(w + P);
+
+  few_barriers(sm, tid, LayerForm<GROUP, 1>::kArrivals);
+  if (tid < kTokenRecord / 4) reinterpret_cast<int*>(sm + kZeroAt)[tid] = 0;
+  for (int i = warp * gridDim.x + blockIdx.x; i < A.T * HT; i += kFewAllWarps * gridDim.x) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(A.x + (size_t)i * 128) + lane);   // the tokens' rows are blocks of 128 in a row
+    const float v[4] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)};
+    put_record<GROUP>(v, A.x8 + (size_t)i * kTokenRecord, lane);
+  }
+  if (A.router) few_logits(A, reinterpret_cast<float*>(scratch), tid, warp, lane);
+  fence_proxy_async_global();   // the records are read by bulk copies
+  few_meet(A, 0, sh, tid);
+  if (A.router) {
+    // Few tokens: every block selects for all of them.  Many: each block for its own, and the
+    // grid meets once more (1.4 us; a warp takes 2 to 3 us for its first token and 1.5 for each
+    // one more).
+    const bool shared_out = A.T > kFewOwnTopk;
+    for (int t = shared_out ? (int)blockIdx.x + (warp ? A.T : 0) : warp; t < A.T; t += shared_out ? gridDim.x : kFewAllWarps) {
+      float wt;
+      const float* l = A.logits + (size_t)t * A.E;
+      const size_t run = (size_t)A.T * A.E;
+      const int id = A.E <= 256 ? warp_topk<8>(l, run, A.splits, A.E, A.k, lane, &wt) : warp_topk<32>(l, run, A.splits, A.E, A.k, lane, &wt);
+      if (lane < A.k) {
+        if (!shared_out) {
+          ids[t * A.k + lane] = id;
+          w[t * A.k + lane] = wt;
+        }
+        if (shared_out || blockIdx.x == 0) {
+          A.ids[t * A.k + lane] = id;
+          A.w[t * A.k + lane] = wt;
+        }
+      }
+    }
+    if (shared_out) few_meet(A, 3, sh, tid);
+  }
+  if (!A.router || A.T > kFewOwnTopk) {
+    for (int p = tid; p < P; p += kFewThreads) {
+      ids[p] = __ldcg(A.ids + p);
+      w[p] = __ldcg(A.w + p);
+    }
+  }
+  __syncthreads();
+  few_tables<kLayerCols>(A, sh, tb, ids, w, scratch2, tid, warp, lane);
+  fence_proxy_async_shared();   // the ring's copies overwrite the scratch
+  __syncthreads();
+
+  // 4-bit stages are short of work: handing one over takes some 300 cycles of a warp's 900.
+  // Two slices per warp halve that where no expert has more than 8 tokens, whose
+  // records would not leave room for a second stage.
+  if (GROUP != 0 && (DIRECT || sh->cap <= 8))
+    layer_products<GROUP, RT2, DIRECT, GROUP != 0 ? 2 : 1>(A, sm, tb, after_tables, zero, tid, warp, lane);
+  else if (GROUP == 0 || !DIRECT)
+    layer_products<GROUP, RT2, DIRECT, 1>(A, sm, tb, after_tables, zero, tid, warp, lane);
   // the last block to leave clears the counters for the next call
   __syncthreads();
   if (tid == 0 && atomicAdd(A.counters + 4, 1) == (int)gridDim.x - 1) {

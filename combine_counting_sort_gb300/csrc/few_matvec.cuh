@@ -18,6 +18,8 @@
 
 namespace moe {
 
+constexpr int kMatvecCols = 16;   // tokens per pass over a stage
+
 template <int GROUP>
 struct MatvecForm {
   static constexpr int kTile = w4_tile_bytes(GROUP);
@@ -102,13 +104,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) matvec_kernel(const MatvecArgs
   FewShared* sh = reinterpret_cast<FewShared*>(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tiles = (A.N + 15) / 16, groups = (tiles + RT - 1) / RT;
-  const int passes = (A.T + kFewMaxCols - 1) / kFewMaxCols, per = (A.T + passes - 1) / passes;
+  const int passes = (A.T + kMatvecCols - 1) / kMatvecCols, per = (A.T + passes - 1) / passes;
   const int items = groups * passes, KT = (A.K + 127) / 128, steps = (KT + kFewWarps - 1) / kFewWarps;
   const int tile_floats = kFewWarps * per * kFewColPitch, bufs = per <= 8 ? 2 : 1;
   constexpr uint32_t tok = RT * F::kRowTile;
   FewRing way = few_sums_ring(sm, 256, RT * tile_floats * 4, bufs);
-  FewRing ring = few_ring(sm, 256 + bufs * RT * tile_floats * 4, A.smem_bytes, (tok + per * F::kTokPitch + 127) & ~127u, 2);
-  if (tid == 0) sh->abort_flag = 0;
+  FewRing ring = few_ring(sm, 256 + bufs * RT * tile_floats * 4, A.smem_bytes, (tok + per * F::kTokPitch + 127) & ~127u);
+  few_barriers(sm, tid, 2);
   __syncthreads();
 
   if (warp == kFewWarps) {
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) matvec_kernel(const MatvecArgs
 
 template <int GROUP, int RT>
 int launch_matvec_rt(const MatvecArgs& a, int nsm, cudaStream_t s) {
-  const int groups = ((a.N + 15) / 16 + RT - 1) / RT, passes = (a.T + kFewMaxCols - 1) / kFewMaxCols;
+  const int groups = ((a.N + 15) / 16 + RT - 1) / RT, passes = (a.T + kMatvecCols - 1) / kMatvecCols;
   return few_launch(matvec_kernel<GROUP, RT>, a, kFewThreads, std::min(groups * passes, nsm), false, s);
 }
 template <int GROUP>
