@@ -14,7 +14,9 @@ extern "C" int moe_matvec_w4(const uint16_t* x, int T, int K, const uint8_t* Wp,
   if (rc) return rc;
   const int nsm = device_sm_count();
   if (nsm <= 0) return MOE_ERR_CUDA;
-  MatvecArgs a{x, Wp, y, status, T, N, K, 0};
+  MatvecArgs a = {};
+  a.x = x; a.W = Wp; a.y = y; a.status = status;
+  a.T = T; a.N = N; a.K = K;
   cudaStream_t s = (cudaStream_t)stream;
   return group == 32 ? launch_matvec<32>(a, nsm, s) : group == 64 ? launch_matvec<64>(a, nsm, s) : launch_matvec<128>(a, nsm, s);
 }

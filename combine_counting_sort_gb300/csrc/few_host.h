@@ -8,11 +8,13 @@ namespace moe {
 constexpr int kFewMinSmem = 227 * 1024;   // room for a ring beside the largest tables
 
 struct MatvecArgs {
+  CUtensorMap map_w, map_x;   // the wide kernel's: whole tiles, and 64 columns of all tokens
   const uint16_t* x;
   const uint8_t* W;
   uint16_t* y;
   int32_t* status;
   int T, N, K;
+  int slices;          // of the wide kernel's stages
   uint32_t smem_bytes;
 };
 
@@ -38,15 +40,28 @@ struct LayerArgs {
 // them: f16 values, the scale, the groups' sums, and 12 bytes of alignment.
 constexpr int kTokenRecord = 288;
 
+// A tensor map of up to three dimensions, innermost first; strides in bytes of dimensions 1 and 2.
+inline bool encode_few_map(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base, int rank,
+                           const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t d[3], st[2];
+  cuuint32_t b[3], one[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) { d[i] = dims[i]; b[i] = box[i]; }
+  for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
+  return enc(map, type, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // GROUP 0: FP8 (the layer only); 32, 64, 128: 4-bit.
 template <int GROUP> int launch_matvec(const MatvecArgs& a, int nsm, cudaStream_t s);
 template <int GROUP> int launch_layer(const LayerArgs& a, int nsm, cudaStream_t s);
 
 // Row tiles per item: the fewest (rounds over the SMs) x (row tiles), and of
 // those the most row tiles, since a stage's tokens are shared by its row tiles.
-inline int few_row_tiles(int tiles, int nsm) {
+inline int few_row_tiles(int tiles, int nsm, int most = 3) {
   int best = 1, cost = 1 << 30;
-  for (int rt = 1; rt <= 3; ++rt) {
+  for (int rt = 1; rt <= most; ++rt) {
     const int groups = (tiles + rt - 1) / rt, c = (groups + nsm - 1) / nsm * rt;
     if (c <= cost) { cost = c; best = rt; }
   }

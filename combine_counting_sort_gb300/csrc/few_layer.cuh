@@ -1,265 +1,17 @@
-// few_layer.cuh: a whole MoE layer for a few tokens, in one launch.
-//
-// Both products run on f16 MMAs with fp32 sums.  An e4m3 code is one of the f16
-// values (one conversion per two codes).  A 4-bit code takes one AND: the bits
-// 0x000c and 0x00c0 read as f16 are c * 2^-24 and 16 c * 2^-24 (f16 is linear from its
-// subnormals to the end of the first binade), so the four pairs of a word's
-// eight codes take four ANDs and a shift; token values that meet a code with
-// the 16 are divided by it, and the sums are multiplied by 2^24 at the end.  The 8
-// that every 4-bit code has too much is taken out of a group's sum: 8 times the
-// sum of the token's values there, which its record holds.
-//
-// A token's 128 values share a power of two 2^e that brings their largest magnitude
-// into [2^14, 2^15): a bf16 value is then an f16 value as it is, down to 2^-28 of the
-// block's largest (2^-24 where divided by 16), and smaller ones are within 2^-35 of it,
-// below the rounding of an fp32 sum.  The activations between the products,
-// fp32 values, are rounded to f16's 11 bits this way.
-//
-// What bounds it: memory.  Per tile of 16 x 128 weights a warp spends 40 ANDs and
-// shifts (4-bit) or 32 conversions (FP8), both at 64 lanes a clock, 8 MMAs per 8 tokens
-// and some 30 other instructions.  Widening 4-bit codes by the usual offset and
-// subtraction takes 88, FP8 codes to bf16 128, which is longer than the
-// tile's bytes take from memory.
+// few_layer.cuh: a whole MoE layer for a few tokens, in one launch (few_slice.cuh: its
+// products).  What bounds it is memory, but for some 12 us: until the routes are
+// known, no weight can be on its way.
 #pragma once
-
-#include <cuda_fp16.h>
 
 #include <type_traits>
 
-#include "few.cuh"
-#include "few_host.h"
+#include "few_slice.cuh"
 #include "router.cuh"
 
 namespace moe {
 
-// SP: 128-column slices of a stage per warp.
-template <int GROUP, int SP>
-struct LayerForm {
-  static constexpr bool kW4 = GROUP != 0;
-  static constexpr int kTile = w4_tile_bytes(kW4 ? GROUP : 128);
-  static constexpr int kSlices = kFewWarps * SP;
-  // 4-bit: the slices' tiles as they lie in memory.  FP8: per slice 16 rows of
-  // 128 bytes in TMA's 128-byte swizzle, which ldmatrix reads without bank conflicts.
-  static constexpr int kRowTile = kSlices * (kW4 ? kTile : 2048);
-  static constexpr int kAlign = kW4 ? 128 : 1024;           // of a stage
-  static constexpr int kScaleBytes = kW4 ? 0 : 4 * kSlices; // per row tile
-  // A token's records in a stage, 64 mod 128 bytes apart: the 2 tokens x 64 bytes of a
-  // quarter-warp's reads fall on distinct banks.
-  static constexpr int kTokPitch = kSlices * kTokenRecord + 64;
-  // arrivals that complete a stage: weights, tokens, and the lanes' scale copies
-  static constexpr int kArrivals = kW4 ? 2 : 34;
-  static constexpr float kSumScale = kW4 ? 0x1p24f : 1.f;   // what the sums lack
-};
 constexpr int kLayerCols = 16;                  // tokens per pass over a stage
 constexpr int kFewOwnTopk = 2 * kFewAllWarps;   // tokens whose routes every block selects for itself
-
-// ---------------------------------------------------------------- token records
-
-// Four consecutive values v (columns 4 lane ..) of a warp's 128 into the record at
-// `rec`: the 16 bytes at 64 i + 16 t are the B operands that lane t of a column reads for
-// the MMAs 2i and 2i + 1.  4-bit: columns 32 i + 8 t .., the pairs that meet high nibbles
-// divided by 16.  FP8: columns 32 i + 4 t .. and 32 i + 16 + 4 t .., which ldmatrix gives
-// to lane t.
-// Behind the values: the scale, and (4-bit) -8 * 2^-24 times the sum of each group's values.
-template <int GROUP>
-MOE_DEV void put_record(const float (&v)[4], uint8_t* rec, int lane) {
-  constexpr bool kW4 = GROUP != 0;
-  uint32_t big = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) big = max(big, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  big = __reduce_max_sync(0xffffffffu, big);
-  const int e = max((int)(big >> 23) - 127 - 14, -125);
-  const float down = __uint_as_float((uint32_t)(127 - e) << 23), down2 = kW4 ? down * 0.0625f : down;
-  const __half2 a = __floats2half2_rn(v[0] * down, v[1] * down), b = __floats2half2_rn(v[2] * down2, v[3] * down2);
-  const int at = kW4 ? 8 * lane : 64 * (lane >> 3) + 16 * (lane & 3) + 8 * ((lane >> 2) & 1);
-  *reinterpret_cast<uint2*>(rec + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  float* tail = reinterpret_cast<float*>(rec + 256);
-  if (lane == 0) tail[0] = __uint_as_float((uint32_t)(127 + e) << 23);
-  if (kW4) {
-    const float2 fa = __half22float2(a), fb = __half22float2(b);
-    float sum = (fa.x + fa.y) + 16.f * (fb.x + fb.y);
-    constexpr int kLanes = (kW4 ? GROUP : 128) / 4;
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane % kLanes == 0) tail[1 + lane / kLanes] = -8.f * 0x1p-24f * sum;
-  }
-}
-
-// ---------------------------------------------------------------- products
-
-// The codes of a row tile's slice: 4-bit: the lane's words of row g (0-3) and of row
-// g + 8 (4-7).  FP8: words m and m + 8 are columns 16 m + 4 t .. of row g and of row g + 8.
-template <int GROUP>
-MOE_DEV void load_codes(uint32_t wst, int slice, int lane, uint32_t (&c)[GROUP ? 8 : 16]) {
-  using F = LayerForm<GROUP, 1>;
-  if constexpr (F::kW4) {
-    const uint32_t p = wst + slice * F::kTile + lane * 16;
-    const uint4 l = lds128(p), h = lds128(p + 512);
-    c[0] = l.x; c[1] = l.y; c[2] = l.z; c[3] = l.w;
-    c[4] = h.x; c[5] = h.y; c[6] = h.z; c[7] = h.w;
-  } else {
-    const uint32_t row = wst + slice * 2048 + (lane & 15) * 128;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)   // 16-byte chunks 2j (lanes 0-15 give the rows' addresses) and 2j + 1
-      asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(c[2 * j]), "=r"(c[2 * j + 8]), "=r"(c[2 * j + 1]), "=r"(c[2 * j + 9])
-                   : "r"(row + (((2 * j + (lane >> 4)) ^ (lane & 7)) << 4)) : "memory");
-  }
-}
-
-// Four e4m3 codes as f16 values: the first two, and the others.
-MOE_DEV void widen_e4m3(uint32_t codes, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, h;\n\t"
-      "mov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi) : "r"(codes));
-}
-
-// The A operand of MMA m of a slice.
-template <int GROUP>
-MOE_DEV void widen(const uint32_t (&c)[GROUP ? 8 : 16], int m, uint32_t (&a)[4]) {
-  if constexpr (GROUP != 0) {
-    const uint32_t l = c[m >> 1] >> (m & 1 ? 8 : 0), h = c[4 + (m >> 1)] >> (m & 1 ? 8 : 0);
-    a[0] = l & 0x000F000Fu;
-    a[1] = h & 0x000F000Fu;
-    a[2] = l & 0x00F000F0u;
-    a[3] = h & 0x00F000F0u;
-  } else {
-    widen_e4m3(c[m], a[0], a[2]);
-    widen_e4m3(c[m + 8], a[1], a[3]);
-  }
-}
-
-// The scales of a row tile's slice for rows g and g + 8, per group.
-template <int GROUP, int SP>
-MOE_DEV void load_scales(uint32_t wst, uint32_t scales, int rt, int slice, int lane, float (&s)[FewGroups<GROUP>::kCount][2]) {
-  using F = LayerForm<GROUP, SP>;
-#pragma unroll
-  for (int q = 0; q < FewGroups<GROUP>::kCount; ++q) {
-    if (F::kW4) {
-      const uint32_t sc = wst + slice * F::kTile + kW4Codes + 32 * q + 2 * (lane >> 2);
-      s[q][0] = lds_bf16(sc);
-      s[q][1] = lds_bf16(sc + 16);
-    } else {
-      s[q][0] = s[q][1] = lds_f32(scales + 4 * (F::kSlices * rt + slice));
-    }
-  }
-}
-
-// Where a lane finds its columns' tokens in a stage, for NT blocks of 8 columns: its B
-// operand's (column 8 j + lane / 4) and those of its sums (8 j + 2 (lane % 4) and the
-// next); -1 where a column has none.  Bit c of `mask` says that column c has a
-// token, and the number of bits below it which row of the stage is its.
-template <int NT, int PITCH>
-struct LaneTokens {
-  int b[NT], x[NT][2];
-  MOE_DEV LaneTokens(uint32_t mask, uint32_t slice_offset, int lane) {
-    auto at = [&](int c) { return (mask >> c) & 1 ? (int)(slice_offset + __popc(mask & ((1u << c) - 1)) * PITCH) : -1; };
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      b[j] = at(8 * j + (lane >> 2));
-      x[j][0] = at(8 * j + 2 * (lane & 3));
-      x[j][1] = at(8 * j + 2 * (lane & 3) + 1);
-    }
-  }
-};
-
-// One stage's slice of a warp: RT row tiles times NT blocks of 8 columns, added to
-// acc (rows g and g + 8 of the lane's two columns of a block).  Columns without a token
-// read the record of zeros at `zero`.  The MMAs of the row tiles are chains of their own:
-// an MMA's result takes some 20 cycles, and with two warps to a scheduler little else
-// fills them.  A stage with fewer row tiles holds older ones in their place, whose
-// sums are not used.
-template <int GROUP, int SP, int RT, int NT>
-MOE_DEV void layer_slice(uint32_t st, uint32_t scales, uint32_t zero, const LaneTokens<NT, LayerForm<GROUP, SP>::kTokPitch>& lt, int slice,
-                         int lane, float (&acc)[RT][NT][4]) {
-  using F = LayerForm<GROUP, SP>;
-  constexpr int kCount = FewGroups<GROUP>::kCount, kMmas = 8 / kCount;
-  uint32_t c[RT][GROUP ? 8 : 16], b[NT][16];
-  float s[RT][kCount][2], xs[NT][2], sums[NT][2][kCount];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const uint32_t p = lt.b[j] < 0 ? zero : st + lt.b[j] + slice * kTokenRecord;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 v = lds128(p + 64 * i + 16 * (lane & 3));
-      b[j][4 * i] = v.x; b[j][4 * i + 1] = v.y; b[j][4 * i + 2] = v.z; b[j][4 * i + 3] = v.w;
-    }
-  }
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    load_codes<GROUP>(st + rt * F::kRowTile, slice, lane, c[rt]);
-    load_scales<GROUP, SP>(st + rt * F::kRowTile, scales, rt, slice, lane, s[rt]);
-  }
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t p = (lt.x[j][i] < 0 ? zero : st + lt.x[j][i] + slice * kTokenRecord) + 256;
-      if (F::kW4) {
-        const uint4 v = lds128(p);
-        xs[j][i] = __uint_as_float(v.x);
-        sums[j][i][0] = __uint_as_float(v.y);
-        if (kCount > 1) sums[j][i][1 % kCount] = __uint_as_float(v.z);
-        if (kCount > 2) {
-          sums[j][i][2 % kCount] = __uint_as_float(v.w);
-          sums[j][i][3 % kCount] = lds_f32(p + 16);
-        }
-      } else {
-        xs[j][i] = lds_f32(p);
-      }
-    }
-  float v[RT][NT][4];
-#pragma unroll
-  for (int q = 0; q < kCount; ++q) {
-    float part[RT][NT][4];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[rt][j][i] = 0.f;
-#pragma unroll
-    for (int m = q * kMmas; m < (q + 1) * kMmas; ++m)
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        uint32_t a[4];
-        widen<GROUP>(c[rt], m, a);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) mma_f16(part[rt][j], a, b[j][2 * m], b[j][2 * m + 1]);
-      }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = F::kW4 ? part[rt][j][i] + sums[j][i & 1][q] : part[rt][j][i];
-          v[rt][j][i] = q == 0 ? p * s[rt][q][i >> 1] : fmaf(p, s[rt][q][i >> 1], v[rt][j][i]);
-        }
-  }
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[rt][j][i] = fmaf(v[rt][j][i], xs[j][i & 1], acc[rt][j][i]);
-}
-
-// A warp's sums of RT row tiles into the meeting place `red`: [row tile][warp][column].
-template <int RT, int NT>
-MOE_DEV void put_sums(float* red, int pitch, int cols, int warp, int lane, const float (&acc)[RT][NT][4]) {
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = 8 * j + 2 * (lane & 3) + (i & 1);
-        if (c < cols) red[((rt * kFewWarps + warp) * pitch + c) * kFewColPitch + (lane >> 2) + 8 * (i >> 1)] = acc[rt][j][i];
-      }
-}
 
 // ---------------------------------------------------------------- copies
 
@@ -275,7 +27,7 @@ struct LayerMatrix {
 template <int GROUP, int SP>
 MOE_DEV void copy_weights(const LayerMatrix& W, int tile0, int step, int tiles, int kt0, int nk, uint32_t st, uint32_t scales,
                           uint32_t bar, int lane) {
-  using F = LayerForm<GROUP, SP>;
+  using F = FewForm<GROUP, SP>;
   static_assert(F::kW4 || SP == 1, "a box has 8 slices");
   const int KT = W.K / 128;
   if (F::kW4) {
@@ -546,7 +298,7 @@ MOE_DEV LayerMatrix expert_matrix(const uint8_t* W, const CUtensorMap* map, cons
 template <int GROUP, int RT2, bool DIRECT, int SP>
 MOE_DEV void layer_products(const LayerArgs& A, unsigned char* sm, const FewTables& tb, uint32_t after_tables, uint32_t zero, int tid,
                             int warp, int lane) {
-  using F = LayerForm<GROUP, SP>;
+  using F = FewForm<GROUP, SP>;
   constexpr int kRT = RT2 > 2 ? RT2 : 2;
   FewShared* sh = reinterpret_cast<FewShared*>(sm);
   const int HT = A.H / 128, FT = A.F / 128;
@@ -664,13 +416,13 @@ MOE_DEV void layer_products(const LayerArgs& A, unsigned char* sm, const FewTabl
         const int cols = __popcll(tb.seg_mask[item / ftiles]);
         auto item_sums = [&](auto nt) {
           constexpr int NT = decltype(nt)::value;
-          const LaneTokens<NT, F::kTokPitch> lt((1u << cols) - 1, tok, lane);
+          const LaneTokens<NT> lt((1u << cols) - 1, F::kTokPitch, lane);
           float acc[2][NT][4] = {};
           for (int s = 0; s < steps1; ++s, ring.next()) {
             if (!wait(ring.full_bar(), ring.phase)) return;
 #pragma unroll
             for (int i = warp; i < F::kSlices; i += kFewWarps)
-              if (s * F::kSlices + i < HT) layer_slice<GROUP, SP, 2, NT>(ring.stage(), ring.stage() + sco, zero, lt, i, lane, acc);
+              if (s * F::kSlices + i < HT) few_slice<GROUP, SP, 2, NT>(ring.stage(), ring.stage() + sco, ring.stage() + tok + i * kTokenRecord, zero, lt, i, lane, acc);
             arrive(ring.empty_bar());
           }
           if (!wait(way.empty_bar(), way.phase ^ 1)) return;
@@ -742,12 +494,12 @@ MOE_DEV void layer_products(const LayerArgs& A, unsigned char* sm, const FewTabl
         if constexpr (DIRECT) {
           float acc[RT2][1][4] = {};
           for (int seg = 0; ok && seg < segs; ++seg) {
-            const LaneTokens<1, F::kTokPitch> lt((uint32_t)tb.seg_mask[seg], tok, lane);
+            const LaneTokens<1> lt((uint32_t)tb.seg_mask[seg], F::kTokPitch, lane);
             for (int s = 0; s < steps2; ++s, ring.next()) {
               if (!wait(ring.full_bar(), ring.phase)) break;
 #pragma unroll
               for (int i = warp; i < F::kSlices; i += kFewWarps)
-                if (s * F::kSlices + i < FT) layer_slice<GROUP, SP, RT2, 1>(ring.stage(), ring.stage() + sco, zero, lt, i, lane, acc);
+                if (s * F::kSlices + i < FT) few_slice<GROUP, SP, RT2, 1>(ring.stage(), ring.stage() + sco, ring.stage() + tok + i * kTokenRecord, zero, lt, i, lane, acc);
               arrive(ring.empty_bar());
             }
           }
@@ -760,13 +512,13 @@ MOE_DEV void layer_products(const LayerArgs& A, unsigned char* sm, const FewTabl
             const int cols = __popcll(tb.seg_mask[seg]);
             auto segment_sums = [&](auto nt) {
               constexpr int NT = decltype(nt)::value;
-              const LaneTokens<NT, F::kTokPitch> lt((1u << cols) - 1, tok, lane);
+              const LaneTokens<NT> lt((1u << cols) - 1, F::kTokPitch, lane);
               float acc[RT2][NT][4] = {};
               for (int s = 0; s < steps2; ++s, ring.next()) {
                 if (!wait(ring.full_bar(), ring.phase)) return;
 #pragma unroll
                 for (int i = warp; i < F::kSlices; i += kFewWarps)
-                  if (s * F::kSlices + i < FT) layer_slice<GROUP, SP, RT2, NT>(ring.stage(), ring.stage() + sco, zero, lt, i, lane, acc);
+                  if (s * F::kSlices + i < FT) few_slice<GROUP, SP, RT2, NT>(ring.stage(), ring.stage() + sco, ring.stage() + tok + i * kTokenRecord, zero, lt, i, lane, acc);
                 arrive(ring.empty_bar());
               }
               if (!wait(way.empty_bar(), way.phase ^ 1)) return;
@@ -815,7 +567,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
   float* w = reinterpret_cast<float*>(ids + P);
   unsigned char* scratch2 = reinterpret_cast<unsigned char*>(w + P);
 
-  few_barriers(sm, tid, LayerForm<GROUP, 1>::kArrivals);
+  few_barriers(sm, tid, FewForm<GROUP, 1>::kArrivals);
   if (tid < kTokenRecord / 4) reinterpret_cast<int*>(sm + kZeroAt)[tid] = 0;
   for (int i = warp * gridDim.x + blockIdx.x; i < A.T * HT; i += kFewAllWarps * gridDim.x) {
     const uint2 x = __ldg(reinterpret_cast<const uint2*>(A.x + (size_t)i * 128) + lane);   // the tokens' rows are blocks of 128 in a row

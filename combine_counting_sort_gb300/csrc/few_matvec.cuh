@@ -1,143 +1,60 @@
-// few_matvec.cuh: products of up to 64 tokens with one 4-bit matrix.
+// few_matvec.cuh: products of up to 64 tokens with one 4-bit matrix, in two kernels.
 //
-// Codes are widened by one AND: the bits 0x000c and 0x00c0 read as bf16 are
-// c * 2^-133 and 16 c * 2^-133 (bf16 is linear from its subnormals to the end of the
-// first binade), so the four pairs of a word's eight codes take four ANDs and a
-// shift.  The tokens are multiplied by 2^64, or by 2^60 where the code
-// carries the 16, which keeps the products within fp32's normal range for any
-// token value between 2^-57 and 2^63; the sums are multiplied by 2^69 at the
-// end.  The 8 that every code has too much is taken out by the tensor core: a
-// group's sum starts from -8 times its tokens.
-// Both the AND and the shift run at 64 lanes a clock, so widening by the usual
-// 0x4300 | c and a subtraction (11 instructions per 8 codes) held the kernel at
-// the ALU's rate, below that of memory.
+// matvec_few_kernel, up to 8 tokens whose records fit beside the ring: every block makes
+// the records of all tokens for itself while its first weights are on their way, and a
+// stage holds weights alone (few_slice.cuh: the products).
+//
+// matvec_wide_kernel, more tokens: a block of eight warps is KS slices of 128 columns x 8 /
+// KS groups of 32 rows, each warp all tokens (up to 8 blocks of 8) on its 32 rows, so
+// that a code is widened once for all of them: to bf16, 0x4300 | c less 136.  It is
+// bound by the MMAs, 8 per 16 x 128 weights and 8 tokens at half an instruction a
+// clock, from some 24 tokens up.  With few rows the slices are many, so that
+// every SM has work, and their sums meet in shared memory; with many rows they are
+// few, since every block reads all tokens.  A copy costs some 70 cycles of an SM's
+// copies whatever its size (row by row, 48 tokens took 140 us over 32768 x 7168), so
+// a stage's weights are one box of whole tiles, its tokens one of 64 columns.
 #pragma once
 
-#include "few.cuh"
-#include "few_host.h"
+#include "few_slice.cuh"
 
 namespace moe {
 
-constexpr int kMatvecCols = 16;   // tokens per pass over a stage
+constexpr int kMatvecTokenRoom = 96 * 1024;   // of the few kernel's records
 
-template <int GROUP>
-struct MatvecForm {
-  static constexpr int kTile = w4_tile_bytes(GROUP);
-  static constexpr int kRowTile = kFewWarps * kTile;   // bytes of a row tile in a stage
-  // bf16 token rows; 64 mod 128 bytes, so that the 2 rows x 64 bytes of a
-  // quarter-warp's 16-byte reads fall on distinct banks
-  static constexpr int kTokPitch = 2 * 128 * kFewWarps + 64;
-};
+__host__ __device__ __forceinline__ int matvec_token_pitch(int KT) { return ((KT * kTokenRecord + 127) & ~127) + 64; }
 
-// One stage's slice of a warp: RT row tiles times NT blocks of 8 tokens, the lane's
-// token of a block at `row` (0: none; `b` then stays the zeros that the caller
-// put there).  A stage with fewer row tiles holds older ones in their place,
-// whose sums are not used.
-template <int GROUP, int RT, int NT>
-MOE_DEV void matvec_slice(uint32_t st, const uint32_t (&row)[2], int slice, int lane,
-                          uint32_t (&b)[2][16], float (&acc)[RT][2][4]) {
-  using F = MatvecForm<GROUP>;
-  constexpr int kCount = FewGroups<GROUP>::kCount, kMmas = 8 / kCount;
-  uint4 lo[RT], hi[RT];
-  float s[RT][kCount][2];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const uint32_t w = st + rt * F::kRowTile + slice * F::kTile;
-    lo[rt] = lds128(w + lane * 16);
-    hi[rt] = lds128(w + 512 + lane * 16);
-#pragma unroll
-    for (int q = 0; q < kCount; ++q) {
-      const uint32_t sc = w + kW4Codes + 32 * q + 2 * (lane >> 2);
-      s[rt][q][0] = lds_bf16(sc);
-      s[rt][q][1] = lds_bf16(sc + 16);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    if (row[j]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 v = lds128(row[j] + slice * 256 + (4 * i + (lane & 3)) * 16);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-          asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(b[j][4 * i + p]) : "r"(w[p]), "r"(p & 1 ? 0x5D805D80u : 0x5F805F80u));
-      }
-    }
-  }
-  __syncwarp();
-  // The MMAs of the row tiles, and those of the eights, are chains of their own: an
-  // MMA's result takes some 20 cycles, and with two warps to a scheduler nothing
-  // else would fill them.
-  const uint32_t minus8[4] = {0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u};   // -8, -128 times 2^-133
-#pragma unroll
-  for (int q = 0; q < kCount; ++q) {
-    float part[RT][NT][4] = {}, eights[NT][4] = {};
-#pragma unroll
-    for (int m = q * kMmas; m < (q + 1) * kMmas; ++m) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) mma_bf16(eights[j], minus8, b[j][2 * m], b[j][2 * m + 1]);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const uint32_t l[4] = {lo[rt].x, lo[rt].y, lo[rt].z, lo[rt].w}, h[4] = {hi[rt].x, hi[rt].y, hi[rt].z, hi[rt].w};
-        const uint32_t wl = l[m >> 1] >> (m & 1 ? 8 : 0), wh = h[m >> 1] >> (m & 1 ? 8 : 0);
-        const uint32_t a[4] = {wl & 0x000F000Fu, wh & 0x000F000Fu, wl & 0x00F000F0u, wh & 0x00F000F0u};
-#pragma unroll
-        for (int j = 0; j < NT; ++j) mma_bf16(part[rt][j], a, b[j][2 * m], b[j][2 * m + 1]);
-      }
-    }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[rt][j][i] = fmaf(part[rt][j][i] + eights[j][i], s[rt][q][i >> 1], acc[rt][j][i]);
-  }
-}
-
-// Work items: (group of RT row tiles, pass of up to 16 tokens), the passes of a
-// group next to one another so that the second finds the weights in L2.
 template <int GROUP, int RT>
-__global__ void __launch_bounds__(kFewThreads, 1) matvec_kernel(const MatvecArgs A) {
+__global__ void __launch_bounds__(kFewThreads, 1) matvec_few_kernel(const __grid_constant__ MatvecArgs A) {
   extern __shared__ __align__(1024) unsigned char sm[];
-  using F = MatvecForm<GROUP>;
+  using F = FewForm<GROUP, 2>;
   FewShared* sh = reinterpret_cast<FewShared*>(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int tiles = (A.N + 15) / 16, groups = (tiles + RT - 1) / RT;
-  const int passes = (A.T + kMatvecCols - 1) / kMatvecCols, per = (A.T + passes - 1) / passes;
-  const int items = groups * passes, KT = (A.K + 127) / 128, steps = (KT + kFewWarps - 1) / kFewWarps;
-  const int tile_floats = kFewWarps * per * kFewColPitch, bufs = per <= 8 ? 2 : 1;
-  constexpr uint32_t tok = RT * F::kRowTile;
-  FewRing way = few_sums_ring(sm, 256, RT * tile_floats * 4, bufs);
-  FewRing ring = few_ring(sm, 256 + bufs * RT * tile_floats * 4, A.smem_bytes, (tok + per * F::kTokPitch + 127) & ~127u);
-  few_barriers(sm, tid, 2);
+  const int tiles = (A.N + 15) / 16, items = (tiles + RT - 1) / RT;
+  const int KT = (A.K + 127) / 128, steps = (KT + F::kSlices - 1) / F::kSlices, pitch = matvec_token_pitch(KT);
+  constexpr uint32_t kZeroAt = 256, kTokensAt = kZeroAt + kTokenRecord;
+  const uint32_t zero = smem_u32(sm) + kZeroAt, tokens = smem_u32(sm) + kTokensAt;
+  const int tile_floats = kFewWarps * A.T * kFewColPitch;
+  const uint32_t sums_at = kTokensAt + A.T * pitch;
+  FewRing way = few_sums_ring(sm, sums_at, RT * tile_floats * 4, 2);
+  FewRing ring = few_ring(sm, sums_at + 2 * RT * tile_floats * 4, A.smem_bytes, (RT * F::kRowTile + 127) & ~127u);
+  few_barriers(sm, tid, 1);
+  if (tid < kTokenRecord / 4) reinterpret_cast<int*>(sm + kZeroAt)[tid] = 0;
   __syncthreads();
 
   if (warp == kFewWarps) {
     int issued = 0;
     bool ok = true;
     for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
-      const int group = item / passes, t0 = item % passes * per, cols = min(per, A.T - t0), nrt = min(RT, tiles - group * RT);
+      const int nrt = min(RT, tiles - item * RT);
       for (int s = 0; s < steps; ++s) {
         ok = ring_wait(ring.empty_bar(), ring.phase ^ 1, &sh->abort_flag, A.status);
         if (!ok) break;
-        const int kt0 = s * kFewWarps, nk = min(kFewWarps, KT - kt0), valid = min(nk * 128, A.K - kt0 * 128);
+        const int kt0 = s * F::kSlices, nk = min(F::kSlices, KT - kt0);
         const uint32_t st = ring.stage(), bar = ring.full_bar();
-        if (valid < nk * 128) {   // zeros past K: the codes there are zero, the products must be too
-          for (int c = 0; c < cols; ++c)
-            for (int i = valid * 2 + lane * 16; i < nk * 256; i += 512)
-              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" :: "r"(st + tok + c * F::kTokPitch + i), "r"(0) : "memory");
-          fence_proxy_async_shared();   // a later stage's bulk copy may overwrite them
-          __syncwarp();
-        }
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar, nrt * nk * F::kTile);
-          mbar_arrive_expect_tx(bar, cols * valid * 2);
-        }
+        if (lane == 0) mbar_arrive_expect_tx(bar, nrt * nk * F::kTile);
         __syncwarp();
         if (lane < nrt)
-          bulk_load(st + lane * F::kRowTile, A.W + ((size_t)(group * RT + lane) * KT + kt0) * F::kTile, nk * F::kTile, bar);
-        if (lane < cols) bulk_load(st + tok + lane * F::kTokPitch, A.x + (size_t)(t0 + lane) * A.K + kt0 * 128, valid * 2, bar);
+          bulk_load_once(st + lane * F::kRowTile, A.W + ((size_t)(item * RT + lane) * KT + kt0) * F::kTile, nk * F::kTile, bar);
         ring.next();
         ++issued;
       }
@@ -146,16 +63,23 @@ __global__ void __launch_bounds__(kFewThreads, 1) matvec_kernel(const MatvecArgs
     return;
   }
 
+  for (int i = warp > kFewWarps ? warp - 1 : warp; i < A.T * KT; i += kFewAllWarps - 1) {
+    const int t = i / KT, kt = i % KT, k = kt * 128 + 4 * lane;   // K is a multiple of 32
+    const uint2 x = k < A.K ? __ldg(reinterpret_cast<const uint2*>(A.x + (size_t)t * A.K + k)) : make_uint2(0, 0);
+    const float v[4] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)};
+    put_record<GROUP>(v, sm + kTokensAt + t * pitch + kt * kTokenRecord, lane);
+  }
+  consumer_sync_all(true);
+
   if (warp > kFewWarps) {
     const int fid = tid - 32 * (kFewWarps + 1);
     for (int item = blockIdx.x; item < items; item += gridDim.x, way.next()) {
       if (!ring_wait_idle(way.full_bar(), way.phase, &sh->abort_flag, A.status)) return;
-      const int group = item / passes, t0 = item % passes * per, cols = min(per, A.T - t0), nrt = min(RT, tiles - group * RT);
+      const int rows = 16 * min(RT, tiles - item * RT);
       const float* r = reinterpret_cast<const float*>(sm + way.stage());
-      for (int i = fid; i < nrt * 16 * cols; i += kFewFinishThreads) {
-        const int row = i % (nrt * 16), c = i / (nrt * 16), n = group * RT * 16 + row;
-        if (n < A.N)
-          A.y[(size_t)(t0 + c) * A.N + n] = to_bf16(get_sum(r + (row >> 4) * tile_floats, per, row & 15, c) * 0x1p69f);
+      for (int i = fid; i < rows * A.T; i += kFewFinishThreads) {
+        const int row = i % rows, t = i / rows, n = item * RT * 16 + row;
+        if (n < A.N) A.y[(size_t)t * A.N + n] = to_bf16(get_sum(r + (row >> 4) * tile_floats, A.T, row & 15, t) * F::kSumScale);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(way.empty_bar());
@@ -163,51 +87,225 @@ __global__ void __launch_bounds__(kFewThreads, 1) matvec_kernel(const MatvecArgs
     return;
   }
 
+  const LaneTokens<1> lt((1u << A.T) - 1, pitch, lane);
   for (int item = blockIdx.x; item < items; item += gridDim.x, way.next()) {
-    const int t0 = item % passes * per, cols = min(per, A.T - t0);
-    float acc[RT][2][4] = {};
-    uint32_t b[2][16] = {};
+    float acc[RT][1][4] = {};
     for (int s = 0; s < steps; ++s, ring.next()) {
       if (!ring_wait(ring.full_bar(), ring.phase, &sh->abort_flag, A.status)) return;
-      if (s * kFewWarps + warp < KT) {
-        const uint32_t st = ring.stage();
-        const int c = lane >> 2;
-        const uint32_t row[2] = {c < cols ? st + tok + c * F::kTokPitch : 0, c + 8 < cols ? st + tok + (c + 8) * F::kTokPitch : 0};
-        if (cols <= 8)
-          matvec_slice<GROUP, RT, 1>(st, row, warp, lane, b, acc);
-        else
-          matvec_slice<GROUP, RT, 2>(st, row, warp, lane, b, acc);
+#pragma unroll
+      for (int i = warp; i < F::kSlices; i += kFewWarps) {
+        const int kt = s * F::kSlices + i;
+        if (kt < KT) few_slice<GROUP, 2, RT, 1>(ring.stage(), 0, tokens + kt * kTokenRecord, zero, lt, i, lane, acc);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(ring.empty_bar());
     }
     if (!ring_wait(way.empty_bar(), way.phase ^ 1, &sh->abort_flag, A.status)) return;
-    float* red = reinterpret_cast<float*>(sm + way.stage());
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = 8 * j + 2 * (lane & 3) + (i & 1);
-          if (col < cols) red[rt * tile_floats + (warp * per + col) * kFewColPitch + (lane >> 2) + 8 * (i >> 1)] = acc[rt][j][i];
-        }
+    put_sums<RT, 1>(reinterpret_cast<float*>(sm + way.stage()), A.T, A.T, warp, lane, acc);
     __syncwarp();
     if (lane == 0) mbar_arrive(way.full_bar());
   }
 }
 
+// ---------------------------------------------------------------- more tokens
+
+constexpr int kWideThreads = (kFewWarps + 1) * 32;
+
+MOE_DEV bool wide_sync_all(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 3, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all) : "r"((uint32_t)ok) : "memory");
+  return all != 0;
+}
+
+// Two row tiles' 64 columns [64 half, 64 half + 64) of a slice times NT blocks of 8 tokens.
+// tok: these columns of token lane / 4, 128 bytes in TMA's swizzle; 128 bytes to the next.
+template <int GROUP, int NT>
+MOE_DEV void wide_half(uint32_t w, uint32_t row_tile, uint32_t tok, int half, int lane, float (&acc)[2][NT][4]) {
+  constexpr int kGroups = GROUP == 32 ? 2 : 1, kMmas = 4 / kGroups;   // groups that these columns touch
+  uint32_t a[2][4][4];
+  float s[2][kGroups][2];
+#pragma unroll
+  for (int rt = 0; rt < 2; ++rt) {
+    const uint32_t p = w + rt * row_tile + lane * 16 + 8 * half;
+    uint32_t c[2][2];   // row g's words, row g + 8's
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(c[0][0]), "=r"(c[0][1]) : "r"(p));
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(c[1][0]), "=r"(c[1][1]) : "r"(p + 512));
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t v;
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(c[i & 1][m >> 1] >> (4 * (2 * (m & 1) + (i >> 1)))), "n"(0x000F000F), "n"(0x43004300));
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(a[rt][m][i]) : "r"(v), "r"(0x43084308));
+      }
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+      const uint32_t sc = w + rt * row_tile + kW4Codes + 32 * (64 * half / GROUP + q) + 2 * (lane >> 2);
+      s[rt][q][0] = lds_bf16(sc);
+      s[rt][q][1] = lds_bf16(sc + 16);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {   // without a branch, so that the blocks' loads and MMAs overlap
+    const uint32_t chunk = (lane & 3) ^ (lane >> 2);
+    const uint4 u = lds128(tok + 1024 * j + 16 * chunk), v = lds128(tok + 1024 * j + 16 * (chunk ^ 4));
+    const uint32_t b[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+      float part[2][4] = {};
+#pragma unroll
+      for (int m = q * kMmas; m < (q + 1) * kMmas; ++m)
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) mma_bf16(part[rt], a[rt][m], b[2 * m], b[2 * m + 1]);
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[rt][j][i] = fmaf(part[rt][i], s[rt][q][i >> 1], acc[rt][j][i]);
+    }
+  }
+}
+
+template <int GROUP, int NT>
+__global__ void __launch_bounds__(kWideThreads, 1) matvec_wide_kernel(const __grid_constant__ MatvecArgs A) {
+  extern __shared__ __align__(1024) unsigned char sm[];
+  constexpr int kTile = w4_tile_bytes(GROUP);
+  FewShared* sh = reinterpret_cast<FewShared*>(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int KS = A.slices, RT = 2 * (kFewWarps / KS);   // slices and row tiles of a stage: 16 tiles of weights
+  const int tiles = (A.N + 15) / 16, items = (tiles + RT - 1) / RT, KT = (A.K + 127) / 128, steps = (KT + KS - 1) / KS;
+  constexpr uint32_t kRedAt = 256, kBox = NT * 8 * 128;   // a box of tokens: 64 columns of NT * 8, those past T zeros
+  const uint32_t row_tile = KS * kTile, tok = (RT * row_tile + 1023) & ~1023u;
+  float4* red = reinterpret_cast<float4*>(sm + kRedAt);   // [warp][row tile][lane]
+  FewRing ring = few_ring(sm, kRedAt + kFewWarps * 2 * 512, A.smem_bytes, tok + 2 * KS * kBox);
+  few_barriers(sm, tid, 1);
+  __syncthreads();
+
+  if (warp == kFewWarps) {
+    int issued = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+      for (int s = 0; s < steps; ++s) {
+        ok = ring_wait(ring.empty_bar(), ring.phase ^ 1, &sh->abort_flag, A.status);
+        if (!ok) break;
+        // boxes that reach past the matrix or the tokens are filled with zeros, and count as bytes
+        if (lane == 0) mbar_arrive_expect_tx(ring.full_bar(), 16 * kTile + 2 * KS * kBox);
+        __syncwarp();
+        if (lane == 0) tma_load_3d_once(ring.stage(), &A.map_w, 0, s * KS, item * RT, ring.full_bar());
+        if (lane < 2 * KS) tma_load_2d(ring.stage() + tok + lane * kBox, &A.map_x, (2 * s * KS + lane) * 64, 0, ring.full_bar());
+        ring.next();
+        ++issued;
+      }
+    }
+    drain(ring, issued, 0, lane);
+    return;
+  }
+
+  const int slice = warp % KS, group = warp / KS;
+  bool ok = true;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int nrt = tiles - item * RT;
+    float acc[2][NT][4] = {};
+    for (int s = 0; s < steps; ++s, ring.next()) {
+      ok = ring_wait(ring.full_bar(), ring.phase, &sh->abort_flag, A.status);
+      if (!ok) break;
+      if (s * KS + slice < KT && 2 * group < nrt) {
+        const uint32_t w = ring.stage() + 2 * group * row_tile + slice * kTile;
+        const uint32_t t = ring.stage() + tok + 2 * slice * kBox + (lane >> 2) * 128;
+        wide_half<GROUP, NT>(w, row_tile, t, 0, lane, acc);
+        wide_half<GROUP, NT>(w, row_tile, t + kBox, 1, lane, acc);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ring.empty_bar());
+    }
+    if (!wide_sync_all(ok)) return;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      if (8 * j < A.T) {
+        if (KS > 1) {
+          if (slice > 0) {
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt)
+              red[(warp * 2 + rt) * 32 + lane] = make_float4(acc[rt][j][0], acc[rt][j][1], acc[rt][j][2], acc[rt][j][3]);
+          }
+          wide_sync_all(true);
+        }
+        if (slice == 0) {
+#pragma unroll
+          for (int rt = 0; rt < 2; ++rt) {
+            float v[4] = {acc[rt][j][0], acc[rt][j][1], acc[rt][j][2], acc[rt][j][3]};
+            for (int i = 1; i < KS; ++i) {   // the slices in their order
+              const float4 o = red[((warp + i) * 2 + rt) * 32 + lane];
+              v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int t = 8 * j + 2 * (lane & 3) + (i & 1), n = (item * RT + 2 * group + rt) * 16 + (lane >> 2) + 8 * (i >> 1);
+              if (t < A.T && n < A.N) A.y[(size_t)t * A.N + n] = to_bf16(v[i]);
+            }
+          }
+        }
+        if (KS > 1) wide_sync_all(true);   // the meeting place is free again
+      }
+    }
+  }
+}
+
+// Slices of the wide kernel's stages: the fewest stages over the rounds that the SMs make,
+// each as long as its copies (some 40 bytes a clock, with the tokens out of L2) or
+// its MMAs (16 clocks per tile and block of tokens, and 600 beside them), where two
+// stages fit.
+inline int wide_slices(int tiles, int KT, int nt, int nsm) {
+  int best = 1;
+  long long cost = 1LL << 60;
+  for (int ks = 1; ks <= 8; ks *= 2) {
+    const int rows = 2 * (8 / ks), rounds = ((tiles + rows - 1) / rows + nsm - 1) / nsm;
+    const long long stage = std::max((16 * 1100 + 2 * ks * nt * 1024) / 40, 16 * nt * 16 + 600);
+    const long long c = (long long)rounds * ((KT + ks - 1) / ks) * stage;
+    if (2 * ks * nt * 1024 <= 80 * 1024 && c < cost) { cost = c; best = ks; }
+  }
+  return best;
+}
+
 template <int GROUP, int RT>
-int launch_matvec_rt(const MatvecArgs& a, int nsm, cudaStream_t s) {
-  const int groups = ((a.N + 15) / 16 + RT - 1) / RT, passes = (a.T + kMatvecCols - 1) / kMatvecCols;
-  return few_launch(matvec_kernel<GROUP, RT>, a, kFewThreads, std::min(groups * passes, nsm), false, s);
+int launch_matvec_few(const MatvecArgs& a, int nsm, cudaStream_t s) {
+  const int items = ((a.N + 15) / 16 + RT - 1) / RT;
+  return few_launch(matvec_few_kernel<GROUP, RT>, a, kFewThreads, std::min(items, nsm), false, s);
 }
 template <int GROUP>
-int launch_matvec(const MatvecArgs& a, int nsm, cudaStream_t s) {
-  switch (few_row_tiles((a.N + 15) / 16, nsm)) {
-    case 1: return launch_matvec_rt<GROUP, 1>(a, nsm, s);
-    case 2: return launch_matvec_rt<GROUP, 2>(a, nsm, s);
-    default: return launch_matvec_rt<GROUP, 3>(a, nsm, s);
+int launch_matvec(const MatvecArgs& args, int nsm, cudaStream_t s) {
+  const int tiles = (args.N + 15) / 16;
+  const int records = args.T * matvec_token_pitch((args.K + 127) / 128);
+  if (args.T <= 8 && records <= kMatvecTokenRoom) {
+    switch (few_row_tiles(tiles, nsm, records <= kMatvecTokenRoom / 2 ? 3 : 2)) {   // room for two stages
+      case 1: return launch_matvec_few<GROUP, 1>(args, nsm, s);
+      case 2: return launch_matvec_few<GROUP, 2>(args, nsm, s);
+      default: return launch_matvec_few<GROUP, 3>(args, nsm, s);
+    }
+  }
+  MatvecArgs a = args;
+  const int KT = (a.K + 127) / 128, nt = a.T <= 32 ? (a.T + 7) / 8 : a.T <= 48 ? 6 : 8;
+  a.slices = wide_slices(tiles, KT, nt, nsm);
+  const int rows = 2 * (8 / a.slices), blocks = std::min((tiles + rows - 1) / rows, nsm);
+  constexpr int kTile = w4_tile_bytes(GROUP);
+  const uint64_t wd[3] = {kTile / 8, (uint64_t)KT, (uint64_t)tiles}, ws[2] = {kTile, (uint64_t)KT * kTile};
+  const uint32_t wb[3] = {kTile / 8, (uint32_t)a.slices, (uint32_t)rows};
+  const uint64_t xd[2] = {(uint64_t)a.K, (uint64_t)a.T}, xs[1] = {(uint64_t)a.K * 2};
+  const uint32_t xb[2] = {64, (uint32_t)nt * 8};
+  if (!encode_few_map(&a.map_w, CU_TENSOR_MAP_DATA_TYPE_UINT64, CU_TENSOR_MAP_SWIZZLE_NONE, a.W, 3, wd, ws, wb) ||
+      !encode_few_map(&a.map_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.x, 2, xd, xs, xb))
+    return MOE_ERR_CUDA;
+  switch (nt) {
+    case 1: return few_launch(matvec_wide_kernel<GROUP, 1>, a, kWideThreads, blocks, false, s);
+    case 2: return few_launch(matvec_wide_kernel<GROUP, 2>, a, kWideThreads, blocks, false, s);
+    case 3: return few_launch(matvec_wide_kernel<GROUP, 3>, a, kWideThreads, blocks, false, s);
+    case 4: return few_launch(matvec_wide_kernel<GROUP, 4>, a, kWideThreads, blocks, false, s);
+    case 6: return few_launch(matvec_wide_kernel<GROUP, 6>, a, kWideThreads, blocks, false, s);
+    default: return few_launch(matvec_wide_kernel<GROUP, 8>, a, kWideThreads, blocks, false, s);
   }
 }
 
