@@ -37,9 +37,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) matvec_few_kernel(const __grid
   const uint32_t sums_at = kTokensAt + A.T * pitch;
   FewRing way = few_sums_ring(sm, sums_at, RT * tile_floats * 4, 2);
   FewRing ring = few_ring(sm, sums_at + 2 * RT * tile_floats * 4, A.smem_bytes, (RT * F::kRowTile + 127) & ~127u);
+  grid_launch_next();
   few_barriers(sm, tid, 1);
   if (tid < kTokenRecord / 4) reinterpret_cast<int*>(sm + kZeroAt)[tid] = 0;
   __syncthreads();
+  grid_wait_previous();
 
   if (warp == kFewWarps) {
     int issued = 0;
@@ -182,8 +184,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) matvec_wide_kernel(const __gr
   const uint32_t row_tile = KS * kTile, tok = (RT * row_tile + 1023) & ~1023u;
   float4* red = reinterpret_cast<float4*>(sm + kRedAt);   // [warp][row tile][lane]
   FewRing ring = few_ring(sm, kRedAt + kFewWarps * 2 * 512, A.smem_bytes, tok + 2 * KS * kBox);
+  grid_launch_next();
   few_barriers(sm, tid, 1);
   __syncthreads();
+  grid_wait_previous();
 
   if (warp == kFewWarps) {
     int issued = 0;
