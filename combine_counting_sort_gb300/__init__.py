@@ -517,33 +517,6 @@ def w4_packed_shape(E: int, N: int, K: int, group: int):
     return (E, -(-N // 16), -(-K // 128), 1024 + 32 * (128 // group))
 
 
-def moe_quant_weights_w4(W: torch.Tensor, group: int, Wp: torch.Tensor, stream=None):
-    """bf16 weights [E, N, K] -> 4-bit codes and bf16 group scales, laid out."""
-    E, N, K = _dims(W, 3, "W")
-    _shape(Wp, w4_packed_shape(E, N, K, group), "Wp")
-    _check("moe_quant_weights_w4", lib().moe_quant_weights_w4(
-        _ptr(W, torch.bfloat16, "W"), E, N, K, group, _ptr(Wp, torch.uint8, "Wp"), _stream(stream)))
-
-
-def moe_pack_weights_w4(codes: torch.Tensor, scale: torch.Tensor, group: int, Wp: torch.Tensor, stream=None):
-    """Lay out a checkpoint's codes (u8 [E, N, K/2], column 2i in the low
-    nibble of byte i) and scales (bf16 [E, N, K/group])."""
-    E, N, K2 = _dims(codes, 3, "codes")
-    _shape(Wp, w4_packed_shape(E, N, 2 * K2, group), "Wp")
-    _shape(scale, (E, N, 2 * K2 // group), "scale")
-    _check("moe_pack_weights_w4", lib().moe_pack_weights_w4(
-        _ptr(codes, torch.uint8, "codes"), _ptr(scale, torch.bfloat16, "scale"), E, N, 2 * K2, group,
-        _ptr(Wp, torch.uint8, "Wp"), _stream(stream)))
-
-
-def moe_dequant_weights_w4(Wp: torch.Tensor, group: int, W: torch.Tensor, stream=None):
-    """The values that laid-out codes stand for, f32 [E, N, K] (exact)."""
-    E, N, K = _dims(W, 3, "W")
-    _shape(Wp, w4_packed_shape(E, N, K, group), "Wp")
-    _check("moe_dequant_weights_w4", lib().moe_dequant_weights_w4(
-        _ptr(Wp, torch.uint8, "Wp"), E, N, K, group, _ptr(W, torch.float32, "W"), _stream(stream)))
-
-
 def _args(*specs):
     """Addresses of (tensor or None, dtype, shape, name) arguments.  One comparison
     each where they are as they have to be (these calls take as long as their
@@ -564,6 +537,29 @@ def _args(*specs):
 def _raw_stream(stream) -> int:
     """_stream, without building a torch.cuda.Stream for the current one."""
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
+
+
+def moe_quant_weights_w4(W: torch.Tensor, group: int, Wp: torch.Tensor, stream=None):
+    """bf16 weights [E, N, K] -> 4-bit codes and bf16 group scales, laid out."""
+    E, N, K = _dims(W, 3, "W")
+    pw, pp = _args((W, torch.bfloat16, W.shape, "W"), (Wp, torch.uint8, w4_packed_shape(E, N, K, group), "Wp"))
+    _check("moe_quant_weights_w4", lib().moe_quant_weights_w4(pw, E, N, K, group, pp, _raw_stream(stream)))
+
+
+def moe_pack_weights_w4(codes: torch.Tensor, scale: torch.Tensor, group: int, Wp: torch.Tensor, stream=None):
+    """Lay out a checkpoint's codes (u8 [E, N, K/2], column 2i in the low
+    nibble of byte i) and scales (bf16 [E, N, K/group])."""
+    E, N, K2 = _dims(codes, 3, "codes")
+    pc, ps, pp = _args((codes, torch.uint8, codes.shape, "codes"), (scale, torch.bfloat16, (E, N, 2 * K2 // group), "scale"),
+                       (Wp, torch.uint8, w4_packed_shape(E, N, 2 * K2, group), "Wp"))
+    _check("moe_pack_weights_w4", lib().moe_pack_weights_w4(pc, ps, E, N, 2 * K2, group, pp, _raw_stream(stream)))
+
+
+def moe_dequant_weights_w4(Wp: torch.Tensor, group: int, W: torch.Tensor, stream=None):
+    """The values that laid-out codes stand for, f32 [E, N, K] (exact)."""
+    E, N, K = _dims(W, 3, "W")
+    pp, pw = _args((Wp, torch.uint8, w4_packed_shape(E, N, K, group), "Wp"), (W, torch.float32, W.shape, "W"))
+    _check("moe_dequant_weights_w4", lib().moe_dequant_weights_w4(pp, E, N, K, group, pw, _raw_stream(stream)))
 
 
 def moe_matvec_w4(x: torch.Tensor, Wp: torch.Tensor, group: int, y: torch.Tensor, status: torch.Tensor, stream=None):
