@@ -22,9 +22,9 @@ struct LayerMatrix {
   int row0, K;             // FP8: the expert's first row
 };
 
-// Copy `tiles` row tiles (the rt-th at row tile tile0 + rt * step) of the 128-column
+// Copy `tiles` row tiles (the rt-th at row tile tile0 + rt % PER * step + rt / PER) of the 128-column
 // slices [kt0, kt0 + nk) into the stage at `st`; whole warp.
-template <int GROUP, int SP>
+template <int GROUP, int SP, int PER>
 MOE_DEV void copy_weights(const LayerMatrix& W, int tile0, int step, int tiles, int kt0, int nk, uint32_t st, uint32_t scales,
                           uint32_t bar, int lane) {
   using F = FewForm<GROUP, SP>;
@@ -33,16 +33,16 @@ MOE_DEV void copy_weights(const LayerMatrix& W, int tile0, int step, int tiles, 
   if (F::kW4) {
     if (lane == 0) mbar_arrive_expect_tx(bar, tiles * nk * F::kTile);
     __syncwarp();
-    if (lane < tiles) bulk_load_once(st + lane * F::kRowTile, W.p + ((size_t)(tile0 + lane * step) * KT + kt0) * F::kTile, nk * F::kTile, bar);
+    if (lane < tiles) bulk_load_once(st + lane * F::kRowTile, W.p + ((size_t)(tile0 + lane % PER * step + lane / PER) * KT + kt0) * F::kTile, nk * F::kTile, bar);
   } else {
     // a box of min(8, K / 128) slices; slices past K count as bytes and are filled with zeros
     if (lane == 0) mbar_arrive_expect_tx(bar, tiles * min(kFewWarps, KT) * 2048);
     __syncwarp();
-    if (lane < tiles) tma_load_3d_once(st + lane * F::kRowTile, W.map, 0, W.row0 + (tile0 + lane * step) * 16, kt0, bar);
+    if (lane < tiles) tma_load_3d_once(st + lane * F::kRowTile, W.map, 0, W.row0 + (tile0 + lane % PER * step + lane / PER) * 16, kt0, bar);
     for (int i = lane; i < tiles * kFewWarps; i += 32) {
       const int rt = i / kFewWarps, kt = i % kFewWarps;
       const bool on = kt < nk;
-      const float* src = W.scale + (size_t)((tile0 + rt * step) >> 3) * KT + (on ? kt0 + kt : kt0);
+      const float* src = W.scale + (size_t)((tile0 + rt % PER * step + rt / PER) >> 3) * KT + (on ? kt0 + kt : kt0);
       cp_async4(scales + 4 * i, src, on ? 4 : 0);
     }
     cp_async_arrive(bar);
@@ -299,14 +299,17 @@ template <int GROUP, int RT2, bool DIRECT, int SP>
 MOE_DEV void layer_products(const LayerArgs& A, unsigned char* sm, const FewTables& tb, uint32_t after_tables, uint32_t zero, int tid,
                             int warp, int lane) {
   using F = FewForm<GROUP, SP>;
-  constexpr int kRT = RT2 > 2 ? RT2 : 2;
+  // Gate and up row tiles of a stage, two of each where its slices are few and the tokens many:
+  // these then serve twice the weights.
+  constexpr int kPairs = GROUP != 0 && !DIRECT && SP == 1 ? 2 : 1;
+  constexpr int kRT = RT2 > 2 * kPairs ? RT2 : 2 * kPairs;
   FewShared* sh = reinterpret_cast<FewShared*>(sm);
   const int HT = A.H / 128, FT = A.F / 128;
   const int segs = sh->segs, cap = sh->cap;
   // The sums on their way to the finishing warps: gate and up two buffers where the columns
   // are few.  Down: DIRECT one, [row tile][warp][token]; else those, and the output's
   // sums [T][16 RT2].
-  constexpr int kSumTiles = DIRECT ? 2 : kRT;
+  constexpr int kSumTiles = DIRECT || RT2 < 2 ? 2 : RT2;
   const int bufs = DIRECT || cap <= 8 ? 2 : 1;
   const uint32_t buf_bytes = kFewWarps * kSumTiles * cap * kFewColPitch * 4;
   const uint32_t sums_bytes = DIRECT ? max(bufs * buf_bytes, kFewWarps * RT2 * A.T * kFewColPitch * 4) : bufs * buf_bytes;
@@ -316,7 +319,7 @@ MOE_DEV void layer_products(const LayerArgs& A, unsigned char* sm, const FewTabl
   const uint32_t sco = tok + cap * F::kTokPitch;
   FewRing ring = few_ring(sm, after_tables + sums_bytes + (DIRECT ? 0 : A.T * 16 * RT2 * 4), A.smem_bytes,
                           (sco + kRT * F::kScaleBytes + F::kAlign - 1) & ~(F::kAlign - 1));
-  const int ftiles = A.F / 16, items1 = segs * ftiles, steps1 = (HT + F::kSlices - 1) / F::kSlices;
+  const int fitems = A.F / (16 * kPairs), items1 = segs * fitems, steps1 = (HT + F::kSlices - 1) / F::kSlices;
   const int htiles = A.H / 16, items2 = (htiles + RT2 - 1) / RT2, steps2 = (FT + F::kSlices - 1) / F::kSlices;
 
   if (warp == kFewWarps) {
@@ -324,14 +327,14 @@ MOE_DEV void layer_products(const LayerArgs& A, unsigned char* sm, const FewTabl
     bool ok = __all_sync(0xffffffffu, !sh->abort_flag);
     fence_proxy_async_global();
     for (int item = blockIdx.x; ok && item < items1; item += gridDim.x) {
-      const int seg = item / ftiles, f = item % ftiles;
+      const int seg = item / fitems, f = item % fitems;
       const LayerMatrix W = expert_matrix<GROUP>(A.W1, &A.map1, A.W1_scale, tb.seg_expert[seg], 2 * A.F, A.H);
       const int cols = __popcll(tb.seg_mask[seg]), row = tb.seg_row[seg];
       for (int s = 0; s < steps1; ++s) {
         ok = ring_wait(ring.empty_bar(), ring.phase ^ 1, &sh->abort_flag, A.status);
         if (!ok) break;
         const int kt0 = s * F::kSlices, nk = min(F::kSlices, HT - kt0);
-        copy_weights<GROUP, SP>(W, f, ftiles, 2, kt0, nk, ring.stage(), ring.stage() + sco, ring.full_bar(), lane);
+        copy_weights<GROUP, SP, 2>(W, f * kPairs, A.F / 16, 2 * kPairs, kt0, nk, ring.stage(), ring.stage() + sco, ring.full_bar(), lane);
         copy_tokens<F::kTokPitch>([&](int c) { return A.x8 + (size_t)tb.row_token[row + c] * HT * kTokenRecord; }, cols, kt0, nk,
                     ring.stage() + tok, ring.full_bar(), lane);
         ring.next();
@@ -351,7 +354,7 @@ MOE_DEV void layer_products(const LayerArgs& A, unsigned char* sm, const FewTabl
         if (!ok) break;
         const LayerMatrix W = expert_matrix<GROUP>(A.W2, &A.map2, A.W2_scale, tb.seg_expert[seg], A.H, A.F);
         const int kt0 = s * F::kSlices, nk = min(F::kSlices, FT - kt0);
-        copy_weights<GROUP, SP>(W, item * RT2, 1, min(RT2, htiles - item * RT2), kt0, nk, ring.stage(), ring.stage() + sco,
+        copy_weights<GROUP, SP, 1>(W, item * RT2, 0, min(RT2, htiles - item * RT2), kt0, nk, ring.stage(), ring.stage() + sco,
                             ring.full_bar(), lane);
         ring.next();
         ++begun;
@@ -393,17 +396,19 @@ MOE_DEV void layer_products(const LayerArgs& A, unsigned char* sm, const FewTabl
     };
 
     if (finisher) {
-      for (int item = blockIdx.x; item < items1; item += gridDim.x, way.next()) {
-        if (!(ok = ring_wait_idle(way.full_bar(), way.phase, &sh->abort_flag, A.status))) break;
-        const int seg = item / ftiles, f = item % ftiles;
+      for (int item = blockIdx.x; ok && item < items1; item += gridDim.x) {
+        const int seg = item / fitems, f = item % fitems;
         const int cols = __popcll(tb.seg_mask[seg]), first = tb.seg_row[seg];
-        const float* r = reinterpret_cast<const float*>(sm + way.stage());
-        for (int i = fid; i < 16 * cols; i += kFewFinishThreads) {
-          const int row = i & 15, c = i >> 4;
-          const float g = get_sum(r, cap, row, c) * F::kSumScale, u = get_sum(r + kFewWarps * cap * kFewColPitch, cap, row, c) * F::kSumScale;
-          A.h[(size_t)(first + c) * A.F + f * 16 + row] = g / (1.f + expf(-g)) * u * tb.row_weight[first + c];
+        for (int pair = 0; pair < kPairs; ++pair, way.next()) {
+          if (!(ok = ring_wait_idle(way.full_bar(), way.phase, &sh->abort_flag, A.status))) break;
+          const float* r = reinterpret_cast<const float*>(sm + way.stage());
+          for (int i = fid; i < 16 * cols; i += kFewFinishThreads) {
+            const int row = i & 15, c = i >> 4;
+            const float g = get_sum(r, cap, row, c) * F::kSumScale, u = get_sum(r + kFewWarps * cap * kFewColPitch, cap, row, c) * F::kSumScale;
+            A.h[(size_t)(first + c) * A.F + (f * kPairs + pair) * 16 + row] = g / (1.f + expf(-g)) * u * tb.row_weight[first + c];
+          }
+          arrive(way.empty_bar());
         }
-        arrive(way.empty_bar());
       }
       __threadfence();
       finish_sync();
@@ -413,22 +418,30 @@ MOE_DEV void layer_products(const LayerArgs& A, unsigned char* sm, const FewTabl
       }
     } else {
       for (int item = blockIdx.x; ok && item < items1; item += gridDim.x) {
-        const int cols = __popcll(tb.seg_mask[item / ftiles]);
+        const int cols = __popcll(tb.seg_mask[item / fitems]);
         auto item_sums = [&](auto nt) {
           constexpr int NT = decltype(nt)::value;
           const LaneTokens<NT> lt((1u << cols) - 1, F::kTokPitch, lane);
-          float acc[2][NT][4] = {};
+          float acc[kPairs][2][NT][4] = {};
           for (int s = 0; s < steps1; ++s, ring.next()) {
             if (!wait(ring.full_bar(), ring.phase)) return;
+            const uint32_t st = ring.stage();
 #pragma unroll
             for (int i = warp; i < F::kSlices; i += kFewWarps)
-              if (s * F::kSlices + i < HT) few_slice<GROUP, SP, 2, NT>(ring.stage(), ring.stage() + sco, ring.stage() + tok + i * kTokenRecord, zero, lt, i, lane, acc);
+              if (s * F::kSlices + i < HT) {
+#pragma unroll
+                for (int pair = 0; pair < kPairs; ++pair)
+                  few_slice<GROUP, SP, 2, NT>(st + 2 * pair * F::kRowTile, st + sco, st + tok + i * kTokenRecord, zero, lt, i, lane, acc[pair]);
+              }
             arrive(ring.empty_bar());
           }
-          if (!wait(way.empty_bar(), way.phase ^ 1)) return;
-          put_sums<2, NT>(reinterpret_cast<float*>(sm + way.stage()), cap, cols, warp, lane, acc);
-          arrive(way.full_bar());
-          way.next();
+#pragma unroll
+          for (int pair = 0; pair < kPairs; ++pair) {
+            if (!wait(way.empty_bar(), way.phase ^ 1)) return;
+            put_sums<2, NT>(reinterpret_cast<float*>(sm + way.stage()), cap, cols, warp, lane, acc[pair]);
+            arrive(way.full_bar());
+            way.next();
+          }
         };
         if (SP == 2 || DIRECT || cols <= 8)
           item_sums(std::integral_constant<int, 1>());
