@@ -397,3 +397,143 @@ def test_layer_refusals():
         assert lib.moe_layer_few(*args) == moe.MOE_ERR_INVALID_ARG, i
     torch.cuda.synchronize()
     assert st.item() == 0
+
+
+# ---------------------------------------------------------------- the kernels' own boundaries
+
+# tokens around the switch between the two matvec kernels and the wide one's token blocks,
+# rows around its groups, columns that end inside a stage, a slice and a half
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,N,K", [(8, 64, 4096), (8, 50, 32768), (9, 33, 384), (10, 1, 128), (24, 257, 640), (25, 512, 1152), (31, 4880, 512),
+                                   (41, 31, 2176), (48, 272, 1024), (57, 1000, 896), (64, 16, 7168)])
+def test_matvec_kernel_boundaries(T, N, K, group):
+    Wp, W = w4_matrix(N, K, group, seed=T)
+    xb = rand_bits(T, K, seed=N)
+    y = torch.full((T, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    st = status()
+    moe.moe_matvec_w4(bf16_t(xb), Wp, group, y, st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    within(y, *oracle.matvec_bound(f64(xb), W), "matvec")
+
+
+@pytest.mark.parametrize("T", [1, 6, 20])
+def test_matvec_tokens_of_very_different_sizes(T):
+    # blocks of tiny and of huge values side by side: no token's scale is another block's
+    N, K, group = 48, 512, 64
+    Wp, W = w4_matrix(N, K, group, seed=T)
+    x = f64(rand_bits(T, K, seed=T))
+    x[:, 128:256] *= 2.0 ** -40
+    x[:, 256:384] *= 2.0 ** 40
+    x[0, :128] = 0
+    xb = oracle.f64_to_bf16(x)
+    y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    moe.moe_matvec_w4(bf16_t(xb), Wp, group, y, status())
+    within(y, *oracle.matvec_bound(f64(xb), W), "matvec")
+
+
+# few and many tokens per expert, few and many pairs, segments of 16, batches around the
+# switches of the selection and of the sums
+BOUNDARIES = [(4, 8, 16, 256, 128), (11, 3, 64, 256, 256), (8, 4, 4, 256, 128), (9, 1, 64, 384, 128), (16, 1, 1, 256, 128), (17, 1, 1, 256, 128),
+              (24, 2, 64, 256, 128), (25, 2, 64, 256, 128), (33, 1, 2, 128, 256), (64, 8, 64, 256, 128), (3, 2, 5, 2176, 1152)]
+
+
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("T,k,E,H,F", BOUNDARIES)
+def test_layer_boundaries_with_router(T, k, E, H, F, group):
+    ex = Experts(E, H, F, group, seed=T + E)
+    xb, rb = rand_bits(T, H, seed=T + 1), rand_bits(E, H, seed=T + 2, scale=H ** -0.5)
+    out, ids, w = ex.run(xb, np.zeros((T, k), np.int32), np.zeros((T, k), np.float32), bf16_t(rb))
+    assert ids.min() >= 0 and ids.max() < E and all(len(set(r)) == k for r in ids)
+    within(out, *oracle.layer_few(f64(xb), ids, w, ex.values), "layer")
+    # the same routes given by the caller: the same output, bit for bit
+    again, _, _ = ex.run(xb, ids, w)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_layer_small_tables_with_repeats_and_gaps(group):
+    # at most 32 pairs: an expert three times, one without a route, one out of range
+    ex = Experts(5, 256, 128, group, seed=3)
+    ids = np.array([[4, 4, 4, 1], [0, -1, 4, 0], [-1, -1, -1, -1], [2, 9, 1, 2]], np.int32)
+    w = np.random.default_rng(1).random(ids.shape).astype(np.float32)
+    xb = rand_bits(4, 256, seed=5)
+    out, _, _ = ex.run(xb, ids, w, want_status=moe.MOE_ERR_EXPERT_ID)
+    within(out, *oracle.layer_few(f64(xb), ids, w, ex.values), "layer")
+    assert torch.all(out[2] == 0)
+
+
+@pytest.mark.parametrize("group", [0, 128])
+def test_layer_offsets_past_32_bits(group):
+    # the last of 200 experts' weights lies more than 2^31 (FP8) and 2^30 (4-bit) bytes in;
+    # the others are NaN and unused
+    E, H, F, e = 200, 7168, 1024, 199
+    one = Experts(1, H, F, group, seed=1)
+    fill = lambda t, v: torch.full((E, *t.shape[1:]), v, dtype=t.dtype, device="cuda")   # noqa: E731
+    ex = Experts.__new__(Experts)
+    ex.E, ex.H, ex.F, ex.group, ex.values = E, H, F, group, {e: one.values[0]}
+    ex.W1, ex.W2 = fill(one.W1, 0x7F), fill(one.W2, 0x7F)
+    ex.W1[e], ex.W2[e] = one.W1[0], one.W2[0]
+    ex.W1_scale = ex.W2_scale = None
+    if not group:
+        ex.W1_scale, ex.W2_scale = fill(one.W1_scale, float("nan")), fill(one.W2_scale, float("nan"))
+        ex.W1_scale[e], ex.W2_scale[e] = one.W1_scale[0], one.W2_scale[0]
+    for T in (1, 10):
+        ids, w = np.full((T, 1), e, np.int32), np.full((T, 1), 1.5, np.float32)
+        xb = rand_bits(T, H, seed=2)
+        out, _, _ = ex.run(xb, ids, w)
+        within(out, *oracle.layer_few(f64(xb), ids, w, ex.values), "layer")
+
+
+def test_layer_activations_far_from_one():
+    # activations whose blocks differ by 2^60 and more than f16 holds
+    H, F = 256, 256
+    b1, b2 = rand_bits(1, 2 * F, H, seed=1, scale=H ** -0.5), rand_bits(1, H, F, seed=2, scale=F ** -0.5)
+    f = f64(b1)
+    f[0, F:F + 128] *= 2.0 ** 40
+    f[0, F + 128:] *= 2.0 ** -40
+    b1 = oracle.f64_to_bf16(f)
+    (q1, s1), (q2, s2) = oracle.quantize_w4(b1, 32), oracle.quantize_w4(b2, 32)
+    ex = Experts.__new__(Experts)
+    ex.E, ex.H, ex.F, ex.group, ex.W1_scale, ex.W2_scale = 1, H, F, 32, None, None
+    ex.W1, ex.W2 = (torch.from_numpy(oracle.pack_w4(*v)).cuda() for v in ((q1, s1), (q2, s2)))
+    ex.values = {0: (oracle.w4_values(q1[0], s1[0]), oracle.w4_values(q2[0], s2[0]))}
+    for T in (2, 12):
+        xb = rand_bits(T, H, seed=T)
+        ids, w = np.zeros((T, 1), np.int32), np.ones((T, 1), np.float32)
+        out, _, _ = ex.run(xb, ids, w)
+        within(out, *oracle.layer_few(f64(xb), ids, w, ex.values), "layer")
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("counter", [0, 1, 2])
+def test_layer_meeting_that_cannot_be_complete_gives_up(group, counter):
+    # a counter that starts short of its arrivals: the grid's wait runs out after a second,
+    # the call reports it, leaves the workspace's head zero, and the next call is right
+    T, k, E, H, F = 4, 2, 8, 256, 256
+    ex = Experts(E, H, F, group, seed=1)
+    ids, w = routes(T, k, E, seed=2)
+    xb = rand_bits(T, H, seed=3)
+    ws, st, out = ex.workspace(T, k), status(), torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    ws.view(torch.int32)[counter] = -1
+    args = (bf16_t(xb), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), out, ws, st)
+    ex.call(*args)
+    torch.cuda.synchronize()
+    assert st.item() == moe.MOE_ERR_TIMEOUT and not ws[:256].any()
+    st.zero_()
+    ex.call(*args)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    within(out, *oracle.layer_few(f64(xb), ids, w, ex.values), "layer")
+
+
+@pytest.mark.parametrize("weights", ["w4", "fp8"])
+def test_decode_example_runs(weights):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "decode_moe.py"), "--weights", weights, "--tokens", "3", "--steps", "4",
+                        "--hidden", "256", "--ffn", "128", "--experts", "8", "--topk", "2", "--vocab", "1000"], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert "tokens/s" in r.stdout
