@@ -4,15 +4,16 @@
 // A CTA is eight computing warps, one copying warp and three finishing warps.  The
 // copying warp walks the CTA's work and keeps a ring of shared-memory stages full with bulk copies
 // and TMA loads (counted on an mbarrier per stage): per stage RT row tiles of 16
-// weight rows x 1024 columns, and the same 1024 columns of the tokens that the
-// weights multiply.  Each computing warp takes one 128-column slice of a stage.
+// weight rows x 1024 or 2048 columns, and (the layer) the same columns of the tokens that
+// the weights multiply.  Each computing warp takes one or two 128-column slices of a stage.
 // The eight partial sums of a row go to the finishing warps through shared memory once
 // a row tile is complete; they add them in a fixed order and write the results while
 // the computing warps go on (a block-wide meeting per item had cost a tenth).
 //
-// The products run on mma.sync and not on tcgen05: the tensor work is the
-// weights times 8 columns, far below either's rate, while 4-bit codes have to
-// pass through registers to be widened and FP8 sums to be scaled per 128 columns.
+// The layer's products, and a matrix's with few tokens, run on mma.sync and not on tcgen05:
+// the tensor work is the weights times 8 columns, far below either's rate, while 4-bit codes
+// have to pass through registers to be widened and FP8 sums to be scaled per 128 columns.
+// More tokens on one matrix take tcgen05 (few_tensor.cuh).
 #pragma once
 
 #include "common.cuh"
@@ -125,12 +126,12 @@ struct FewRing {
 };
 
 // All barriers and the abort flag, by the block's first threads; the caller
-// synchronises the block.  `arrivals` complete a stage.
-MOE_DEV void few_barriers(unsigned char* sm, int tid, int arrivals) {
+// synchronises the block.  `arrivals` complete a stage, `readers` free it.
+MOE_DEV void few_barriers(unsigned char* sm, int tid, int arrivals, int readers = kFewWarps) {
   FewShared* sh = reinterpret_cast<FewShared*>(sm);
   if (tid < kFewMaxStages) {
     mbar_init(smem_u32(sh->full + tid), arrivals);
-    mbar_init(smem_u32(sh->empty + tid), kFewWarps);
+    mbar_init(smem_u32(sh->empty + tid), readers);
     if (tid < 2) {
       mbar_init(smem_u32(sh->sums_full + tid), kFewWarps);
       mbar_init(smem_u32(sh->sums_empty + tid), kFewFinish);

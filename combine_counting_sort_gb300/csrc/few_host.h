@@ -8,13 +8,13 @@ namespace moe {
 constexpr int kFewMinSmem = 227 * 1024;   // room for a ring beside the largest tables
 
 struct MatvecArgs {
-  CUtensorMap map_w, map_x;   // the wide kernel's: whole tiles, and 64 columns of all tokens
+  CUtensorMap map_w, map_x;   // wide and tensor kernels: whole tiles, and 64 columns of all tokens
   const uint16_t* x;
   const uint8_t* W;
   uint16_t* y;
   int32_t* status;
   int T, N, K;
-  int slices;          // of the wide kernel's stages
+  int slices;          // wide kernel: of a stage; tensor kernel: blocks that share rows
   uint32_t smem_bytes;
 };
 
@@ -68,9 +68,9 @@ inline int few_row_tiles(int tiles, int nsm, int most = 3) {
   return best;
 }
 
-// Launch with all the shared memory a block can have.
+// Launch with all the shared memory a block can have; `cluster` blocks share rows.
 template <class Kernel, class Args>
-int few_launch(Kernel kernel, Args& a, int threads, int blocks, bool cooperative, cudaStream_t s) {
+int few_launch(Kernel kernel, Args& a, int threads, int blocks, bool cooperative, cudaStream_t s, int cluster = 1) {
   int dev = 0, smem = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   if (cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) return MOE_ERR_CUDA;
@@ -83,7 +83,7 @@ int few_launch(Kernel kernel, Args& a, int threads, int blocks, bool cooperative
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   if (cooperative) {
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
@@ -91,8 +91,11 @@ int few_launch(Kernel kernel, Args& a, int threads, int blocks, bool cooperative
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
   }
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

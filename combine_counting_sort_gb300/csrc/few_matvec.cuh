@@ -1,25 +1,29 @@
-// few_matvec.cuh: products of up to 64 tokens with one 4-bit matrix, in two kernels.
+// few_matvec.cuh: products of up to 64 tokens with one 4-bit matrix, in three kernels.
 //
-// matvec_few_kernel, up to 8 tokens whose records fit beside the ring: every block makes
-// the records of all tokens for itself while its first weights are on their way, and a
-// stage holds weights alone (few_slice.cuh: the products).
+// matvec_few_kernel, one token, or up to 4 on few columns: every block makes the records of
+// all tokens for itself while its first weights are on their way, and a stage holds weights
+// alone (few_slice.cuh: the products).  Bound by memory with many rows (152064 x 4096, groups
+// of 64, one token: 52.6 us, 6.3 TB/s), with few by the way through the block: launch, records,
+// first copies, sums (4096 x 7168, groups of 128: 7.35 us, of which the weights are 2.2).
 //
-// matvec_wide_kernel, more tokens: a block of eight warps is KS slices of 128 columns x 8 /
-// KS groups of 32 rows, each warp all tokens (up to 8 blocks of 8) on its 32 rows, so
-// that a code is widened once for all of them: to bf16, 0x4300 | c less 136.  It is
-// bound by the MMAs, 8 per 16 x 128 weights and 8 tokens at half an instruction a
-// clock, from some 24 tokens up.  With few rows the slices are many, so that
-// every SM has work, and their sums meet in shared memory; with many rows they are
-// few, since every block reads all tokens.  A copy costs some 70 cycles of an SM's
-// copies whatever its size (row by row, 48 tokens took 140 us over 32768 x 7168), so
-// a stage's weights are one box of whole tiles, its tokens one of 64 columns.
+// matvec_wide_kernel, up to 16 tokens and few rows: a block of eight warps is KS slices of 128
+// columns x 8 / KS groups of 32 rows, each warp all tokens (one or two blocks of 8) on its 32
+// rows, so that a code is widened once for all of them: to bf16, 0x4300 | c less 136.  With
+// few rows the slices are many, so that every SM has work, and their sums meet in shared
+// memory; with many rows they are few, since every block reads all tokens.  A copy costs
+// some 70 cycles of an SM's copies whatever its size, so a stage's weights are one box of
+// whole tiles, its tokens one of 64 columns.  4096 x 7168, groups of 128, 8 tokens: 7.8 us.
+//
+// matvec_tensor_kernel (few_tensor.cuh), the rest: more than 16 tokens, or more rows than four
+// row tiles per SM.
 #pragma once
 
 #include "few_slice.cuh"
+#include "few_tensor.cuh"
 
 namespace moe {
 
-constexpr int kMatvecTokenRoom = 96 * 1024;   // of the few kernel's records
+constexpr int kMatvecTokenRoom = 48 * 1024;   // of the few kernel's records beside stages of three row tiles
 
 __host__ __device__ __forceinline__ int matvec_token_pitch(int KT) { return ((KT * kTokenRecord + 127) & ~127) + 64; }
 
@@ -283,16 +287,24 @@ int launch_matvec_few(const MatvecArgs& a, int nsm, cudaStream_t s) {
 template <int GROUP>
 int launch_matvec(const MatvecArgs& args, int nsm, cudaStream_t s) {
   const int tiles = (args.N + 15) / 16;
-  const int records = args.T * matvec_token_pitch((args.K + 127) / 128);
-  if (args.T <= 8 && records <= kMatvecTokenRoom) {
-    switch (few_row_tiles(tiles, nsm, records <= kMatvecTokenRoom / 2 ? 3 : 2)) {   // room for two stages
+  const int KT = (args.K + 127) / 128, records = args.T * matvec_token_pitch(KT);
+  // The records cost a block some 30 ns each; the other kernels take the tokens as they are.  Groups of
+  // 128, few / other kernel: one token x 4096 x 7168 7.35 / 7.81 us, x 32768 x 7168 25.8 /
+  // 29.2; two x 7168 x 2048 (32 records) 4.41 / 4.98, x 4096 x 4096 (64) 5.94 / 5.45; four x 1111 x
+  // 1024 (32) 2.88 / 2.88, x 4096 x 4096 (128) 8.1 / 5.4.
+  if (args.T == 1 || (args.T <= 4 && args.T * KT <= 32)) {
+    switch (few_row_tiles(tiles, nsm, records <= kMatvecTokenRoom ? 3 : 2)) {   // room for two stages
       case 1: return launch_matvec_few<GROUP, 1>(args, nsm, s);
       case 2: return launch_matvec_few<GROUP, 2>(args, nsm, s);
       default: return launch_matvec_few<GROUP, 3>(args, nsm, s);
     }
   }
+  // Groups of 128, wide / tensor kernel: 16 tokens x 8192 x 4096 9.1 / 11.7 us, x 16384 x 4096
+  // 14.5 / 13.3, x 32768 x 7168 48 / 29; 32 tokens x 1024 x 1024 5.7 / 4.5, x 4096 x 7168
+  // 12.7 / 11.8, x 32768 x 7168 59 / 31.
+  if (args.T > 16 || tiles > 4 * nsm) return launch_matvec_tensor<GROUP>(args, nsm, s);
   MatvecArgs a = args;
-  const int KT = (a.K + 127) / 128, nt = a.T <= 32 ? (a.T + 7) / 8 : a.T <= 48 ? 6 : 8;
+  const int nt = (a.T + 7) / 8;
   a.slices = wide_slices(tiles, KT, nt, nsm);
   const int rows = 2 * (8 / a.slices), blocks = std::min((tiles + rows - 1) / rows, nsm);
   constexpr int kTile = w4_tile_bytes(GROUP);
@@ -303,14 +315,8 @@ int launch_matvec(const MatvecArgs& args, int nsm, cudaStream_t s) {
   if (!encode_few_map(&a.map_w, CU_TENSOR_MAP_DATA_TYPE_UINT64, CU_TENSOR_MAP_SWIZZLE_NONE, a.W, 3, wd, ws, wb) ||
       !encode_few_map(&a.map_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.x, 2, xd, xs, xb))
     return MOE_ERR_CUDA;
-  switch (nt) {
-    case 1: return few_launch(matvec_wide_kernel<GROUP, 1>, a, kWideThreads, blocks, false, s);
-    case 2: return few_launch(matvec_wide_kernel<GROUP, 2>, a, kWideThreads, blocks, false, s);
-    case 3: return few_launch(matvec_wide_kernel<GROUP, 3>, a, kWideThreads, blocks, false, s);
-    case 4: return few_launch(matvec_wide_kernel<GROUP, 4>, a, kWideThreads, blocks, false, s);
-    case 6: return few_launch(matvec_wide_kernel<GROUP, 6>, a, kWideThreads, blocks, false, s);
-    default: return few_launch(matvec_wide_kernel<GROUP, 8>, a, kWideThreads, blocks, false, s);
-  }
+  return nt == 1 ? few_launch(matvec_wide_kernel<GROUP, 1>, a, kWideThreads, blocks, false, s)
+                 : few_launch(matvec_wide_kernel<GROUP, 2>, a, kWideThreads, blocks, false, s);
 }
 
 }  // namespace moe

@@ -537,3 +537,44 @@ def test_decode_example_runs(weights):
                         "--hidden", "256", "--ffn", "128", "--experts", "8", "--topk", "2", "--vocab", "1000"], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     assert "tokens/s" in r.stdout
+
+
+# ---------------------------------------------------------------- matvec on many tokens or many rows
+
+# clusters of 8, 4 and 2 blocks and single ones, uneven runs of slices, several rounds over the
+# SMs, rows and tokens that end inside a block, few tokens on many rows
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,N,K", [(17, 3840, 1152), (33, 3841, 640), (64, 9216, 256), (48, 19456, 384), (20, 39000, 128),
+                                   (9, 9744, 256), (16, 40000, 128), (2, 50, 24576), (8, 9731, 8192), (32, 255, 128)])
+def test_matvec_many_tokens_or_rows(T, N, K, group):
+    Wp, W = w4_matrix(N, K, group, seed=T)
+    xb = rand_bits(T, K, seed=N)
+    buf = torch.full((T * N + 64,), -7.0, dtype=torch.bfloat16, device="cuda")
+    y, st = buf[:T * N].view(T, N), status()
+    y.fill_(float("nan"))
+    x = bf16_t(xb)
+    moe.moe_matvec_w4(x, Wp, group, y, st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    within(y, *oracle.matvec_bound(f64(xb), W), "matvec")
+    assert (buf[T * N:] == -7).all()
+    again = torch.empty_like(y)
+    moe.moe_matvec_w4(x, Wp, group, again, st)
+    assert torch.equal(again.view(torch.int16), y.view(torch.int16))
+
+
+def test_matvec_many_tokens_do_not_meet():
+    # a token of infinities and NaN leaves every other token's bits as they were
+    T, N, K, group = 40, 600, 384, 64
+    Wp, _ = w4_matrix(N, K, group, seed=3)
+    x = bf16_t(rand_bits(T, K, seed=4))
+    want, got = (torch.empty(T, N, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    st = status()
+    moe.moe_matvec_w4(x, Wp, group, want, st)
+    x2 = x.clone()
+    x2[7, ::3] = float("inf")
+    x2[7, 1::3] = float("nan")
+    moe.moe_matvec_w4(x2, Wp, group, got, st)
+    keep = [t for t in range(T) if t != 7]
+    assert torch.equal(got[keep].view(torch.int16), want[keep].view(torch.int16))
+    assert got[7].isnan().all() and st.item() == 0
