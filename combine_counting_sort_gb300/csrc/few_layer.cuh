@@ -1,6 +1,14 @@
 // few_layer.cuh: a whole MoE layer for a few tokens, in one launch (few_slice.cuh: its
 // products).  What bounds it is memory, but for some 12 us: until the routes are
 // known, no weight can be on its way.
+//
+// Measured, us and share of the copy bandwidth that the weights were read at (H 7168, F 2048, 8 of 256
+// experts): FP8, 1 token 66 (79%), 16 tokens 641 (103%), 64 tokens 1460 (99%); 4-bit, groups of
+// 128, 1 token 48 (56%), 64 tokens 973 (76%); groups of 32, 8 tokens 252 (83%).  One token's 66
+// us in ns: records 600, logits 1500, meeting 1500, routes 1850, tables 1700, gate and up
+// 33000, meeting and records 5000, down 15400; the 4-bit products take 22600 and 10200, bound by the
+// hand-over of stages that hold half the bytes.  With H or F of a few hundred the stages are
+// mostly empty and the fixed 12 us are most of the time (8 experts, 256 x 256: 12.7 us).
 #pragma once
 
 #include <type_traits>

@@ -19,7 +19,8 @@
 // shifts (4-bit) or 32 conversions (FP8), both at 64 lanes a clock, 8 MMAs per 8 tokens
 // and some 30 other instructions.  Widening 4-bit codes by the usual offset and
 // subtraction takes 88, FP8 codes to bf16 128, which is longer than the
-// tile's bytes take from memory.
+// tile's bytes take from memory.  A stage of 6 x 8 tiles of FP8 took 1150 cycles with the
+// conversions as the compiler unpacks them, 640 as written here (a stage's bytes: 610).
 #pragma once
 
 #include <cuda_fp16.h>

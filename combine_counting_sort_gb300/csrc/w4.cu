@@ -7,7 +7,9 @@ namespace moe {
 // All three kernels: one warp per tile, the warps of a block on neighbouring tiles of a
 // row of tiles.  Quantising and packing, lane 4g + t owns rows g and 8 + g and columns 32 j + 8 t + 0..7: 16
 // bytes of bf16 per j, 4 lanes on 64 bytes of a row, and 16 bytes of codes per half.
-// Bound by memory (quantising: 2.5 bytes a weight, and some 8 instructions).
+// Bound by memory (quantising: 2.5 bytes a weight, and some 8 instructions).  16 matrices of 4096 x
+// 7168, groups of 128: quantised in 178 us (6.7 TB/s), packed in 100 us, read back in 310
+// us, almost all of it the 1.88 GB written.
 constexpr int kW4Warps = 8;
 
 struct W4Tile {

@@ -442,7 +442,8 @@ int moe_dequant_weights_w4(const uint8_t* Wp, int E, int N, int K, int group, fl
 
 /* moe_matvec_w4: y[t, n] = bf16( sum_k x[t, k] * (c[n, k] - 8) * scale[n, k / group] ),
  * fp32 accumulation, one rounding.  For what stands beside the experts: a
- * shared expert's projections, the vocabulary.
+ * shared expert's projections, the vocabulary.  A token's values reach no other
+ * token's results.
  *   x  device bf16 [T, K], 1 <= T <= MOE_FEW_MAX_TOKENS, 16-byte aligned.
  *   Wp one laid-out matrix; y device bf16 [T, N].
  * A bounded wait that gives up writes MOE_ERR_TIMEOUT to *status. */
@@ -457,8 +458,11 @@ int moe_matvec_w4(const uint16_t* x, int T, int K, const uint8_t* Wp, int N, int
  *   g, u = rows [0, F) and [F, 2F) of W1[id] times x[t];  a = g / (1 + exp(-g)) * u
  *   out[t, :] = bf16( sum_j w[t, j] * W2[id[t, j]] * a[t, j] )
  * with each expert's weights read once however many of the tokens use it.
- * Products and sums are fp32; w * a is rounded to bf16 once, for the
- * second product's operands.
+ * Sums are fp32.  w * a, fp32, is rounded once for the second product's operands: to
+ * f16's 11 bits behind a power of two shared by 128 values; what is below 2^-28
+ * of the largest of the 128 loses bits.  Infinite and NaN values of x spoil that
+ * token's out and no other's.  Where fewer than k of a token's logits are not NaN,
+ * the slots left get the id 0x7fffffff and *status is MOE_ERR_EXPERT_ID.
  *   x        device bf16 [T, H].
  *   router   device bf16 [E, H], or NULL: topk_ids and topk_w are then inputs.
  *   topk_ids device int32 [T, k], topk_w device f32 [T, k]: written where router

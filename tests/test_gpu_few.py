@@ -578,3 +578,30 @@ def test_matvec_many_tokens_do_not_meet():
     keep = [t for t in range(T) if t != 7]
     assert torch.equal(got[keep].view(torch.int16), want[keep].view(torch.int16))
     assert got[7].isnan().all() and st.item() == 0
+
+
+@pytest.mark.parametrize("group", [0, 64])
+@pytest.mark.parametrize("T", [5, 14])
+def test_layer_token_that_is_not_finite(T, group):
+    # with the router: no logit of the token is a number, so no expert is its; with given
+    # routes its out is NaN; the others' bits stay as they were
+    E, k, H, F = 12, 3, 256, 384
+    L = Experts(E, H, F, group, seed=5)
+    x = bf16_t(rand_bits(T, H, seed=6))
+    router = bf16_t(rand_bits(E, H, seed=7, scale=0.1))
+    x2 = x.clone()
+    x2[2, :] = float("nan")
+    keep = [t for t in range(T) if t != 2]
+    res = []
+    for r in (router, None):
+        for v in (x, x2):
+            ids, w = routes(T, k, E, seed=8)
+            ids, w = torch.as_tensor(ids, dtype=torch.int32).cuda(), torch.as_tensor(w, dtype=torch.float32).cuda()
+            out, st = torch.full((T, H), -3.0, dtype=torch.bfloat16, device="cuda"), status()
+            L.call(v, ids, w, out, L.workspace(T, k), st, r)
+            torch.cuda.synchronize()
+            res.append((out, ids, st.item()))
+    for clean, spoilt in (res[:2], res[2:]):
+        assert torch.equal(clean[0][keep].view(torch.int16), spoilt[0][keep].view(torch.int16)) and clean[2] == 0
+    assert (res[1][1][2] == 0x7FFFFFFF).all() and (res[1][0][2] == 0).all() and res[1][2] == moe.MOE_ERR_EXPERT_ID
+    assert res[3][0][2].isnan().all() and res[3][2] == 0
