@@ -1,10 +1,11 @@
 // few_matvec.cuh: products of up to 64 tokens with one 4-bit matrix, in three kernels.
 //
-// matvec_few_kernel, one token, or up to 4 on few columns: every block makes the records of
-// all tokens for itself while its first weights are on their way, and a stage holds weights
-// alone (few_slice.cuh: the products).  Bound by memory with many rows (152064 x 4096, groups
-// of 64, one token: 52.6 us, 6.3 TB/s), with few by the way through the block: launch, records,
-// first copies, sums (4096 x 7168, groups of 128: 7.35 us, of which the weights are 2.2).
+// matvec_few_kernel, one or two tokens, or up to four on few columns or many rows: every block
+// makes the records of all tokens for itself while its first weights are on their way, and a
+// stage holds weights alone (few_slice.cuh: the products).  Bound by memory with many rows
+// (152064 x 4096, groups of 64, one token: 52.1 us, 6.4 TB/s), with few by the way through the
+// block: launch, records, first copies, sums (4096 x 7168, groups of 128: 6.2 us, of which the
+// weights are 2.2; 7.35 with the records' loads one after the other).
 //
 // matvec_wide_kernel, up to 16 tokens and few rows: a block of eight warps is KS slices of 128
 // columns x 8 / KS groups of 32 rows, each warp all tokens (one or two blocks of 8) on its 32
@@ -23,7 +24,7 @@
 
 namespace moe {
 
-constexpr int kMatvecTokenRoom = 48 * 1024;   // of the few kernel's records beside stages of three row tiles
+constexpr int kMatvecTokenRoom = 96 * 1024;   // of the few kernel's records beside two stages of two row tiles; half of it beside three
 
 __host__ __device__ __forceinline__ int matvec_token_pitch(int KT) { return ((KT * kTokenRecord + 127) & ~127) + 64; }
 
@@ -69,11 +70,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) matvec_few_kernel(const __grid
     return;
   }
 
-  for (int i = warp > kFewWarps ? warp - 1 : warp; i < A.T * KT; i += kFewAllWarps - 1) {
-    const int t = i / KT, kt = i % KT, k = kt * 128 + 4 * lane;   // K is a multiple of 32
-    const uint2 x = k < A.K ? __ldg(reinterpret_cast<const uint2*>(A.x + (size_t)t * A.K + k)) : make_uint2(0, 0);
-    const float v[4] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)};
-    put_record<GROUP>(v, sm + kTokensAt + t * pitch + kt * kTokenRecord, lane);
+  constexpr int kBatch = 6;   // records of a warp whose loads are in flight together
+  for (int i0 = warp > kFewWarps ? warp - 1 : warp; i0 < A.T * KT; i0 += kBatch * (kFewAllWarps - 1)) {
+    uint2 x[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * (kFewAllWarps - 1), t = i / KT, k = i % KT * 128 + 4 * lane;   // K is a multiple of 32
+      x[b] = t < A.T && k < A.K ? __ldg(reinterpret_cast<const uint2*>(A.x + (size_t)t * A.K + k)) : make_uint2(0, 0);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * (kFewAllWarps - 1), t = i / KT;
+      if (t >= A.T) break;
+      const float v[4] = {bf16_lo(x[b].x), bf16_hi(x[b].x), bf16_lo(x[b].y), bf16_hi(x[b].y)};
+      put_record<GROUP>(v, sm + kTokensAt + t * pitch + i % KT * kTokenRecord, lane);
+    }
   }
   consumer_sync_all(true);
 
@@ -288,12 +299,13 @@ template <int GROUP>
 int launch_matvec(const MatvecArgs& args, int nsm, cudaStream_t s) {
   const int tiles = (args.N + 15) / 16;
   const int KT = (args.K + 127) / 128, records = args.T * matvec_token_pitch(KT);
-  // The records cost a block some 30 ns each; the other kernels take the tokens as they are.  Groups of
-  // 128, few / other kernel: one token x 4096 x 7168 7.35 / 7.81 us, x 32768 x 7168 25.8 /
-  // 29.2; two x 7168 x 2048 (32 records) 4.41 / 4.98, x 4096 x 4096 (64) 5.94 / 5.45; four x 1111 x
-  // 1024 (32) 2.88 / 2.88, x 4096 x 4096 (128) 8.1 / 5.4.
-  if (args.T == 1 || (args.T <= 4 && args.T * KT <= 32)) {
-    switch (few_row_tiles(tiles, nsm, records <= kMatvecTokenRoom ? 3 : 2)) {   // room for two stages
+  // The records cost a block some 20 ns each; the other kernels take the tokens as they are.
+  // Groups of 128, few / other kernel: one token x 4096 x 7168 6.2 / 7.8 us, x 32768 x 7168
+  // 23.9 / 29.2; two x 4096 x 7168 (112 records) 7.4 / 7.9; three x 7168 x 2048 (48) 4.8 / 5.0, x
+  // 4096 x 4096 (96) 5.9 / 5.4, x 32768 x 7168 26.8 / 29.3; four x 2048 x 2048 (64) 3.4 / 3.7, x 4096 x 7168
+  // (224) 10 / 7.9; six x 2048 x 2048 (96) 4.3 / 3.7, x 32768 x 7168 31.3 / 29.2.
+  if (records <= kMatvecTokenRoom && (args.T <= 2 || (args.T <= 4 && (args.T * KT <= 64 || tiles > 4 * nsm)))) {
+    switch (few_row_tiles(tiles, nsm, records <= kMatvecTokenRoom / 2 ? 3 : 2)) {
       case 1: return launch_matvec_few<GROUP, 1>(args, nsm, s);
       case 2: return launch_matvec_few<GROUP, 2>(args, nsm, s);
       default: return launch_matvec_few<GROUP, 3>(args, nsm, s);
