@@ -1,7 +1,7 @@
 // few_matvec.cuh: products of up to 64 tokens with one 4-bit matrix, in three kernels.
 //
-// matvec_few_kernel, one or two tokens, or up to four on few columns or many rows: every block
-// makes the records of all tokens for itself while its first weights are on their way, and a
+// matvec_few_kernel, one token, or up to four on few columns or many rows: every block makes
+// the records of all tokens for itself while its first weights are on their way, and a
 // stage holds weights alone (few_slice.cuh: the products).  Bound by memory with many rows
 // (152064 x 4096, groups of 64, one token: 52.1 us, 6.4 TB/s), with few by the way through the
 // block: launch, records, first copies, sums (4096 x 7168, groups of 128: 6.2 us, of which the
@@ -13,7 +13,7 @@
 // few rows the slices are many, so that every SM has work, and their sums meet in shared
 // memory; with many rows they are few, since every block reads all tokens.  A copy costs
 // some 70 cycles of an SM's copies whatever its size, so a stage's weights are one box of
-// whole tiles, its tokens one of 64 columns.  4096 x 7168, groups of 128, 8 tokens: 7.8 us.
+// whole tiles, its tokens another (with one to 64 columns 4096 x 7168 and 8 tokens took 7.8 us).
 //
 // matvec_tensor_kernel (few_tensor.cuh), the rest: more than 16 tokens, or more rows than four
 // row tiles per SM.
@@ -140,9 +140,9 @@ MOE_DEV bool wide_sync_all(bool ok) {
 }
 
 // Two row tiles' 64 columns [64 half, 64 half + 64) of a slice times NT blocks of 8 tokens.
-// tok: these columns of token lane / 4, 128 bytes in TMA's swizzle; 128 bytes to the next.
+// tok: these columns of token lane / 4, 128 bytes in TMA's swizzle, and `token_pitch` to the next.
 template <int GROUP, int NT>
-MOE_DEV void wide_half(uint32_t w, uint32_t row_tile, uint32_t tok, int half, int lane, float (&acc)[2][NT][4]) {
+MOE_DEV void wide_half(uint32_t w, uint32_t row_tile, uint32_t tok, uint32_t token_pitch, int half, int lane, float (&acc)[2][NT][4]) {
   constexpr int kGroups = GROUP == 32 ? 2 : 1, kMmas = 4 / kGroups;   // groups that these columns touch
   uint32_t a[2][4][4];
   float s[2][kGroups][2];
@@ -169,8 +169,8 @@ MOE_DEV void wide_half(uint32_t w, uint32_t row_tile, uint32_t tok, int half, in
   }
 #pragma unroll
   for (int j = 0; j < NT; ++j) {   // without a branch, so that the blocks' loads and MMAs overlap
-    const uint32_t chunk = (lane & 3) ^ (lane >> 2);
-    const uint4 u = lds128(tok + 1024 * j + 16 * chunk), v = lds128(tok + 1024 * j + 16 * (chunk ^ 4));
+    const uint32_t chunk = (lane & 3) ^ ((tok >> 7) & 7), at = tok + 8 * token_pitch * j;
+    const uint4 u = lds128(at + 16 * chunk), v = lds128(at + 16 * (chunk ^ 4));
     const uint32_t b[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int q = 0; q < kGroups; ++q) {
@@ -187,6 +187,12 @@ MOE_DEV void wide_half(uint32_t w, uint32_t row_tile, uint32_t tok, int half, in
   }
 }
 
+// The tokens of a stage as one box [token][64 columns]; otherwise [64 columns][token], a box
+// each, where 64 does not divide K (the first would reach into the next token) or the boxes are
+// few (8 tokens x 4096 x 7168, eight slices: 7.0 us as one, 7.8 as 16; x 7168 x 2048, two
+// slices: 5.1 as one, 5.0 as four: two tokens then share banks).
+__host__ __device__ __forceinline__ bool wide_whole(int K, int slices) { return K % 64 == 0 && slices >= 4; }
+
 template <int GROUP, int NT>
 __global__ void __launch_bounds__(kWideThreads, 1) matvec_wide_kernel(const __grid_constant__ MatvecArgs A) {
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -197,6 +203,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) matvec_wide_kernel(const __gr
   const int tiles = (A.N + 15) / 16, items = (tiles + RT - 1) / RT, KT = (A.K + 127) / 128, steps = (KT + KS - 1) / KS;
   constexpr uint32_t kRedAt = 256, kBox = NT * 8 * 128;   // a box of tokens: 64 columns of NT * 8, those past T zeros
   const uint32_t row_tile = KS * kTile, tok = (RT * row_tile + 1023) & ~1023u;
+  const bool whole = wide_whole(A.K, KS);
+  const uint32_t token_pitch = whole ? 2 * KS * 128 : 128, half_pitch = whole ? 128 : kBox;
   float4* red = reinterpret_cast<float4*>(sm + kRedAt);   // [warp][row tile][lane]
   FewRing ring = few_ring(sm, kRedAt + kFewWarps * 2 * 512, A.smem_bytes, tok + 2 * KS * kBox);
   grid_launch_next();
@@ -215,7 +223,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) matvec_wide_kernel(const __gr
         if (lane == 0) mbar_arrive_expect_tx(ring.full_bar(), 16 * kTile + 2 * KS * kBox);
         __syncwarp();
         if (lane == 0) tma_load_3d_once(ring.stage(), &A.map_w, 0, s * KS, item * RT, ring.full_bar());
-        if (lane < 2 * KS) tma_load_2d(ring.stage() + tok + lane * kBox, &A.map_x, (2 * s * KS + lane) * 64, 0, ring.full_bar());
+        if (whole) {
+          if (lane == 0) tma_load_3d(ring.stage() + tok, &A.map_x, 0, 2 * s * KS, 0, ring.full_bar());
+        } else if (lane < 2 * KS) tma_load_2d(ring.stage() + tok + lane * kBox, &A.map_x, (2 * s * KS + lane) * 64, 0, ring.full_bar());
         ring.next();
         ++issued;
       }
@@ -234,9 +244,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) matvec_wide_kernel(const __gr
       if (!ok) break;
       if (s * KS + slice < KT && 2 * group < nrt) {
         const uint32_t w = ring.stage() + 2 * group * row_tile + slice * kTile;
-        const uint32_t t = ring.stage() + tok + 2 * slice * kBox + (lane >> 2) * 128;
-        wide_half<GROUP, NT>(w, row_tile, t, 0, lane, acc);
-        wide_half<GROUP, NT>(w, row_tile, t + kBox, 1, lane, acc);
+        const uint32_t t = ring.stage() + tok + 2 * slice * half_pitch + (lane >> 2) * token_pitch;
+        wide_half<GROUP, NT>(w, row_tile, t, token_pitch, 0, lane, acc);
+        wide_half<GROUP, NT>(w, row_tile, t + half_pitch, token_pitch, 1, lane, acc);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(ring.empty_bar());
@@ -300,11 +310,11 @@ int launch_matvec(const MatvecArgs& args, int nsm, cudaStream_t s) {
   const int tiles = (args.N + 15) / 16;
   const int KT = (args.K + 127) / 128, records = args.T * matvec_token_pitch(KT);
   // The records cost a block some 20 ns each; the other kernels take the tokens as they are.
-  // Groups of 128, few / other kernel: one token x 4096 x 7168 6.2 / 7.8 us, x 32768 x 7168
-  // 23.9 / 29.2; two x 4096 x 7168 (112 records) 7.4 / 7.9; three x 7168 x 2048 (48) 4.8 / 5.0, x
-  // 4096 x 4096 (96) 5.9 / 5.4, x 32768 x 7168 26.8 / 29.3; four x 2048 x 2048 (64) 3.4 / 3.7, x 4096 x 7168
-  // (224) 10 / 7.9; six x 2048 x 2048 (96) 4.3 / 3.7, x 32768 x 7168 31.3 / 29.2.
-  if (records <= kMatvecTokenRoom && (args.T <= 2 || (args.T <= 4 && (args.T * KT <= 64 || tiles > 4 * nsm)))) {
+  // Groups of 128, few / other kernel: one token x 4096 x 7168 6.2 / 6.9 us, x 32768 x 7168
+  // 23.9 / 29.2; two x 4096 x 4096 (64 records) 4.95 / 5.2, x 4096 x 7168 (112) 7.4 / 6.9; three x
+  // 32768 x 7168 26.8 / 29.3; four x 2048 x 2048 (64) 3.4 / 3.6, x 4096 x 7168 (224) 10 / 6.9;
+  // six x 2048 x 2048 (96) 4.3 / 3.6, x 32768 x 7168 31.3 / 29.2.
+  if (records <= kMatvecTokenRoom && (args.T == 1 || (args.T <= 4 && (args.T * KT <= 64 || tiles > 4 * nsm)))) {
     switch (few_row_tiles(tiles, nsm, records <= kMatvecTokenRoom / 2 ? 3 : 2)) {
       case 1: return launch_matvec_few<GROUP, 1>(args, nsm, s);
       case 2: return launch_matvec_few<GROUP, 2>(args, nsm, s);
@@ -322,10 +332,14 @@ int launch_matvec(const MatvecArgs& args, int nsm, cudaStream_t s) {
   constexpr int kTile = w4_tile_bytes(GROUP);
   const uint64_t wd[3] = {kTile / 8, (uint64_t)KT, (uint64_t)tiles}, ws[2] = {kTile, (uint64_t)KT * kTile};
   const uint32_t wb[3] = {kTile / 8, (uint32_t)a.slices, (uint32_t)rows};
-  const uint64_t xd[2] = {(uint64_t)a.K, (uint64_t)a.T}, xs[1] = {(uint64_t)a.K * 2};
-  const uint32_t xb[2] = {64, (uint32_t)nt * 8};
+  const bool whole = wide_whole(a.K, a.slices);
+  const uint64_t xd[3] = {64, (uint64_t)a.K / 64, (uint64_t)a.T}, xs[2] = {128, (uint64_t)a.K * 2};
+  const uint32_t xb[3] = {64, 2 * (uint32_t)a.slices, (uint32_t)nt * 8};
+  const uint64_t xd2[2] = {(uint64_t)a.K, (uint64_t)a.T}, xs2[1] = {(uint64_t)a.K * 2};
+  const uint32_t xb2[2] = {64, (uint32_t)nt * 8};
   if (!encode_few_map(&a.map_w, CU_TENSOR_MAP_DATA_TYPE_UINT64, CU_TENSOR_MAP_SWIZZLE_NONE, a.W, 3, wd, ws, wb) ||
-      !encode_few_map(&a.map_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.x, 2, xd, xs, xb))
+      !encode_few_map(&a.map_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.x, whole ? 3 : 2, whole ? xd : xd2, whole ? xs : xs2,
+                      whole ? xb : xb2))
     return MOE_ERR_CUDA;
   return nt == 1 ? few_launch(matvec_wide_kernel<GROUP, 1>, a, kWideThreads, blocks, false, s)
                  : few_launch(matvec_wide_kernel<GROUP, 2>, a, kWideThreads, blocks, false, s);

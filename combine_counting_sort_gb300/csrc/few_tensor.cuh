@@ -1,4 +1,4 @@
-// few_tensor.cuh: products of 3 to 64 tokens with one 4-bit matrix on the fifth-generation
+// few_tensor.cuh: products of 2 to 64 tokens with one 4-bit matrix on the fifth-generation
 // tensor cores.
 //
 // y[t][n] = sum over groups q of scale[n][q] * sum over the group's k of (code[n][k] - 8) * x[t][k].
