@@ -520,7 +520,7 @@ MOE_DEV void layer_products(const LayerArgs& A, unsigned char* sm, const FewTabl
               if (!wait(ring.full_bar(), ring.phase)) break;
 #pragma unroll
               for (int i = warp; i < F::kSlices; i += kFewWarps)
-                if (s * F::kSlices + i < FT) few_slice<GROUP, SP, RT2, 1>(ring.stage(), ring.stage() + sco, ring.stage() + tok + i * kTokenRecord, zero, lt, i, lane, acc);
+                if (s * F::kSlices + i < FT) few_slice<GROUP, SP, RT2, 1, true>(ring.stage(), ring.stage() + sco, ring.stage() + tok + i * kTokenRecord, zero, lt, i, lane, acc);
               arrive(ring.empty_bar());
             }
           }
@@ -571,7 +571,7 @@ MOE_DEV void layer_products(const LayerArgs& A, unsigned char* sm, const FewTabl
 //   sums of every token on chip, so the output is written once, without atomics,
 //   in a fixed order.
 // DIRECT (T <= 8): a token is a column of the down products, and its sums over all
-// experts stay in registers.  Otherwise the columns are a segment's tokens, and the
+// experts stay in registers (an expert adds to its own tokens' only).  Otherwise the columns are a segment's tokens, and the
 // segments' sums are added up in shared memory.
 template <int GROUP, int RT2, bool DIRECT>
 __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_constant__ LayerArgs A) {

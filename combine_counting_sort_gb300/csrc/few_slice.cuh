@@ -165,8 +165,9 @@ struct LaneTokens {
 // of these columns is at `tokens`; columns without a token read the zeros at `zero`.  The MMAs of the row tiles are chains of their own:
 // an MMA's result takes some 20 cycles, and with two warps to a scheduler little else
 // fills them.  A stage with fewer row tiles holds older ones in their place, whose
-// sums are not used.
-template <int GROUP, int SP, int RT, int NT>
+// sums are not used.  OWN: the sums of a column without a token stay as they are: they are
+// used, and zeros times weights that are infinite or NaN are NaN.
+template <int GROUP, int SP, int RT, int NT, bool OWN = false>
 MOE_DEV void few_slice(uint32_t st, uint32_t scales, uint32_t tokens, uint32_t zero, const LaneTokens<NT>& lt, int slice, int lane,
                        float (&acc)[RT][NT][4]) {
   using F = FewForm<GROUP, SP>;
@@ -239,7 +240,8 @@ MOE_DEV void few_slice(uint32_t st, uint32_t scales, uint32_t tokens, uint32_t z
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[rt][j][i] = fmaf(v[rt][j][i], xs[j][i & 1], acc[rt][j][i]);
+      for (int i = 0; i < 4; ++i)
+        if (!OWN || lt.x[j][i & 1] >= 0) acc[rt][j][i] = fmaf(v[rt][j][i], xs[j][i & 1], acc[rt][j][i]);
 }
 
 // A warp's sums of RT row tiles into the meeting place `red`: [row tile][warp][column].

@@ -461,7 +461,8 @@ int moe_matvec_w4(const uint16_t* x, int T, int K, const uint8_t* Wp, int N, int
  * Sums are fp32.  w * a, fp32, is rounded once for the second product's operands: to
  * f16's 11 bits behind a power of two shared by 128 values; what is below 2^-28
  * of the largest of the 128 loses bits.  Infinite and NaN values of x spoil that
- * token's out and no other's.  Where fewer than k of a token's logits are not NaN,
+ * token's out and no other's, and those of an expert's weights the out of its
+ * own tokens alone.  Where fewer than k of a token's logits are not NaN,
  * the slots left get the id 0x7fffffff and *status is MOE_ERR_EXPERT_ID.
  *   x        device bf16 [T, H].
  *   router   device bf16 [E, H], or NULL: topk_ids and topk_w are then inputs.
