@@ -36,9 +36,9 @@ struct LayerArgs {
   uint32_t smem_bytes;
 };
 
-// Bytes of the record that holds 128 values of a token as the layer's MMAs take
-// them: f16 values, the scale, the groups' sums, and 12 bytes of alignment.
-constexpr int kTokenRecord = 288;
+// Bytes of the record that holds 128 values of a token as the MMAs take them: f16
+// values, the scale, and 12 bytes of alignment.
+constexpr int kTokenRecord = 272;
 
 // A tensor map of up to three dimensions, innermost first; strides in bytes of dimensions 1 and 2.
 inline bool encode_few_map(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base, int rank,

@@ -1,25 +1,23 @@
 // few_slice.cuh: weights times tokens on a stage's slices.
 //
 // The products run on f16 MMAs with fp32 sums.  An e4m3 code is one of the f16
-// values (one conversion per two codes).  A 4-bit code takes one AND: the bits
-// 0x000c and 0x00c0 read as f16 are c * 2^-24 and 16 c * 2^-24 (f16 is linear from its
-// subnormals to the end of the first binade), so the four pairs of a word's
-// eight codes take four ANDs and a shift; token values that meet a code with
-// the 16 are divided by it, and the sums are multiplied by 2^24 at the end.  The 8
-// that every 4-bit code has too much is taken out of a group's sum: 8 times the
-// sum of the token's values there, which its record holds.
+// values (one conversion per two codes).  A pair of 4-bit codes takes an AND and a
+// multiply-add, and two pairs a shift: the bits 0x000c and 0x00c0 read as f16 are c * 2^-24 and
+// 16 c * 2^-24 (f16 is linear from its subnormals to the end of the first binade), of which
+// the multiply-add makes (c - 8) * 2^-9, exactly; the sums are multiplied by 2^9 at the
+// end.  (Taking the 8 out of a group's sum instead, as 8 times the sum of the token's values,
+// saves the multiply-adds but loses the low bits of that sum to a large value that
+// meets a weight of zero.)
 //
 // A token's 128 values share a power of two 2^e that brings their largest magnitude
-// into [2^14, 2^15): a bf16 value is then an f16 value as it is, down to 2^-28 of the
-// block's largest (2^-24 where divided by 16), and smaller ones are within 2^-35 of it,
-// below the rounding of an fp32 sum.  The layer's activations between its
-// products, fp32 values, are rounded to f16's 11 bits this way.
+// into [2^14, 2^15): a bf16 value is then an f16 value as it is, down to 2^-31 of the
+// block's largest, and smaller ones are within 2^-39 of that largest.  The layer's activations
+// between its products, fp32 values, are rounded to f16's 11 bits this way, those below
+// 2^-28 of the largest to within 2^-39 of it.
 //
 // What bounds it: memory.  Per tile of 16 x 128 weights a warp spends 40 ANDs and
-// shifts (4-bit) or 32 conversions (FP8), both at 64 lanes a clock, 8 MMAs per 8 tokens
-// and some 30 other instructions.  Widening 4-bit codes by the usual offset and
-// subtraction takes 88, FP8 codes to bf16 128, which is longer than the
-// tile's bytes take from memory.  A stage of 6 x 8 tiles of FP8 took 1150 cycles with the
+// shifts and 32 multiply-adds (4-bit) or 32 conversions (FP8), 8 MMAs per 8 tokens
+// and some 30 other instructions.  A stage of 6 x 8 tiles of FP8 took 1150 cycles with the
 // conversions as the compiler unpacks them, 640 as written here (a stage's bytes: 610).
 #pragma once
 
@@ -46,38 +44,26 @@ struct FewForm {
   static constexpr int kTokPitch = kSlices * kTokenRecord + 64;
   // arrivals that complete a stage: weights, tokens, and the lanes' scale copies
   static constexpr int kArrivals = kW4 ? 2 : 34;
-  static constexpr float kSumScale = kW4 ? 0x1p24f : 1.f;   // what the sums lack
+  static constexpr float kSumScale = kW4 ? 0x1p9f : 1.f;   // what the sums lack
 };
 // ---------------------------------------------------------------- token records
 
 // Four consecutive values v (columns 4 lane ..) of a warp's 128 into the record at
 // `rec`: the 16 bytes at 64 i + 16 t are the B operands that lane t of a column reads for
-// the MMAs 2i and 2i + 1.  4-bit: columns 32 i + 8 t .., the pairs that meet high nibbles
-// divided by 16.  FP8: columns 32 i + 4 t .. and 32 i + 16 + 4 t .., which ldmatrix gives
-// to lane t.
-// Behind the values: the scale, and (4-bit) -8 * 2^-24 times the sum of each group's values.
+// the MMAs 2i and 2i + 1.  4-bit: columns 32 i + 8 t ...  FP8: columns 32 i + 4 t .. and
+// 32 i + 16 + 4 t .., which ldmatrix gives to lane t.  Behind the values: the scale.
 template <int GROUP>
 MOE_DEV void put_record(const float (&v)[4], uint8_t* rec, int lane) {
-  constexpr bool kW4 = GROUP != 0;
   uint32_t big = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) big = max(big, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   big = __reduce_max_sync(0xffffffffu, big);
   const int e = max((int)(big >> 23) - 127 - 14, -125);
-  const float down = __uint_as_float((uint32_t)(127 - e) << 23), down2 = kW4 ? down * 0.0625f : down;
-  const __half2 a = __floats2half2_rn(v[0] * down, v[1] * down), b = __floats2half2_rn(v[2] * down2, v[3] * down2);
-  const int at = kW4 ? 8 * lane : 64 * (lane >> 3) + 16 * (lane & 3) + 8 * ((lane >> 2) & 1);
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+  const __half2 a = __floats2half2_rn(v[0] * down, v[1] * down), b = __floats2half2_rn(v[2] * down, v[3] * down);
+  const int at = GROUP != 0 ? 8 * lane : 64 * (lane >> 3) + 16 * (lane & 3) + 8 * ((lane >> 2) & 1);
   *reinterpret_cast<uint2*>(rec + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  float* tail = reinterpret_cast<float*>(rec + 256);
-  if (lane == 0) tail[0] = __uint_as_float((uint32_t)(127 + e) << 23);
-  if (kW4) {
-    const float2 fa = __half22float2(a), fb = __half22float2(b);
-    float sum = (fa.x + fa.y) + 16.f * (fb.x + fb.y);
-    constexpr int kLanes = (kW4 ? GROUP : 128) / 4;
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane % kLanes == 0) tail[1 + lane / kLanes] = -8.f * 0x1p-24f * sum;
-  }
+  if (lane == 0) *reinterpret_cast<float*>(rec + 256) = __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
 // ---------------------------------------------------------------- products
@@ -111,15 +97,20 @@ MOE_DEV void widen_e4m3(uint32_t codes, uint32_t& lo, uint32_t& hi) {
       : "=r"(lo), "=r"(hi) : "r"(codes));
 }
 
+// Two pairs of 4-bit codes, at the low and at the high nibbles of a word's lower bytes, as f16 (c - 8) * 2^-9:
+// c * 2^-24 times 2^15, 16 c * 2^-24 times 2^11, less 2^-6.
+MOE_DEV void widen_w4(uint32_t word, uint32_t& lo, uint32_t& hi) {
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(lo) : "r"(word & 0x000F000Fu), "r"(0x78007800u), "r"(0xA400A400u));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(hi) : "r"(word & 0x00F000F0u), "r"(0x68006800u), "r"(0xA400A400u));
+}
+
 // The A operand of MMA m of a slice.
 template <int GROUP>
 MOE_DEV void widen(const uint32_t (&c)[GROUP ? 8 : 16], int m, uint32_t (&a)[4]) {
   if constexpr (GROUP != 0) {
     const uint32_t l = c[m >> 1] >> (m & 1 ? 8 : 0), h = c[4 + (m >> 1)] >> (m & 1 ? 8 : 0);
-    a[0] = l & 0x000F000Fu;
-    a[1] = h & 0x000F000Fu;
-    a[2] = l & 0x00F000F0u;
-    a[3] = h & 0x00F000F0u;
+    widen_w4(l, a[0], a[2]);
+    widen_w4(h, a[1], a[3]);
   } else {
     widen_e4m3(c[m], a[0], a[2]);
     widen_e4m3(c[m + 8], a[1], a[3]);
@@ -173,7 +164,7 @@ MOE_DEV void few_slice(uint32_t st, uint32_t scales, uint32_t tokens, uint32_t z
   using F = FewForm<GROUP, SP>;
   constexpr int kCount = FewGroups<GROUP>::kCount, kMmas = 8 / kCount;
   uint32_t c[RT][GROUP ? 8 : 16], b[NT][16];
-  float s[RT][kCount][2], xs[NT][2], sums[NT][2][kCount];
+  float s[RT][kCount][2], xs[NT][2];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const uint32_t p = lt.b[j] < 0 ? zero : tokens + lt.b[j];
@@ -191,21 +182,7 @@ MOE_DEV void few_slice(uint32_t st, uint32_t scales, uint32_t tokens, uint32_t z
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t p = (lt.x[j][i] < 0 ? zero : tokens + lt.x[j][i]) + 256;
-      if (F::kW4) {
-        const uint4 v = lds128(p);
-        xs[j][i] = __uint_as_float(v.x);
-        sums[j][i][0] = __uint_as_float(v.y);
-        if (kCount > 1) sums[j][i][1 % kCount] = __uint_as_float(v.z);
-        if (kCount > 2) {
-          sums[j][i][2 % kCount] = __uint_as_float(v.w);
-          sums[j][i][3 % kCount] = lds_f32(p + 16);
-        }
-      } else {
-        xs[j][i] = lds_f32(p);
-      }
-    }
+    for (int i = 0; i < 2; ++i) xs[j][i] = lds_f32((lt.x[j][i] < 0 ? zero : tokens + lt.x[j][i]) + 256);
   float v[RT][NT][4];
 #pragma unroll
   for (int q = 0; q < kCount; ++q) {
@@ -230,10 +207,8 @@ MOE_DEV void few_slice(uint32_t st, uint32_t scales, uint32_t tokens, uint32_t z
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = F::kW4 ? part[rt][j][i] + sums[j][i & 1][q] : part[rt][j][i];
-          v[rt][j][i] = q == 0 ? p * s[rt][q][i >> 1] : fmaf(p, s[rt][q][i >> 1], v[rt][j][i]);
-        }
+        for (int i = 0; i < 4; ++i)
+          v[rt][j][i] = q == 0 ? part[rt][j][i] * s[rt][q][i >> 1] : fmaf(part[rt][j][i], s[rt][q][i >> 1], v[rt][j][i]);
   }
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)

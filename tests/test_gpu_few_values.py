@@ -1,9 +1,12 @@
 """The decoding operators on values where they can go wrong."""
+import numpy as np
 import pytest
 import torch
 
+import combine_counting_sort_gb300 as moe
+import oracle
 from tests.gpu_util import build
-from tests.test_gpu_few import Experts, rand_bits, routes
+from tests.test_gpu_few import Experts, bf16_t, f64, rand_bits, routes, status, w4_matrix, within
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +47,69 @@ def test_layer_weights_that_are_not_finite_reach_their_own_tokens_alone(group, h
     keep = [t for t in range(T) if t != 1]
     assert torch.equal(out[keep].view(torch.int16), clean[keep].view(torch.int16))
     assert not torch.isfinite(out[1]).all()
+
+
+# ---------------------------------------------------------------- large values that meet weights of zero
+
+def run_matvec(xb, Wp, N, group):
+    y, st = torch.full((len(xb), N), float("nan"), dtype=torch.bfloat16, device="cuda"), status()
+    moe.moe_matvec_w4(bf16_t(xb), Wp, group, y, st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    return y
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,N,K", [(1, 48, 1024), (1, 5000, 256), (2, 48, 2048), (4, 33, 512), (7, 48, 1024), (20, 48, 1024)])
+def test_matvec_large_values_on_zero_weights(T, N, K, group):
+    # some columns' weights are zero (code 8) and their values 2^20 of either sign: the bound is that of
+    # what the other columns add up to
+    b = rand_bits(1, N, K, seed=T + N, scale=K ** -0.5)
+    at = np.arange(5, K, 97)
+    b[..., at] = 0
+    q, s = oracle.quantize_w4(b, group)
+    assert np.all(q[..., at] == 8)
+    x = f64(rand_bits(T, K, seed=K))
+    x[:, at] = np.where(np.arange(len(at)) % 2, 1.0, -1.0) * 2.0 ** 20
+    xb = oracle.f64_to_bf16(x)
+    y = run_matvec(xb, torch.from_numpy(oracle.pack_w4(q, s)[0]).cuda(), N, group)
+    within(y, *oracle.matvec_bound(f64(xb), oracle.w4_values(q, s)[0]), "matvec")
+
+
+@pytest.mark.parametrize("T", [1, 4, 7, 20])
+def test_matvec_small_results(T):
+    # results near 2^-120, bf16's normal values end at 2^-126
+    N, K, group = 48, 512, 32
+    Wp, W = w4_matrix(N, K, group, seed=T, scale=2.0 ** -100)
+    xb = rand_bits(T, K, seed=T, scale=2.0 ** -24)
+    within(run_matvec(xb, Wp, N, group), *oracle.matvec_bound(f64(xb), W), "matvec")
+
+
+def experts_of(b1, b2, group):
+    ex = Experts.__new__(Experts)
+    ex.E, ex.H, ex.F, ex.group, ex.W1_scale, ex.W2_scale = b1.shape[0], b1.shape[2], b2.shape[2], group, None, None
+    (q1, s1), (q2, s2) = oracle.quantize_w4(b1, group), oracle.quantize_w4(b2, group)
+    ex.W1, ex.W2 = (torch.from_numpy(oracle.pack_w4(*v)).cuda() for v in ((q1, s1), (q2, s2)))
+    ex.values = {e: (oracle.w4_values(q1[e], s1[e]), oracle.w4_values(q2[e], s2[e])) for e in range(ex.E)}
+    return ex
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T", [1, 6, 12, 40])
+def test_layer_large_values_on_zero_weights(T, group):
+    # columns of x at 2^20 whose gate and up weights are zero; features whose activations are 2^20
+    # times the others' and whose down weights are zero
+    E, k, H, F = 4, 2, 512, 256
+    b1, b2 = rand_bits(E, 2 * F, H, seed=1, scale=H ** -0.5), rand_bits(E, H, F, seed=2, scale=F ** -0.5)
+    at, feature = np.arange(3, H, 61), np.arange(7, F, 71)
+    b1[..., at] = 0
+    up = f64(b1)
+    up[:, F + feature] *= 2.0 ** 20
+    b1, b2[..., feature] = oracle.f64_to_bf16(up), 0
+    ex = experts_of(b1, b2, group)
+    x = f64(rand_bits(T, H, seed=T))
+    x[:, at] = np.where(np.arange(len(at)) % 2, 1.0, -1.0) * 2.0 ** 20
+    xb = oracle.f64_to_bf16(x)
+    ids, w = routes(T, k, E, seed=T)
+    out, _, _ = ex.run(xb, ids, w)
+    within(out, *oracle.layer_few(f64(xb), ids, w, ex.values), "layer")
