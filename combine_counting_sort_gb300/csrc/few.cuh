@@ -17,15 +17,14 @@
 #pragma once
 
 #include "common.cuh"
+#include "few_plan.h"
 #include "w4.cuh"
 
 namespace moe {
 
-constexpr int kFewWarps = 8;                       // computing warps, one per 128-column slice of a stage
 constexpr int kFewFinish = 3;                      // finishing warps
 constexpr int kFewAllWarps = kFewWarps + 1 + kFewFinish, kFewThreads = kFewAllWarps * 32;
 constexpr int kFewFinishThreads = 32 * kFewFinish;
-constexpr int kFewMaxStages = 12;
 constexpr uint64_t kFewTimeoutNs = 1000000000ull;  // bound of every wait
 
 // Untiled bulk copy global -> shared (16-byte aligned, size a multiple of 16).
@@ -208,10 +207,6 @@ MOE_DEV void drain(FewRing r, int issued, int partial, int lane) {
 
 // ---------------------------------------------------------------- sums over the warps
 
-// A warp's sums of one row tile: column c of rows 0..15 lies at 24 c floats of the
-// warp's part, so that neither the lanes' stores nor the reads along the rows meet
-// in a bank.
-constexpr int kFewColPitch = 24;
 // The sum over the warps, in their order.
 MOE_DEV float get_sum(const float* red, int pitch, int row, int col) {
   float s = 0.f;

@@ -1,11 +1,10 @@
 // few_host.h: arguments of the decoding kernels and their launches per weight form.
 #pragma once
 
+#include "few_plan.h"
 #include "host_util.h"
 
 namespace moe {
-
-constexpr int kFewMinSmem = 227 * 1024;   // room for a ring beside the largest tables
 
 struct MatvecArgs {
   CUtensorMap map_w, map_x;   // wide and tensor kernels: whole tiles, and 64 columns of all tokens
@@ -33,12 +32,9 @@ struct LayerArgs {
   int32_t* status;
   int T, H, E, k, F;
   int splits;          // runs of columns of the logits
+  int cols;            // tokens of a segment, at most
   uint32_t smem_bytes;
 };
-
-// Bytes of the record that holds 128 values of a token as the MMAs take them: f16
-// values, the scale, and 12 bytes of alignment.
-constexpr int kTokenRecord = 272;
 
 // A tensor map of up to three dimensions, innermost first; strides in bytes of dimensions 1 and 2.
 inline bool encode_few_map(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base, int rank,
@@ -74,7 +70,7 @@ int few_launch(Kernel kernel, Args& a, int threads, int blocks, bool cooperative
   int dev = 0, smem = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   if (cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) return MOE_ERR_CUDA;
-  if (smem < kFewMinSmem) return MOE_ERR_UNSUPPORTED;
+  if (smem < (int)kFewMinSmem) return MOE_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return MOE_ERR_CUDA;
   auto args = a;
   args.smem_bytes = smem;

@@ -18,7 +18,6 @@
 
 namespace moe {
 
-constexpr int kLayerCols = 16;                  // tokens per pass over a stage
 constexpr int kFewOwnTopk = 2 * kFewAllWarps;   // tokens whose routes every block selects for itself
 
 // ---------------------------------------------------------------- copies
@@ -68,7 +67,7 @@ MOE_DEV void copy_tokens(RecordOf record_of, int cols, int kt0, int nk, uint32_t
 // ---------------------------------------------------------------- routes
 
 // Tables of the routes in shared memory, sized by the P = T k pairs.  A segment is
-// one expert and as many of the tokens routed to it as a stage has room for; row r of the activations
+// one expert and up to A.cols of the tokens routed to it; row r of the activations
 // belongs to one (token, expert).
 struct FewTables {
   uint64_t* seg_mask;
@@ -148,7 +147,6 @@ MOE_DEV void few_meet(const LayerArgs& A, int counter, FewShared* sh, int tid) {
 
 // The tables of at most 32 pairs, by one warp: lane p is pair p, the lowest lane of those
 // with the same expert makes its segment.
-template <int MAXCOLS>
 MOE_DEV void few_tables_small(const LayerArgs& A, FewShared* sh, const FewTables& tb, const int* ids, const float* w, int lane) {
   const int P = A.T * A.k, t = lane / A.k;
   const int e = lane < P ? ids[lane] : -1;
@@ -169,7 +167,7 @@ MOE_DEV void few_tables_small(const LayerArgs& A, FewShared* sh, const FewTables
     }
   }
   const bool leads = on && lane == __ffs(same) - 1;
-  const int c = leads ? __popc(tokens) : 0, s = (c + MAXCOLS - 1) / MAXCOLS;
+  const int c = leads ? __popc(tokens) : 0, s = (c + A.cols - 1) / A.cols;
   int incl = c | s << 16;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -182,9 +180,9 @@ MOE_DEV void few_tables_small(const LayerArgs& A, FewShared* sh, const FewTables
   if (leads) {
     for (uint32_t m = tokens; m;) {
       uint32_t take = m;
-      if (__popc(m) > MAXCOLS) {
+      if (__popc(m) > A.cols) {
         take = 0;
-        for (int b = 0; b < MAXCOLS; ++b) take |= (m ^ take) & (~(m ^ take) + 1);   // the lowest bit left
+        for (int b = 0; b < A.cols; ++b) take |= (m ^ take) & (~(m ^ take) + 1);   // the lowest bit left
       }
       m ^= take;
       tb.seg_mask[seg] = take;
@@ -201,18 +199,17 @@ MOE_DEV void few_tables_small(const LayerArgs& A, FewShared* sh, const FewTables
   if (lane == 0) {
     sh->rows = all & 0xFFFF;
     sh->segs = all >> 16;
-    sh->cap = max(1, min(most, MAXCOLS));
+    sh->cap = max(1, min(most, A.cols));
   }
 }
 
 // The tables from the pairs' ids and weights (in shared memory).  scratch: E masks,
 // E first rows, a count per warp.
-template <int MAXCOLS>
 MOE_DEV void few_tables(const LayerArgs& A, FewShared* sh, const FewTables& tb, const int* ids, const float* w,
                         unsigned char* scratch, int tid, int warp, int lane) {
   const int P = A.T * A.k;
   if (P <= 32) {   // 0.4 us, and 1.7 us the other way
-    if (warp == 0) few_tables_small<MAXCOLS>(A, sh, tb, ids, w, lane);
+    if (warp == 0) few_tables_small(A, sh, tb, ids, w, lane);
     return;
   }
   uint64_t* mask = reinterpret_cast<uint64_t*>(scratch);
@@ -238,7 +235,7 @@ MOE_DEV void few_tables(const LayerArgs& A, FewShared* sh, const FewTables& tb, 
   for (int i = 0; i < 4; ++i) {
     m4[i] = 4 * tid + i < A.E ? mask[4 * tid + i] : 0;
     const int c = __popcll(m4[i]);
-    counts += c | ((c + MAXCOLS - 1) / MAXCOLS) << 16;
+    counts += c | ((c + A.cols - 1) / A.cols) << 16;
     most = max(most, c);
   }
   int incl = counts;
@@ -249,7 +246,7 @@ MOE_DEV void few_tables(const LayerArgs& A, FewShared* sh, const FewTables& tb, 
   }
   most = __reduce_max_sync(0xffffffffu, most);
   if (lane == 31) totals[warp] = incl;
-  if (lane == 0 && most > 1) atomicMax(&sh->cap, min(most, MAXCOLS));
+  if (lane == 0 && most > 1) atomicMax(&sh->cap, min(most, A.cols));
   __syncthreads();
   int at = incl - counts;
   for (int i = 0; i < warp; ++i) at += totals[i];
@@ -260,9 +257,9 @@ MOE_DEV void few_tables(const LayerArgs& A, FewShared* sh, const FewTables& tb, 
     if (4 * tid + i < A.E) first[4 * tid + i] = row;
     while (m) {
       uint64_t take = m;
-      if (__popcll(m) > MAXCOLS) {
+      if (__popcll(m) > A.cols) {
         take = 0;
-        for (int b = 0; b < MAXCOLS; ++b) take |= (m ^ take) & (~(m ^ take) + 1);   // the lowest bit left
+        for (int b = 0; b < A.cols; ++b) take |= (m ^ take) & (~(m ^ take) + 1);   // the lowest bit left
       }
       m ^= take;
       tb.seg_mask[seg] = take;
@@ -307,26 +304,17 @@ template <int GROUP, int RT2, bool DIRECT, int SP>
 MOE_DEV void layer_products(const LayerArgs& A, unsigned char* sm, const FewTables& tb, uint32_t after_tables, uint32_t zero, int tid,
                             int warp, int lane) {
   using F = FewForm<GROUP, SP>;
-  // Gate and up row tiles of a stage, two of each where its slices are few and the tokens many:
-  // these then serve twice the weights.
-  constexpr int kPairs = GROUP != 0 && !DIRECT && SP == 1 ? 2 : 1;
-  constexpr int kRT = RT2 > 2 * kPairs ? RT2 : 2 * kPairs;
+  constexpr int kPairs = layer_pairs(GROUP, SP, DIRECT);   // gate and up row tiles of a stage
   FewShared* sh = reinterpret_cast<FewShared*>(sm);
   const int HT = A.H / 128, FT = A.F / 128;
   const int segs = sh->segs, cap = sh->cap;
-  // The sums on their way to the finishing warps: gate and up two buffers where the columns
-  // are few.  Down: DIRECT one, [row tile][warp][token]; else those, and the output's
-  // sums [T][16 RT2].
-  constexpr int kSumTiles = DIRECT || RT2 < 2 ? 2 : RT2;
-  const int bufs = DIRECT || cap <= 8 ? 2 : 1;
-  const uint32_t buf_bytes = kFewWarps * kSumTiles * cap * kFewColPitch * 4;
-  const uint32_t sums_bytes = DIRECT ? max(bufs * buf_bytes, kFewWarps * RT2 * A.T * kFewColPitch * 4) : bufs * buf_bytes;
-  FewRing way = few_sums_ring(sm, after_tables, buf_bytes, bufs);
-  float* sums = reinterpret_cast<float*>(sm + after_tables + sums_bytes);
-  constexpr uint32_t tok = kRT * F::kRowTile;
-  const uint32_t sco = tok + cap * F::kTokPitch;
-  FewRing ring = few_ring(sm, after_tables + sums_bytes + (DIRECT ? 0 : A.T * 16 * RT2 * 4), A.smem_bytes,
-                          (sco + kRT * F::kScaleBytes + F::kAlign - 1) & ~(F::kAlign - 1));
+  // The sums on their way to the finishing warps.  Down: DIRECT one buffer,
+  // [row tile][warp][token]; else as gate and up, and the output's sums [T][16 RT2].
+  const LayerRoom room = layer_room(GROUP, SP, RT2, DIRECT, A.T, A.T * A.k, cap, A.smem_bytes);
+  FewRing way = few_sums_ring(sm, after_tables, room.buf, room.bufs);
+  float* sums = reinterpret_cast<float*>(sm + after_tables + room.sums);
+  const uint32_t tok = room.tok, sco = room.scale;
+  FewRing ring = few_ring(sm, after_tables + room.sums + room.out, A.smem_bytes, room.stage);
   const int fitems = A.F / (16 * kPairs), items1 = segs * fitems, steps1 = (HT + F::kSlices - 1) / F::kSlices;
   const int htiles = A.H / 16, items2 = (htiles + RT2 - 1) / RT2, steps2 = (FT + F::kSlices - 1) / F::kSlices;
 
@@ -579,9 +567,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
   FewShared* sh = reinterpret_cast<FewShared*>(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int P = A.T * A.k, HT = A.H / 128;
-  constexpr uint32_t kZeroAt = 256, kTablesAt = kZeroAt + (kTokenRecord + 15) / 16 * 16;
   const FewTables tb(sm + kTablesAt, P);
-  const uint32_t after_tables = (kTablesAt + P * 21 + 127) & ~127;
+  const uint32_t after_tables = few_tables_end(P);
   const uint32_t zero = smem_u32(sm) + kZeroAt;
   unsigned char* scratch = sm + after_tables;   // until the ring takes it
   int* ids = reinterpret_cast<int*>(scratch);
@@ -628,14 +615,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
     }
   }
   __syncthreads();
-  few_tables<kLayerCols>(A, sh, tb, ids, w, scratch2, tid, warp, lane);
+  few_tables(A, sh, tb, ids, w, scratch2, tid, warp, lane);
   fence_proxy_async_shared();   // the ring's copies overwrite the scratch
   __syncthreads();
 
-  // 4-bit stages are short of work: handing one over takes some 300 cycles of a warp's 900.
-  // Two slices per warp halve that where no expert has more than 8 tokens, whose
-  // records would not leave room for a second stage.
-  if (GROUP != 0 && (DIRECT || sh->cap <= 8))
+  if (layer_slices(GROUP, RT2, DIRECT, A.T, P, sh->cap, A.smem_bytes) == 2)
     layer_products<GROUP, RT2, DIRECT, GROUP != 0 ? 2 : 1>(A, sm, tb, after_tables, zero, tid, warp, lane);
   else if (GROUP == 0 || !DIRECT)
     layer_products<GROUP, RT2, DIRECT, 1>(A, sm, tb, after_tables, zero, tid, warp, lane);
@@ -648,7 +632,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) layer_few_kernel(const __grid_
 }
 
 template <int GROUP, int RT2>
-int launch_layer_rt(const LayerArgs& a, int nsm, cudaStream_t s) {
+int launch_layer_rt(const LayerArgs& args, int nsm, cudaStream_t s) {
+  LayerArgs a = args;
+  a.cols = layer_cols(GROUP, RT2, a.T <= 8, a.T, a.T * a.k, kFewMinSmem);
   return a.T <= 8 ? few_launch(layer_few_kernel<GROUP, RT2, true>, a, kFewThreads, nsm, true, s)
                   : few_launch(layer_few_kernel<GROUP, RT2, false>, a, kFewThreads, nsm, true, s);
 }

@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) matvec_few_kernel(const __grid
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tiles = (A.N + 15) / 16, items = (tiles + RT - 1) / RT;
   const int KT = (A.K + 127) / 128, steps = (KT + F::kSlices - 1) / F::kSlices, pitch = matvec_token_pitch(KT);
-  constexpr uint32_t kZeroAt = 256, kTokensAt = kZeroAt + kTokenRecord;
+  constexpr uint32_t kTokensAt = kZeroAt + kTokenRecord;
   const uint32_t zero = smem_u32(sm) + kZeroAt, tokens = smem_u32(sm) + kTokensAt;
   const int tile_floats = kFewWarps * A.T * kFewColPitch;
   const uint32_t sums_at = kTokensAt + A.T * pitch;

@@ -32,16 +32,12 @@ namespace moe {
 template <int GROUP, int SP>
 struct FewForm {
   static constexpr bool kW4 = GROUP != 0;
-  static constexpr int kTile = w4_tile_bytes(kW4 ? GROUP : 128);
+  static constexpr int kTile = few_tile_bytes(GROUP);
   static constexpr int kSlices = kFewWarps * SP;
   // 4-bit: the slices' tiles as they lie in memory.  FP8: per slice 16 rows of
   // 128 bytes in TMA's 128-byte swizzle, which ldmatrix reads without bank conflicts.
-  static constexpr int kRowTile = kSlices * (kW4 ? kTile : 2048);
-  static constexpr int kAlign = kW4 ? 128 : 1024;           // of a stage
-  static constexpr int kScaleBytes = kW4 ? 0 : 4 * kSlices; // per row tile
-  // A token's records in a stage, 64 mod 128 bytes apart: the 2 tokens x 64 bytes of a
-  // quarter-warp's reads fall on distinct banks.
-  static constexpr int kTokPitch = kSlices * kTokenRecord + 64;
+  static constexpr int kRowTile = kSlices * kTile;
+  static constexpr int kTokPitch = few_token_pitch(kSlices);
   // arrivals that complete a stage: weights, tokens, and the lanes' scale copies
   static constexpr int kArrivals = kW4 ? 2 : 34;
   static constexpr float kSumScale = kW4 ? 0x1p9f : 1.f;   // what the sums lack

@@ -1,0 +1,59 @@
+"""The decoding layer's division of shared memory (csrc/few_plan.h): every call
+that is accepted leaves its ring two stages, within what a block has."""
+import os
+import subprocess
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+PROBE = r"""
+#include <stdio.h>
+#include "few_plan.h"
+using namespace moe;
+// every batch, number of pairs, form and fullest segment: one line for each that has fewer than two
+// stages or leaves the block's shared memory, and the counts
+int main() {
+  long calls = 0, fewer = 0, two_slices = 0;
+  int fewer_least = 1 << 30;
+  const int groups[4] = {0, 32, 64, 128};
+  for (int g : groups)
+    for (int rt2 = 1; rt2 <= 3; ++rt2)
+      for (int T = 1; T <= 64; ++T)
+        for (int k = 1; k <= 32 && T * k <= 1024; ++k) {
+          const bool direct = T <= 8;
+          const int P = T * k, cols = layer_cols(g, rt2, direct, T, P, kFewMinSmem);
+          if (cols < kLayerCols) {
+            ++fewer;
+            if (P < fewer_least) fewer_least = P;
+            if (cols < 12 || g != 0 || rt2 != 3) printf("narrow %d %d %d %d: %d\n", g, rt2, T, k, cols);
+          }
+          for (int cap = 1; cap <= (T < cols ? T : cols); ++cap) {
+            const int sp = layer_slices(g, rt2, direct, T, P, cap, kFewMinSmem);
+            const LayerRoom r = layer_room(g, sp, rt2, direct, T, P, cap, kFewMinSmem);
+            const int gate_up = 2 * layer_pairs(g, sp, direct), rt = rt2 > gate_up ? rt2 : gate_up;
+            const uint32_t weights = rt * 8 * sp * (g ? 1024 + 4096 / g : 2048), records = cap * (8 * sp * kTokenRecord + 64);
+            const uint32_t ring = (few_tables_end(P) + r.sums + r.out + 1023) / 1024 * 1024;
+            const bool fits = r.stage >= weights + records + (g ? 0 : 32 * rt) && ring + r.stages * r.stage <= kFewMinSmem &&
+                              r.sums >= r.bufs * r.buf && r.buf >= (uint32_t)(8 * (direct ? 2 : rt2) * cap * kFewColPitch * 4) &&
+                              (!direct || r.sums >= (uint32_t)(8 * rt2 * T * kFewColPitch * 4)) && few_tables_end(P) >= kTablesAt + 21 * P;
+            if (r.stages < 2 || !fits) printf("call %d %d %d %d cap %d: %d stages, fits %d\n", g, rt2, T, k, cap, r.stages, (int)fits);
+            ++calls;
+            two_slices += sp == 2;
+          }
+        }
+  printf("counts %ld %ld %d %ld\n", calls, fewer, fewer_least, two_slices);
+  return 0;
+}
+"""
+
+
+def test_every_call_leaves_the_ring_two_stages(tmp_path):
+    src, exe = tmp_path / "probe.cpp", tmp_path / "probe"
+    src.write_text(PROBE)
+    csrc = os.path.join(ROOT, "combine_counting_sort_gb300", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", csrc, str(src), "-o", str(exe)], check=True)
+    lines = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.splitlines()
+    assert len(lines) == 1, lines[:20]
+    calls, fewer, least, two_slices = (int(v) for v in lines[0].split()[1:])
+    assert calls > 100000 and two_slices > 10000
+    # segments of fewer than 16 tokens for FP8 with three row tiles and many pairs alone
+    assert fewer > 0 and least >= 700

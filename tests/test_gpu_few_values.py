@@ -1,4 +1,4 @@
-"""The decoding operators on values where they can go wrong."""
+"""The decoding operators on values and sizes where they can go wrong."""
 import numpy as np
 import pytest
 import torch
@@ -111,5 +111,45 @@ def test_layer_large_values_on_zero_weights(T, group):
     x[:, at] = np.where(np.arange(len(at)) % 2, 1.0, -1.0) * 2.0 ** 20
     xb = oracle.f64_to_bf16(x)
     ids, w = routes(T, k, E, seed=T)
+    out, _, _ = ex.run(xb, ids, w)
+    within(out, *oracle.layer_few(f64(xb), ids, w, ex.values), "layer")
+
+
+# ---------------------------------------------------------------- row tiles of a down item, fullest segments
+
+def capped_routes(T, k, E, cap, seed):
+    """Routes of which expert 0 has exactly `cap` tokens and no other more."""
+    rng = np.random.default_rng(seed)
+    ids, left = np.zeros((T, k), np.int32), np.full(E, cap)
+    ids[:], at = -1, rng.permutation(T)
+    ids[at[:cap], 0] = 0
+    for t in range(T):
+        free = [j for j in range(k) if ids[t, j] < 0]
+        order = 1 + np.argsort(-left[1:] + rng.random(E - 1))[:len(free)]
+        assert np.all(left[order] > 0)
+        left[order] -= 1
+        ids[t, free] = order
+    assert np.bincount(ids.ravel(), minlength=E).max() == cap
+    return ids, (rng.random((T, k)) + 0.1).astype(np.float32)
+
+
+_experts = {}
+
+
+def experts(E, H, F, group):
+    if (E, H, F, group) not in _experts:
+        _experts.clear()
+        _experts[E, H, F, group] = Experts(E, H, F, group, seed=11)
+    return _experts[E, H, F, group]
+
+
+@pytest.mark.parametrize("T,cap", [(57, 16), (64, 25)])
+def test_layer_narrow_segments(T, cap):
+    # FP8 weights, three row tiles and about 1000 pairs: segments of fewer than 16 tokens
+    E, k, H, F = 48, 16, 7168, 128
+    ex = experts(E, H, F, 0)
+    ids, w = capped_routes(T, k, E, cap, seed=T) if cap == 25 else capped_routes(T, 16, 64, cap, seed=T)
+    ids = np.where(ids >= E, -1, ids)
+    xb = rand_bits(T, H, seed=T)
     out, _, _ = ex.run(xb, ids, w)
     within(out, *oracle.layer_few(f64(xb), ids, w, ex.values), "layer")
