@@ -89,4 +89,15 @@ MOE_PLAN int layer_cols(int group, int rt2, bool direct, int T, int pairs, uint3
   return cols;
 }
 
+// The tensor kernel's warps (few_tensor.cuh): 0-15 widen, 16-23 sum, 24 copies, 25 and 26 issue
+// MMAs, 27 makes up a warpgroup; their registers by setmaxnreg.  Its inc draws on what the block was
+// launched with and waits for it without end, so a kernel with fewer registers a thread
+// than the split needs (72) must not be launched.
+constexpr int kTensorSum = 16, kTensorCopy = 24, kTensorMma = 25, kTensorWarps = 28;
+constexpr int kTensorWidenRegs = 56, kTensorSumRegs = 120, kTensorRestRegs = 40;
+MOE_PLAN bool tensor_split_fits(int regs) {
+  return kTensorSum * kTensorWidenRegs + (kTensorCopy - kTensorSum) * kTensorSumRegs + (kTensorWarps - kTensorCopy) * kTensorRestRegs <=
+         kTensorWarps * regs;
+}
+
 }  // namespace moe

@@ -33,9 +33,8 @@
 namespace moe {
 
 constexpr int kTensorRows = 256;   // of a block
-// Warps 0-15 widen, 16-23 sum, 24 copies, 25 and 26 issue MMAs; registers by setmaxnreg,
-// 28 x 72 at launch = 16 x 56 + 8 x 120 + 4 x 40.
-constexpr int kTensorSum = 16, kTensorCopy = 24, kTensorMma = 25, kTensorThreads = 28 * 32;
+constexpr int kTensorThreads = kTensorWarps * 32;
+static_assert(tensor_split_fits(65536 / kTensorThreads / 8 * 8), "register split exceeds launch");
 
 // 16 TMEM columns of this thread's lane; complete behind the next tmem_got of the same registers.
 MOE_DEV void tmem_get(uint32_t taddr, float (&v)[16]) {
@@ -157,7 +156,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) matvec_tensor_kernel(const 
     tc_fence_after();
   };
 
-  if (warp >= kTensorCopy) regs_dealloc<40>();
+  if (warp >= kTensorCopy) regs_dealloc<kTensorRestRegs>();
   if (warp == kTensorCopy) {
     int issued = 0;
     bool ok = true;
@@ -217,7 +216,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) matvec_tensor_kernel(const 
     meet();
     if (warp == kTensorMma) tmem_dealloc(tmem, 512);
   } else if (warp < kTensorSum) {
-    regs_dealloc<56>();
+    regs_dealloc<kTensorWidenRegs>();
     const uint32_t at = tile + (lane & 15) * 64;
     const int rot = (lane >> 1) & 3;   // the row's four 16-byte chunks in an order without bank conflicts
     uint32_t w[4][4];                  // [chunk t][word j]: columns 32 j + 8 t ..
@@ -265,7 +264,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) matvec_tensor_kernel(const 
     }
     meet();
   } else {
-    regs_alloc<120>();
+    regs_alloc<kTensorSumRegs>();
     float acc[kN];
     const uint32_t d_full = smem_u32(ts->d_full + block * kUnits), d_empty = smem_u32(ts->d_empty + block * kUnits);
     const uint32_t sums = tmem + ((uint32_t)(32 * quad) << 16) + kSums + block * kUnits * kPitch;
@@ -349,6 +348,16 @@ inline int tensor_cluster(int items, int KT, int nsm) {
   return c;
 }
 
+template <int GROUP, int NT>
+int launch_tensor_nt(const MatvecArgs& a, int blocks, cudaStream_t s) {
+  static const bool split_ok = [] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, matvec_tensor_kernel<GROUP, NT>) == cudaSuccess && tensor_split_fits(f.numRegs);
+  }();
+  if (!split_ok) return MOE_ERR_UNSUPPORTED;
+  return few_launch(matvec_tensor_kernel<GROUP, NT>, a, kTensorThreads, blocks, false, s, a.slices);
+}
+
 template <int GROUP>
 int launch_matvec_tensor(const MatvecArgs& args, int nsm, cudaStream_t s) {
   MatvecArgs a = args;
@@ -364,10 +373,10 @@ int launch_matvec_tensor(const MatvecArgs& args, int nsm, cudaStream_t s) {
       !encode_few_map(&a.map_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.x, 2, xd, xs, xb))
     return MOE_ERR_CUDA;
   switch (nt) {
-    case 2: return few_launch(matvec_tensor_kernel<GROUP, 2>, a, kTensorThreads, blocks, false, s, a.slices);
-    case 4: return few_launch(matvec_tensor_kernel<GROUP, 4>, a, kTensorThreads, blocks, false, s, a.slices);
-    case 6: return few_launch(matvec_tensor_kernel<GROUP, 6>, a, kTensorThreads, blocks, false, s, a.slices);
-    default: return few_launch(matvec_tensor_kernel<GROUP, 8>, a, kTensorThreads, blocks, false, s, a.slices);
+    case 2: return launch_tensor_nt<GROUP, 2>(a, blocks, s);
+    case 4: return launch_tensor_nt<GROUP, 4>(a, blocks, s);
+    case 6: return launch_tensor_nt<GROUP, 6>(a, blocks, s);
+    default: return launch_tensor_nt<GROUP, 8>(a, blocks, s);
   }
 }
 

@@ -1,5 +1,4 @@
-"""The decoding layer's division of shared memory (csrc/few_plan.h): every call
-that is accepted leaves its ring two stages, within what a block has."""
+"""The decoding kernels' divisions of shared memory and registers (csrc/few_plan.h)."""
 import os
 import subprocess
 
@@ -46,14 +45,31 @@ int main() {
 """
 
 
-def test_every_call_leaves_the_ring_two_stages(tmp_path):
+def run(tmp_path, text):
     src, exe = tmp_path / "probe.cpp", tmp_path / "probe"
-    src.write_text(PROBE)
+    src.write_text(text)
     csrc = os.path.join(ROOT, "combine_counting_sort_gb300", "csrc")
     subprocess.run(["g++", "-std=c++17", "-O1", "-I", csrc, str(src), "-o", str(exe)], check=True)
-    lines = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.splitlines()
+    return subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.splitlines()
+
+
+def test_every_call_leaves_the_ring_two_stages(tmp_path):
+    lines = run(tmp_path, PROBE)
     assert len(lines) == 1, lines[:20]
     calls, fewer, least, two_slices = (int(v) for v in lines[0].split()[1:])
     assert calls > 100000 and two_slices > 10000
     # segments of fewer than 16 tokens for FP8 with three row tiles and many pairs alone
     assert fewer > 0 and least >= 700
+
+
+def test_a_kernel_with_too_few_registers_for_the_split_is_refused(tmp_path):
+    # 16 x 56 + 8 x 120 + 4 x 40 warps x registers = 28 x 72
+    text = """
+#include <stdio.h>
+#include "few_plan.h"
+int main() { for (int r = 24; r <= 72; ++r) if (moe::tensor_split_fits(r)) printf("%d\\n", r); }
+"""
+    assert run(tmp_path, text) == ["72"]
+    # and the launch asks before it launches
+    launch = open(os.path.join(ROOT, "combine_counting_sort_gb300", "csrc", "few_tensor.cuh")).read()
+    assert launch.count("few_launch(matvec_tensor_kernel") == 1 and launch.index("if (!split_ok) return") < launch.index("few_launch(matvec_tensor_kernel")
