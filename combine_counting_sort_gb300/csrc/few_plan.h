@@ -100,4 +100,17 @@ MOE_PLAN bool tensor_split_fits(int regs) {
          kTensorWarps * regs;
 }
 
+// Its ring: stages of 16 row tiles' slice of 128 columns and that of n tokens (8 to 64), behind 1 KB of barriers.
+// Its two sets of widening warps wait for every second stage each.  With an odd number of stages
+// a slot changes sets from round to round, and a wait by parity would take the round before
+// last's fill for this one's, did the wait for an A buffer two slices earlier not imply that slice
+// i - 4 is done, and so slice i - stages: with four stages or more.
+constexpr int kTensorMinStages = 4;
+MOE_PLAN uint32_t tensor_tokens_at(int group) { return (16 * few_tile_bytes(group) + 1023) & ~1023u; }
+MOE_PLAN uint32_t tensor_stage(int group, int n) { return tensor_tokens_at(group) + 2 * n * 128; }
+MOE_PLAN int tensor_stages(int group, int n, uint32_t smem) {
+  const int s = (smem - 1024) / tensor_stage(group, n);
+  return s < kFewMaxStages ? s : kFewMaxStages;
+}
+
 }  // namespace moe

@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(kTensorThreads, 1) matvec_tensor_kernel(const 
   constexpr int kN = 8 * NT, kPer = kN > 32 ? 1 : kGroups < 64 / kN ? kGroups : 64 / kN;   // groups per unit of sums
   constexpr int kUnits = kPer * kN <= 32 ? 4 : 2;                                          // units per block of rows
   constexpr uint32_t kBox = kN * 128;   // 64 columns of all tokens, those past T zeros
-  constexpr uint32_t kTok = (16 * kTile + 1023) & ~1023u, kStage = kTok + 2 * kBox;
+  constexpr uint32_t kTok = tensor_tokens_at(GROUP), kStage = tensor_stage(GROUP, kN);
+  static_assert(tensor_stages(GROUP, kN, kFewMinSmem) >= kTensorMinStages, "the widening warps' waits");
   constexpr uint32_t kAcols = 64, kSums = 4 * kAcols;   // columns of an A buffer; where the sums' units begin,
   constexpr uint32_t kPitch = (512 - kSums) / (2 * kUnits);   // and from one to the next
   static_assert(kPitch >= kPer * kN, "");
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) matvec_tensor_kernel(const 
     const int odd_slices = warp >> 3;  // each warp every second slice, for one of the A buffers
     const uint32_t a = tmem + ((uint32_t)(32 * quad) << 16) + (odd_slices * 2 + block) * kAcols;
     const uint32_t full = smem_u32(ts->a_full + odd_slices * 2 + block), empty = smem_u32(ts->a_empty + odd_slices * 2 + block);
-    if (odd_slices) ring.next();
+    if (odd_slices) ring.next();   // kTensorMinStages: why its waits are safe with an odd number of stages
     for (int n = odd_slices; n < mine; n += 2) {
       if (!wait(ring.full_bar(), ring.phase)) break;
 #pragma unroll

@@ -73,3 +73,28 @@ int main() { for (int r = 24; r <= 72; ++r) if (moe::tensor_split_fits(r)) print
     # and the launch asks before it launches
     launch = open(os.path.join(ROOT, "combine_counting_sort_gb300", "csrc", "few_tensor.cuh")).read()
     assert launch.count("few_launch(matvec_tensor_kernel") == 1 and launch.index("if (!split_ok) return") < launch.index("few_launch(matvec_tensor_kernel")
+
+
+def test_the_tensor_kernels_ring_has_the_stages_that_its_waits_need(tmp_path):
+    # a model of the widening warps' waits: a wait by parity is safe only if the slot's fill before
+    # the one waited for is known to be complete, and what a set knows is that slices up to i - 4
+    # are done (its A buffer's last use) and its own i - 2 and before
+    text = """
+#include <stdio.h>
+#include "few_plan.h"
+int main() {
+  for (int g = 32; g <= 128; g *= 2)
+    for (int n = 16; n <= 64; n += 16) printf("%d\\n", moe::tensor_stages(g, n, moe::kFewMinSmem));
+  printf("%d\\n", moe::kTensorMinStages);
+}
+"""
+    *stages, least = (int(v) for v in run(tmp_path, text))
+
+    def safe(count):
+        known = lambda i: {j for j in range(i) if j <= i - 4 or (i - j) % 2 == 0}   # noqa: E731
+        return all(i - count < 0 or i - count in known(i) for i in range(40))
+
+    assert all(safe(s) for s in range(least, 13)) and not safe(3)
+    assert len(stages) == 12 and min(stages) >= least and any(s % 2 for s in stages)
+    kernel = open(os.path.join(ROOT, "combine_counting_sort_gb300", "csrc", "few_tensor.cuh")).read()
+    assert "static_assert(tensor_stages(GROUP, kN, kFewMinSmem) >= kTensorMinStages" in kernel
