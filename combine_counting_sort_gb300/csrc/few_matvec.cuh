@@ -286,8 +286,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) matvec_wide_kernel(const __gr
 
 // Slices of the wide kernel's stages: the fewest stages over the rounds that the SMs make,
 // each as long as its copies (some 40 bytes a clock, with the tokens out of L2) or
-// its MMAs (16 clocks per tile and block of tokens, and 600 beside them), where two
-// stages fit.
+// its MMAs (16 clocks per tile and block of tokens, and 600 beside them).
 inline int wide_slices(int tiles, int KT, int nt, int nsm) {
   int best = 1;
   long long cost = 1LL << 60;
@@ -295,7 +294,7 @@ inline int wide_slices(int tiles, int KT, int nt, int nsm) {
     const int rows = 2 * (8 / ks), rounds = ((tiles + rows - 1) / rows + nsm - 1) / nsm;
     const long long stage = std::max((16 * 1100 + 2 * ks * nt * 1024) / 40, 16 * nt * 16 + 600);
     const long long c = (long long)rounds * ((KT + ks - 1) / ks) * stage;
-    if (2 * ks * nt * 1024 <= 80 * 1024 && c < cost) { cost = c; best = ks; }
+    if (c < cost) { cost = c; best = ks; }
   }
   return best;
 }
