@@ -68,16 +68,24 @@ def matvec(x: np.ndarray, W: np.ndarray):
 
 
 # Rounding: bf16 keeps 8 significant bits, so one rounding is within 2^-8 of the
-# value; fp32 24.  A product of two bf16 values (or bf16 and a 4-bit or e4m3
+# value; f16 11, fp32 24.  A product of two bf16 values (or bf16 and a 4-bit or e4m3
 # code) is exact in fp32, so a sum of n products with group scales applied to
 # partial sums has at most n + 2 roundings of 2^-24 of the magnitudes' sum.
-U_BF16, U_F32 = 2.0 ** -8, 2.0 ** -24
+U_BF16, U_F16, U_F32 = 2.0 ** -8, 2.0 ** -11, 2.0 ** -24
+
+
+def record_step(v: np.ndarray) -> np.ndarray:
+    """How far a value of v [.., K] may be moved where the products take it as f16 behind a power of
+    two that its 128 columns share: their largest comes to 2^14 or more, f16's values end in steps of 2^-24."""
+    K = v.shape[-1]
+    most = np.abs(np.pad(v, [(0, 0)] * (v.ndim - 1) + [(0, -K % 128)])).reshape(*v.shape[:-1], -1, 128).max(-1)
+    return np.repeat(most, 128, -1)[..., :K] * 2.0 ** -39
 
 
 def matvec_bound(x: np.ndarray, W: np.ndarray):
     """(y, how far a bf16 result of fp32 sums may be from y), elementwise."""
     y, mag = matvec(x, W)
-    err = (W.shape[1] + 2) * U_F32 * mag
+    err = (W.shape[1] + 2) * U_F32 * mag + record_step(x) @ np.abs(W).T
     return y, U_BF16 * (np.abs(y) + err) + err + 2.0 ** -133   # half a bf16 subnormal step
 
 
@@ -85,7 +93,8 @@ def layer_few(x: np.ndarray, ids: np.ndarray, w: np.ndarray, experts: dict):
     """x [T, H] fp64, ids / w [T, k], experts[e] = (W1 [2F, H], W2 [H, F]) fp64.
     Ids outside `experts` have no route.  Returns (out, bound): the fp64
     layer and how far a bf16 result may be from it, elementwise, where sums are
-    fp32, w * silu(g) * u is rounded to bf16 once and expf is good to 2^-21."""
+    fp32, w * silu(g) * u is rounded to f16 once, behind a power of two that 128 features share,
+    and expf is good to 2^-21."""
     T, H = x.shape
     out, err = np.zeros((T, H)), np.zeros((T, H))
     n_terms = 2
@@ -98,14 +107,14 @@ def layer_few(x: np.ndarray, ids: np.ndarray, w: np.ndarray, experts: dict):
             F = W2.shape[1]
             n_terms += F + 1
             y, mag = matvec(x[t:t + 1], W1)
-            dy = (H + 2) * U_F32 * mag[0]
+            dy = (H + 2) * U_F32 * mag[0] + np.abs(W1) @ record_step(x[t])
             g, u = y[0, :F], y[0, F:]
             sig = 1 / (1 + np.exp(-g))
             silu = g * sig
             a = float(w[t, j]) * silu * u
             # |silu'| <= 1.1; exp's argument error is inside dy; sigmoid's own relative error 2^-20
             da = abs(float(w[t, j])) * (1.1 * dy[:F] * (np.abs(u) + dy[F:]) + np.abs(silu) * dy[F:] + 2.0 ** -19 * np.abs(silu * u))
-            da = da + U_BF16 * (np.abs(a) + da)
+            da = da + U_F16 * (np.abs(a) + da) + record_step(np.abs(a) + da)
             out[t] += W2 @ a
             err[t] += np.abs(W2) @ da + (n_terms * U_F32) * (np.abs(W2) @ (np.abs(a) + da))
     return out, U_BF16 * (np.abs(out) + err) + err + 2.0 ** -133

@@ -6,7 +6,7 @@ import torch
 import combine_counting_sort_gb300 as moe
 import oracle
 from tests.gpu_util import build
-from tests.test_gpu_few import Experts, bf16_t, f64, rand_bits, routes, status, w4_matrix, within
+from tests.test_gpu_few import GROUPS, Experts, bf16_t, f64, rand_bits, routes, status, w4_matrix, within
 
 pytestmark = pytest.mark.gpu
 
@@ -153,3 +153,28 @@ def test_layer_narrow_segments(T, cap):
     xb = rand_bits(T, H, seed=T)
     out, _, _ = ex.run(xb, ids, w)
     within(out, *oracle.layer_few(f64(xb), ids, w, ex.values), "layer")
+
+
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("T", [3, 21])
+def test_layer_activations_keep_eleven_bits(T, group):
+    # one weight in each row of W2, so that no activation's rounding is averaged out
+    E, H, F = 2, 256, 256
+    b1, rng = rand_bits(E, 2 * F, H, seed=T, scale=H ** -0.5), np.random.default_rng(T)
+    b2 = np.zeros((E, H, F), np.uint16)
+    for e in range(E):
+        b2[e, np.arange(H), rng.permutation(F)] = 0x3F30
+    ex = experts_of(b1, b2, group) if group else fp8_experts_of(b1, b2)
+    xb = rand_bits(T, H, seed=T + 1)
+    ids, w = routes(T, 1, E, seed=T)
+    out, _, _ = ex.run(xb, ids, w)
+    within(out, *oracle.layer_few(f64(xb), ids, w, ex.values), "layer")
+
+
+def fp8_experts_of(b1, b2):
+    ex = Experts.__new__(Experts)
+    ex.E, ex.H, ex.F, ex.group = b1.shape[0], b1.shape[2], b2.shape[2], 0
+    (q1, s1), (q2, s2) = oracle.quantize_weights(b1), oracle.quantize_weights(b2)
+    ex.W1, ex.W1_scale, ex.W2, ex.W2_scale = (torch.from_numpy(v).cuda() for v in (q1, s1, q2, s2))
+    ex.values = {e: (oracle.fp8_values(q1[e], s1[e]), oracle.fp8_values(q2[e], s2[e])) for e in range(ex.E)}
+    return ex
