@@ -97,8 +97,8 @@ def layer_few(x: np.ndarray, ids: np.ndarray, w: np.ndarray, experts: dict):
     and expf is good to 2^-21."""
     T, H = x.shape
     out, err = np.zeros((T, H)), np.zeros((T, H))
-    n_terms = 2
     for t in range(T):
+        n_terms, moved = 2, np.zeros(H)   # terms of this token's sums, and their magnitudes' sum
         for j in range(ids.shape[1]):
             e = int(ids[t, j])
             if e not in experts:
@@ -116,5 +116,7 @@ def layer_few(x: np.ndarray, ids: np.ndarray, w: np.ndarray, experts: dict):
             da = abs(float(w[t, j])) * (1.1 * dy[:F] * (np.abs(u) + dy[F:]) + np.abs(silu) * dy[F:] + 2.0 ** -19 * np.abs(silu * u))
             da = da + U_F16 * (np.abs(a) + da) + record_step(np.abs(a) + da)
             out[t] += W2 @ a
-            err[t] += np.abs(W2) @ da + (n_terms * U_F32) * (np.abs(W2) @ (np.abs(a) + da))
+            err[t] += np.abs(W2) @ da
+            moved += np.abs(W2) @ (np.abs(a) + da)
+        err[t] += n_terms * U_F32 * moved
     return out, U_BF16 * (np.abs(out) + err) + err + 2.0 ** -133

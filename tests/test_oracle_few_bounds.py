@@ -41,3 +41,13 @@ def test_a_records_step_covers_what_f16_leaves_out():
     assert np.all(np.abs(as_records(x) - x) <= oracle.few_oracle.record_step(x))
     big = np.abs(x).reshape(5, 3, 128).max(-1).repeat(128, 1)
     assert np.all((as_records(x) == x)[np.abs(x) >= big * 2.0 ** -31])
+
+
+def test_a_tokens_bound_is_its_own():
+    # whatever the batch: the same token's bound, alone and as the last of many
+    rng = np.random.default_rng(4)
+    T, H, F, k = 9, 128, 128, 2
+    x, ids, w = rng.standard_normal((T, H)), np.tile([1, 0], (T, 1)), rng.random((T, k))
+    ex = {e: (rng.standard_normal((2 * F, H)), rng.standard_normal((H, F))) for e in range(2)}
+    for got, alone in zip(oracle.layer_few(x, ids, w, ex), oracle.layer_few(x[-1:], ids[-1:], w[-1:], ex)):
+        assert np.allclose(got[-1], alone[0], rtol=1e-12, atol=0)
