@@ -143,6 +143,24 @@ def experts(E, H, F, group):
     return _experts[E, H, F, group]
 
 
+# H 2560: two row tiles to a down item on 152 SMs, 7040: three, and two in the last item.  Experts with 8
+# tokens and fewer (one block of columns, two slices a warp), 9 and 16 (two blocks), 25 (two segments);
+# a token's sums over several experts, one that it names twice, slots without a route.
+@pytest.mark.parametrize("T,k,cap", [(3, 4, 3), (8, 3, 8), (9, 4, 8), (33, 4, 9), (33, 4, 16), (64, 2, 8), (64, 4, 25)])
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("H", [2560, 7040])
+def test_layer_row_tiles_of_a_down_item(H, group, T, k, cap):
+    E, F = 17, 128
+    ex = experts(E, H, F, group)
+    ids, w = capped_routes(T, k, E, cap, seed=T + cap)
+    ids[1, 1], ids[2, 0] = ids[1, 0], -1
+    xb = rand_bits(T, H, seed=T)
+    out, _, _ = ex.run(xb, ids, w)
+    within(out, *oracle.layer_few(f64(xb), ids, w, ex.values), "layer")
+    again, _, _ = ex.run(xb, ids, w)
+    assert torch.equal(again, out)
+
+
 @pytest.mark.parametrize("T,cap", [(57, 16), (64, 25)])
 def test_layer_narrow_segments(T, cap):
     # FP8 weights, three row tiles and about 1000 pairs: segments of fewer than 16 tokens
