@@ -68,7 +68,9 @@ MOE_DEV void copy_tokens(RecordOf record_of, int cols, int kt0, int nk, uint32_t
 
 // Tables of the routes in shared memory, sized by the P = T k pairs.  A segment is
 // one expert and up to A.cols of the tokens routed to it; row r of the activations
-// belongs to one (token, expert).
+// belongs to one (token, expert).  An expert's segments follow one another, so that what its weights
+// are copied for again comes out of L2 (64 tokens on all of 8 experts, FP8: 354 MB read from memory,
+// the weights' own bytes, in 303 us; one pass over them would take 52).
 struct FewTables {
   uint64_t* seg_mask;
   int *seg_expert, *seg_row;

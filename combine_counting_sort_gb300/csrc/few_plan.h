@@ -81,8 +81,8 @@ MOE_PLAN int layer_slices(int group, int rt2, bool direct, int T, int pairs, int
   return group != 0 && (direct || (cap <= 8 && layer_room(group, 2, rt2, false, T, pairs, cap, smem).stages >= 2)) ? 2 : 1;
 }
 
-// Tokens of a segment, at most: as many as leave two stages of them (fewer than 16 for FP8
-// weights alone, with H above 4864 and some 800 pairs).
+// Tokens of a segment, at most: as many as leave two stages of them (15 for FP8 weights with three
+// row tiles and more than some 800 pairs, else 16).
 MOE_PLAN int layer_cols(int group, int rt2, bool direct, int T, int pairs, uint32_t smem) {
   int cols = kLayerCols;
   while (!direct && cols > 8 && layer_room(group, 1, rt2, false, T, pairs, cols, smem).stages < 2) --cols;

@@ -402,7 +402,7 @@ int moe_dequant_rows(const uint8_t* A, const float* A_scale, int H, const moe_la
                      uint16_t* Y, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
- * Decoding: few tokens, so the time is that of reading the weights once.
+ * Decoding: few tokens, so the time is that of reading the weights.
  *
  * 4-bit weights with group scales.  A matrix [N, K] has a code c in 0..15 per
  * value and a bf16 scale per row and group of 32, 64 or 128 columns; a code
@@ -459,8 +459,9 @@ int moe_matvec_w4(const uint16_t* x, int T, int K, const uint8_t* Wp, int N, int
  *   (id, w)[t, j] = the k largest logits, softmax over them (moe_router_topk's rule)
  *   g, u = rows [0, F) and [F, 2F) of W1[id] times x[t];  a = g / (1 + exp(-g)) * u
  *   out[t, :] = bf16( sum_j w[t, j] * W2[id[t, j]] * a[t, j] )
- * with each expert's weights read once however many of the tokens use it.
- * Sums are fp32.  w * a, fp32, is rounded once for the second product's operands: to
+ * with each expert's weights read from memory once, and copied out of L2 and
+ * multiplied anew for every 16 of its tokens (15 with FP8 weights, H above 4864
+ * and T * k above 800).  Sums are fp32.  w * a, fp32, is rounded once for the second product's operands: to
  * f16's 11 bits behind a power of two shared by 128 values; what is below 2^-28
  * of the largest of the 128 is within 2^-39 of that largest.  x enters its products
  * in the same form, exactly down to 2^-31 of the largest.  Infinite and NaN values of x spoil that

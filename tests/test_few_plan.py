@@ -23,7 +23,7 @@ int main() {
           if (cols < kLayerCols) {
             ++fewer;
             if (P < fewer_least) fewer_least = P;
-            if (cols < 12 || g != 0 || rt2 != 3) printf("narrow %d %d %d %d: %d\n", g, rt2, T, k, cols);
+            if (cols < 15 || g != 0 || rt2 != 3) printf("narrow %d %d %d %d: %d\n", g, rt2, T, k, cols);
           }
           for (int cap = 1; cap <= (T < cols ? T : cols); ++cap) {
             const int sp = layer_slices(g, rt2, direct, T, P, cap, kFewMinSmem);
@@ -58,8 +58,8 @@ def test_every_call_leaves_the_ring_two_stages(tmp_path):
     assert len(lines) == 1, lines[:20]
     calls, fewer, least, two_slices = (int(v) for v in lines[0].split()[1:])
     assert calls > 100000 and two_slices > 10000
-    # segments of fewer than 16 tokens for FP8 with three row tiles and many pairs alone
-    assert fewer > 0 and least >= 700
+    # segments of 15 tokens for FP8 with three row tiles and many pairs alone
+    assert fewer > 0 and least > 800
 
 
 def test_a_kernel_with_too_few_registers_for_the_split_is_refused(tmp_path):

@@ -163,7 +163,7 @@ def test_layer_row_tiles_of_a_down_item(H, group, T, k, cap):
 
 @pytest.mark.parametrize("T,cap", [(57, 16), (64, 25)])
 def test_layer_narrow_segments(T, cap):
-    # FP8 weights, three row tiles and about 1000 pairs: segments of fewer than 16 tokens
+    # FP8 weights, three row tiles and about 1000 pairs: segments of 15 tokens
     E, k, H, F = 48, 16, 7168, 128
     ex = experts(E, H, F, 0)
     ids, w = capped_routes(T, k, E, cap, seed=T) if cap == 25 else capped_routes(T, 16, 64, cap, seed=T)
