@@ -32,8 +32,8 @@ MOE_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t b
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                :: "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar) : "memory");
 }
-// As bulk_load and tma_load_3d for weights, which are read once: first to leave L2, so
-// that the tokens, the tables and the kernel's own code stay (they are few, and
+// As bulk_load and tma_load_3d for weights, which are read once, or again soon after (an expert's
+// next 16 tokens): first to leave L2, so that the tokens, the tables and the kernel's own code stay (they are few, and
 // each miss of theirs is waited for).
 MOE_DEV uint64_t evict_first_policy() {
   uint64_t p;

@@ -3,12 +3,13 @@
 // known, no weight can be on its way.
 //
 // Measured, us and share of the copy bandwidth that the weights were read at (H 7168, F 2048, 8 of 256
-// experts): FP8, 1 token 66 (79%), 16 tokens 641 (103%), 64 tokens 1460 (99%); 4-bit, groups of
-// 128, 1 token 48 (56%), 64 tokens 973 (76%); groups of 32, 8 tokens 252 (83%).  One token's 66
-// us in ns: records 600, logits 1500, meeting 1500, routes 1850, tables 1700, gate and up
-// 33000, meeting and records 5000, down 15400; the 4-bit products take 22600 and 10200, bound by the
-// hand-over of stages that hold half the bytes.  With H or F of a few hundred the stages are
-// mostly empty and the fixed 12 us are most of the time (8 experts, 256 x 256: 12.7 us).
+// experts): FP8, 1 token 66 (79%), 16 tokens 640 (103%), 64 tokens 1458 (99%); 4-bit, groups of
+// 128, 1 token 52 (53%), 64 tokens 1031 (72%); groups of 32, 8 tokens 267 (79%).  One token's 66
+// us in ns, by a block's own clock: records 670, logits 1570, meeting 1470, routes 1820, tables 1890 (the
+// block's meetings around them included), gate and up 33700, meeting and records 6100, down
+// 15200; the 4-bit products take 25200 and 11000, bound by the hand-over of stages that hold half the
+// bytes and by widening.  With H or F of a few hundred the stages are
+// mostly empty and the fixed 12 us are most of the time (8 experts, 256 x 256: 12.8 us).
 #pragma once
 
 #include <type_traits>

@@ -2,10 +2,10 @@
 //
 // matvec_few_kernel, one token, or up to four on few columns or many rows: every block makes
 // the records of all tokens for itself while its first weights are on their way, and a
-// stage holds weights alone (few_slice.cuh: the products).  Bound by memory with many rows
-// (152064 x 4096, groups of 64, one token: 52.1 us, 6.4 TB/s), with few by the way through the
-// block: launch, records, first copies, sums (4096 x 7168, groups of 128: 6.2 us, of which the
-// weights are 2.2; 7.35 with the records' loads one after the other).
+// stage holds weights alone (few_slice.cuh: the products).  Bound by memory and the products with
+// many rows (152064 x 4096, groups of 64, one token: 57.3 us, 5.8 TB/s), with few by the way through the
+// block: launch, records, first copies, sums (4096 x 7168, groups of 128: 6.65 us, of which the
+// weights are 2.2; a microsecond more with the records' loads one after the other).
 //
 // matvec_wide_kernel, up to 16 tokens and few rows: a block of eight warps is KS slices of 128
 // columns x 8 / KS groups of 32 rows, each warp all tokens (one or two blocks of 8) on its 32
@@ -309,10 +309,10 @@ int launch_matvec(const MatvecArgs& args, int nsm, cudaStream_t s) {
   const int tiles = (args.N + 15) / 16;
   const int KT = (args.K + 127) / 128, records = args.T * matvec_token_pitch(KT);
   // The records cost a block some 20 ns each; the other kernels take the tokens as they are.
-  // Groups of 128, few / other kernel: one token x 4096 x 7168 6.2 / 6.9 us, x 32768 x 7168
-  // 23.9 / 29.2; two x 4096 x 4096 (64 records) 4.95 / 5.2, x 4096 x 7168 (112) 7.4 / 6.9; three x
-  // 32768 x 7168 26.8 / 29.3; four x 2048 x 2048 (64) 3.4 / 3.6, x 4096 x 7168 (224) 10 / 6.9;
-  // six x 2048 x 2048 (96) 4.3 / 3.6, x 32768 x 7168 31.3 / 29.2.
+  // Groups of 128, few / other kernel: one token x 4096 x 7168 6.65 / 6.9 us, x 32768 x 7168
+  // 26.4 / 29.2; two x 4096 x 4096 (64 records) 4.8 / 5.2, x 4096 x 7168 (112) 7.2 / 7.0, x 32768 x
+  // 7168 27.4 / 29.2; three x 32768 x 7168 28.4 / 29.1; four x 2048 x 2048 (64) 2.95 / 3.65, x 4096 x
+  // 7168 (224) 9.1 / 6.9, x 32768 x 4096 18.7 / 18.4; six x 2048 x 2048 (96) 3.7 / 3.7.
   if (records <= kMatvecTokenRoom && (args.T == 1 || (args.T <= 4 && (args.T * KT <= 64 || tiles > 4 * nsm)))) {
     switch (few_row_tiles(tiles, nsm, records <= kMatvecTokenRoom / 2 ? 3 : 2)) {
       case 1: return launch_matvec_few<GROUP, 1>(args, nsm, s);

@@ -443,9 +443,9 @@ int moe_dequant_weights_w4(const uint8_t* Wp, int E, int N, int K, int group, fl
 /* moe_matvec_w4: y[t, n] = bf16( sum_k x[t, k] * (c[n, k] - 8) * scale[n, k / group] ),
  * fp32 accumulation, one rounding.  For what stands beside the experts: a
  * shared expert's projections, the vocabulary.  A token's values reach no other
- * token's results.  Up to four tokens may enter the products as f16 behind a power of two
- * shared by 128 columns: exactly, but for values below 2^-31 of the largest of
- * the 128, which are within 2^-39 of that largest.
+ * token's results.  Up to four tokens may enter the products as f16 behind a
+ * power of two shared by 128 columns: exactly, but for values below 2^-31 of
+ * the largest of the 128, which are within 2^-39 of that largest.
  *   x  device bf16 [T, K], 1 <= T <= MOE_FEW_MAX_TOKENS, 16-byte aligned.
  *   Wp one laid-out matrix; y device bf16 [T, N].
  * A bounded wait that gives up writes MOE_ERR_TIMEOUT to *status. */
@@ -461,13 +461,14 @@ int moe_matvec_w4(const uint16_t* x, int T, int K, const uint8_t* Wp, int N, int
  *   out[t, :] = bf16( sum_j w[t, j] * W2[id[t, j]] * a[t, j] )
  * with each expert's weights read from memory once, and copied out of L2 and
  * multiplied anew for every 16 of its tokens (15 with FP8 weights, H above 4864
- * and T * k above 800).  Sums are fp32.  w * a, fp32, is rounded once for the second product's operands: to
- * f16's 11 bits behind a power of two shared by 128 values; what is below 2^-28
- * of the largest of the 128 is within 2^-39 of that largest.  x enters its products
- * in the same form, exactly down to 2^-31 of the largest.  Infinite and NaN values of x spoil that
- * token's out and no other's, and those of an expert's weights the out of its
- * own tokens alone.  Where fewer than k of a token's logits are not NaN,
- * the slots left get the id 0x7fffffff and *status is MOE_ERR_EXPERT_ID.
+ * and T * k above 800).  Sums are fp32.  w * a, fp32, is rounded once for the
+ * second product's operands: to f16's 11 bits behind a power of two shared by
+ * 128 values; what is below 2^-28 of the largest of the 128 is within 2^-39 of
+ * that largest.  x enters its products in the same form, exactly down to 2^-31
+ * of the largest.  Infinite and NaN values of x spoil that token's out and no
+ * other's, and those of an expert's weights the out of its own tokens alone.
+ * Where fewer than k of a token's logits are not NaN, the slots left get the id
+ * 0x7fffffff and *status is MOE_ERR_EXPERT_ID.
  *   x        device bf16 [T, H].
  *   router   device bf16 [E, H], or NULL: topk_ids and topk_w are then inputs.
  *   topk_ids device int32 [T, k], topk_w device f32 [T, k]: written where router
