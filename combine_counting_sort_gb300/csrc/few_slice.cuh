@@ -34,6 +34,7 @@ template <int GROUP, int SP>
 struct FewForm {
   static constexpr bool kW4 = GROUP != 0;
   static constexpr int kTile = few_tile_bytes(GROUP);
+  static_assert(!kW4 || kTile == w4_tile_bytes(kW4 ? GROUP : 128), "");
   static constexpr int kSlices = kFewWarps * SP;
   // 4-bit: the slices' tiles as they lie in memory.  FP8: per slice 16 rows of
   // 128 bytes in TMA's 128-byte swizzle, which ldmatrix reads without bank conflicts.

@@ -161,6 +161,19 @@ def test_layer_row_tiles_of_a_down_item(H, group, T, k, cap):
     assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("group", GROUPS)
+def test_layer_one_buffer_of_sums(group):
+    # 1024 pairs, most of them without a route: the tables leave two stages beside one buffer alone
+    T, E, H, F, cap = 64, 17, 7040, 128, 8
+    ex = experts(E, H, F, group)
+    few, w2 = capped_routes(T, 2, E, cap, seed=5)
+    ids, w = np.full((T, 16), -1, np.int32), np.full((T, 16), np.nan, np.float32)
+    ids[:, [3, 15]], w[:, [3, 15]] = few, w2
+    xb = rand_bits(T, H, seed=6)
+    out, _, _ = ex.run(xb, ids, w)
+    within(out, *oracle.layer_few(f64(xb), few, w2, ex.values), "layer")
+
+
 @pytest.mark.parametrize("T,cap", [(57, 16), (64, 25)])
 def test_layer_narrow_segments(T, cap):
     # FP8 weights, three row tiles and about 1000 pairs: segments of 15 tokens
