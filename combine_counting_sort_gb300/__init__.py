@@ -32,6 +32,8 @@ EXPORTS = [
     "moe_grouped_gemm1_pair",
     "moe_w4_packed_bytes", "moe_quant_weights_w4", "moe_pack_weights_w4", "moe_dequant_weights_w4", "moe_matvec_w4",
     "moe_layer_few_ws_bytes", "moe_layer_few",
+    "moe_layernorm", "moe_layernorm_bwd_ws_bytes", "moe_layernorm_bwd", "moe_linear", "moe_linear_bwd_ws_bytes",
+    "moe_linear_bwd", "moe_gated", "moe_gated_bwd_ws_bytes", "moe_gated_bwd",
 ]
 
 
@@ -115,6 +117,16 @@ def lib() -> ctypes.CDLL:
         L.moe_matvec_w4.argtypes = [vp, i32, i32, vp, i32, i32, vp, vp, vp]
         L.moe_layer_few_ws_bytes.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
         L.moe_layer_few.argtypes = [vp, i32, i32, vp, i32, i32, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, sz, vp, vp]
+        f32 = ctypes.c_float
+        L.moe_layernorm.argtypes = [vp, i32, i32, i32, vp, vp, i32, f32, vp, vp, vp, vp]
+        L.moe_layernorm_bwd_ws_bytes.argtypes = [i32, i32, ctypes.POINTER(sz)]
+        L.moe_layernorm_bwd.argtypes = [vp, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_linear.argtypes = [vp, i32, i32, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp]
+        L.moe_linear_bwd_ws_bytes.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
+        L.moe_linear_bwd.argtypes = [vp, vp, i32, i32, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp, vp]
+        L.moe_gated.argtypes = [vp, i32, i32, vp, i32, i32, i32, vp, vp, vp, vp]
+        L.moe_gated_bwd_ws_bytes.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
+        L.moe_gated_bwd.argtypes = [vp, vp, i32, i32, vp, i32, i32, vp, vp, vp, vp, sz, vp, vp]
         for n in EXPORTS:
             if n != "moe_status_string":
                 getattr(L, n).restype = i32
@@ -612,3 +624,154 @@ def moe_layer_few(x: torch.Tensor, W1: torch.Tensor, W1_scale: Optional[torch.Te
     _check("moe_layer_few", lib().moe_layer_few(
         px, T, H, pr, E, k, p1, ps1, p2, ps2, F, group, pids, pw, pout, _ptr(ws, None, "ws"), ws.numel() * ws.element_size(), pst,
         _raw_stream(stream)))
+
+
+# ---------------------------------------------------------------- dense operators beside the experts
+
+MOE_BF16, MOE_F16, MOE_F32 = range(3)
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = range(5)
+MOE_NORM_MAX_H, MOE_DENSE_MAX = 16384, 1 << 20
+_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
+
+
+def _dtype(t: torch.Tensor, name: str, allowed) -> int:
+    if t.dtype not in allowed:
+        raise ValueError(f"{name} must be one of {', '.join(str(d) for d in allowed)}, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _here(*tensors):
+    """Refuse tensors of another device than the current one, which the kernel
+    is launched on."""
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on the current device {dev}, got one on {t.device}")
+
+
+def _bytes(ws: Optional[torch.Tensor], name="ws"):
+    """Address and size of a workspace."""
+    return _ptr(ws, None, name), ws.numel() * ws.element_size()
+
+
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def moe_layernorm(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor], eps: float, y: torch.Tensor,
+                  mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None, stream=None):
+    """Layer norm of each row of x [T, H] (bf16, f16 or f32) into y; weight and
+    bias [H] of x's type or f32, or None; mean and rstd (f32 [T]) are written
+    where given, for moe_layernorm_bwd."""
+    T, H = _dims(x, 2, "x")
+    dt = _dtype(x, "x", tuple(_DTYPES))
+    p = weight if weight is not None else bias
+    wd = x.dtype if p is None else p.dtype
+    if wd not in (x.dtype, torch.float32):
+        raise ValueError(f"weight and bias must be {x.dtype} or torch.float32, got {wd}")
+    px, pw, pb, py, pm, pr = _args((x, x.dtype, (T, H), "x"), (weight, wd, (H,), "weight"), (bias, wd, (H,), "bias"),
+                                   (y, x.dtype, (T, H), "y"), (mean, torch.float32, (T,), "mean"), (rstd, torch.float32, (T,), "rstd"))
+    _here(x, weight, bias, y, mean, rstd)
+    _check("moe_layernorm", lib().moe_layernorm(px, T, H, dt, pw, pb, _DTYPES[wd], eps, py, pm, pr, _raw_stream(stream)))
+
+
+def moe_layernorm_bwd_ws_bytes(T: int, H: int) -> int:
+    out = ctypes.c_size_t()
+    _check("moe_layernorm_bwd_ws_bytes", lib().moe_layernorm_bwd_ws_bytes(T, H, ctypes.byref(out)))
+    return out.value
+
+
+def moe_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor, rstd: torch.Tensor,
+                      dx: torch.Tensor, dweight: Optional[torch.Tensor], dbias: Optional[torch.Tensor], ws: torch.Tensor, stream=None):
+    """Gradients of moe_layernorm: dx [T, H], and the sums over the rows dweight
+    and dbias [H] (of weight's type; of x's or f32 where weight is None), each
+    None where it is not wanted."""
+    T, H = _dims(x, 2, "x")
+    dt = _dtype(x, "x", tuple(_DTYPES))
+    p = next((t for t in (weight, dweight, dbias) if t is not None), None)
+    wd = x.dtype if p is None else p.dtype
+    if wd not in (x.dtype, torch.float32):
+        raise ValueError(f"weight, dweight and dbias must be {x.dtype} or torch.float32, got {wd}")
+    pdy, px, pw, pm, pr, pdx, pdw, pdb = _args(
+        (dy, x.dtype, (T, H), "dy"), (x, x.dtype, (T, H), "x"), (weight, wd, (H,), "weight"), (mean, torch.float32, (T,), "mean"),
+        (rstd, torch.float32, (T,), "rstd"), (dx, x.dtype, (T, H), "dx"), (dweight, wd, (H,), "dweight"), (dbias, wd, (H,), "dbias"))
+    pws, nws = _bytes(ws)
+    _here(dy, x, weight, mean, rstd, dx, dweight, dbias, ws)
+    _check("moe_layernorm_bwd", lib().moe_layernorm_bwd(pdy, px, T, H, dt, pw, _DTYPES[wd], pm, pr, pdx, pdw, pdb, pws, nws,
+                                                        _raw_stream(stream)))
+
+
+def moe_linear(x: torch.Tensor, W: torch.Tensor, y: torch.Tensor, status: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, act: int = MOE_ACT_NONE, slope: Optional[torch.Tensor] = None, stream=None):
+    """y = act(x W^T + bias) + residual for x [T, K] and W [N, K] in bf16 or
+    f16; y may be residual.  slope [T, N], written where given, is what
+    moe_linear_bwd needs of the activation."""
+    T, K = _dims(x, 2, "x")
+    N = _dims(W, 2, "W")[0]
+    dt, d = _dtype(x, "x", _HALF), x.dtype
+    _status(status)
+    px, pw, py, pst, pb, pr, ps = _args((x, d, (T, K), "x"), (W, d, (N, K), "W"), (y, d, (T, N), "y"),
+                                        (status, torch.int32, status.shape, "status"), (bias, d, (N,), "bias"),
+                                        (residual, d, (T, N), "residual"), (slope, d, (T, N), "slope"))
+    _here(x, W, y, status, bias, residual, slope)
+    _check("moe_linear", lib().moe_linear(px, T, K, pw, N, dt, pb, pr, act, py, ps, pst, _raw_stream(stream)))
+
+
+def moe_linear_bwd_ws_bytes(T: int, N: int, K: int) -> int:
+    out = ctypes.c_size_t()
+    _check("moe_linear_bwd_ws_bytes", lib().moe_linear_bwd_ws_bytes(T, N, K, ctypes.byref(out)))
+    return out.value
+
+
+def moe_linear_bwd(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, dx: Optional[torch.Tensor], dW: Optional[torch.Tensor],
+                   ws: torch.Tensor, status: torch.Tensor, dbias: Optional[torch.Tensor] = None, slope: Optional[torch.Tensor] = None,
+                   stream=None):
+    """Gradients of moe_linear: dx [T, K], dW [N, K] and dbias [N], each None
+    where it is not wanted; slope as moe_linear wrote it (None: no activation).
+    The residual's gradient is dy."""
+    T, K = _dims(x, 2, "x")
+    N = _dims(W, 2, "W")[0]
+    dt, d = _dtype(x, "x", _HALF), x.dtype
+    _status(status)
+    pdy, px, pw, pdx, pdw, pst, pdb, ps = _args(
+        (dy, d, (T, N), "dy"), (x, d, (T, K), "x"), (W, d, (N, K), "W"), (dx, d, (T, K), "dx"), (dW, d, (N, K), "dW"),
+        (status, torch.int32, status.shape, "status"), (dbias, d, (N,), "dbias"), (slope, d, (T, N), "slope"))
+    pws, nws = _bytes(ws)
+    _here(dy, x, W, dx, dW, ws, status, dbias, slope)
+    _check("moe_linear_bwd", lib().moe_linear_bwd(pdy, px, T, K, pw, N, dt, ps, pdx, pdw, pdb, pws, nws, pst, _raw_stream(stream)))
+
+
+def moe_gated(x: torch.Tensor, W1: torch.Tensor, h: torch.Tensor, status: torch.Tensor, act: int = MOE_ACT_SILU,
+              factors: Optional[torch.Tensor] = None, stream=None):
+    """h = act(x Wg^T) * (x Wu^T) for x [T, H] and W1 [2F, H] (gate rows, then up
+    rows) in bf16 or f16.  factors [T, 2F], written where given, is what
+    moe_gated_bwd multiplies dh by."""
+    T, H = _dims(x, 2, "x")
+    F = _dims(h, 2, "h")[1]
+    dt, d = _dtype(x, "x", _HALF), x.dtype
+    _status(status)
+    px, pw, ph, pst, pf = _args((x, d, (T, H), "x"), (W1, d, (2 * F, H), "W1"), (h, d, (T, F), "h"),
+                                (status, torch.int32, status.shape, "status"), (factors, d, (T, 2 * F), "factors"))
+    _here(x, W1, h, status, factors)
+    _check("moe_gated", lib().moe_gated(px, T, H, pw, F, dt, act, ph, pf, pst, _raw_stream(stream)))
+
+
+def moe_gated_bwd_ws_bytes(T: int, F: int, H: int) -> int:
+    out = ctypes.c_size_t()
+    _check("moe_gated_bwd_ws_bytes", lib().moe_gated_bwd_ws_bytes(T, F, H, ctypes.byref(out)))
+    return out.value
+
+
+def moe_gated_bwd(dh: torch.Tensor, x: torch.Tensor, W1: torch.Tensor, factors: torch.Tensor, dx: Optional[torch.Tensor],
+                  dW1: Optional[torch.Tensor], ws: torch.Tensor, status: torch.Tensor, stream=None):
+    """Gradients of moe_gated: dx [T, H] and dW1 [2F, H], each None where it is
+    not wanted; factors as moe_gated wrote them."""
+    T, H = _dims(x, 2, "x")
+    F = _dims(dh, 2, "dh")[1]
+    dt, d = _dtype(x, "x", _HALF), x.dtype
+    _status(status)
+    pdh, px, pw, pf, pdx, pdw, pst = _args((dh, d, (T, F), "dh"), (x, d, (T, H), "x"), (W1, d, (2 * F, H), "W1"),
+                                           (factors, d, (T, 2 * F), "factors"), (dx, d, (T, H), "dx"), (dW1, d, (2 * F, H), "dW1"),
+                                           (status, torch.int32, status.shape, "status"))
+    pws, nws = _bytes(ws)
+    _here(dh, x, W1, factors, dx, dW1, ws, status)
+    _check("moe_gated_bwd", lib().moe_gated_bwd(pdh, px, T, H, pw, F, dt, pf, pdx, pdw, pws, nws, pst, _raw_stream(stream)))

@@ -1,0 +1,224 @@
+// dense.cu: moe_linear and moe_gated with their backward passes, and the
+// elementwise kernels in front of the backward products.
+#include "dense_host.cuh"
+
+namespace moe {
+
+// ---------------------------------------------------------------- d = dy * slope and dbias
+//
+// Memory bound: reads dy and slope, writes d.  A block of 8 warps takes 256
+// columns; the blocks of a cluster (gridDim.y of them) share the rows, and
+// add up their column sums through distributed shared memory in rank order.
+// V = 8: lane l holds columns 8 l.., in 16-byte vectors; V = 1: columns l, l + 32, ...
+template <typename T, int V>
+__global__ void __launch_bounds__(256)
+    dense_d_kernel(const T* dy, const T* slope, int I, int J, T* d, long long ldd, T* dbias) {
+  __shared__ float sums[8][256];
+  __shared__ float total[256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j0 = blockIdx.x * 256;
+  constexpr int NV = 8 / V, STEP = V == 8 ? 256 : 32;
+  float acc[8] = {};
+  for (long long i = (long long)blockIdx.y * 8 + warp; i < I; i += 8LL * gridDim.y) {
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      const int j = j0 + c * STEP + lane * V;
+      if (j >= J) continue;
+      const Vec<T, V> a = *reinterpret_cast<const Vec<T, V>*>(dy + i * J + j);
+      Vec<T, V> s, o;
+      if (slope) s = *reinterpret_cast<const Vec<T, V>*>(slope + i * J + j);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float f = slope ? to_f32(a.v[v]) * to_f32(s.v[v]) : to_f32(a.v[v]);
+        acc[c * V + v] += f;
+        o.v[v] = from_f32<T>(f);
+      }
+      if (d) *reinterpret_cast<Vec<T, V>*>(d + i * ldd + j) = o;
+    }
+  }
+  if (!dbias) return;
+#pragma unroll
+  for (int c = 0; c < NV; ++c)
+#pragma unroll
+    for (int v = 0; v < V; ++v) sums[warp][c * STEP + lane * V + v] = acc[c * V + v];
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) s += sums[w][threadIdx.x];
+  total[threadIdx.x] = s;
+  cluster_sync();
+  if (blockIdx.y == 0) {
+    s = 0.f;
+    const uint32_t at = smem_u32(&total[threadIdx.x]);
+    for (uint32_t r = 0; r < gridDim.y; ++r) s += ld_shared_cluster_f32(mapa_shared(at, r));
+    const int j = j0 + threadIdx.x;
+    if (j < J) dbias[j] = from_f32<T>(s);
+  }
+  cluster_sync();
+}
+
+// d = [dh * factors[:, :F], dh * factors[:, F:]]
+template <typename T, int V>
+__global__ void __launch_bounds__(256) gated_d_kernel(const T* dh, const T* factors, int I, int F, T* d, long long ldd) {
+  const int j = (blockIdx.x * 256 + threadIdx.x) * V;
+  if (j >= F) return;
+  for (long long i = blockIdx.y; i < I; i += gridDim.y) {
+    const Vec<T, V> a = *reinterpret_cast<const Vec<T, V>*>(dh + i * F + j);
+    const Vec<T, V> p = *reinterpret_cast<const Vec<T, V>*>(factors + i * 2 * F + j);
+    const Vec<T, V> q = *reinterpret_cast<const Vec<T, V>*>(factors + i * 2 * F + F + j);
+    Vec<T, V> o, u;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float f = to_f32(a.v[v]);
+      o.v[v] = from_f32<T>(f * to_f32(p.v[v]));
+      u.v[v] = from_f32<T>(f * to_f32(q.v[v]));
+    }
+    *reinterpret_cast<Vec<T, V>*>(d + i * ldd + j) = o;
+    *reinterpret_cast<Vec<T, V>*>(d + i * ldd + F + j) = u;
+  }
+}
+
+template <typename T>
+int launch_d(const void* dy, const void* slope, int I, int J, void* d, long long ldd, void* dbias, cudaStream_t st) {
+  const bool vec = J % 8 == 0 && aligned16(dy) && aligned16(slope);
+  const int strips = (J + 255) / 256;
+  // rows of a strip over up to 8 blocks (a cluster, where they add up their sums); without sums, over more
+  const long long want = std::max(1, 4 * 152 / strips), cap = dbias ? 8 : 1024;
+  const int ys = (int)std::min({cap, want, ((long long)I + 7) / 8});
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = attr[0].val.clusterDim.z = 1;
+  attr[0].val.clusterDim.y = dbias ? (unsigned)ys : 1u;
+  cfg.gridDim = dim3((unsigned)strips, (unsigned)ys);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto kernel = vec ? dense_d_kernel<T, 8> : dense_d_kernel<T, 1>;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<const T*>(dy), static_cast<const T*>(slope), I, J, static_cast<T*>(d), ldd,
+                            static_cast<T*>(dbias)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <typename T>
+int launch_gated_d(const void* dh, const void* factors, int I, int F, void* d, long long ldd, cudaStream_t st) {
+  const bool vec = F % 8 == 0 && aligned16(dh) && aligned16(factors);
+  const int per = vec ? 2048 : 256, strips = (F + per - 1) / per;
+  const dim3 grid((unsigned)strips, (unsigned)std::min(I, std::max(1, 16 * 152 / strips)));
+  if (vec)
+    gated_d_kernel<T, 8><<<grid, 256, 0, st>>>(static_cast<const T*>(dh), static_cast<const T*>(factors), I, F, static_cast<T*>(d), ldd);
+  else
+    gated_d_kernel<T, 1><<<grid, 256, 0, st>>>(static_cast<const T*>(dh), static_cast<const T*>(factors), I, F, static_cast<T*>(d), ldd);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+constexpr int kDenseMaxT = 1 << 24;
+
+inline bool dense_shape_ok(int T, int N, int K) {
+  return T >= 0 && T <= kDenseMaxT && N >= 1 && N <= MOE_DENSE_MAX && K >= 8 && K <= MOE_DENSE_MAX && K % 8 == 0;
+}
+inline bool half_type(int dtype) { return dtype == MOE_BF16 || dtype == MOE_F16; }
+inline bool aligned2(const void* p) { return ((uintptr_t)p & 1) == 0; }
+inline bool aligned256(const void* p) { return ((uintptr_t)p & 255) == 0; }
+inline long long padded(int n) { return ((long long)n + 7) / 8 * 8; }
+
+int dense(int kind, int dtype, const DenseOperand& P, const DenseOperand& Q, const DenseArgs& g, cudaStream_t st) {
+  return dtype == MOE_BF16 ? dense_product_bf16(kind, P, Q, g, st) : dense_product_f16(kind, P, Q, g, st);
+}
+
+// dx = d W and dW = d^T x; d is [T, n] with rows of ldd
+int dense_backward(int dtype, const void* d, long long ldd, int T, int n, const void* x, int K, const void* W, void* dx, void* dW,
+                   int32_t* status, cudaStream_t st) {
+  int rc = MOE_OK;
+  if (dx) {
+    DenseArgs g = {T, K, n, dx, nullptr, nullptr, nullptr, MOE_ACT_NONE, aligned16(dx), 0, status, 0};
+    rc = dense(kDenseDx, dtype, {d, false, T, ldd}, {W, true, K, K}, g, st);
+  }
+  if (rc == MOE_OK && dW) {
+    DenseArgs g = {n, K, T, dW, nullptr, nullptr, nullptr, MOE_ACT_NONE, aligned16(dW), 0, status, 0};
+    rc = dense(kDenseDw, dtype, {d, true, n, ldd}, {x, true, K, K}, g, st);
+  }
+  return rc;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_linear(const void* x, int T, int K, const void* W, int N, int dtype, const void* bias, const void* residual, int act,
+                          void* y, void* slope, int32_t* status, moe_stream_t stream) {
+  if (!dense_shape_ok(T, N, K) || !half_type(dtype) || act < MOE_ACT_NONE || act > MOE_ACT_GELU_TANH) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !W || !y || !aligned16(x) || !aligned16(W) || !aligned2(y) || !aligned2(bias) || !aligned2(residual) || !aligned2(slope))
+    return MOE_ERR_INVALID_ARG;
+  const bool vec = N % 8 == 0 && aligned16(y) && aligned16(residual) && aligned16(slope);
+  DenseArgs g = {T, N, K, y, bias, residual, slope, act, vec, N % 8 == 0 && aligned16(bias), status, 0};
+  return dense(kDenseLinear, dtype, {x, false, T, K}, {W, false, N, K}, g, (cudaStream_t)stream);
+}
+
+extern "C" int moe_linear_bwd_ws_bytes(int T, int N, int K, size_t* bytes) {
+  if (!bytes || !dense_shape_ok(T, N, K)) return MOE_ERR_INVALID_ARG;
+  *bytes = (size_t)T * padded(N) * 2;
+  return MOE_OK;
+}
+
+extern "C" int moe_linear_bwd(const void* dy, const void* x, int T, int K, const void* W, int N, int dtype, const void* slope, void* dx,
+                              void* dW, void* dbias, void* ws, size_t ws_bytes, int32_t* status, moe_stream_t stream) {
+  if (!dense_shape_ok(T, N, K) || !half_type(dtype)) return MOE_ERR_INVALID_ARG;
+  if (!aligned2(dx) || !aligned2(dW) || !aligned2(dbias)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (T == 0) {   // sums over no rows
+    if (dW && cudaMemsetAsync(dW, 0, (size_t)N * K * 2, st) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dbias && cudaMemsetAsync(dbias, 0, (size_t)N * 2, st) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  size_t need = 0;
+  moe_linear_bwd_ws_bytes(T, N, K, &need);
+  if (!dy || !aligned2(dy) || !aligned2(slope) || !ws || !aligned256(ws) || ws_bytes < need) return MOE_ERR_INVALID_ARG;
+  if ((dx && (!W || !aligned16(W))) || (dW && (!x || !aligned16(x)))) return MOE_ERR_INVALID_ARG;
+  // without an activation dy itself is d, where the copy engine can read its rows
+  const bool direct = !slope && N % 8 == 0 && aligned16(dy);
+  const bool products = dx || dW;
+  if (dbias || (products && !direct)) {
+    void* d = products && !direct ? ws : nullptr;
+    const int rc = dtype == MOE_BF16 ? launch_d<__nv_bfloat16>(dy, slope, T, N, d, padded(N), dbias, st)
+                                     : launch_d<__half>(dy, slope, T, N, d, padded(N), dbias, st);
+    if (rc) return rc;
+  }
+  return dense_backward(dtype, direct ? dy : ws, padded(N), T, N, x, K, W, dx, dW, status, st);
+}
+
+extern "C" int moe_gated(const void* x, int T, int H, const void* W1, int F, int dtype, int act, void* h, void* factors, int32_t* status,
+                         moe_stream_t stream) {
+  if (F < 1 || F > MOE_DENSE_MAX / 2 || !dense_shape_ok(T, 2 * F, H) || !half_type(dtype) || act < MOE_ACT_NONE || act > MOE_ACT_GELU_TANH)
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !W1 || !h || !aligned16(x) || !aligned16(W1) || !aligned2(h) || !aligned2(factors)) return MOE_ERR_INVALID_ARG;
+  DenseArgs g = {T, F, H, h, nullptr, nullptr, factors, act, F % 8 == 0 && aligned16(h) && aligned16(factors), 0, status, 0};
+  return dense(kDenseGated, dtype, {x, false, T, H}, {W1, false, 2LL * F, H}, g, (cudaStream_t)stream);
+}
+
+extern "C" int moe_gated_bwd_ws_bytes(int T, int F, int H, size_t* bytes) {
+  if (!bytes || F < 1 || F > MOE_DENSE_MAX / 2 || !dense_shape_ok(T, 2 * F, H)) return MOE_ERR_INVALID_ARG;
+  *bytes = (size_t)T * padded(2 * F) * 2;
+  return MOE_OK;
+}
+
+extern "C" int moe_gated_bwd(const void* dh, const void* x, int T, int H, const void* W1, int F, int dtype, const void* factors, void* dx,
+                             void* dW1, void* ws, size_t ws_bytes, int32_t* status, moe_stream_t stream) {
+  if (F < 1 || F > MOE_DENSE_MAX / 2 || !dense_shape_ok(T, 2 * F, H) || !half_type(dtype)) return MOE_ERR_INVALID_ARG;
+  if (!aligned2(dx) || !aligned2(dW1)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (T == 0) {   // sums over no rows
+    if (dW1 && cudaMemsetAsync(dW1, 0, (size_t)2 * F * H * 2, st) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  size_t need = 0;
+  moe_gated_bwd_ws_bytes(T, F, H, &need);
+  if (!dh || !factors || !aligned2(dh) || !aligned2(factors) || !ws || !aligned256(ws) || ws_bytes < need) return MOE_ERR_INVALID_ARG;
+  if ((dx && (!W1 || !aligned16(W1))) || (dW1 && (!x || !aligned16(x)))) return MOE_ERR_INVALID_ARG;
+  if (!dx && !dW1) return MOE_OK;
+  const int rc = dtype == MOE_BF16 ? launch_gated_d<__nv_bfloat16>(dh, factors, T, F, ws, padded(2 * F), st)
+                                   : launch_gated_d<__half>(dh, factors, T, F, ws, padded(2 * F), st);
+  if (rc) return rc;
+  return dense_backward(dtype, ws, padded(2 * F), T, 2 * F, x, H, W1, dx, dW1, status, st);
+}

@@ -1,0 +1,6 @@
+// dense_bf16.cu: the dense products of bf16 operands.
+#include "dense_host.cuh"
+
+int moe::dense_product_bf16(int kind, const DenseOperand& P, const DenseOperand& Q, const DenseArgs& g, cudaStream_t st) {
+  return dense_product<__nv_bfloat16>(kind, P, Q, g, st);
+}

@@ -1,0 +1,220 @@
+// dense_few.cuh: the dense product for few rows (or few tiles): bound by
+// reading Q, or by how many SMs have work.
+//
+// Roles are swapped against dense_pair.cuh: 128 rows j of Q (gated: 64 gate rows
+// and the 64 up rows beside them) are the tensor core's M, and nt = 16 to 256
+// rows i of P its N, so one row i costs a product of 128 x 16 and not one of 128 x
+// 128.  The contraction is split over the CTAs of a cluster: each streams its
+// share of k through a ring of stages into its own accumulator, then all lay their
+// sums in shared memory, and each CTA adds up its part of the outputs over the
+// cluster, in the CTAs' order, and finishes it.  No atomics, no workspace, one
+// launch; results do not change from run to run.
+#pragma once
+
+#include "dense.cuh"
+
+namespace moe {
+
+constexpr int kDFewThreads = 256;
+constexpr int kDFewMaxStages = 12;
+constexpr int kDFewMaxSplit = 8;
+
+struct DFewShared {
+  uint64_t full[kDFewMaxStages], empty[kDFewMaxStages], tfull;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+inline uint32_t dfew_stage_bytes(int nt) { return 2 * kDenseChunk + (uint32_t)nt * 128; }
+inline size_t dfew_smem_bytes(int nt, int stages) { return 1024 + (size_t)stages * dfew_stage_bytes(nt) + sizeof(DFewShared); }
+
+struct DFewPlan {
+  int nt, stages, split;   // tokens a tile, ring stages, CTAs a cluster
+  int ti;                  // tiles of i
+};
+
+MOE_DEV float ld_shared_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// 16 consecutive fp32 TMEM columns of this thread's lane.
+MOE_DEV void tmem_drain16(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Q's rows j are the M operand, P's rows i the N operand.
+template <typename T, bool PMN, bool QMN, int EPI>
+__global__ void __launch_bounds__(kDFewThreads)
+    dense_few_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                     const __grid_constant__ DenseArgs g, const DFewPlan plan) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const uint32_t stage_bytes = 2 * kDenseChunk + (uint32_t)plan.nt * 128;
+  DFewShared* sh = reinterpret_cast<DFewShared*>(ring + (size_t)plan.stages * stage_bytes);
+  const int warp = threadIdx.x >> 5;
+  const int split = plan.split, rank = split > 1 ? (int)cluster_ctarank() : 0;
+  const int tile = (int)blockIdx.x / split;
+  constexpr int kRows = EPI == kEpiGated ? 64 : 128;   // columns of out a tile
+  const int i0 = tile % plan.ti * plan.nt, j0 = tile / plan.ti * kRows;
+  const int KB = (g.K + kDenseBK - 1) / kDenseBK;
+  const int kb0 = (int)((long long)KB * rank / split), kb1 = (int)((long long)KB * (rank + 1) / split);
+  const uint32_t cols = plan.nt < 32 ? 32u : (uint32_t)plan.nt;
+
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmP);
+    tma_prefetch_desc(&tmQ);
+    for (int s = 0; s < plan.stages; ++s) {
+      mbar_init(smem_u32(&sh->full[s]), 1);
+      mbar_init(smem_u32(&sh->empty[s]), 1);
+    }
+    mbar_init(smem_u32(&sh->tfull), 1);
+    sh->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sh->tmem_base), cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+
+  if (warp == 0) {
+    if (elect_one()) {
+      int s = 0, issued = 0;
+      uint32_t ph = 1;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(smem_u32(&sh->empty[s]), ph, &sh->abort_flag, g.status, g.timeout_ns)) break;
+        const uint32_t full = smem_u32(&sh->full[s]), q = smem_u32(ring + (size_t)s * stage_bytes), p = q + 2 * kDenseChunk;
+        mbar_arrive_expect_tx(full, stage_bytes);
+        const int k0 = kb * kDenseBK;
+        if (QMN) {
+          tma_load_2d(q, &tmQ, j0, k0, full);
+          tma_load_2d(q + kDenseChunk, &tmQ, j0 + 64, k0, full);
+        } else if (EPI == kEpiGated) {
+          tma_load_2d(q, &tmQ, k0, j0, full);
+          tma_load_2d(q + kDenseChunk, &tmQ, k0, g.J + j0, full);
+        } else {
+          tma_load_2d(q, &tmQ, k0, j0, full);
+        }
+        if (PMN)
+          for (int c = 0; c < plan.nt / 64; ++c) tma_load_2d(p + c * kDenseChunk, &tmP, i0 + 64 * c, k0, full);
+        else
+          tma_load_2d(p, &tmP, k0, i0, full);
+        ++issued;
+        if (++s == plan.stages) { s = 0; ph ^= 1u; }
+      }
+      // no copy may be in flight at the end, even where a wait gave up
+      int dummy = 0;
+      for (int i = max(0, issued - plan.stages); i < issued; ++i)
+        mbar_wait(smem_u32(&sh->full[i % plan.stages]), (uint32_t)(i / plan.stages) & 1u, &dummy, nullptr, g.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_f16<T>(128, 0, QMN, PMN) | ((uint32_t)(plan.nt >> 3) << 17);
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      ok = mbar_wait(smem_u32(&sh->full[s]), ph, &sh->abort_flag, g.status, g.timeout_ns);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t q = smem_u32(ring + (size_t)s * stage_bytes), p = q + 2 * kDenseChunk;
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kDenseBK / 16; ++k)
+          umma_f16(tmem, operand_desc<QMN>(q, k), operand_desc<PMN>(p, k), idesc, kb > kb0 || k > 0 ? 1u : 0u);
+        umma_commit(smem_u32(&sh->empty[s]));
+      }
+      __syncwarp();
+      if (++s == plan.stages) { s = 0; ph ^= 1u; }
+    }
+    // every product issued is complete (also where a wait gave up: nothing may be in flight at the end)
+    if (elect_one()) umma_commit(smem_u32(&sh->tfull));
+    __syncwarp();
+  }
+  // tfull comes even after a wait that gave up
+  int dummy = 0;
+  mbar_wait(smem_u32(&sh->tfull), 0u, &dummy, g.status, g.timeout_ns + g.timeout_ns / 2);
+  tc_fence_after();
+
+  // this CTA's sums, [i][j] with j contiguous, over the ring (every stage has been read)
+  float* sums = reinterpret_cast<float*>(ring);
+  const int tv = min(plan.nt, g.I - i0);
+  {
+    const int q = warp & 3, row = 32 * q + (threadIdx.x & 31);
+    for (int c = (warp >> 2) * 16; c < tv; c += 32) {
+      float v[16];
+      tmem_drain16(tmem + ((uint32_t)(32 * q) << 16) + c, v);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sums[(c + e) * 128 + row] = v[e];
+    }
+  }
+  tc_fence_before();
+  if (split > 1) cluster_sync();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, cols);
+  }
+
+  // this CTA's part of the tile's outputs
+  const uint32_t local = smem_u32(sums);
+  uint32_t peer[kDFewMaxSplit];
+#pragma unroll
+  for (int r = 0; r < kDFewMaxSplit; ++r) peer[r] = r < split ? mapa_shared(local, (uint32_t)r) : 0u;
+  const T* bias = static_cast<const T*>(g.bias);
+  const T* residual = static_cast<const T*>(g.residual);
+  T* out = static_cast<T*>(g.out);
+  T* aux = static_cast<T*>(g.aux);
+  with_act(EPI == kEpiPlain ? MOE_ACT_NONE : g.act, [&](auto act) {
+    for (int e = rank * kDFewThreads + (int)threadIdx.x; e < tv * kRows; e += split * kDFewThreads) {
+      const int t = e / kRows, r = e % kRows, j = j0 + r;
+      const long long i = i0 + t;
+      if (j >= g.J) continue;
+      const uint32_t at = (uint32_t)(t * 128 + r) * 4u;
+      float a[kDFewMaxSplit], b[kDFewMaxSplit];
+#pragma unroll
+      for (int c = 0; c < kDFewMaxSplit; ++c)
+        if (c < split) {
+          a[c] = ld_shared_cluster_f32(peer[c] + at);
+          if (EPI == kEpiGated) b[c] = ld_shared_cluster_f32(peer[c] + at + 256u);
+        }
+      float v = a[0], u = EPI == kEpiGated ? b[0] : 0.f;
+#pragma unroll
+      for (int c = 1; c < kDFewMaxSplit; ++c)
+        if (c < split) {
+          v += a[c];
+          if (EPI == kEpiGated) u += b[c];
+        }
+      const long long o = i * g.J + j;
+      if (EPI == kEpiGated) {
+        const float2 s = act_slope<decltype(act)::value>(v);
+        if (aux) {
+          aux[2 * i * g.J + j] = from_f32<T>(s.y * u);
+          aux[2 * i * g.J + g.J + j] = from_f32<T>(s.x);
+        }
+        v = s.x * u;
+      } else if (EPI == kEpiLinear) {
+        if (bias) v += to_f32(bias[j]);
+        const float2 s = act_slope<decltype(act)::value>(v);
+        if (aux) aux[o] = from_f32<T>(s.y);
+        v = s.x;
+        if (residual) v += to_f32(residual[o]);
+      }
+      out[o] = from_f32<T>(v);
+    }
+  });
+  if (split > 1) cluster_sync();   // no CTA leaves while another reads its sums
+}
+
+}  // namespace moe

@@ -1,0 +1,95 @@
+// dense_host.cuh: the launches of one dense product, for one 16-bit type.
+#pragma once
+
+#include "dense_few.cuh"
+#include "dense_pair.cuh"
+#include "dense_plan.h"
+#include "host_util.h"
+
+namespace moe {
+
+// One operand: `rows` of i (or j) by g.K of k; ld is the length of its rows in memory.
+struct DenseOperand {
+  const void* p;
+  bool mn;         // rows contiguous in memory, k strided
+  long long rows, ld;
+};
+
+// Swizzled map of one operand: boxes of 64 k x `box` rows, or 64 rows x 64 k.
+template <typename T>
+bool encode_operand(CUtensorMap* map, const DenseOperand& o, int K, int box) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t d[2] = {(cuuint64_t)(o.mn ? o.rows : K), (cuuint64_t)(o.mn ? K : o.rows)}, s[1] = {(cuuint64_t)o.ld * 2};
+  cuuint32_t b[2] = {64, (cuuint32_t)(o.mn ? 64 : box)}, es[2] = {1, 1};
+  return enc(map, std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+             const_cast<void*>(o.p), d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, bool PMN, bool QMN, int EPI>
+int launch_dense(const DenseOperand& P, const DenseOperand& Q, DenseArgs g, cudaStream_t st) {
+  const int nsm = device_sm_count();
+  if (nsm < 2 || !device_has_tcgen05()) return MOE_ERR_UNSUPPORTED;
+  g.timeout_ns = 2000000000ull;
+  const DensePlan plan = dense_plan(g.I, g.J, g.K, EPI == kEpiGated, PMN, nsm);
+  CUtensorMap tmP, tmQ;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (plan.pair) {
+    if (!encode_operand<T>(&tmP, P, g.K, 128) || !encode_operand<T>(&tmQ, Q, g.K, 128)) return MOE_ERR_CUDA;
+    auto kernel = dense_pair_kernel<T, PMN, QMN, EPI>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDPairSmemBytes) != cudaSuccess) return MOE_ERR_CUDA;
+    attr[0].val.clusterDim.x = 2;
+    cfg.blockDim = dim3(kDPairThreads);
+    cfg.dynamicSmemBytes = kDPairSmemBytes;
+    cfg.gridDim = dim3(2 * (nsm / 2));
+    int resident = 0;
+    if (cudaOccupancyMaxActiveClusters(&resident, kernel, &cfg) != cudaSuccess || resident < 1) return MOE_ERR_CUDA;
+    constexpr int kTileJ = EPI == kEpiGated ? 128 : 256;
+    const long long tiles = ((long long)g.I + 255) / 256 * (((long long)g.J + kTileJ - 1) / kTileJ);
+    if (tiles > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
+    cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(std::min(resident, nsm / 2), tiles));
+    return cudaLaunchKernelEx(&cfg, kernel, tmP, tmQ, g) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  if (!encode_operand<T>(&tmP, P, g.K, plan.nt) || !encode_operand<T>(&tmQ, Q, g.K, EPI == kEpiGated ? 64 : 128)) return MOE_ERR_CUDA;
+  auto kernel = dense_few_kernel<T, PMN, QMN, EPI>;
+  const size_t smem = dfew_smem_bytes(plan.nt, plan.stages);
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return MOE_ERR_CUDA;
+  constexpr int kRows = EPI == kEpiGated ? 64 : 128;
+  DFewPlan fp;
+  fp.nt = plan.nt;
+  fp.stages = plan.stages;
+  fp.split = plan.split;
+  fp.ti = (int)(((long long)g.I + plan.nt - 1) / plan.nt);
+  const long long ctas = (long long)fp.ti * (((long long)g.J + kRows - 1) / kRows) * plan.split;
+  if (ctas > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+  attr[0].val.clusterDim.x = (unsigned)plan.split;
+  cfg.blockDim = dim3(kDFewThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3((unsigned)ctas);
+  return cudaLaunchKernelEx(&cfg, kernel, tmP, tmQ, g, fp) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// The products that the operators take: x W^T (linear, gated), d W and d^T x.
+enum { kDenseLinear = 0, kDenseGated = 1, kDenseDx = 2, kDenseDw = 3 };
+
+template <typename T>
+int dense_product(int kind, const DenseOperand& P, const DenseOperand& Q, const DenseArgs& g, cudaStream_t st) {
+  switch (kind) {
+    case kDenseLinear: return launch_dense<T, false, false, kEpiLinear>(P, Q, g, st);
+    case kDenseGated: return launch_dense<T, false, false, kEpiGated>(P, Q, g, st);
+    case kDenseDx: return launch_dense<T, false, true, kEpiPlain>(P, Q, g, st);
+    default: return launch_dense<T, true, true, kEpiPlain>(P, Q, g, st);
+  }
+}
+
+int dense_product_bf16(int kind, const DenseOperand& P, const DenseOperand& Q, const DenseArgs& g, cudaStream_t st);
+int dense_product_f16(int kind, const DenseOperand& P, const DenseOperand& Q, const DenseArgs& g, cudaStream_t st);
+
+}  // namespace moe

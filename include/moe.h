@@ -494,6 +494,92 @@ int moe_layer_few(const uint16_t* x, int T, int H, const uint16_t* router, int E
                   int32_t* topk_ids, float* topk_w, uint16_t* out, void* ws, size_t ws_bytes,
                   int32_t* status, moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Dense operators beside the experts, for serving and for training: the norm
+ * before a router, a shared expert's gated block, projections that end in the
+ * residual stream.  Tensors are contiguous.  Sums are fp32 and taken in a fixed
+ * order: a call's results do not change from run to run.
+ *
+ * Types: MOE_BF16 or MOE_F16 for every tensor of a call (layer norm also takes
+ * MOE_F32, and its weight and bias may be MOE_F32 beside rows of another type).
+ * Pointers are aligned to their elements; where a product reads a tensor, to 16
+ * bytes.  T = 0 is a call without rows: nothing is written but sums over them.
+ * ------------------------------------------------------------------------- */
+typedef enum moe_dtype { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;
+
+/* Activations: a; max(a, 0); a / (1 + exp(-a)); a * (1 + erf(a / sqrt 2)) / 2;
+ * a * (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3))) / 2. */
+typedef enum moe_act {
+  MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4
+} moe_act;
+
+/* moe_layernorm: each row of x [T, H] to
+ *   y = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps)
+ * with the mean and the variance (over H, not H - 1) of that row in fp32, one
+ * rounding at the end.
+ *   weight, bias  device wdtype [H] (dtype or MOE_F32), each NULL where there is none.
+ *   y             device dtype [T, H]; may be x.
+ *   mean, rstd    device f32 [T], written where given: the backward pass reads them.
+ * Limits: 1 <= H <= MOE_NORM_MAX_H, eps >= 0. */
+#define MOE_NORM_MAX_H 16384
+int moe_layernorm(const void* x, int T, int H, int dtype, const void* weight, const void* bias, int wdtype,
+                  float eps, void* y, float* mean, float* rstd, moe_stream_t stream);
+
+/* moe_layernorm_bwd: with n = (x - mean) * rstd and g = dy * weight,
+ *   dx = rstd * (g - mean_H(g) - n * mean_H(g * n)),  dweight = sum_t dy * n,  dbias = sum_t dy.
+ *   dx              device dtype [T, H]; may be dy or x.
+ *   dweight, dbias  device wdtype [H], each NULL where it is not wanted.
+ *   ws              device workspace of moe_layernorm_bwd_ws_bytes, 16-byte aligned; any contents. */
+int moe_layernorm_bwd_ws_bytes(int T, int H, size_t* bytes);
+int moe_layernorm_bwd(const void* dy, const void* x, int T, int H, int dtype, const void* weight, int wdtype,
+                      const float* mean, const float* rstd, void* dx, void* dweight, void* dbias, void* ws,
+                      size_t ws_bytes, moe_stream_t stream);
+
+/* moe_linear: y = act(x W^T + bias) + residual, fp32 from the products to the
+ * one rounding at the end.
+ *   x         device dtype [T, K], 16-byte aligned; W device dtype [N, K], 16-byte aligned.
+ *   bias      device dtype [N] or NULL; residual device dtype [T, N] or NULL.
+ *   y         device dtype [T, N]; may be residual.
+ *   slope     device dtype [T, N] or NULL: act'(x W^T + bias), written for the
+ *             backward pass (from the unrounded sums; one rounding).
+ * A bounded wait that gives up writes MOE_ERR_TIMEOUT to *status.
+ * Limits: K a multiple of 8, 8 <= K <= MOE_DENSE_MAX; 1 <= N <= MOE_DENSE_MAX; T <= 2^24. */
+#define MOE_DENSE_MAX (1 << 20)
+int moe_linear(const void* x, int T, int K, const void* W, int N, int dtype, const void* bias,
+               const void* residual, int act, void* y, void* slope, int32_t* status, moe_stream_t stream);
+
+/* moe_linear_bwd: with d = dy * slope (slope NULL: d = dy, no activation) rounded to dtype for the
+ * products,
+ *   dx = d W,  dW = d^T x,  dbias = sum_t dy * slope (fp32, from the unrounded d);
+ * the residual's gradient is dy itself.
+ *   dx device dtype [T, K], dW device dtype [N, K], dbias device dtype [N]; each NULL where
+ *   it is not wanted (W, or x, is then not read and may be NULL).
+ *   ws device workspace of moe_linear_bwd_ws_bytes, 256-byte aligned; any contents. */
+int moe_linear_bwd_ws_bytes(int T, int N, int K, size_t* bytes);
+int moe_linear_bwd(const void* dy, const void* x, int T, int K, const void* W, int N, int dtype,
+                   const void* slope, void* dx, void* dW, void* dbias, void* ws, size_t ws_bytes,
+                   int32_t* status, moe_stream_t stream);
+
+/* moe_gated: the gated feed-forward block's first half in one kernel,
+ *   h = act(x Wg^T) * (x Wu^T),  Wg and Wu the rows [0, F) and [F, 2F) of W1,
+ * fp32 from the products to the one rounding at the end.
+ *   x device dtype [T, H], W1 device dtype [2F, H], 16-byte aligned; h device dtype [T, F].
+ *   factors  device dtype [T, 2F] or NULL: what the backward pass multiplies dh
+ *            by, u * act'(g) then act(g) (from the unrounded sums; one rounding).
+ * Limits: H a multiple of 8, 8 <= H <= MOE_DENSE_MAX; 1 <= F <= MOE_DENSE_MAX / 2; T <= 2^24. */
+int moe_gated(const void* x, int T, int H, const void* W1, int F, int dtype, int act, void* h,
+              void* factors, int32_t* status, moe_stream_t stream);
+
+/* moe_gated_bwd: with d = [dh * factors[:, :F], dh * factors[:, F:]] rounded to
+ * dtype for the products,  dx = d W1,  dW1 = d^T x.
+ *   dx device dtype [T, H], dW1 device dtype [2F, H]; each NULL where it is not wanted
+ *   (W1, or x, is then not read and may be NULL).
+ *   ws device workspace of moe_gated_bwd_ws_bytes, 256-byte aligned; any contents. */
+int moe_gated_bwd_ws_bytes(int T, int F, int H, size_t* bytes);
+int moe_gated_bwd(const void* dh, const void* x, int T, int H, const void* W1, int F, int dtype,
+                  const void* factors, void* dx, void* dW1, void* ws, size_t ws_bytes, int32_t* status,
+                  moe_stream_t stream);
+
 /* Number of SMs of the current device (0 on error): the persistent grids'
  * size. */
 int moe_device_sm_count(void);
