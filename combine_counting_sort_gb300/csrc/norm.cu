@@ -1,315 +1,199 @@
-// norm.cu: layer norm over each row of [T, H], forward and backward.
+// norm.cu: layer norm over each row of [T, H], forward.
 //
 //   n = (x - mean) * rstd,  rstd = 1 / sqrt(var + eps),  y = n * weight + bias
-//   g = dy * weight,  dx = rstd * (g - mean(g) - n * mean(g * n))
-//   dweight = sum_t dy * n,  dbias = sum_t dy
 //
-// Memory bound: forward reads x and writes y, backward reads x and dy and
-// writes dx, once each.  A row lies in the registers of the threads that work
-// on it, so mean and variance are taken in two passes over registers (no
-// cancellation for rows far from zero) while memory is read once.  All sums
-// are fp32, in a fixed order: results do not change from run to run.
-#include "dtype.cuh"
-#include "host_util.h"
+// Memory bound: reads x and writes y once.  Mean and variance come from one
+// exchange between a row's warps: each takes its own mean, then its squares about
+// that mean, and the warps' sums and squares are joined about the row's mean, so
+// nothing cancels for rows far from zero.  Sums are fp32 in a fixed order.
+#include "norm.cuh"
 
 namespace moe {
 
-constexpr int kNormMaxH = MOE_NORM_MAX_H;
+// Blocks an SM: two, unless registers hold weights and biases too.
+template <typename T, int NV, bool MASK>
+constexpr int kFwdPerSm = !MASK && NV * kVec16<T> <= 32 ? 2 : 1;
 
-template <int TPR>
-struct RowGroup {   // TPR threads of a block that work on one row
-  static constexpr int kWarps = TPR / 32;
-  // Sum of (a, b) over the group; every thread gets it.  `scratch` holds one
-  // float2 per warp of the block; the caller alternates between two of them.
-  static MOE_DEV float2 sum(float a, float b, float2* scratch) {
+template <typename T, typename W, int TPR, int NV, int D, bool MASK>
+__global__ void __launch_bounds__(kNormThreads, kFwdPerSm<T, NV, MASK>) norm_fwd_kernel(const NormArgs p) {
+  constexpr int V = kVec16<T>, P = V / 2, WARPS = TPR / 32, GROUPS = kNormThreads / TPR;
+  extern __shared__ uint8_t ring[];   // [D][NV][threads] vectors
+  __shared__ float2 stats[2][kNormThreads / 32];
+  __shared__ float counts[kNormThreads / 32];
+  const int grp = (int)threadIdx.x / TPR, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long groups = (long long)gridDim.x * GROUPS, g = (long long)blockIdx.x * GROUPS + grp;
+  const RowPart<T, TPR, NV, MASK> part(p.H, g);
+  constexpr uint32_t STEP = kNormThreads * 16, SLOT = NV * STEP;
+  uint8_t* mine = ring + threadIdx.x * 16;
+  const uint32_t mine_at = smem_u32(mine);
+  const long long stride = groups * p.H;
+  const T* src = static_cast<const T*>(p.x) + g * p.H + part.first;   // vector 0 of the next row to fetch
+  T* dst = static_cast<T*>(p.y) + g * p.H + part.first;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    if (kWarps == 1) return make_float2(a, b);
-    const int warp = threadIdx.x >> 5, first = (threadIdx.x / TPR) * kWarps;
-    if ((threadIdx.x & 31) == 0) scratch[warp] = make_float2(a, b);
-    if (TPR == (int)blockDim.x) __syncthreads();
-    else asm volatile("bar.sync %0, %1;" ::"r"((int)(threadIdx.x / TPR) + 1), "n"(TPR) : "memory");
-    a = b = 0.f;
-    // every lane sums the warps' values in the same order
-    const int lane = threadIdx.x & 31;
-    if (lane < kWarps) { const float2 v = scratch[first + lane]; a = v.x; b = v.y; }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    return make_float2(a, b);
+  for (int d = 0; d < D - 1; ++d, src += stride) {
+    if (g + d * groups < p.T) part.fetch(src, g + d * groups == p.T - 1, mine_at + d * SLOT, STEP);
+    cp_async_commit();
   }
-};
-
-// weight or bias values j, .., j + V - 1 as fp32: the rows' type or fp32 (where
-// V > 1, 16-byte aligned), `none` where there is no such tensor.
-template <typename T, int V>
-MOE_DEV void param(const void* p, bool f32, int j, float none, float* out) {
-  if (!p) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) out[v] = none;
-  } else if (f32) {
-    constexpr int L = V < 4 ? V : 4;
-#pragma unroll
-    for (int v = 0; v < V; v += L) {
-      const Vec<float, L> a = *reinterpret_cast<const Vec<float, L>*>(static_cast<const float*>(p) + j + v);
-#pragma unroll
-      for (int i = 0; i < L; ++i) out[v + i] = a.v[i];
-    }
-  } else {
-    const Vec<T, V> a = *reinterpret_cast<const Vec<T, V>*>(static_cast<const T*>(p) + j);
-#pragma unroll
-    for (int v = 0; v < V; ++v) out[v] = to_f32(a.v[v]);
+  W* const ws = reinterpret_cast<W*>(ring + D * SLOT);
+  W* const bs = ws + p.H;
+  ParamVec<T, W> w[MASK ? NV : 1], b[MASK ? NV : 1];
+  if (!MASK) {
+    copy_params(ws, p.weight, 1.f, p.H);
+    copy_params(bs, p.bias, 0.f, p.H);
   }
-}
-
-struct NormArgs {
-  const void* x;
-  const void* dy;
-  const void* weight;
-  const void* bias;
-  bool wf32;
-  int T, H;
-  float eps;
-  void* y;      // y, or dx
-  float* mean;
-  float* rstd;
-  float* part;  // backward: [groups][2][H] sums of each group's rows
-};
-
-// ---------------------------------------------------------------- forward
-
-// TPR threads a row, NV vectors of V values each: H <= TPR * NV * V.
-template <typename T, int V, int NV, int TPR, int BLOCK>
-__global__ void __launch_bounds__(BLOCK) norm_fwd_kernel(const NormArgs p) {
-  using Vc = Vec<T, V>;
-  __shared__ float2 scratch[2][BLOCK / 32];
-  const int tid = threadIdx.x % TPR;
-  const long long row = (long long)blockIdx.x * (BLOCK / TPR) + threadIdx.x / TPR;
-  const bool live = row < p.T;
-  const T* x = static_cast<const T*>(p.x) + (live ? row : 0) * p.H;
-  Vc raw[NV];
-  float s = 0.f;
+  int mine_n = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int j = (i * TPR + tid) * V;
-    if (j < p.H) raw[i] = *reinterpret_cast<const Vc*>(x + j);
+    if (MASK) {
+      w[i] = part.template params<W>(p.weight, 1.f, i);
+      b[i] = part.template params<W>(p.bias, 0.f, i);
+    }
+    mine_n += max(0, part.hi(i) - part.lo(i));
   }
+  // values of a row in each warp: the same for every row
+  const float warp_n = warp_sum((float)mine_n), warp_inv = warp_n > 0.f ? 1.f / warp_n : 0.f;
+  if (lane == 0) counts[warp] = warp_n;
+  __syncthreads();
+  const int peer = grp * WARPS + lane % WARPS;   // the warp whose sums this lane joins
+  const float peer_n = counts[peer], peer_inv = peer_n > 0.f ? 1.f / peer_n : 0.f, inv_h = 1.f / (float)p.H;
+
+  int slot = 0, turn = 0;
+  for (long long row = g; row < p.T; row += groups, turn ^= 1) {
+    cp_async_wait<D - 2>();
+    f32x2 v[NV][P];
+    f32x2 s = 0;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if ((i * TPR + tid) * V < p.H) {
+    for (int i = 0; i < NV; ++i)
+      if (part.any(i)) {
+        Pairs<T>::get(*reinterpret_cast<const uint4*>(mine + slot * SLOT + i * STEP), v[i]);
+        part.mask(i, v[i]);
 #pragma unroll
-      for (int v = 0; v < V; ++v) s += to_f32(raw[i].v[v]);
-    }
-  const float mean = RowGroup<TPR>::sum(s, 0.f, scratch[0]).x / (float)p.H;
-  float q = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if ((i * TPR + tid) * V < p.H) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float d = to_f32(raw[i].v[v]) - mean;
-        q = fmaf(d, d, q);
+        for (int e = 0; e < P; ++e) s = add2(s, v[i][e]);
       }
+    const int next = slot == 0 ? D - 1 : slot - 1;   // the slot read a row ago
+    const long long ahead = row + (D - 1) * groups;
+    if (ahead < p.T) part.fetch(src, ahead == p.T - 1, mine_at + next * SLOT, STEP);
+    cp_async_commit();
+    src += stride;
+    slot = slot == D - 1 ? 0 : slot + 1;
+
+    const float warp_s = warp_sum(sum2(s)), m = warp_s * warp_inv;
+    f32x2 q = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (part.any(i)) {
+        f32x2 d[P];
+#pragma unroll
+        for (int e = 0; e < P; ++e) d[e] = add2(v[i][e], both(-m));
+        part.mask(i, d);
+#pragma unroll
+        for (int e = 0; e < P; ++e) q = fma2(d[e], d[e], q);
+      }
+    const float warp_q = warp_sum(sum2(q));
+    float mean = m, var = warp_q * inv_h;
+    if (WARPS > 1) {
+      if (lane == 0) stats[turn][warp] = make_float2(warp_s, warp_q);
+      group_sync<TPR>();
+      const float2 o = stats[turn][peer];
+      float t = o.x;
+#pragma unroll
+      for (int k = WARPS / 2; k > 0; k >>= 1) t += __shfl_xor_sync(0xffffffffu, t, k);
+      mean = t * inv_h;
+      const float off = o.x * peer_inv - mean;
+      t = fmaf(peer_n * off, off, o.y);
+#pragma unroll
+      for (int k = WARPS / 2; k > 0; k >>= 1) t += __shfl_xor_sync(0xffffffffu, t, k);
+      var = t * inv_h;
     }
-  const float var = RowGroup<TPR>::sum(q, 0.f, scratch[1]).x / (float)p.H;
-  const float rstd = 1.f / sqrtf(var + p.eps);
-  if (!live) return;
-  if (tid == 0) {
+    const float rstd = 1.f / sqrtf(var + p.eps);
+    if (part.tid == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (part.any(i)) {
+        f32x2 wp[P], bp[P], o[P];
+        if (MASK) {
+          w[i].get(wp);
+          b[i].get(bp);
+        } else {
+          reinterpret_cast<const ParamVec<T, W>*>(ws + part.col(i))->get(wp);
+          reinterpret_cast<const ParamVec<T, W>*>(bs + part.col(i))->get(bp);
+        }
+#pragma unroll
+        for (int e = 0; e < P; ++e) o[e] = fma2(mul2(add2(v[i][e], both(-mean)), both(rstd)), wp[e], bp[e]);
+        part.store(dst, i, Pairs<T>::put(o));
+      }
+    dst += stride;
+  }
+  cp_async_wait<0>();
+}
+
+// Tensors that do not start on 16 bytes (and the odd lengths just below 16384): a
+// block a row, read three times.
+template <typename T, typename W>
+__global__ void __launch_bounds__(kNormThreads) norm_fwd_any_kernel(const NormArgs p) {
+  __shared__ float scratch[kNormThreads / 32];
+  const long long row = blockIdx.x;
+  const T* x = static_cast<const T*>(p.x) + row * p.H;
+  T* y = static_cast<T*>(p.y) + row * p.H;
+  float s = 0.f;
+  for (int j = threadIdx.x; j < p.H; j += kNormThreads) s += to_f32(x[j]);
+  const float mean = block_sum(s, scratch) / (float)p.H;
+  s = 0.f;
+  for (int j = threadIdx.x; j < p.H; j += kNormThreads) {
+    const float d = to_f32(x[j]) - mean;
+    s = fmaf(d, d, s);
+  }
+  const float rstd = 1.f / sqrtf(block_sum(s, scratch) / (float)p.H + p.eps);
+  if (threadIdx.x == 0) {
     if (p.mean) p.mean[row] = mean;
     if (p.rstd) p.rstd[row] = rstd;
   }
-  T* y = static_cast<T*>(p.y) + row * p.H;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int j = (i * TPR + tid) * V;
-    if (j < p.H) {
-      float w[V], b[V];
-      param<T, V>(p.weight, p.wf32, j, 1.f, w);
-      param<T, V>(p.bias, p.wf32, j, 0.f, b);
-      Vc o;
-#pragma unroll
-      for (int v = 0; v < V; ++v) o.v[v] = from_f32<T>(fmaf((to_f32(raw[i].v[v]) - mean) * rstd, w[v], b[v]));
-      *reinterpret_cast<Vc*>(y + j) = o;
-    }
-  }
+  for (int j = threadIdx.x; j < p.H; j += kNormThreads)
+    y[j] = from_f32<T>(fmaf((to_f32(x[j]) - mean) * rstd, param<W>(p.weight, j, 1.f), param<W>(p.bias, j, 0.f)));
 }
 
-// ---------------------------------------------------------------- backward
-
-// A group of TPR threads walks rows g, g + groups, ... and keeps its columns'
-// sums for dweight and dbias in registers; the next row's loads are in flight
-// while this one is worked on.
-template <typename T, int V, int NV, int TPR, int BLOCK>
-__global__ void __launch_bounds__(BLOCK) norm_bwd_kernel(const NormArgs p) {
-  using Vc = Vec<T, V>;
-  __shared__ float2 scratch[2][BLOCK / 32];
-  const int tid = threadIdx.x % TPR;
-  const int groups = gridDim.x * (BLOCK / TPR), g = blockIdx.x * (BLOCK / TPR) + threadIdx.x / TPR;
-  const float inv = 1.f / (float)p.H;
-  Vc rx[NV], rd[NV];
-  float w[NV * V], dw[NV * V] = {}, db[NV * V] = {};
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if ((i * TPR + tid) * V < p.H) param<T, V>(p.weight, p.wf32, (i * TPR + tid) * V, 1.f, w + i * V);
-  auto load = [&](long long row) {
-    const T* x = static_cast<const T*>(p.x) + row * p.H;
-    const T* dy = static_cast<const T*>(p.dy) + row * p.H;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int j = (i * TPR + tid) * V;
-      if (j < p.H) {
-        rx[i] = *reinterpret_cast<const Vc*>(x + j);
-        rd[i] = *reinterpret_cast<const Vc*>(dy + j);
-      }
-    }
-  };
-  if (g < p.T) load(g);
-  int turn = 0;
-  for (long long row = g; row < p.T; row += groups, turn ^= 1) {
-    const float mean = p.mean[row], rstd = p.rstd[row];
-    Vc cx[NV], cd[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) { cx[i] = rx[i]; cd[i] = rd[i]; }
-    if (row + groups < p.T) load(row + groups);
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int j = (i * TPR + tid) * V;
-      if (j < p.H) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float n = (to_f32(cx[i].v[v]) - mean) * rstd, d = to_f32(cd[i].v[v]);
-          const float gr = d * w[i * V + v];
-          s1 += gr;
-          s2 = fmaf(gr, n, s2);
-          dw[i * V + v] = fmaf(d, n, dw[i * V + v]);
-          db[i * V + v] += d;
-        }
-      }
-    }
-    const float2 s = RowGroup<TPR>::sum(s1, s2, scratch[turn]);
-    const float m1 = s.x * inv, m2 = s.y * inv;
-    T* dx = static_cast<T*>(p.y) + row * p.H;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int j = (i * TPR + tid) * V;
-      if (j < p.H) {
-        Vc o;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float n = (to_f32(cx[i].v[v]) - mean) * rstd;
-          const float gr = to_f32(cd[i].v[v]) * w[i * V + v];
-          o.v[v] = from_f32<T>(rstd * (gr - m1 - n * m2));
-        }
-        *reinterpret_cast<Vc*>(dx + j) = o;
-      }
-    }
-  }
-  float* pw = p.part + (long long)g * 2 * p.H;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int j = (i * TPR + tid) * V + v;
-      if (j < p.H) {
-        pw[j] = dw[i * V + v];
-        pw[p.H + j] = db[i * V + v];
-      }
-    }
-}
-
-// dweight (blockIdx.y 0) and dbias (1): the groups' sums added up.  A block
-// takes 32 columns, its 16 warps every 16th group.
-template <typename T>
-__global__ void __launch_bounds__(512) norm_sums_kernel(const float* part, int groups, int H, bool wf32, void* dweight,
-                                                        void* dbias) {
-  __shared__ float acc[16][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int j = blockIdx.x * 32 + lane;
-  void* out = blockIdx.y ? dbias : dweight;
-  if (!out) return;
-  float s = 0.f;
-  if (j < H)
-    for (int g = warp; g < groups; g += 16) s += part[((long long)g * 2 + blockIdx.y) * H + j];
-  acc[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && j < H) {
-    s = 0.f;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) s += acc[w][lane];
-    if (wf32) static_cast<float*>(out)[j] = s;
-    else static_cast<T*>(out)[j] = from_f32<T>(s);
-  }
-}
-
-template <typename T, int V, int NV, int TPR>
+template <typename T, typename W, int TPR, int NV, int D, bool MASK>
 int launch_fwd(const NormArgs& p, cudaStream_t st) {
-  constexpr int BLOCK = TPR < 256 ? 256 : TPR;
-  const long long blocks = ((long long)p.T + BLOCK / TPR - 1) / (BLOCK / TPR);
-  norm_fwd_kernel<T, V, NV, TPR, BLOCK><<<(unsigned)blocks, BLOCK, 0, st>>>(p);
+  const size_t smem = (size_t)D * NV * kNormThreads * 16 + (MASK ? 0 : 2 * (size_t)p.H * sizeof(W));
+  auto kernel = norm_fwd_kernel<T, W, TPR, NV, D, MASK>;
+  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024);
+  if (attr != cudaSuccess) return MOE_ERR_CUDA;
+  const int per_sm = smem <= 112 * 1024 ? kFwdPerSm<T, NV, MASK> : 1;
+  kernel<<<norm_blocks(p.T, kNormThreads / TPR, per_sm, device_sm_count()), kNormThreads, smem, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// E values a thread
-template <typename T, int V, int E>
-int fwd_of(const NormArgs& p, cudaStream_t st) {
-  if (p.H <= 32 * E) return launch_fwd<T, V, E / V, 32>(p, st);
-  if (p.H <= 128 * E) return launch_fwd<T, V, E / V, 128>(p, st);
-  if (p.H <= 256 * E) return launch_fwd<T, V, E / V, 256>(p, st);
-  return launch_fwd<T, V, E / V, 1024>(p, st);
-}
-
-template <typename T>
-int fwd_typed(const NormArgs& p, bool vec, cudaStream_t st) {
-  constexpr int V = kVec16<T>;
-  if (!vec) return fwd_of<T, 1, 32>(p, st);
-  // few rows: more threads a row, since one row's latency is the time
-  if (p.T <= 2 * 152 && p.H <= 1024 * 8) return fwd_of<T, V, 8>(p, st);
-  return fwd_of<T, V, 32>(p, st);
-}
-
-// Backward: threads a row by its length, 16 values a thread.
-constexpr int kBwdE = 16;
-inline int bwd_tpr(int H) { return H <= 32 * kBwdE ? 32 : H <= 128 * kBwdE ? 128 : H <= 512 * kBwdE ? 512 : 1024; }
-inline int bwd_block(int tpr) { return tpr < 256 ? 256 : tpr; }
-
-// Groups that walk the rows: a block or two for each SM, no more than rows.
-inline long long bwd_blocks(int T, int H) {
-  const int tpr = bwd_tpr(H), per = bwd_block(tpr) / tpr;
-  return std::min<long long>(((long long)T + per - 1) / per, tpr >= 512 ? 152 : 304);
-}
-
-template <typename T, int V, int TPR>
-int launch_bwd(const NormArgs& p, void* dweight, void* dbias, cudaStream_t st) {
-  constexpr int BLOCK = TPR < 256 ? 256 : TPR;
-  const int blocks = (int)bwd_blocks(p.T, p.H), groups = blocks * (BLOCK / TPR);
-  norm_bwd_kernel<T, V, kBwdE / V, TPR, BLOCK><<<blocks, BLOCK, 0, st>>>(p);
-  if (dweight || dbias)
-    norm_sums_kernel<T><<<dim3((p.H + 31) / 32, 2), 512, 0, st>>>(p.part, groups, p.H, p.wf32, dweight, dbias);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-}
-
-template <typename T, int V>
-int bwd_of(const NormArgs& p, void* dweight, void* dbias, cudaStream_t st) {
-  switch (bwd_tpr(p.H)) {
-    case 32: return launch_bwd<T, V, 32>(p, dweight, dbias, st);
-    case 128: return launch_bwd<T, V, 128>(p, dweight, dbias, st);
-    case 512: return launch_bwd<T, V, 512>(p, dweight, dbias, st);
-    default: return launch_bwd<T, V, 1024>(p, dweight, dbias, st);
+template <typename T, typename W, bool MASK>
+int norm_fwd(const NormArgs& p, cudaStream_t st) {
+  // values a thread: as many as leave two blocks an SM room in registers and shared memory
+  constexpr int V = kVec16<T>, E = sizeof(T) == 2 ? 32 : 16, NV = E / V, D = 2;
+  // few rows: the latency of one is the time, and more threads shorten it
+  if (p.T <= 304 && p.H > 2048 && norm_tpr(p.H, V, 16) <= kNormThreads) return launch_fwd<T, W, 512, 16 / V, D, MASK>(p, st);
+  switch (norm_tpr(p.H, V, E)) {
+    case 32: return launch_fwd<T, W, 32, NV, D, MASK>(p, st);
+    case 64: return launch_fwd<T, W, 64, NV, D, MASK>(p, st);
+    case 128: return launch_fwd<T, W, 128, NV, D, MASK>(p, st);
+    case 256: return launch_fwd<T, W, 256, NV, D, MASK>(p, st);
+    case 512: return launch_fwd<T, W, 512, NV, D, MASK>(p, st);
+    case 1024:   // fp32 beyond 8192 values: weights and biases in registers, for they do not fit beside the ring
+      if (sizeof(T) == 4) return launch_fwd<T, W, 512, 2 * NV, D, true>(p, st);
+    default: break;
   }
+  norm_fwd_any_kernel<T, W><<<p.T, kNormThreads, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-inline size_t elem_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
-
-inline bool norm_shape_ok(int T, int H) { return T >= 0 && H >= 1 && H <= kNormMaxH; }
-
-// a tensor of this type starts where its elements may start
-inline bool elem_aligned(const void* p, int dtype) { return (uintptr_t)p % elem_bytes(dtype) == 0; }
+template <typename T, typename W>
+int norm_fwd(const NormArgs& p, cudaStream_t st) {
+  if (!aligned16(p.x) || !aligned16(p.y)) {
+    norm_fwd_any_kernel<T, W><<<p.T, kNormThreads, 0, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  return p.H % kVec16<T> ? norm_fwd<T, W, true>(p, st) : norm_fwd<T, W, false>(p, st);
+}
 
 }  // namespace moe
 
@@ -324,43 +208,9 @@ extern "C" int moe_layernorm(const void* x, int T, int H, int dtype, const void*
   if (!elem_aligned(x, dtype) || !elem_aligned(y, dtype) || !elem_aligned(weight, wdtype) || !elem_aligned(bias, wdtype) ||
       !elem_aligned(mean, MOE_F32) || !elem_aligned(rstd, MOE_F32))
     return MOE_ERR_INVALID_ARG;
-  NormArgs p = {x, nullptr, weight, bias, wdtype == MOE_F32, T, H, eps, y, mean, rstd, nullptr};
-  const bool vec = aligned16(x) && aligned16(y) && aligned16(weight) && aligned16(bias) && (H * elem_bytes(dtype)) % 16 == 0;
+  const NormArgs p = {x, nullptr, weight, bias, T, H, eps, y, mean, rstd, nullptr};
   cudaStream_t st = (cudaStream_t)stream;
-  if (dtype == MOE_BF16) return fwd_typed<__nv_bfloat16>(p, vec, st);
-  if (dtype == MOE_F16) return fwd_typed<__half>(p, vec, st);
-  return fwd_typed<float>(p, vec, st);
-}
-
-extern "C" int moe_layernorm_bwd_ws_bytes(int T, int H, size_t* bytes) {
-  if (!bytes || !norm_shape_ok(T, H)) return MOE_ERR_INVALID_ARG;
-  const int tpr = bwd_tpr(H);
-  *bytes = (size_t)bwd_blocks(T, H) * (bwd_block(tpr) / tpr) * 2 * H * sizeof(float);
-  return MOE_OK;
-}
-
-extern "C" int moe_layernorm_bwd(const void* dy, const void* x, int T, int H, int dtype, const void* weight, int wdtype,
-                                 const float* mean, const float* rstd, void* dx, void* dweight, void* dbias, void* ws,
-                                 size_t ws_bytes, moe_stream_t stream) {
-  if (!norm_shape_ok(T, H) || dtype < MOE_BF16 || dtype > MOE_F32 || (wdtype != dtype && wdtype != MOE_F32)) return MOE_ERR_INVALID_ARG;
-  if (!elem_aligned(weight, wdtype) || !elem_aligned(dweight, wdtype) || !elem_aligned(dbias, wdtype)) return MOE_ERR_INVALID_ARG;
-  cudaStream_t st = (cudaStream_t)stream;
-  if (T == 0) {   // sums over no rows
-    if (dweight && cudaMemsetAsync(dweight, 0, H * elem_bytes(wdtype), st) != cudaSuccess) return MOE_ERR_CUDA;
-    if (dbias && cudaMemsetAsync(dbias, 0, H * elem_bytes(wdtype), st) != cudaSuccess) return MOE_ERR_CUDA;
-    return MOE_OK;
-  }
-  size_t need = 0;
-  moe_layernorm_bwd_ws_bytes(T, H, &need);
-  if (!dy || !x || !mean || !rstd || !dx || !ws || ws_bytes < need) return MOE_ERR_INVALID_ARG;
-  if (!elem_aligned(x, dtype) || !elem_aligned(dy, dtype) || !elem_aligned(dx, dtype) || !elem_aligned(mean, MOE_F32) ||
-      !elem_aligned(rstd, MOE_F32) || !aligned16(ws))
-    return MOE_ERR_INVALID_ARG;
-  NormArgs p = {x, dy, weight, nullptr, wdtype == MOE_F32, T, H, 0.f, dx, const_cast<float*>(mean), const_cast<float*>(rstd),
-                static_cast<float*>(ws)};
-  const bool vec = aligned16(x) && aligned16(dy) && aligned16(dx) && aligned16(weight) && (H * elem_bytes(dtype)) % 16 == 0;
-  if (dtype == MOE_BF16)
-    return vec ? bwd_of<__nv_bfloat16, 8>(p, dweight, dbias, st) : bwd_of<__nv_bfloat16, 1>(p, dweight, dbias, st);
-  if (dtype == MOE_F16) return vec ? bwd_of<__half, 8>(p, dweight, dbias, st) : bwd_of<__half, 1>(p, dweight, dbias, st);
-  return vec ? bwd_of<float, 4>(p, dweight, dbias, st) : bwd_of<float, 1>(p, dweight, dbias, st);
+  if (dtype == MOE_F32) return norm_fwd<float, float>(p, st);
+  if (dtype == MOE_BF16) return wdtype == MOE_F32 ? norm_fwd<__nv_bfloat16, float>(p, st) : norm_fwd<__nv_bfloat16, __nv_bfloat16>(p, st);
+  return wdtype == MOE_F32 ? norm_fwd<__half, float>(p, st) : norm_fwd<__half, __half>(p, st);
 }

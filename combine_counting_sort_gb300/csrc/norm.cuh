@@ -1,0 +1,236 @@
+// norm.cuh: what the forward and the backward pass of layer norm share.
+//
+// A row lies in the registers of the TPR threads that work on it, NV vectors of
+// 16 bytes a thread, so memory is read once whatever the formula passes over.  A
+// group of TPR threads walks the rows g, g + groups, ...; each thread keeps
+// the next rows' vectors coming by cp.async into a ring in shared memory that
+// it alone reads, so nothing is waited for but a thread's own copies.
+//
+// Rows whose length is no whole number of vectors start inside one.  `groups` is a
+// multiple of 8, so all rows of a group start at the same place s inside a
+// vector: a thread's columns are the same in each of them, and weights and column
+// sums stay in registers there too.  The vectors at a row's ends are masked,
+// and stored value by value.
+#pragma once
+
+#include "dtype.cuh"
+#include "host_util.h"
+
+namespace moe {
+
+constexpr int kNormThreads = 512;
+constexpr int kNormMaxBlocks = 160;   // of the backward pass, one an SM
+
+struct NormArgs {
+  const void* x;
+  const void* dy;
+  const void* weight;
+  const void* bias;
+  int T, H;
+  float eps;
+  void* y;      // y, or dx
+  float* mean;
+  float* rstd;
+  float* part;  // backward: [blocks][2][H] sums of each block's rows
+};
+
+// ---------------------------------------------------------------- pairs of fp32 (.f32x2 instructions)
+
+using f32x2 = unsigned long long;
+MOE_DEV f32x2 add2(f32x2 a, f32x2 b) { f32x2 r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
+MOE_DEV f32x2 mul2(f32x2 a, f32x2 b) { f32x2 r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
+MOE_DEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+MOE_DEV f32x2 both(float v) { return pack_f32x2(v, v); }
+MOE_DEV float lo2(f32x2 v) { return __uint_as_float((uint32_t)v); }
+MOE_DEV float hi2(f32x2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
+MOE_DEV float sum2(f32x2 v) { return lo2(v) + hi2(v); }
+
+// 16 bytes of T as pairs
+template <typename T>
+struct Pairs;
+template <>
+struct Pairs<float> {
+  static constexpr int N = 2;
+  static MOE_DEV void get(const uint4& r, f32x2* out) {
+    out[0] = (f32x2)r.x | ((f32x2)r.y << 32);
+    out[1] = (f32x2)r.z | ((f32x2)r.w << 32);
+  }
+  static MOE_DEV uint4 put(const f32x2* v) {
+    return make_uint4((uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32));
+  }
+};
+template <>
+struct Pairs<__nv_bfloat16> {
+  static constexpr int N = 4;
+  static MOE_DEV f32x2 one(uint32_t v) { return pack_f32x2(bf16_lo(v), bf16_hi(v)); }
+  static MOE_DEV void get(const uint4& r, f32x2* out) { out[0] = one(r.x); out[1] = one(r.y); out[2] = one(r.z); out[3] = one(r.w); }
+  static MOE_DEV uint4 put(const f32x2* v) {
+    return make_uint4(pack_bf16x2_from_pair(v[0]), pack_bf16x2_from_pair(v[1]), pack_bf16x2_from_pair(v[2]), pack_bf16x2_from_pair(v[3]));
+  }
+};
+template <>
+struct Pairs<__half> {
+  static constexpr int N = 4;
+  static MOE_DEV f32x2 one(uint32_t v) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+    return pack_f32x2(f.x, f.y);
+  }
+  static MOE_DEV uint32_t pack(f32x2 v) {
+    const __half2 h = __floats2half2_rn(lo2(v), hi2(v));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static MOE_DEV void get(const uint4& r, f32x2* out) { out[0] = one(r.x); out[1] = one(r.y); out[2] = one(r.z); out[3] = one(r.w); }
+  static MOE_DEV uint4 put(const f32x2* v) { return make_uint4(pack(v[0]), pack(v[1]), pack(v[2]), pack(v[3])); }
+};
+
+// A vector's worth of weights: W's own 16 bytes where W is the rows' type, else fp32.
+// Rows of whole vectors read them from a copy in shared memory; those of MASK, whose
+// vectors start at another column in each group, keep them in registers.
+template <typename T, typename W>
+struct ParamVec {
+  f32x2 p[kVec16<T> / 2];
+  MOE_DEV void set(const f32x2* v) {
+#pragma unroll
+    for (int e = 0; e < kVec16<T> / 2; ++e) p[e] = v[e];
+  }
+  MOE_DEV void get(f32x2* out) const {
+#pragma unroll
+    for (int e = 0; e < kVec16<T> / 2; ++e) out[e] = p[e];
+  }
+};
+template <typename T>
+struct ParamVec<T, T> {
+  uint4 p;
+  MOE_DEV void set(const f32x2* v) { p = Pairs<T>::put(v); }   // exact: the values come from T
+  MOE_DEV void get(f32x2* out) const { Pairs<T>::get(p, out); }
+};
+
+// ---------------------------------------------------------------- a thread's part of its group's rows
+
+// 16 bytes global -> shared, of which the first `bytes` are read and the rest are zeros.
+MOE_DEV void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes) : "memory");
+}
+
+// MASK: rows of no whole number of vectors, whose first and last vectors are shared
+// with the rows beside them.
+template <typename T, int TPR, int NV, bool MASK>
+struct RowPart {
+  static constexpr int V = kVec16<T>;
+  int H, tid, first;   // first: column of this thread's vector 0
+
+  MOE_DEV RowPart(int H_, long long first_row) : H(H_), tid((int)threadIdx.x % TPR), first(tid * V - (MASK ? (int)(first_row * H_ % V) : 0)) {}
+  // first column of vector i, and the part [lo, hi) of it that is this row's
+  MOE_DEV int col(int i) const { return first + i * TPR * V; }
+  MOE_DEV int lo(int i) const { return max(0, -col(i)); }
+  MOE_DEV int hi(int i) const { return min(V, H - col(i)); }
+  MOE_DEV bool any(int i) const { return col(i) < H; }
+  MOE_DEV bool whole(int i) const { return !MASK || (col(i) >= 0 && col(i) + V <= H); }
+
+  // Start copying this thread's vectors of a row into its slots, `step` bytes apart; `src` is
+  // vector 0.  A vector reaches into the rows beside it, but not past the last row.
+  MOE_DEV void fetch(const T* src, bool last_row, uint32_t slot, uint32_t step) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (any(i)) cp_async16(slot + i * step, src + i * TPR * V, MASK && last_row ? (uint32_t)(hi(i) * sizeof(T)) : 16u);
+  }
+  // store vector i of the row whose vector 0 is at `dst`
+  MOE_DEV void store(T* dst, int i, const uint4& v) const {
+    T* p = dst + i * TPR * V;
+    if (whole(i)) {
+      *reinterpret_cast<uint4*>(p) = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      const int a = lo(i), b = hi(i);
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e >= a && e < b) {
+          if (sizeof(T) == 4) reinterpret_cast<uint32_t*>(p)[e] = w[e % 4];
+          else reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+        }
+    }
+  }
+  // zeros where vector i is not this row's
+  MOE_DEV void mask(int i, f32x2* v) const {
+    if (whole(i)) return;
+    const int a = lo(i), b = hi(i);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e)
+      v[e] = pack_f32x2(2 * e >= a && 2 * e < b ? lo2(v[e]) : 0.f, 2 * e + 1 >= a && 2 * e + 1 < b ? hi2(v[e]) : 0.f);
+  }
+  // this thread's weights (or biases) of vector i, for registers; zeros outside the row
+  template <typename W>
+  MOE_DEV ParamVec<T, W> params(const void* src, float none, int i) const {
+    const W* p = static_cast<const W*>(src);
+    f32x2 v[V / 2];
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      const int j = col(i) + e;
+      const float a = j >= 0 && j < H ? (p ? to_f32(p[j]) : none) : 0.f;
+      const float b = j + 1 >= 0 && j + 1 < H ? (p ? to_f32(p[j + 1]) : none) : 0.f;
+      v[e / 2] = pack_f32x2(a, b);
+    }
+    ParamVec<T, W> r;
+    r.set(v);
+    return r;
+  }
+};
+
+MOE_DEV float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The sum over a block of kNormThreads, for every thread.
+MOE_DEV float block_sum(float v, float* scratch) {
+  v = warp_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_sum((threadIdx.x & 31) < kNormThreads / 32 ? scratch[threadIdx.x & 31] : 0.f);
+}
+
+// weight or bias value j, `none` where there is no such tensor
+template <typename W>
+MOE_DEV float param(const void* p, int j, float none) { return p ? to_f32(static_cast<const W*>(p)[j]) : none; }
+
+// [H] weights (or biases) into shared memory
+template <typename W>
+MOE_DEV void copy_params(W* dst, const void* src, float none, int H) {
+  for (int j = threadIdx.x; j < H; j += kNormThreads) dst[j] = src ? static_cast<const W*>(src)[j] : from_f32<W>(none);
+}
+
+// all threads of this thread's group
+template <int TPR>
+MOE_DEV void group_sync() {
+  if (TPR == kNormThreads) __syncthreads();
+  else if (TPR == 32) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"((int)threadIdx.x / TPR + 1), "n"(TPR) : "memory");
+}
+
+// Columns that a row's vectors cover, wherever it starts inside its first one.
+inline int norm_span(int H, int vec) { return H % vec == 0 ? H : (H + 2 * (vec - 1)) / vec * vec; }
+// threads a row at `values` values a thread (beyond kNormThreads: it does not fit a block)
+inline int norm_tpr(int H, int vec, int values) {
+  int tpr = 32;
+  while (tpr * values < norm_span(H, vec)) tpr *= 2;
+  return tpr;
+}
+
+inline size_t elem_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
+inline bool norm_shape_ok(int T, int H) { return T >= 0 && H >= 1 && H <= MOE_NORM_MAX_H; }
+// a tensor of this type starts where its elements may start
+inline bool elem_aligned(const void* p, int dtype) { return (uintptr_t)p % elem_bytes(dtype) == 0; }
+
+// Blocks: `per_sm` on each SM (their number a multiple of 8), or as many as the rows need.
+inline int norm_blocks(int T, int groups_a_block, int per_sm, int sms) {
+  const long long full = (long long)(sms / 8 * 8) * per_sm, need = ((long long)T + groups_a_block - 1) / groups_a_block;
+  return (int)std::max(1LL, std::min(full, need));
+}
+
+}  // namespace moe
