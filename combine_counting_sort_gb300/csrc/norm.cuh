@@ -18,8 +18,7 @@
 
 namespace moe {
 
-constexpr int kNormThreads = 512;
-constexpr int kNormMaxBlocks = 160;   // of the backward pass, one an SM
+constexpr int kNormMaxBlocks = 320;   // of the backward pass, two an SM
 
 struct NormArgs {
   const void* x;
@@ -186,13 +185,14 @@ MOE_DEV float warp_sum(float v) {
   return v;
 }
 
-// The sum over a block of kNormThreads, for every thread.
+// The sum over a block, for every thread.
+template <int BLOCK>
 MOE_DEV float block_sum(float v, float* scratch) {
   v = warp_sum(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
   __syncthreads();
-  return warp_sum((threadIdx.x & 31) < kNormThreads / 32 ? scratch[threadIdx.x & 31] : 0.f);
+  return warp_sum((threadIdx.x & 31) < BLOCK / 32 ? scratch[threadIdx.x & 31] : 0.f);
 }
 
 // weight or bias value j, `none` where there is no such tensor
@@ -200,22 +200,24 @@ template <typename W>
 MOE_DEV float param(const void* p, int j, float none) { return p ? to_f32(static_cast<const W*>(p)[j]) : none; }
 
 // [H] weights (or biases) into shared memory
-template <typename W>
+template <int BLOCK, typename W>
 MOE_DEV void copy_params(W* dst, const void* src, float none, int H) {
-  for (int j = threadIdx.x; j < H; j += kNormThreads) dst[j] = src ? static_cast<const W*>(src)[j] : from_f32<W>(none);
+  for (int j = threadIdx.x; j < H; j += BLOCK) dst[j] = src ? static_cast<const W*>(src)[j] : from_f32<W>(none);
 }
 
-// all threads of this thread's group
-template <int TPR>
+// All threads of this thread's group.  Barriers 1 to 15, and the block's own for the last of 16
+// groups (whose kernel has no barrier of the block after this).
+template <int TPR, int BLOCK>
 MOE_DEV void group_sync() {
-  if (TPR == kNormThreads) __syncthreads();
+  static_assert(TPR == 32 || BLOCK / TPR <= 16, "named barriers");
+  if (TPR == BLOCK) __syncthreads();
   else if (TPR == 32) __syncwarp();
-  else asm volatile("bar.sync %0, %1;" ::"r"((int)threadIdx.x / TPR + 1), "n"(TPR) : "memory");
+  else asm volatile("bar.sync %0, %1;" ::"r"(((int)threadIdx.x / TPR + 1) % 16), "n"(TPR) : "memory");
 }
 
 // Columns that a row's vectors cover, wherever it starts inside its first one.
 inline int norm_span(int H, int vec) { return H % vec == 0 ? H : (H + 2 * (vec - 1)) / vec * vec; }
-// threads a row at `values` values a thread (beyond kNormThreads: it does not fit a block)
+// threads a row at `values` values a thread
 inline int norm_tpr(int H, int vec, int values) {
   int tpr = 32;
   while (tpr * values < norm_span(H, vec)) tpr *= 2;
