@@ -87,6 +87,12 @@ MOE_DEV void fence_proxy_async_global() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
+// Programmatic launches: the next kernel of the stream may start its blocks as this
+// one's leave (launch), and waits here for all of this one's writes before it reads
+// anything (wait): the barriers' set-up and the launch itself are out of the way.
+MOE_DEV void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+MOE_DEV void grid_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- bf16 / fp8
 
 MOE_DEV float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }

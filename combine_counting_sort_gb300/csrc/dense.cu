@@ -18,6 +18,8 @@ __global__ void __launch_bounds__(256)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j0 = blockIdx.x * 256;
   constexpr int NV = 8 / V, STEP = V == 8 ? 256 : 32;
   float acc[8] = {};
+  grid_launch_next();
+  grid_wait_previous();
   for (long long i = (long long)blockIdx.y * 8 + warp; i < I; i += 8LL * gridDim.y) {
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
@@ -60,6 +62,8 @@ __global__ void __launch_bounds__(256)
 template <typename T, int V>
 __global__ void __launch_bounds__(256) gated_d_kernel(const T* dh, const T* factors, int I, int F, T* d, long long ldd) {
   const int j = (blockIdx.x * 256 + threadIdx.x) * V;
+  grid_launch_next();
+  grid_wait_previous();
   if (j >= F) return;
   for (long long i = blockIdx.y; i < I; i += gridDim.y) {
     const Vec<T, V> a = *reinterpret_cast<const Vec<T, V>*>(dh + i * F + j);
@@ -84,19 +88,9 @@ int launch_d(const void* dy, const void* slope, int I, int J, void* d, long long
   // rows of a strip over up to 8 blocks (a cluster, where they add up their sums); without sums, over more
   const long long want = std::max(1, 4 * 152 / strips), cap = dbias ? 8 : 1024;
   const int ys = (int)std::min({cap, want, ((long long)I + 7) / 8});
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = attr[0].val.clusterDim.z = 1;
-  attr[0].val.clusterDim.y = dbias ? (unsigned)ys : 1u;
-  cfg.gridDim = dim3((unsigned)strips, (unsigned)ys);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   auto kernel = vec ? dense_d_kernel<T, 8> : dense_d_kernel<T, 1>;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<const T*>(dy), static_cast<const T*>(slope), I, J, static_cast<T*>(d), ldd,
-                            static_cast<T*>(dbias)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_next(kernel, dim3((unsigned)strips, (unsigned)ys), 256, 0, st, 1, dbias ? (unsigned)ys : 1u, static_cast<const T*>(dy),
+                     static_cast<const T*>(slope), I, J, static_cast<T*>(d), ldd, static_cast<T*>(dbias));
 }
 
 template <typename T>
@@ -104,11 +98,8 @@ int launch_gated_d(const void* dh, const void* factors, int I, int F, void* d, l
   const bool vec = F % 8 == 0 && aligned16(dh) && aligned16(factors);
   const int per = vec ? 2048 : 256, strips = (F + per - 1) / per;
   const dim3 grid((unsigned)strips, (unsigned)std::min(I, std::max(1, 16 * 152 / strips)));
-  if (vec)
-    gated_d_kernel<T, 8><<<grid, 256, 0, st>>>(static_cast<const T*>(dh), static_cast<const T*>(factors), I, F, static_cast<T*>(d), ldd);
-  else
-    gated_d_kernel<T, 1><<<grid, 256, 0, st>>>(static_cast<const T*>(dh), static_cast<const T*>(factors), I, F, static_cast<T*>(d), ldd);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  auto kernel = vec ? gated_d_kernel<T, 8> : gated_d_kernel<T, 1>;
+  return launch_next(kernel, grid, 256, 0, st, 1, 1, static_cast<const T*>(dh), static_cast<const T*>(factors), I, F, static_cast<T*>(d), ldd);
 }
 
 constexpr int kDenseMaxT = 1 << 24;

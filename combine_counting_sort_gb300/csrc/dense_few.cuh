@@ -87,6 +87,8 @@ __global__ void __launch_bounds__(kDFewThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
+  grid_launch_next();
+  grid_wait_previous();
 
   if (warp == 0) {
     if (elect_one()) {

@@ -27,6 +27,24 @@ bool encode_operand(CUtensorMap* map, const DenseOperand& o, int K, int box) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters of two CTAs that the device holds at once; 0 where it cannot be said.
+template <typename K>
+int resident_pairs(K kernel, int nsm) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDPairSmemBytes) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(2 * (nsm / 2));
+  cfg.blockDim = dim3(kDPairThreads);
+  cfg.dynamicSmemBytes = kDPairSmemBytes;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+}
+
 template <typename T, bool PMN, bool QMN, int EPI>
 int launch_dense(const DenseOperand& P, const DenseOperand& Q, DenseArgs g, cudaStream_t st) {
   const int nsm = device_sm_count();
@@ -34,33 +52,22 @@ int launch_dense(const DenseOperand& P, const DenseOperand& Q, DenseArgs g, cuda
   g.timeout_ns = 2000000000ull;
   const DensePlan plan = dense_plan(g.I, g.J, g.K, EPI == kEpiGated, PMN, nsm);
   CUtensorMap tmP, tmQ;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   if (plan.pair) {
     if (!encode_operand<T>(&tmP, P, g.K, 128) || !encode_operand<T>(&tmQ, Q, g.K, 128)) return MOE_ERR_CUDA;
     auto kernel = dense_pair_kernel<T, PMN, QMN, EPI>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDPairSmemBytes) != cudaSuccess) return MOE_ERR_CUDA;
-    attr[0].val.clusterDim.x = 2;
-    cfg.blockDim = dim3(kDPairThreads);
-    cfg.dynamicSmemBytes = kDPairSmemBytes;
-    cfg.gridDim = dim3(2 * (nsm / 2));
-    int resident = 0;
-    if (cudaOccupancyMaxActiveClusters(&resident, kernel, &cfg) != cudaSuccess || resident < 1) return MOE_ERR_CUDA;
+    static const int resident = resident_pairs(kernel, nsm);   // once: the grid is persistent
+    if (resident < 1) return MOE_ERR_CUDA;
     constexpr int kTileJ = EPI == kEpiGated ? 128 : 256;
     const long long tiles = ((long long)g.I + 255) / 256 * (((long long)g.J + kTileJ - 1) / kTileJ);
     if (tiles > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
-    cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(std::min(resident, nsm / 2), tiles));
-    return cudaLaunchKernelEx(&cfg, kernel, tmP, tmQ, g) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return launch_next(kernel, dim3(2 * (unsigned)std::min<long long>(std::min(resident, nsm / 2), tiles)), kDPairThreads, kDPairSmemBytes, st,
+                       2, 1, tmP, tmQ, g);
   }
   if (!encode_operand<T>(&tmP, P, g.K, plan.nt) || !encode_operand<T>(&tmQ, Q, g.K, EPI == kEpiGated ? 64 : 128)) return MOE_ERR_CUDA;
   auto kernel = dense_few_kernel<T, PMN, QMN, EPI>;
   const size_t smem = dfew_smem_bytes(plan.nt, plan.stages);
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return MOE_ERR_CUDA;
+  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (attr != cudaSuccess) return MOE_ERR_CUDA;
   constexpr int kRows = EPI == kEpiGated ? 64 : 128;
   DFewPlan fp;
   fp.nt = plan.nt;
@@ -69,11 +76,7 @@ int launch_dense(const DenseOperand& P, const DenseOperand& Q, DenseArgs g, cuda
   fp.ti = (int)(((long long)g.I + plan.nt - 1) / plan.nt);
   const long long ctas = (long long)fp.ti * (((long long)g.J + kRows - 1) / kRows) * plan.split;
   if (ctas > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
-  attr[0].val.clusterDim.x = (unsigned)plan.split;
-  cfg.blockDim = dim3(kDFewThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.gridDim = dim3((unsigned)ctas);
-  return cudaLaunchKernelEx(&cfg, kernel, tmP, tmQ, g, fp) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_next(kernel, dim3((unsigned)ctas), kDFewThreads, smem, st, (unsigned)plan.split, 1, tmP, tmQ, g, fp);
 }
 
 // The products that the operators take: x W^T (linear, gated), d W and d^T x.

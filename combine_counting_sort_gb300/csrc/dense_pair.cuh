@@ -93,6 +93,8 @@ __global__ void __launch_bounds__(kDPairThreads, 1)
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
+  grid_launch_next();
+  grid_wait_previous();
 
   constexpr int kTileJ = EPI == kEpiGated ? 128 : 256;
   const int ti = (g.I + 255) / 256, tj = (g.J + kTileJ - 1) / kTileJ, tiles = ti * tj;

@@ -95,12 +95,6 @@ struct FewGroups {
   static constexpr int kCount = GROUP == 32 ? 4 : GROUP == 64 ? 2 : 1;   // scales per row and 128-column slice
 };
 
-// Programmatic launches: the next kernel of the stream may start its blocks as this
-// one's leave (launch), and waits here for all of this one's writes before it reads
-// anything (wait): the barriers' set-up and the launch itself are out of the way.
-MOE_DEV void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-MOE_DEV void grid_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // ---------------------------------------------------------------- the ring
 
 // Barriers of the ring and the block's flags at the start of shared memory.

@@ -98,4 +98,25 @@ inline bool encode_u8_map(CUtensorMap* map, const void* base, int rank, const ui
   return r == CUDA_SUCCESS;
 }
 
+// Launch with programmatic serialisation (the kernel waits for the kernel before it
+// by grid_wait_previous), in clusters of cx x cy blocks.
+template <typename... P, typename... A>
+int launch_next(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, unsigned cx, unsigned cy, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cx;
+  attr[1].val.clusterDim.y = cy;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cx * cy > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 }  // namespace moe

@@ -25,6 +25,8 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdPerSm<T, NV, MASK>) norm_fwd_
   const long long groups = (long long)gridDim.x * GROUPS, g = (long long)blockIdx.x * GROUPS + grp;
   const RowPart<T, TPR, NV, MASK> part(p.H, g);
   constexpr uint32_t STEP = BLOCK * 16, SLOT = NV * STEP;
+  grid_launch_next();
+  grid_wait_previous();
   uint8_t* mine = ring + threadIdx.x * 16;
   const uint32_t mine_at = smem_u32(mine);
   const long long stride = groups * p.H;
@@ -145,6 +147,8 @@ __global__ void __launch_bounds__(BLOCK) norm_fwd_few_kernel(const NormArgs p) {
   const RowPart<T, BLOCK, 1, MASK> part(p.H, row);
   const T* src = static_cast<const T*>(p.x) + row * p.H + part.first;
   f32x2 v[P], w[P], b[P];
+  grid_launch_next();
+  grid_wait_previous();
 #pragma unroll
   for (int e = 0; e < P; ++e) v[e] = w[e] = b[e] = 0;
   if (part.any(0)) {
@@ -204,6 +208,8 @@ __global__ void __launch_bounds__(512) norm_fwd_any_kernel(const NormArgs p) {
   const T* x = static_cast<const T*>(p.x) + row * p.H;
   T* y = static_cast<T*>(p.y) + row * p.H;
   float s = 0.f;
+  grid_launch_next();
+  grid_wait_previous();
   for (int j = threadIdx.x; j < p.H; j += 512) s += to_f32(x[j]);
   const float mean = block_sum<512>(s, scratch) / (float)p.H;
   s = 0.f;
@@ -227,23 +233,20 @@ int launch_fwd(const NormArgs& p, cudaStream_t st) {
   static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024);
   if (attr != cudaSuccess) return MOE_ERR_CUDA;
   const int per_sm = smem <= 112 * 1024 ? kFwdPerSm<T, NV, MASK> : 1;
-  kernel<<<norm_blocks(p.T, kFwdThreads / TPR, per_sm, device_sm_count()), kFwdThreads, smem, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_next(kernel, dim3(norm_blocks(p.T, kFwdThreads / TPR, per_sm, device_sm_count())), kFwdThreads, smem, st, 1, 1, p);
 }
 
 template <typename T, typename W>
 int launch_fwd_any(const NormArgs& p, cudaStream_t st) {
-  norm_fwd_any_kernel<T, W><<<p.T, 512, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_next(norm_fwd_any_kernel<T, W>, dim3(p.T), 512, 0, st, 1, 1, p);
 }
 
 template <typename T, typename W, bool MASK>
 int norm_fwd(const NormArgs& p, cudaStream_t st) {
   constexpr int V = kVec16<T>;
   if (p.T <= 304 && norm_tpr(p.H, V, V) <= 1024) {
-    if (norm_tpr(p.H, V, V) <= 256) norm_fwd_few_kernel<T, W, 256, MASK><<<p.T, 256, 0, st>>>(p);
-    else norm_fwd_few_kernel<T, W, 1024, MASK><<<p.T, 1024, 0, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    if (norm_tpr(p.H, V, V) <= 256) return launch_next(norm_fwd_few_kernel<T, W, 256, MASK>, dim3(p.T), 256, 0, st, 1, 1, p);
+    return launch_next(norm_fwd_few_kernel<T, W, 1024, MASK>, dim3(p.T), 1024, 0, st, 1, 1, p);
   }
   // Values a thread: as many as leave two blocks an SM room in registers and shared memory.
   // (One block of 1024 threads with a turn more in its ring: 50.8 us against 46.9 at 8192 x 7168.)

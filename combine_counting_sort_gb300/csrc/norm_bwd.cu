@@ -24,6 +24,8 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) norm_bwd_kernel(const Norm
   const int groups = gridDim.x * GROUPS, g = blockIdx.x * GROUPS + grp;
   const RowPart<T, TPR, NV, MASK> part(p.H, g);
   constexpr uint32_t STEP = BLOCK * 16, HALF = NV * STEP, SLOT = 2 * HALF;
+  grid_launch_next();
+  grid_wait_previous();
   uint8_t* mine = ring + threadIdx.x * 16;
   const uint32_t mine_at = smem_u32(mine);
   const long long stride = (long long)groups * p.H;
@@ -163,15 +165,15 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) norm_bwd_kernel(const Norm
 }
 
 // dweight (blockIdx.y 0) and dbias (1): the blocks' sums added up.  A block
-// takes 32 columns, its 16 warps every 16th of the sums.  Launched while the rows'
-// kernel still runs; its sums are read once that has ended.
+// takes 32 columns, its 16 warps every 16th of the sums.
 template <typename W>
 __global__ void __launch_bounds__(512) norm_sums_kernel(const float* part, int n, int H, W* dweight, W* dbias) {
   __shared__ float acc[16][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int j = blockIdx.x * 32 + lane;
   W* out = blockIdx.y ? dbias : dweight;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_launch_next();
+  grid_wait_previous();
   if (!out) return;
   float s = 0.f;
   if (j < H) {
@@ -197,6 +199,8 @@ __global__ void __launch_bounds__(512) norm_bwd_any_kernel(const NormArgs p) {
   const long long row = blockIdx.x;
   const T *x = static_cast<const T*>(p.x) + row * p.H, *dy = static_cast<const T*>(p.dy) + row * p.H;
   T* dx = static_cast<T*>(p.y) + row * p.H;
+  grid_launch_next();
+  grid_wait_previous();
   const float mean = p.mean[row], rstd = p.rstd[row];
   float a = 0.f, b = 0.f;
   for (int j = threadIdx.x; j < p.H; j += 512) {
@@ -216,6 +220,8 @@ __global__ void __launch_bounds__(512) norm_bwd_any_kernel(const NormArgs p) {
 template <typename T>
 __global__ void __launch_bounds__(256) norm_sums_any_kernel(const NormArgs p) {
   const int j = blockIdx.x * 256 + threadIdx.x;
+  grid_launch_next();
+  grid_wait_previous();
   if (j >= p.H) return;
   float a = 0.f, b = 0.f;
   for (long long row = blockIdx.y; row < p.T; row += gridDim.y) {
@@ -229,20 +235,9 @@ __global__ void __launch_bounds__(256) norm_sums_any_kernel(const NormArgs p) {
 
 template <typename W>
 int launch_sums(const NormArgs& p, int n, void* dweight, void* dbias, cudaStream_t st) {
-  if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
   if (!dweight && !dbias) return MOE_OK;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((p.H + 31) / 32, 2);
-  cfg.blockDim = dim3(512);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   const float* part = p.part;
-  return cudaLaunchKernelEx(&cfg, norm_sums_kernel<W>, part, n, p.H, static_cast<W*>(dweight), static_cast<W*>(dbias)) == cudaSuccess
-             ? MOE_OK : MOE_ERR_CUDA;
+  return launch_next(norm_sums_kernel<W>, dim3((p.H + 31) / 32, 2), 512, 0, st, 1, 1, part, n, p.H, static_cast<W*>(dweight), static_cast<W*>(dbias));
 }
 
 template <typename T, typename W, int TPR, int NV, int D, bool MASK>
@@ -255,17 +250,17 @@ int launch_bwd(const NormArgs& p, void* dweight, void* dbias, cudaStream_t st) {
   static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024);
   if (attr != cudaSuccess) return MOE_ERR_CUDA;
   const int blocks = norm_blocks(p.T, BLOCK / TPR, BLOCK == 256 && smem <= 112 * 1024 ? 2 : 1, device_sm_count());
-  kernel<<<blocks, BLOCK, smem, st>>>(p);
-  return launch_sums<W>(p, blocks, dweight, dbias, st);
+  const int rc = launch_next(kernel, dim3(blocks), BLOCK, smem, st, 1, 1, p);
+  return rc ? rc : launch_sums<W>(p, blocks, dweight, dbias, st);
 }
 
 template <typename T, typename W>
 int launch_bwd_any(const NormArgs& p, void* dweight, void* dbias, cudaStream_t st) {
   // the sums first: dx may be x or dy
   const int n = std::min(p.T, kNormMaxBlocks);
-  if (dweight || dbias) norm_sums_any_kernel<T><<<dim3((p.H + 255) / 256, n), 256, 0, st>>>(p);
-  norm_bwd_any_kernel<T, W><<<p.T, 512, 0, st>>>(p);
-  return launch_sums<W>(p, n, dweight, dbias, st);
+  int rc = dweight || dbias ? launch_next(norm_sums_any_kernel<T>, dim3((p.H + 255) / 256, n), 256, 0, st, 1, 1, p) : MOE_OK;
+  if (rc == MOE_OK) rc = launch_next(norm_bwd_any_kernel<T, W>, dim3(p.T), 512, 0, st, 1, 1, p);
+  return rc ? rc : launch_sums<W>(p, n, dweight, dbias, st);
 }
 
 template <typename T, typename W, bool MASK>
