@@ -6,54 +6,65 @@ namespace moe {
 
 // ---------------------------------------------------------------- d = dy * slope and dbias
 //
-// Memory bound: reads dy and slope, writes d.  A block of 8 warps takes 256
-// columns; the blocks of a cluster (gridDim.y of them) share the rows, and
-// add up their column sums through distributed shared memory in rank order.
-// V = 8: lane l holds columns 8 l.., in 16-byte vectors; V = 1: columns l, l + 32, ...
+// Memory bound: reads dy and slope, writes d.  A block of 8 warps takes 128
+// columns, a row for each half warp, four rows in flight; the blocks of a cluster
+// (gridDim.y of them) share the rows, and add up their column sums through distributed
+// shared memory in rank order.  V = 8: half-warp lane l holds columns 8 l.., in 16-byte
+// vectors; V = 1: columns l, l + 16, ...
 template <typename T, int V>
 __global__ void __launch_bounds__(256)
     dense_d_kernel(const T* dy, const T* slope, int I, int J, T* d, long long ldd, T* dbias) {
-  __shared__ float sums[8][256];
-  __shared__ float total[256];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j0 = blockIdx.x * 256;
-  constexpr int NV = 8 / V, STEP = V == 8 ? 256 : 32;
+  __shared__ float sums[16][128];
+  __shared__ float total[128];
+  const int lane = threadIdx.x & 15, slot = threadIdx.x >> 4, j0 = blockIdx.x * 128;
+  constexpr int NV = 8 / V, ROWS = 4;
   float acc[8] = {};
   grid_launch_next();
   grid_wait_previous();
-  for (long long i = (long long)blockIdx.y * 8 + warp; i < I; i += 8LL * gridDim.y) {
+  const int step = 16 * gridDim.y;
+  for (long long i = blockIdx.y * 16 + slot; i < I; i += (long long)ROWS * step) {
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const int j = j0 + c * STEP + lane * V;
+      const int j = j0 + (V == 8 ? 8 * lane : 16 * c + lane);
       if (j >= J) continue;
-      const Vec<T, V> a = *reinterpret_cast<const Vec<T, V>*>(dy + i * J + j);
-      Vec<T, V> s, o;
-      if (slope) s = *reinterpret_cast<const Vec<T, V>*>(slope + i * J + j);
+      Vec<T, V> a[ROWS], s[ROWS];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float f = slope ? to_f32(a.v[v]) * to_f32(s.v[v]) : to_f32(a.v[v]);
-        acc[c * V + v] += f;
-        o.v[v] = from_f32<T>(f);
-      }
-      if (d) *reinterpret_cast<Vec<T, V>*>(d + i * ldd + j) = o;
+      for (int r = 0; r < ROWS; ++r)
+        if (i + r * step < I) {
+          a[r] = *reinterpret_cast<const Vec<T, V>*>(dy + (i + r * step) * J + j);
+          if (slope) s[r] = *reinterpret_cast<const Vec<T, V>*>(slope + (i + r * step) * J + j);
+        }
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r)
+        if (i + r * step < I) {
+          Vec<T, V> o;
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float f = slope ? to_f32(a[r].v[v]) * to_f32(s[r].v[v]) : to_f32(a[r].v[v]);
+            acc[c * V + v] += f;
+            o.v[v] = from_f32<T>(f);
+          }
+          if (d) *reinterpret_cast<Vec<T, V>*>(d + (i + r * step) * ldd + j) = o;
+        }
     }
   }
   if (!dbias) return;
 #pragma unroll
-  for (int c = 0; c < NV; ++c)
-#pragma unroll
-    for (int v = 0; v < V; ++v) sums[warp][c * STEP + lane * V + v] = acc[c * V + v];
+  for (int e = 0; e < 8; ++e) sums[slot][V == 8 ? 8 * lane + e : 16 * e + lane] = acc[e];
   __syncthreads();
-  float s = 0.f;
+  if (threadIdx.x < 128) {
+    float s = 0.f;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) s += sums[w][threadIdx.x];
-  total[threadIdx.x] = s;
+    for (int w = 0; w < 16; ++w) s += sums[w][threadIdx.x];
+    total[threadIdx.x] = s;
+  }
   cluster_sync();
-  if (blockIdx.y == 0) {
-    s = 0.f;
+  const int j = j0 + threadIdx.x;
+  if (blockIdx.y == 0 && threadIdx.x < 128 && j < J) {
+    float s = 0.f;
     const uint32_t at = smem_u32(&total[threadIdx.x]);
     for (uint32_t r = 0; r < gridDim.y; ++r) s += ld_shared_cluster_f32(mapa_shared(at, r));
-    const int j = j0 + threadIdx.x;
-    if (j < J) dbias[j] = from_f32<T>(s);
+    dbias[j] = from_f32<T>(s);
   }
   cluster_sync();
 }
@@ -65,29 +76,42 @@ __global__ void __launch_bounds__(256) gated_d_kernel(const T* dh, const T* fact
   grid_launch_next();
   grid_wait_previous();
   if (j >= F) return;
-  for (long long i = blockIdx.y; i < I; i += gridDim.y) {
-    const Vec<T, V> a = *reinterpret_cast<const Vec<T, V>*>(dh + i * F + j);
-    const Vec<T, V> p = *reinterpret_cast<const Vec<T, V>*>(factors + i * 2 * F + j);
-    const Vec<T, V> q = *reinterpret_cast<const Vec<T, V>*>(factors + i * 2 * F + F + j);
-    Vec<T, V> o, u;
+  constexpr int ROWS = 2;   // in flight
+  for (long long i = blockIdx.y; i < I; i += (long long)ROWS * gridDim.y) {
+    Vec<T, V> a[ROWS], p[ROWS], q[ROWS];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float f = to_f32(a.v[v]);
-      o.v[v] = from_f32<T>(f * to_f32(p.v[v]));
-      u.v[v] = from_f32<T>(f * to_f32(q.v[v]));
+    for (int r = 0; r < ROWS; ++r) {
+      const long long at = i + r * (long long)gridDim.y;
+      if (at < I) {
+        a[r] = *reinterpret_cast<const Vec<T, V>*>(dh + at * F + j);
+        p[r] = *reinterpret_cast<const Vec<T, V>*>(factors + at * 2 * F + j);
+        q[r] = *reinterpret_cast<const Vec<T, V>*>(factors + at * 2 * F + F + j);
+      }
     }
-    *reinterpret_cast<Vec<T, V>*>(d + i * ldd + j) = o;
-    *reinterpret_cast<Vec<T, V>*>(d + i * ldd + F + j) = u;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const long long at = i + r * (long long)gridDim.y;
+      if (at >= I) break;
+      Vec<T, V> o, u;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float f = to_f32(a[r].v[v]);
+        o.v[v] = from_f32<T>(f * to_f32(p[r].v[v]));
+        u.v[v] = from_f32<T>(f * to_f32(q[r].v[v]));
+      }
+      *reinterpret_cast<Vec<T, V>*>(d + at * ldd + j) = o;
+      *reinterpret_cast<Vec<T, V>*>(d + at * ldd + F + j) = u;
+    }
   }
 }
 
 template <typename T>
 int launch_d(const void* dy, const void* slope, int I, int J, void* d, long long ldd, void* dbias, cudaStream_t st) {
   const bool vec = J % 8 == 0 && aligned16(dy) && aligned16(slope);
-  const int strips = (J + 255) / 256;
+  const int strips = (J + 127) / 128;
   // rows of a strip over up to 8 blocks (a cluster, where they add up their sums); without sums, over more
-  const long long want = std::max(1, 4 * 152 / strips), cap = dbias ? 8 : 1024;
-  const int ys = (int)std::min({cap, want, ((long long)I + 7) / 8});
+  const long long want = std::max(1, 6 * 152 / strips), cap = dbias ? 8 : 1024;
+  const int ys = (int)std::min({cap, want, ((long long)I + 15) / 16});
   auto kernel = vec ? dense_d_kernel<T, 8> : dense_d_kernel<T, 1>;
   return launch_next(kernel, dim3((unsigned)strips, (unsigned)ys), 256, 0, st, 1, dbias ? (unsigned)ys : 1u, static_cast<const T*>(dy),
                      static_cast<const T*>(slope), I, J, static_cast<T*>(d), ldd, static_cast<T*>(dbias));

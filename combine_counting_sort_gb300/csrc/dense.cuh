@@ -122,76 +122,120 @@ MOE_DEV void with_act(int act, F&& f) {
 
 // ---------------------------------------------------------------- 32 x 32 blocks between registers and rows
 //
-// A warp's block: lane l holds 32 columns j0.. of row i0 + l.  With vectors each
-// lane moves its own row; rows that no vector fits (an odd row length, an
-// unaligned start) go through `stage` (32 x 33 floats of the warp's own), so
-// that each access covers 32 neighbouring columns of one row.
+// A warp reads its accumulators with lane l holding 32 columns of row i0 + l.  Stored
+// like that, one access would touch 32 rows for 16 bytes each; so a block goes through
+// 4 KB of shared memory of the warp's own, and each access covers whole sectors of
+// few rows: with vectors 64 bytes of 8 rows, and where no vector fits (an odd row
+// length, an unaligned start) 32 neighbouring values of one row.  Chunks of 16 bytes
+// are swizzled so that neither side meets a bank twice.
 
+constexpr uint32_t kBlockBytes = 32 * 32 * 4;
+
+// The block rounded to T, to rows of `out`.
 template <typename T>
-MOE_DEV void store_block(const float (&v)[32], T* out, long long ld, int i0, int j0, int I, int J, bool vec, float* stage) {
+MOE_DEV void store_block(const float (&v)[32], T* out, long long ld, int i0, int j0, int I, int J, bool vec, uint8_t* stage) {
   const int lane = threadIdx.x & 31;
-  if (vec) {
-    if (i0 + lane >= I) return;
-    T* p = out + (long long)(i0 + lane) * ld + j0;
+  __syncwarp();   // the last block has left the stage
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (j0 + 8 * c < J) {
-        Vec<T, 8> o;
+  for (int c = 0; c < 4; ++c) {
+    Vec<T, 8> o;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o.v[e] = from_f32<T>(v[8 * c + e]);
-        reinterpret_cast<Vec<T, 8>*>(p)[c] = o;
-      }
-    return;
+    for (int e = 0; e < 8; ++e) o.v[e] = from_f32<T>(v[8 * c + e]);
+    *reinterpret_cast<Vec<T, 8>*>(stage + lane * 64 + ((c ^ (lane >> 1)) & 3) * 16) = o;
   }
   __syncwarp();
+  if (vec) {
+    const int c = lane & 3;
 #pragma unroll
-  for (int c = 0; c < 32; ++c) stage[lane * 33 + c] = v[c];
-  __syncwarp();
-  const int rows = min(32, I - i0);
-  if (j0 + lane < J)
-    for (int r = 0; r < rows; ++r) out[(long long)(i0 + r) * ld + j0 + lane] = from_f32<T>(stage[r * 33 + lane]);
+    for (int k = 0; k < 4; ++k) {
+      const int r = 8 * k + (lane >> 2);
+      if (i0 + r < I && j0 + 8 * c < J)
+        *reinterpret_cast<uint4*>(out + (long long)(i0 + r) * ld + j0 + 8 * c) =
+            *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ (r >> 1)) & 3) * 16);
+    }
+  } else if (j0 + lane < J) {
+    const int rows = min(32, I - i0);
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r)
+      out[(long long)(i0 + r) * ld + j0 + lane] =
+          *reinterpret_cast<const T*>(stage + r * 64 + (((lane >> 3) ^ (r >> 1)) & 3) * 16 + (lane & 7) * 2);
+  }
 }
 
-// v += the block of `in`
+// act(block + bias) + residual to rows of g.out, and act' to rows of g.aux.  The
+// arithmetic is done where the columns lie beside one another, so bias and residual are
+// read in whole sectors too; `pre` holds them, fetched ahead (vectors only).
 template <typename T>
-MOE_DEV void add_block(float (&v)[32], const T* in, long long ld, int i0, int j0, int I, int J, bool vec, float* stage) {
-  const int lane = threadIdx.x & 31;
-  if (vec) {
-    if (i0 + lane >= I) return;
-    const T* p = in + (long long)(i0 + lane) * ld + j0;
+struct LinearAhead {
+  Vec<T, 8> bias, res[4];
+};
+
+template <typename T>
+MOE_DEV void linear_fetch(LinearAhead<T>& pre, const DenseArgs& g, int i0, int j0) {
+  const int lane = threadIdx.x & 31, j = j0 + 8 * (lane & 3);
+  if (!g.vec || j >= g.J) return;
+  if (g.bias && g.bias_vec) pre.bias = *reinterpret_cast<const Vec<T, 8>*>(static_cast<const T*>(g.bias) + j);
+  if (g.residual)
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (j0 + 8 * c < J) {
-        const Vec<T, 8> o = reinterpret_cast<const Vec<T, 8>*>(p)[c];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[8 * c + e] += to_f32(o.v[e]);
-      }
-    return;
-  }
-  __syncwarp();
-  const int rows = min(32, I - i0);
-  for (int r = 0; r < rows; ++r) stage[r * 33 + lane] = j0 + lane < J ? to_f32(in[(long long)(i0 + r) * ld + j0 + lane]) : 0.f;
-  __syncwarp();
-  if (lane < rows)
-#pragma unroll
-    for (int c = 0; c < 32; ++c) v[c] += stage[lane * 33 + c];
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + 8 * k + (lane >> 2);
+      if (i < g.I) pre.res[k] = *reinterpret_cast<const Vec<T, 8>*>(static_cast<const T*>(g.residual) + (long long)i * g.J + j);
+    }
 }
 
 template <typename T>
-MOE_DEV void add_bias(float (&v)[32], const T* bias, int j0, int J, bool vec) {
-  if (vec) {
+MOE_DEV void linear_block(const float (&v)[32], const LinearAhead<T>& pre, const DenseArgs& g, int i0, int j0, uint8_t* stage) {
+  const int lane = threadIdx.x & 31;
+  T* out = static_cast<T*>(g.out);
+  T* aux = static_cast<T*>(g.aux);
+  const T* bias = static_cast<const T*>(g.bias);
+  const T* residual = static_cast<const T*>(g.residual);
+  __syncwarp();
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (j0 + 8 * c < J) {
-        const Vec<T, 8> o = reinterpret_cast<const Vec<T, 8>*>(bias + j0)[c];
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<float4*>(stage + lane * 128 + ((c ^ lane) & 7) * 16) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  __syncwarp();
+  if (g.vec) {
+    const int c = lane & 3, j = j0 + 8 * c;
+    if (j >= g.J) return;
+    float b[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[8 * c + e] += to_f32(o.v[e]);
+    for (int e = 0; e < 8; ++e) b[e] = !bias ? 0.f : to_f32(g.bias_vec ? pre.bias.v[e] : bias[j + e]);
+    with_act(g.act, [&](auto act) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = 8 * k + (lane >> 2), i = i0 + r;
+        if (i >= g.I) continue;
+        const float4 lo = *reinterpret_cast<const float4*>(stage + r * 128 + (((2 * c) ^ r) & 7) * 16);
+        const float4 hi = *reinterpret_cast<const float4*>(stage + r * 128 + (((2 * c + 1) ^ r) & 7) * 16);
+        const float a[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        const long long at = (long long)i * g.J + j;
+        Vec<T, 8> y, s;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 f = act_slope<decltype(act)::value>(a[e] + b[e]);
+          s.v[e] = from_f32<T>(f.y);
+          y.v[e] = from_f32<T>(residual ? f.x + to_f32(pre.res[k].v[e]) : f.x);
+        }
+        if (aux) *reinterpret_cast<Vec<T, 8>*>(aux + at) = s;
+        *reinterpret_cast<Vec<T, 8>*>(out + at) = y;
       }
-    return;
+    });
+  } else {
+    const int j = j0 + lane, rows = min(32, g.I - i0);
+    if (j >= g.J) return;
+    const float b = bias ? to_f32(bias[j]) : 0.f;
+    with_act(g.act, [&](auto act) {
+#pragma unroll 8
+      for (int r = 0; r < rows; ++r) {
+        const float a = *reinterpret_cast<const float*>(stage + r * 128 + (((lane >> 2) ^ r) & 7) * 16 + (lane & 3) * 4);
+        const long long at = (long long)(i0 + r) * g.J + j;
+        const float2 f = act_slope<decltype(act)::value>(a + b);
+        if (aux) aux[at] = from_f32<T>(f.y);
+        out[at] = from_f32<T>(residual ? f.x + to_f32(residual[at]) : f.x);
+      }
+    });
   }
-#pragma unroll
-  for (int c = 0; c < 32; ++c)
-    if (j0 + c < J) v[c] += to_f32(bias[j0 + c]);
 }
 
 }  // namespace moe

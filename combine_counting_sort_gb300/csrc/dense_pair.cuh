@@ -29,8 +29,7 @@ struct DPairShared {
   int abort_flag;
 };
 
-constexpr size_t kDPairStageFloats = 32 * 33;
-constexpr size_t kDPairSmemBytes = 1024 + kDPairStages * kDPairStageBytes + kDPairEpiWarps * kDPairStageFloats * 4 + sizeof(DPairShared);
+constexpr size_t kDPairSmemBytes = 1024 + kDPairStages * kDPairStageBytes + kDPairEpiWarps * kBlockBytes + sizeof(DPairShared);
 static_assert(kDPairSmemBytes <= 227 * 1024, "shared memory of one CTA");
 
 struct DTile {
@@ -64,8 +63,8 @@ __global__ void __launch_bounds__(kDPairThreads, 1)
                       const __grid_constant__ DenseArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  float* epi_stage = reinterpret_cast<float*>(stages + kDPairStages * kDPairStageBytes);
-  DPairShared* sh = reinterpret_cast<DPairShared*>(epi_stage + kDPairEpiWarps * kDPairStageFloats);
+  uint8_t* epi_stage = stages + kDPairStages * kDPairStageBytes;
+  DPairShared* sh = reinterpret_cast<DPairShared*>(epi_stage + kDPairEpiWarps * kBlockBytes);
   const int warp = threadIdx.x >> 5;
   const uint32_t rank = cluster_ctarank();
   const uint64_t tmo = g.timeout_ns;
@@ -164,22 +163,24 @@ __global__ void __launch_bounds__(kDPairThreads, 1)
     }
   } else if (warp >= kDPairEpiWarp0) {
     const int q = warp & 3, half = (warp - kDPairEpiWarp0) >> 2;
-    float* stage = epi_stage + (warp - kDPairEpiWarp0) * kDPairStageFloats;
+    uint8_t* stage = epi_stage + (warp - kDPairEpiWarp0) * kBlockBytes;
     const uint32_t tmem = sh->tmem_base + ((uint32_t)(32 * q) << 16);
     const uint32_t tempty_even = mapa_shared(smem_u32(&sh->tempty[0]), 0);
     T* out = static_cast<T*>(g.out);
     T* aux = static_cast<T*>(g.aux);
+    constexpr int kChunks = kTileJ / 2 / 32;   // of this warp
     int n = 0;
     for (int t = cluster; t < tiles; t += clusters, ++n) {
       const uint32_t p = (uint32_t)n & 1u;
+      const DTile x = dense_tile(t, ti, tj, kTileJ);
+      const int i0 = x.i0 + (int)rank * 128 + 32 * q, jw = x.j0 + half * (kTileJ / 2);
+      LinearAhead<T> ahead;
+      if (EPI == kEpiLinear) linear_fetch(ahead, g, i0, jw);
       if (!mbar_wait(smem_u32(&sh->tfull[p]), ((uint32_t)n >> 1) & 1u, &sh->abort_flag, g.status, tmo)) break;
       tc_fence_after();
-      const DTile x = dense_tile(t, ti, tj, kTileJ);
-      const int i0 = x.i0 + (int)rank * 128 + 32 * q;
-      constexpr int kChunks = kTileJ / 2 / 32;   // of this warp
 #pragma unroll 1
       for (int c = 0; c < kChunks; ++c) {
-        const int col = half * (kTileJ / 2) + 32 * c, j0 = x.j0 + col;
+        const int col = half * (kTileJ / 2) + 32 * c, j0 = jw + 32 * c;
         float v[32];
         tmem_drain32(tmem + p * 256 + col, v);
         float u[32];
@@ -212,28 +213,11 @@ __global__ void __launch_bounds__(kDPairThreads, 1)
             });
           }
           store_block(u, out, g.J, i0, j0, g.I, g.J, g.vec, stage);
+        } else if (EPI == kEpiLinear) {
+          const LinearAhead<T> now = ahead;
+          if (c + 1 < kChunks) linear_fetch(ahead, g, i0, j0 + 32);
+          linear_block(v, now, g, i0, j0, stage);
         } else {
-          if (EPI == kEpiLinear) {
-            if (g.bias) add_bias(v, static_cast<const T*>(g.bias), j0, g.J, g.bias_vec);
-            if (aux) {
-              float f[32];
-              with_act(g.act, [&](auto act) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const float2 a = act_slope<decltype(act)::value>(v[e]);
-                  v[e] = a.x;
-                  f[e] = a.y;
-                }
-              });
-              store_block(f, aux, g.J, i0, j0, g.I, g.J, g.vec, stage);
-            } else {
-              with_act(g.act, [&](auto act) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = act_slope<decltype(act)::value>(v[e]).x;
-              });
-            }
-            if (g.residual) add_block(v, static_cast<const T*>(g.residual), g.J, i0, j0, g.I, g.J, g.vec, stage);
-          }
           store_block(v, out, g.J, i0, j0, g.I, g.J, g.vec, stage);
         }
       }
