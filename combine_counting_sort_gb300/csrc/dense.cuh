@@ -83,24 +83,56 @@ MOE_DEV void umma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint
 
 // ---------------------------------------------------------------- activations
 
-// act(a) and act'(a) in fp32.
+// act(a) and act'(a) in fp32, two values at a time.
+//   silu       s = 1 / (1 + exp(-a)):  a s,  s + a s (1 - s)
+//   gelu_tanh  (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)) = s, 2 z = c a (1 + 0.044715 a^2):  a s,  s + a s (1 - s) (2 z)'
+//   gelu       the normal distribution's tail q(|a|) = exp(-a^2 / 2) t (c1 + t (c2 + ...)), t = 1 / (1 + 0.36 |a|): seven
+//              terms, least largest error of the ratio over |a| <= 14 (2^-20, so small values far below zero
+//              keep their digits); the density comes of the same exponential
+// One exponential and one reciprocal each, both by the approximate instructions (2^-22 of
+// the value): 8 issue cycles each for a warp, so they bound the epilogue's arithmetic.
+MOE_DEV float ex2(float v) { float r; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v)); return r; }
+MOE_DEV float rcp(float v) { float r; asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v)); return r; }
+MOE_DEV f32x2 ex2_pair(f32x2 v) { return pack_f32x2(ex2(lo2(v)), ex2(hi2(v))); }
+MOE_DEV f32x2 rcp_pair(f32x2 v) { return pack_f32x2(rcp(lo2(v)), rcp(hi2(v))); }
+
 template <int ACT>
-MOE_DEV float2 act_slope(float a) {
-  if (ACT == MOE_ACT_RELU) return make_float2(a < 0.f ? 0.f : a, a > 0.f ? 1.f : 0.f);
-  if (ACT == MOE_ACT_SILU) {
-    const float s = __fdividef(1.f, 1.f + __expf(-a));
-    return make_float2(a * s, s * (1.f + a * (1.f - s)));
+MOE_DEV void act_pair(f32x2 a, f32x2& y, f32x2& slope) {
+  constexpr float kLog2e = 1.44269504f;
+  const f32x2 one = both(1.f);
+  if (ACT == MOE_ACT_RELU) {
+    const float l = lo2(a), h = hi2(a);
+    y = pack_f32x2(l < 0.f ? 0.f : l, h < 0.f ? 0.f : h);   // (a NaN stays)
+    slope = pack_f32x2(l > 0.f ? 1.f : 0.f, h > 0.f ? 1.f : 0.f);
+  } else if (ACT == MOE_ACT_SILU) {
+    const f32x2 s = rcp_pair(add2(ex2_pair(mul2(a, both(-kLog2e))), one));
+    y = mul2(a, s);
+    slope = fma2(y, fma2(s, both(-1.f), one), s);
+  } else if (ACT == MOE_ACT_GELU_TANH) {
+    constexpr float c = 1.59576912f, d = 0.044715f * c;   // 2 sqrt(2 / pi)
+    const f32x2 a2 = mul2(a, a);
+    const f32x2 s = rcp_pair(add2(ex2_pair(mul2(a, fma2(a2, both(-d * kLog2e), both(-c * kLog2e)))), one));
+    y = mul2(a, s);
+    slope = fma2(mul2(y, fma2(s, both(-1.f), one)), fma2(a2, both(3.f * d), both(c)), s);
+  } else if (ACT == MOE_ACT_GELU) {
+    const f32x2 b = pack_f32x2(fabsf(lo2(a)), fabsf(hi2(a)));
+    const f32x2 e = ex2_pair(mul2(mul2(a, a), both(-0.5f * kLog2e)));
+    const f32x2 t = rcp_pair(fma2(b, both(0.36f), one));
+    f32x2 q = fma2(t, both(0.0470560688f), both(-0.179763952f));
+    q = fma2(q, t, both(0.180953031f));
+    q = fma2(q, t, both(0.0265499758f));
+    q = fma2(q, t, both(0.13971904f));
+    q = fma2(q, t, both(0.141772491f));
+    q = fma2(q, t, both(0.143713043f));
+    q = mul2(mul2(q, t), e);
+    const f32x2 p = fma2(q, both(-1.f), one);
+    const f32x2 cdf = pack_f32x2(lo2(a) < 0.f ? lo2(q) : lo2(p), hi2(a) < 0.f ? hi2(q) : hi2(p));
+    y = mul2(a, cdf);
+    slope = fma2(mul2(a, e), both(0.39894228f), cdf);
+  } else {
+    y = a;
+    slope = one;
   }
-  if (ACT == MOE_ACT_GELU) {   // erfc: no cancellation for a far below zero
-    const float cdf = 0.5f * erfcf(-0.70710678f * a);
-    return make_float2(a * cdf, cdf + a * (0.39894228f * __expf(-0.5f * a * a)));
-  }
-  if (ACT == MOE_ACT_GELU_TANH) {   // (1 + tanh z) / 2 = 1 / (1 + exp(-2 z))
-    const float z2 = 1.5957691f * a * fmaf(0.044715f * a, a, 1.f);
-    const float s = __fdividef(1.f, 1.f + __expf(-z2)), r = 1.f - s;
-    return make_float2(a * s, s + (r > 0.f ? a * s * r * (1.5957691f * fmaf(0.134145f * a, a, 1.f)) : 0.f));
-  }
-  return make_float2(a, 1.f);
 }
 
 template <int ACT>
@@ -122,27 +154,35 @@ MOE_DEV void with_act(int act, F&& f) {
 
 // ---------------------------------------------------------------- 32 x 32 blocks between registers and rows
 //
-// A warp reads its accumulators with lane l holding 32 columns of row i0 + l.  Stored
-// like that, one access would touch 32 rows for 16 bytes each; so a block goes through
-// 4 KB of shared memory of the warp's own, and each access covers whole sectors of
-// few rows: with vectors 64 bytes of 8 rows, and where no vector fits (an odd row
-// length, an unaligned start) 32 neighbouring values of one row.  Chunks of 16 bytes
-// are swizzled so that neither side meets a bank twice.
+// A warp holds its accumulators with lane l having 32 columns of row i0 + l, and works
+// on them there.  Moved like that, one access would touch 32 rows for 16 bytes each; so
+// blocks go, in the type's 16 bits, through 2 KB of shared memory, and each access covers
+// whole sectors of few rows: with vectors 64 bytes of 8 rows, and where no vector fits (an
+// odd row length, an unaligned start) 32 neighbouring values of one row.  Chunks of
+// 16 bytes are swizzled so that neither side meets a bank twice.  (Working on the block
+// where its columns lie beside one another, through fp32 in shared memory: 36 us against
+// 21 for 4096 x 7168 x 512.)
 
-constexpr uint32_t kBlockBytes = 32 * 32 * 4;
+constexpr uint32_t kBlockBytes = 32 * 64;
+
+// where chunk c (8 columns) of row r is
+MOE_DEV uint32_t block_at(int r, int c) { return (uint32_t)(r * 64 + ((c ^ (r >> 1)) & 3) * 16); }
+
+// 32 columns of this lane's accumulator row, in pairs
+MOE_DEV void drain_block(uint32_t taddr, f32x2 (&v)[16]) {
+  float f[32];
+  tmem_drain32(taddr, f);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = pack_f32x2(f[2 * e], f[2 * e + 1]);
+}
 
 // The block rounded to T, to rows of `out`.
 template <typename T>
-MOE_DEV void store_block(const float (&v)[32], T* out, long long ld, int i0, int j0, int I, int J, bool vec, uint8_t* stage) {
+MOE_DEV void store_block(const f32x2 (&v)[16], T* out, long long ld, int i0, int j0, int I, int J, bool vec, uint8_t* stage) {
   const int lane = threadIdx.x & 31;
   __syncwarp();   // the last block has left the stage
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    Vec<T, 8> o;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o.v[e] = from_f32<T>(v[8 * c + e]);
-    *reinterpret_cast<Vec<T, 8>*>(stage + lane * 64 + ((c ^ (lane >> 1)) & 3) * 16) = o;
-  }
+  for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(stage + block_at(lane, c)) = Pairs<T>::put(v + 4 * c);
   __syncwarp();
   if (vec) {
     const int c = lane & 3;
@@ -150,92 +190,88 @@ MOE_DEV void store_block(const float (&v)[32], T* out, long long ld, int i0, int
     for (int k = 0; k < 4; ++k) {
       const int r = 8 * k + (lane >> 2);
       if (i0 + r < I && j0 + 8 * c < J)
-        *reinterpret_cast<uint4*>(out + (long long)(i0 + r) * ld + j0 + 8 * c) =
-            *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ (r >> 1)) & 3) * 16);
+        *reinterpret_cast<uint4*>(out + (long long)(i0 + r) * ld + j0 + 8 * c) = *reinterpret_cast<const uint4*>(stage + block_at(r, c));
     }
   } else if (j0 + lane < J) {
     const int rows = min(32, I - i0);
 #pragma unroll 8
     for (int r = 0; r < rows; ++r)
-      out[(long long)(i0 + r) * ld + j0 + lane] =
-          *reinterpret_cast<const T*>(stage + r * 64 + (((lane >> 3) ^ (r >> 1)) & 3) * 16 + (lane & 7) * 2);
+      out[(long long)(i0 + r) * ld + j0 + lane] = *reinterpret_cast<const T*>(stage + block_at(r, lane >> 3) + (lane & 7) * 2);
   }
 }
 
-// act(block + bias) + residual to rows of g.out, and act' to rows of g.aux.  The
-// arithmetic is done where the columns lie beside one another, so bias and residual are
-// read in whole sectors too; `pre` holds them, fetched ahead (vectors only).
-template <typename T>
-struct LinearAhead {
-  Vec<T, 8> bias, res[4];
+// A block's residual as its rows lie, fetched ahead of its use where vectors fit.
+struct ResidualAhead {
+  uint4 v[4];
 };
 
 template <typename T>
-MOE_DEV void linear_fetch(LinearAhead<T>& pre, const DenseArgs& g, int i0, int j0) {
+MOE_DEV void fetch_residual(ResidualAhead& a, const DenseArgs& g, int i0, int j0) {
   const int lane = threadIdx.x & 31, j = j0 + 8 * (lane & 3);
-  if (!g.vec || j >= g.J) return;
-  if (g.bias && g.bias_vec) pre.bias = *reinterpret_cast<const Vec<T, 8>*>(static_cast<const T*>(g.bias) + j);
-  if (g.residual)
+  if (!g.residual || !g.vec || j >= g.J) return;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + 8 * k + (lane >> 2);
-      if (i < g.I) pre.res[k] = *reinterpret_cast<const Vec<T, 8>*>(static_cast<const T*>(g.residual) + (long long)i * g.J + j);
+  for (int k = 0; k < 4; ++k) {
+    const int i = i0 + 8 * k + (lane >> 2);
+    if (i < g.I) a.v[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(g.residual) + (long long)i * g.J + j);
+  }
+}
+
+// 32 columns of the accumulator plus their bias, which every lane reads whole (from L1 but for a
+// tile's first rows) while the accumulator comes.
+template <typename T>
+MOE_DEV void drain_biased(uint32_t taddr, f32x2 (&v)[16], const DenseArgs& g, int j0) {
+  const T* bias = static_cast<const T*>(g.bias) + j0;
+  if (g.bias && g.bias_vec && j0 + 32 <= g.J) {
+    uint4 b[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) b[c] = reinterpret_cast<const uint4*>(bias)[c];
+    drain_block(taddr, v);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      f32x2 f[4];
+      Pairs<T>::get(b[c], f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * c + e] = add2(v[4 * c + e], f[e]);
     }
+  } else {
+    drain_block(taddr, v);
+    if (g.bias)
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const int n = g.J - j0 - 2 * c;
+        v[c] = add2(v[c], pack_f32x2(n > 0 ? to_f32(bias[2 * c]) : 0.f, n > 1 ? to_f32(bias[2 * c + 1]) : 0.f));
+      }
+  }
+}
+
+// The residual's block into shared memory, and from there to the lanes of its rows.
+template <typename T>
+MOE_DEV void put_residual(const ResidualAhead& a, const DenseArgs& g, int i0, int j0, uint8_t* stage) {
+  const int lane = threadIdx.x & 31;
+  if (g.vec) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(stage + block_at(8 * k + (lane >> 2), lane & 3)) = a.v[k];
+  } else if (j0 + lane < g.J) {
+    const int rows = min(32, g.I - i0);
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r)
+      *reinterpret_cast<T*>(stage + block_at(r, lane >> 3) + (lane & 7) * 2) =
+          static_cast<const T*>(g.residual)[(long long)(i0 + r) * g.J + j0 + lane];
+  }
 }
 
 template <typename T>
-MOE_DEV void linear_block(const float (&v)[32], const LinearAhead<T>& pre, const DenseArgs& g, int i0, int j0, uint8_t* stage) {
+MOE_DEV void add_residual(f32x2 (&v)[16], const uint8_t* stage) {
   const int lane = threadIdx.x & 31;
-  T* out = static_cast<T*>(g.out);
-  T* aux = static_cast<T*>(g.aux);
-  const T* bias = static_cast<const T*>(g.bias);
-  const T* residual = static_cast<const T*>(g.residual);
   __syncwarp();
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<float4*>(stage + lane * 128 + ((c ^ lane) & 7) * 16) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-  __syncwarp();
-  if (g.vec) {
-    const int c = lane & 3, j = j0 + 8 * c;
-    if (j >= g.J) return;
-    float b[8];
+  for (int c = 0; c < 4; ++c) {
+    f32x2 r[4];
+    Pairs<T>::get(*reinterpret_cast<const uint4*>(stage + block_at(lane, c)), r);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) b[e] = !bias ? 0.f : to_f32(g.bias_vec ? pre.bias.v[e] : bias[j + e]);
-    with_act(g.act, [&](auto act) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = 8 * k + (lane >> 2), i = i0 + r;
-        if (i >= g.I) continue;
-        const float4 lo = *reinterpret_cast<const float4*>(stage + r * 128 + (((2 * c) ^ r) & 7) * 16);
-        const float4 hi = *reinterpret_cast<const float4*>(stage + r * 128 + (((2 * c + 1) ^ r) & 7) * 16);
-        const float a[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        const long long at = (long long)i * g.J + j;
-        Vec<T, 8> y, s;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 f = act_slope<decltype(act)::value>(a[e] + b[e]);
-          s.v[e] = from_f32<T>(f.y);
-          y.v[e] = from_f32<T>(residual ? f.x + to_f32(pre.res[k].v[e]) : f.x);
-        }
-        if (aux) *reinterpret_cast<Vec<T, 8>*>(aux + at) = s;
-        *reinterpret_cast<Vec<T, 8>*>(out + at) = y;
-      }
-    });
-  } else {
-    const int j = j0 + lane, rows = min(32, g.I - i0);
-    if (j >= g.J) return;
-    const float b = bias ? to_f32(bias[j]) : 0.f;
-    with_act(g.act, [&](auto act) {
-#pragma unroll 8
-      for (int r = 0; r < rows; ++r) {
-        const float a = *reinterpret_cast<const float*>(stage + r * 128 + (((lane >> 2) ^ r) & 7) * 16 + (lane & 3) * 4);
-        const long long at = (long long)(i0 + r) * g.J + j;
-        const float2 f = act_slope<decltype(act)::value>(a + b);
-        if (aux) aux[at] = from_f32<T>(f.y);
-        out[at] = from_f32<T>(residual ? f.x + to_f32(residual[at]) : f.x);
-      }
-    });
+    for (int e = 0; e < 4; ++e) v[4 * c + e] = add2(v[4 * c + e], r[e]);
   }
+  __syncwarp();
 }
 
 }  // namespace moe

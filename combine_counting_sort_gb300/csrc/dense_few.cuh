@@ -33,6 +33,11 @@ struct DFewPlan {
   int ti;                  // tiles of i
 };
 
+MOE_DEV float4 ld_shared_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 MOE_DEV float ld_shared_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -48,6 +53,32 @@ MOE_DEV void tmem_drain16(uint32_t taddr, float (&v)[16]) {
         "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
       : "r"(taddr)
       : "memory");
+}
+
+// Four values, n of them there, 8 bytes at a time where they lie so.
+template <typename T>
+MOE_DEV void store_quad(const f32x2 (&v)[2], T* p, int n, bool vec) {
+  const T o[4] = {from_f32<T>(lo2(v[0])), from_f32<T>(hi2(v[0])), from_f32<T>(lo2(v[1])), from_f32<T>(hi2(v[1]))};
+  if (vec) {
+    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(o);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) p[e] = o[e];
+  }
+}
+template <typename T>
+MOE_DEV void add_quad(f32x2 (&v)[2], const T* p, int n, bool vec) {
+  T x[4] = {};
+  if (vec) {
+    *reinterpret_cast<uint2*>(x) = *reinterpret_cast<const uint2*>(p);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) x[e] = p[e];
+  }
+  v[0] = add2(v[0], pack_f32x2(to_f32(x[0]), to_f32(x[1])));
+  v[1] = add2(v[1], pack_f32x2(to_f32(x[2]), to_f32(x[3])));
 }
 
 // Q's rows j are the M operand, P's rows i the N operand.
@@ -178,42 +209,48 @@ __global__ void __launch_bounds__(kDFewThreads)
   const T* residual = static_cast<const T*>(g.residual);
   T* out = static_cast<T*>(g.out);
   T* aux = static_cast<T*>(g.aux);
+  constexpr int kQuads = kRows / 4;   // four columns a thread
   with_act(EPI == kEpiPlain ? MOE_ACT_NONE : g.act, [&](auto act) {
-    for (int e = rank * kDFewThreads + (int)threadIdx.x; e < tv * kRows; e += split * kDFewThreads) {
-      const int t = e / kRows, r = e % kRows, j = j0 + r;
-      const long long i = i0 + t;
-      if (j >= g.J) continue;
+    for (int e = rank * kDFewThreads + (int)threadIdx.x; e < tv * kQuads; e += split * kDFewThreads) {
+      const int t = e / kQuads, r = e % kQuads * 4, j = j0 + r, n = min(4, g.J - j);
+      const long long i = i0 + t, o = i * g.J + j;
+      if (n <= 0) continue;
       const uint32_t at = (uint32_t)(t * 128 + r) * 4u;
-      float a[kDFewMaxSplit], b[kDFewMaxSplit];
+      float4 a[kDFewMaxSplit], b[kDFewMaxSplit];
 #pragma unroll
       for (int c = 0; c < kDFewMaxSplit; ++c)
         if (c < split) {
-          a[c] = ld_shared_cluster_f32(peer[c] + at);
-          if (EPI == kEpiGated) b[c] = ld_shared_cluster_f32(peer[c] + at + 256u);
+          a[c] = ld_shared_cluster_f32x4(peer[c] + at);
+          if (EPI == kEpiGated) b[c] = ld_shared_cluster_f32x4(peer[c] + at + 256u);
         }
-      float v = a[0], u = EPI == kEpiGated ? b[0] : 0.f;
+      f32x2 v[2] = {pack_f32x2(a[0].x, a[0].y), pack_f32x2(a[0].z, a[0].w)}, u[2] = {0, 0}, s[2];
+      if (EPI == kEpiGated) u[0] = pack_f32x2(b[0].x, b[0].y), u[1] = pack_f32x2(b[0].z, b[0].w);
 #pragma unroll
       for (int c = 1; c < kDFewMaxSplit; ++c)
         if (c < split) {
-          v += a[c];
-          if (EPI == kEpiGated) u += b[c];
+          v[0] = add2(v[0], pack_f32x2(a[c].x, a[c].y));
+          v[1] = add2(v[1], pack_f32x2(a[c].z, a[c].w));
+          if (EPI == kEpiGated) {
+            u[0] = add2(u[0], pack_f32x2(b[c].x, b[c].y));
+            u[1] = add2(u[1], pack_f32x2(b[c].z, b[c].w));
+          }
         }
-      const long long o = i * g.J + j;
+      if (EPI == kEpiLinear && bias) add_quad(v, bias + j, n, g.bias_vec);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) act_pair<decltype(act)::value>(v[k], v[k], s[k]);
       if (EPI == kEpiGated) {
-        const float2 s = act_slope<decltype(act)::value>(v);
         if (aux) {
-          aux[2 * i * g.J + j] = from_f32<T>(s.y * u);
-          aux[2 * i * g.J + g.J + j] = from_f32<T>(s.x);
+          const f32x2 f[2] = {mul2(s[0], u[0]), mul2(s[1], u[1])};
+          store_quad(f, aux + 2 * i * g.J + j, n, g.vec);
+          store_quad(v, aux + 2 * i * g.J + g.J + j, n, g.vec);
         }
-        v = s.x * u;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) v[k] = mul2(v[k], u[k]);
       } else if (EPI == kEpiLinear) {
-        if (bias) v += to_f32(bias[j]);
-        const float2 s = act_slope<decltype(act)::value>(v);
-        if (aux) aux[o] = from_f32<T>(s.y);
-        v = s.x;
-        if (residual) v += to_f32(residual[o]);
+        if (aux) store_quad(s, aux + o, n, g.vec);
+        if (residual) add_quad(v, residual + o, n, g.vec);
       }
-      out[o] = from_f32<T>(v);
+      store_quad(v, out + o, n, g.vec);
     }
   });
   if (split > 1) cluster_sync();   // no CTA leaves while another reads its sums

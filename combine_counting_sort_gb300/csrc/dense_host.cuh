@@ -45,6 +45,18 @@ int resident_pairs(K kernel, int nsm) {
   return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
 }
 
+template <typename T, bool PMN, bool QMN, int EPI, bool AUX>
+int launch_pair(const CUtensorMap& tmP, const CUtensorMap& tmQ, const DenseArgs& g, int nsm, cudaStream_t st) {
+  auto kernel = dense_pair_kernel<T, PMN, QMN, EPI, AUX>;
+  static const int resident = resident_pairs(kernel, nsm);   // once: the grid is persistent
+  if (resident < 1) return MOE_ERR_CUDA;
+  constexpr int kTileJ = EPI == kEpiGated ? 128 : 256;
+  const long long tiles = ((long long)g.I + 255) / 256 * (((long long)g.J + kTileJ - 1) / kTileJ);
+  if (tiles > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
+  return launch_next(kernel, dim3(2 * (unsigned)std::min<long long>(std::min(resident, nsm / 2), tiles)), kDPairThreads, kDPairSmemBytes, st,
+                     2, 1, tmP, tmQ, g);
+}
+
 template <typename T, bool PMN, bool QMN, int EPI>
 int launch_dense(const DenseOperand& P, const DenseOperand& Q, DenseArgs g, cudaStream_t st) {
   const int nsm = device_sm_count();
@@ -54,14 +66,8 @@ int launch_dense(const DenseOperand& P, const DenseOperand& Q, DenseArgs g, cuda
   CUtensorMap tmP, tmQ;
   if (plan.pair) {
     if (!encode_operand<T>(&tmP, P, g.K, 128) || !encode_operand<T>(&tmQ, Q, g.K, 128)) return MOE_ERR_CUDA;
-    auto kernel = dense_pair_kernel<T, PMN, QMN, EPI>;
-    static const int resident = resident_pairs(kernel, nsm);   // once: the grid is persistent
-    if (resident < 1) return MOE_ERR_CUDA;
-    constexpr int kTileJ = EPI == kEpiGated ? 128 : 256;
-    const long long tiles = ((long long)g.I + 255) / 256 * (((long long)g.J + kTileJ - 1) / kTileJ);
-    if (tiles > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
-    return launch_next(kernel, dim3(2 * (unsigned)std::min<long long>(std::min(resident, nsm / 2), tiles)), kDPairThreads, kDPairSmemBytes, st,
-                       2, 1, tmP, tmQ, g);
+    if (EPI != kEpiPlain && g.aux) return launch_pair<T, PMN, QMN, EPI, EPI != kEpiPlain>(tmP, tmQ, g, nsm, st);
+    return launch_pair<T, PMN, QMN, EPI, false>(tmP, tmQ, g, nsm, st);
   }
   if (!encode_operand<T>(&tmP, P, g.K, plan.nt) || !encode_operand<T>(&tmQ, Q, g.K, EPI == kEpiGated ? 64 : 128)) return MOE_ERR_CUDA;
   auto kernel = dense_few_kernel<T, PMN, QMN, EPI>;

@@ -29,7 +29,7 @@ struct DPairShared {
   int abort_flag;
 };
 
-constexpr size_t kDPairSmemBytes = 1024 + kDPairStages * kDPairStageBytes + kDPairEpiWarps * kBlockBytes + sizeof(DPairShared);
+constexpr size_t kDPairSmemBytes = 1024 + kDPairStages * kDPairStageBytes + kDPairEpiWarps * 2 * kBlockBytes + sizeof(DPairShared);
 static_assert(kDPairSmemBytes <= 227 * 1024, "shared memory of one CTA");
 
 struct DTile {
@@ -57,14 +57,15 @@ MOE_DEV void load_operand_pair(uint32_t dst, const CUtensorMap* map, int r0, int
   }
 }
 
-template <typename T, bool PMN, bool QMN, int EPI>
+// AUX: what the backward pass needs is written too.
+template <typename T, bool PMN, bool QMN, int EPI, bool AUX>
 __global__ void __launch_bounds__(kDPairThreads, 1)
     dense_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ DenseArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* epi_stage = stages + kDPairStages * kDPairStageBytes;
-  DPairShared* sh = reinterpret_cast<DPairShared*>(epi_stage + kDPairEpiWarps * kBlockBytes);
+  DPairShared* sh = reinterpret_cast<DPairShared*>(epi_stage + kDPairEpiWarps * 2 * kBlockBytes);
   const int warp = threadIdx.x >> 5;
   const uint32_t rank = cluster_ctarank();
   const uint64_t tmo = g.timeout_ns;
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kDPairThreads, 1)
     }
   } else if (warp >= kDPairEpiWarp0) {
     const int q = warp & 3, half = (warp - kDPairEpiWarp0) >> 2;
-    uint8_t* stage = epi_stage + (warp - kDPairEpiWarp0) * kBlockBytes;
+    uint8_t* stage = epi_stage + (warp - kDPairEpiWarp0) * 2 * kBlockBytes;
     const uint32_t tmem = sh->tmem_base + ((uint32_t)(32 * q) << 16);
     const uint32_t tempty_even = mapa_shared(smem_u32(&sh->tempty[0]), 0);
     T* out = static_cast<T*>(g.out);
@@ -174,17 +175,17 @@ __global__ void __launch_bounds__(kDPairThreads, 1)
       const uint32_t p = (uint32_t)n & 1u;
       const DTile x = dense_tile(t, ti, tj, kTileJ);
       const int i0 = x.i0 + (int)rank * 128 + 32 * q, jw = x.j0 + half * (kTileJ / 2);
-      LinearAhead<T> ahead;
-      if (EPI == kEpiLinear) linear_fetch(ahead, g, i0, jw);
+      ResidualAhead ahead;
+      if (EPI == kEpiLinear) fetch_residual<T>(ahead, g, i0, jw);
       if (!mbar_wait(smem_u32(&sh->tfull[p]), ((uint32_t)n >> 1) & 1u, &sh->abort_flag, g.status, tmo)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < kChunks; ++c) {
         const int col = half * (kTileJ / 2) + 32 * c, j0 = jw + 32 * c;
-        float v[32];
-        tmem_drain32(tmem + p * 256 + col, v);
-        float u[32];
-        if (EPI == kEpiGated) tmem_drain32(tmem + p * 256 + 128 + col, u);
+        f32x2 v[16], u[16];
+        if (EPI == kEpiLinear) drain_biased<T>(tmem + p * 256 + col, v, g, j0);
+        else drain_block(tmem + p * 256 + col, v);
+        if (EPI == kEpiGated) drain_block(tmem + p * 256 + 128 + col, u);
         if (c == kChunks - 1) {   // the accumulator is read: the next tile may have it
           tc_fence_before();
           __syncwarp();
@@ -193,15 +194,16 @@ __global__ void __launch_bounds__(kDPairThreads, 1)
         }
         if (i0 >= g.I || j0 >= g.J) continue;
         if (EPI == kEpiGated) {
-          if (aux) {
-            float f[32];
+          if (AUX) {
+            f32x2 f[16];
             with_act(g.act, [&](auto act) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float2 a = act_slope<decltype(act)::value>(v[e]);
-                v[e] = a.x;
-                f[e] = a.y * u[e];
-                u[e] *= a.x;
+              for (int e = 0; e < 16; ++e) {
+                f32x2 y, s;
+                act_pair<decltype(act)::value>(v[e], y, s);
+                v[e] = y;
+                f[e] = mul2(s, u[e]);
+                u[e] = mul2(y, u[e]);
               }
             });
             store_block(f, aux, 2LL * g.J, i0, j0, g.I, g.J, g.vec, stage);
@@ -209,14 +211,35 @@ __global__ void __launch_bounds__(kDPairThreads, 1)
           } else {
             with_act(g.act, [&](auto act) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) u[e] *= act_slope<decltype(act)::value>(v[e]).x;
+              for (int e = 0; e < 16; ++e) {
+                f32x2 y, s;
+                act_pair<decltype(act)::value>(v[e], y, s);
+                u[e] = mul2(y, u[e]);
+              }
             });
           }
           store_block(u, out, g.J, i0, j0, g.I, g.J, g.vec, stage);
         } else if (EPI == kEpiLinear) {
-          const LinearAhead<T> now = ahead;
-          if (c + 1 < kChunks) linear_fetch(ahead, g, i0, j0 + 32);
-          linear_block(v, now, g, i0, j0, stage);
+          if (g.residual) put_residual<T>(ahead, g, i0, j0, stage + kBlockBytes);
+          if (c + 1 < kChunks) fetch_residual<T>(ahead, g, i0, j0 + 32);
+          if (AUX) {
+            f32x2 f[16];
+            with_act(g.act, [&](auto act) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) act_pair<decltype(act)::value>(v[e], v[e], f[e]);
+            });
+            store_block(f, aux, g.J, i0, j0, g.I, g.J, g.vec, stage);
+          } else {
+            with_act(g.act, [&](auto act) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                f32x2 s;
+                act_pair<decltype(act)::value>(v[e], v[e], s);
+              }
+            });
+          }
+          if (g.residual) add_residual<T>(v, stage + kBlockBytes);
+          store_block(v, out, g.J, i0, j0, g.I, g.J, g.vec, stage);
         } else {
           store_block(v, out, g.J, i0, j0, g.I, g.J, g.vec, stage);
         }

@@ -36,4 +36,57 @@ struct alignas(V == 1 ? sizeof(T) : 16) Vec {
 template <typename T>
 constexpr int kVec16 = 16 / (int)sizeof(T);
 
+// ---------------------------------------------------------------- pairs of fp32 (.f32x2 instructions)
+
+using f32x2 = unsigned long long;
+MOE_DEV f32x2 add2(f32x2 a, f32x2 b) { f32x2 r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
+MOE_DEV f32x2 mul2(f32x2 a, f32x2 b) { f32x2 r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
+MOE_DEV f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+MOE_DEV f32x2 both(float v) { return pack_f32x2(v, v); }
+MOE_DEV float lo2(f32x2 v) { return __uint_as_float((uint32_t)v); }
+MOE_DEV float hi2(f32x2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
+MOE_DEV float sum2(f32x2 v) { return lo2(v) + hi2(v); }
+
+// 16 bytes of T as pairs
+template <typename T>
+struct Pairs;
+template <>
+struct Pairs<float> {
+  static constexpr int N = 2;
+  static MOE_DEV void get(const uint4& r, f32x2* out) {
+    out[0] = (f32x2)r.x | ((f32x2)r.y << 32);
+    out[1] = (f32x2)r.z | ((f32x2)r.w << 32);
+  }
+  static MOE_DEV uint4 put(const f32x2* v) {
+    return make_uint4((uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32));
+  }
+};
+template <>
+struct Pairs<__nv_bfloat16> {
+  static constexpr int N = 4;
+  static MOE_DEV f32x2 one(uint32_t v) { return pack_f32x2(bf16_lo(v), bf16_hi(v)); }
+  static MOE_DEV void get(const uint4& r, f32x2* out) { out[0] = one(r.x); out[1] = one(r.y); out[2] = one(r.z); out[3] = one(r.w); }
+  static MOE_DEV uint4 put(const f32x2* v) {
+    return make_uint4(pack_bf16x2_from_pair(v[0]), pack_bf16x2_from_pair(v[1]), pack_bf16x2_from_pair(v[2]), pack_bf16x2_from_pair(v[3]));
+  }
+};
+template <>
+struct Pairs<__half> {
+  static constexpr int N = 4;
+  static MOE_DEV f32x2 one(uint32_t v) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+    return pack_f32x2(f.x, f.y);
+  }
+  static MOE_DEV uint32_t pack(f32x2 v) {
+    const __half2 h = __floats2half2_rn(lo2(v), hi2(v));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static MOE_DEV void get(const uint4& r, f32x2* out) { out[0] = one(r.x); out[1] = one(r.y); out[2] = one(r.z); out[3] = one(r.w); }
+  static MOE_DEV uint4 put(const f32x2* v) { return make_uint4(pack(v[0]), pack(v[1]), pack(v[2]), pack(v[3])); }
+};
+
 }  // namespace moe
