@@ -193,26 +193,41 @@ MOE_DEV void store_block(const f32x2 (&v)[16], T* out, long long ld, int i0, int
         *reinterpret_cast<uint4*>(out + (long long)(i0 + r) * ld + j0 + 8 * c) = *reinterpret_cast<const uint4*>(stage + block_at(r, c));
     }
   } else if (j0 + lane < J) {
-    const int rows = min(32, I - i0);
-#pragma unroll 8
-    for (int r = 0; r < rows; ++r)
-      out[(long long)(i0 + r) * ld + j0 + lane] = *reinterpret_cast<const T*>(stage + block_at(r, lane >> 3) + (lane & 7) * 2);
+#pragma unroll
+    for (int k = 0; k < 32; k += 8) {   // eight rows read before they are written: the compiler may not swap the two
+      T v[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) v[r] = *reinterpret_cast<const T*>(stage + block_at(k + r, lane >> 3) + (lane & 7) * 2);
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (i0 + k + r < I) out[(long long)(i0 + k + r) * ld + j0 + lane] = v[r];
+    }
   }
 }
 
-// A block's residual as its rows lie, fetched ahead of its use where vectors fit.
-struct ResidualAhead {
-  uint4 v[4];
+// A block's residual as its rows lie, fetched ahead of its use: with vectors 16 bytes of rows
+// 8 k + lane / 4, otherwise a column's 32 values, two rows a word.
+struct alignas(16) ResidualAhead {
+  uint32_t v[16];
 };
 
 template <typename T>
 MOE_DEV void fetch_residual(ResidualAhead& a, const DenseArgs& g, int i0, int j0) {
-  const int lane = threadIdx.x & 31, j = j0 + 8 * (lane & 3);
-  if (!g.residual || !g.vec || j >= g.J) return;
+  const int lane = threadIdx.x & 31, j = j0 + (g.vec ? 8 * (lane & 3) : lane);
+  if (!g.residual || j >= g.J) return;
+  const uint16_t* p = static_cast<const uint16_t*>(g.residual) + (long long)i0 * g.J + j;
+  if (g.vec) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int i = i0 + 8 * k + (lane >> 2);
-    if (i < g.I) a.v[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(g.residual) + (long long)i * g.J + j);
+    for (int k = 0; k < 4; ++k) {
+      const int r = 8 * k + (lane >> 2);
+      if (i0 + r < g.I) *reinterpret_cast<uint4*>(a.v + 4 * k) = *reinterpret_cast<const uint4*>(p + (long long)r * g.J);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const uint32_t lo = i0 + 2 * k < g.I ? p[(long long)(2 * k) * g.J] : 0u, hi = i0 + 2 * k + 1 < g.I ? p[(long long)(2 * k + 1) * g.J] : 0u;
+      a.v[k] = lo | hi << 16;
+    }
   }
 }
 
@@ -245,18 +260,18 @@ MOE_DEV void drain_biased(uint32_t taddr, f32x2 (&v)[16], const DenseArgs& g, in
 }
 
 // The residual's block into shared memory, and from there to the lanes of its rows.
-template <typename T>
-MOE_DEV void put_residual(const ResidualAhead& a, const DenseArgs& g, int i0, int j0, uint8_t* stage) {
+MOE_DEV void put_residual(const ResidualAhead& a, bool vec, uint8_t* stage) {
   const int lane = threadIdx.x & 31;
-  if (g.vec) {
+  if (vec) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(stage + block_at(8 * k + (lane >> 2), lane & 3)) = a.v[k];
-  } else if (j0 + lane < g.J) {
-    const int rows = min(32, g.I - i0);
-#pragma unroll 8
-    for (int r = 0; r < rows; ++r)
-      *reinterpret_cast<T*>(stage + block_at(r, lane >> 3) + (lane & 7) * 2) =
-          static_cast<const T*>(g.residual)[(long long)(i0 + r) * g.J + j0 + lane];
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<uint4*>(stage + block_at(8 * k + (lane >> 2), lane & 3)) = *reinterpret_cast<const uint4*>(a.v + 4 * k);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      *reinterpret_cast<uint16_t*>(stage + block_at(2 * k, lane >> 3) + (lane & 7) * 2) = (uint16_t)a.v[k];
+      *reinterpret_cast<uint16_t*>(stage + block_at(2 * k + 1, lane >> 3) + (lane & 7) * 2) = (uint16_t)(a.v[k] >> 16);
+    }
   }
 }
 

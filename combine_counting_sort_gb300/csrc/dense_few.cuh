@@ -57,7 +57,14 @@ MOE_DEV void tmem_drain16(uint32_t taddr, float (&v)[16]) {
 
 // Four values, n of them there, 8 bytes at a time where they lie so.
 template <typename T>
-MOE_DEV void store_quad(const f32x2 (&v)[2], T* p, int n, bool vec) {
+MOE_DEV uint2 load_quad(const T* p, int n, bool vec) {
+  if (vec) return *reinterpret_cast<const uint2*>(p);
+  const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+  const uint32_t a = q[0], b = n > 1 ? q[1] : 0u, c = n > 2 ? q[2] : 0u, d = n > 3 ? q[3] : 0u;
+  return make_uint2(a | b << 16, c | d << 16);
+}
+template <typename T>
+MOE_DEV void store_quad(const f32x2* v, T* p, int n, bool vec) {
   const T o[4] = {from_f32<T>(lo2(v[0])), from_f32<T>(hi2(v[0])), from_f32<T>(lo2(v[1])), from_f32<T>(hi2(v[1]))};
   if (vec) {
     *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(o);
@@ -67,18 +74,74 @@ MOE_DEV void store_quad(const f32x2 (&v)[2], T* p, int n, bool vec) {
       if (e < n) p[e] = o[e];
   }
 }
+
+// What finishes a tile: this thread's four columns of the rows t0, t0 + step, ..., summed over the
+// CTAs' sums in their order (one row's loads from all of them in flight).  bias and
+// the first row's residual were fetched while the products ran; the next row's is on its way while a
+// row is worked on.  Rolled up: the code runs a few times only, and then its length counts.
 template <typename T>
-MOE_DEV void add_quad(f32x2 (&v)[2], const T* p, int n, bool vec) {
-  T x[4] = {};
-  if (vec) {
-    *reinterpret_cast<uint2*>(x) = *reinterpret_cast<const uint2*>(p);
-  } else {
+struct FinishAhead {
+  uint2 bias, residual;
+};
+
+template <typename T, int EPI>
+MOE_DEV void finish_rows(const DenseArgs& g, const FinishAhead<T>& ahead, uint32_t sums, int split, int i0, int j, int r, int t0, int step, int rows) {
+  const int n = min(4, g.J - j);
+  if (n <= 0) return;
+  uint32_t peer[kDFewMaxSplit];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < n) x[e] = p[e];
+  for (int c = 0; c < kDFewMaxSplit; ++c) peer[c] = c < split ? mapa_shared(sums + r * 4u, (uint32_t)c) : 0u;
+  uint2 next = ahead.residual;
+#pragma unroll 1
+  for (int t = t0; t < rows; t += step) {
+    const long long i = i0 + t;
+    const uint2 add = next;
+    if (EPI == kEpiLinear && g.residual && t + step < rows) next = load_quad(static_cast<const T*>(g.residual) + (i + step) * g.J + j, n, g.vec);
+    float4 a[kDFewMaxSplit], b[kDFewMaxSplit];
+#pragma unroll
+    for (int c = 0; c < kDFewMaxSplit; ++c)
+      if (c < split) {
+        a[c] = ld_shared_cluster_f32x4(peer[c] + (uint32_t)t * 512u);
+        if (EPI == kEpiGated) b[c] = ld_shared_cluster_f32x4(peer[c] + (uint32_t)t * 512u + 256u);
+      }
+    f32x2 v[2] = {0, 0}, w[2] = {0, 0};
+#pragma unroll
+    for (int c = 0; c < kDFewMaxSplit; ++c)
+      if (c < split) {
+        v[0] = add2(v[0], pack_f32x2(a[c].x, a[c].y));
+        v[1] = add2(v[1], pack_f32x2(a[c].z, a[c].w));
+        if (EPI == kEpiGated) {
+          w[0] = add2(w[0], pack_f32x2(b[c].x, b[c].y));
+          w[1] = add2(w[1], pack_f32x2(b[c].z, b[c].w));
+        }
+      }
+    if (EPI == kEpiLinear && g.bias) {
+      v[0] = add2(v[0], Pairs<T>::one(ahead.bias.x));
+      v[1] = add2(v[1], Pairs<T>::one(ahead.bias.y));
+    }
+    f32x2 s[2];
+    with_act(EPI == kEpiPlain ? MOE_ACT_NONE : g.act, [&](auto act) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) act_pair<decltype(act)::value>(v[k], v[k], s[k]);
+    });
+    if (EPI == kEpiGated) {
+      if (g.aux) {
+        const f32x2 f[2] = {mul2(s[0], w[0]), mul2(s[1], w[1])};
+        T* aux = static_cast<T*>(g.aux) + 2 * i * g.J + j;
+        store_quad(f, aux, n, g.vec);
+        store_quad(v, aux + g.J, n, g.vec);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) v[k] = mul2(v[k], w[k]);
+    } else if (EPI == kEpiLinear) {
+      if (g.aux) store_quad(s, static_cast<T*>(g.aux) + i * g.J + j, n, g.vec);
+      if (g.residual) {
+        v[0] = add2(v[0], Pairs<T>::one(add.x));
+        v[1] = add2(v[1], Pairs<T>::one(add.y));
+      }
+    }
+    store_quad(v, static_cast<T*>(g.out) + i * g.J + j, n, g.vec);
   }
-  v[0] = add2(v[0], pack_f32x2(to_f32(x[0]), to_f32(x[1])));
-  v[1] = add2(v[1], pack_f32x2(to_f32(x[2]), to_f32(x[3])));
 }
 
 // Q's rows j are the M operand, P's rows i the N operand.
@@ -99,50 +162,70 @@ __global__ void __launch_bounds__(kDFewThreads)
   const int kb0 = (int)((long long)KB * rank / split), kb1 = (int)((long long)KB * (rank + 1) / split);
   const uint32_t cols = plan.nt < 32 ? 32u : (uint32_t)plan.nt;
 
-  if (threadIdx.x == 0) {
-    tma_prefetch_desc(&tmP);
-    tma_prefetch_desc(&tmQ);
-    for (int s = 0; s < plan.stages; ++s) {
-      mbar_init(smem_u32(&sh->full[s]), 1);
-      mbar_init(smem_u32(&sh->empty[s]), 1);
+  // The copying warp sets up the barriers by itself and fills the ring before it meets the others,
+  // so the first copies do not wait for tensor memory.
+  if (warp == 0) {
+    const int lane = (int)threadIdx.x & 31;
+    if (lane == 0) {
+      tma_prefetch_desc(&tmP);
+      tma_prefetch_desc(&tmQ);
+      mbar_init(smem_u32(&sh->tfull), 1);
+      sh->abort_flag = 0;
     }
-    mbar_init(smem_u32(&sh->tfull), 1);
-    sh->abort_flag = 0;
+    if (lane < plan.stages) {
+      mbar_init(smem_u32(&sh->full[lane]), 1);
+      mbar_init(smem_u32(&sh->empty[lane]), 1);
+    }
     fence_mbar_init();
-  }
-  if (warp == 1) {
+    __syncwarp();
+  } else if (warp == 1) {
     tmem_alloc(smem_u32(&sh->tmem_base), cols);
     tmem_relinquish();
+  }
+  grid_launch_next();
+  grid_wait_previous();
+  // one k's stage of both operands into the ring
+  auto copy_stage = [&](int kb, int s) {
+    const uint32_t full = smem_u32(&sh->full[s]), q = smem_u32(ring + (size_t)s * stage_bytes), p = q + 2 * kDenseChunk;
+    mbar_arrive_expect_tx(full, stage_bytes);
+    const int k0 = kb * kDenseBK;
+    tma_load_2d(q, &tmQ, QMN ? j0 : k0, QMN ? k0 : j0, full);
+    if (QMN) tma_load_2d(q + kDenseChunk, &tmQ, j0 + 64, k0, full);
+    else if (EPI == kEpiGated) tma_load_2d(q + kDenseChunk, &tmQ, k0, g.J + j0, full);
+    if (PMN)
+      for (int c = 0; c < plan.nt / 64; ++c) tma_load_2d(p + c * kDenseChunk, &tmP, i0 + 64 * c, k0, full);
+    else
+      tma_load_2d(p, &tmP, k0, i0, full);
+  };
+  const int first = min(plan.stages, kb1 - kb0);
+  if (warp == 0) {
+    if (elect_one())
+      for (int s = 0; s < first; ++s) copy_stage(kb0 + s, s);
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
-  grid_launch_next();
-  grid_wait_previous();
+
+  // what this thread finishes: four columns of the rows t0, t0 + step, ...
+  constexpr int kQuads = kRows / 4;
+  const int tv = min(plan.nt, g.I - i0), r = (int)threadIdx.x % kQuads * 4;
+  const int t0 = rank * (kDFewThreads / kQuads) + (int)threadIdx.x / kQuads, step = split * (kDFewThreads / kQuads);
+  FinishAhead<T> ahead = {};
+  if (EPI == kEpiLinear && j0 + r < g.J) {
+    const int n = min(4, g.J - j0 - r);
+    if (g.bias) ahead.bias = load_quad(static_cast<const T*>(g.bias) + j0 + r, n, g.bias_vec);
+    if (g.residual && t0 < tv) ahead.residual = load_quad(static_cast<const T*>(g.residual) + (long long)(i0 + t0) * g.J + j0 + r, n, g.vec);
+  }
 
   if (warp == 0) {
     if (elect_one()) {
-      int s = 0, issued = 0;
-      uint32_t ph = 1;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      int s = 0, issued = first;
+      uint32_t ph = 0;
+      for (int kb = kb0 + first; kb < kb1; ++kb) {
         if (!mbar_wait(smem_u32(&sh->empty[s]), ph, &sh->abort_flag, g.status, g.timeout_ns)) break;
-        const uint32_t full = smem_u32(&sh->full[s]), q = smem_u32(ring + (size_t)s * stage_bytes), p = q + 2 * kDenseChunk;
-        mbar_arrive_expect_tx(full, stage_bytes);
-        const int k0 = kb * kDenseBK;
-        if (QMN) {
-          tma_load_2d(q, &tmQ, j0, k0, full);
-          tma_load_2d(q + kDenseChunk, &tmQ, j0 + 64, k0, full);
-        } else if (EPI == kEpiGated) {
-          tma_load_2d(q, &tmQ, k0, j0, full);
-          tma_load_2d(q + kDenseChunk, &tmQ, k0, g.J + j0, full);
-        } else {
-          tma_load_2d(q, &tmQ, k0, j0, full);
-        }
-        if (PMN)
-          for (int c = 0; c < plan.nt / 64; ++c) tma_load_2d(p + c * kDenseChunk, &tmP, i0 + 64 * c, k0, full);
-        else
-          tma_load_2d(p, &tmP, k0, i0, full);
+        copy_stage(kb, s);
         ++issued;
         if (++s == plan.stages) { s = 0; ph ^= 1u; }
       }
@@ -182,7 +265,6 @@ __global__ void __launch_bounds__(kDFewThreads)
 
   // this CTA's sums, [i][j] with j contiguous, over the ring (every stage has been read)
   float* sums = reinterpret_cast<float*>(ring);
-  const int tv = min(plan.nt, g.I - i0);
   {
     const int q = warp & 3, row = 32 * q + (threadIdx.x & 31);
     for (int c = (warp >> 2) * 16; c < tv; c += 32) {
@@ -200,59 +282,7 @@ __global__ void __launch_bounds__(kDFewThreads)
     tmem_dealloc(tmem, cols);
   }
 
-  // this CTA's part of the tile's outputs
-  const uint32_t local = smem_u32(sums);
-  uint32_t peer[kDFewMaxSplit];
-#pragma unroll
-  for (int r = 0; r < kDFewMaxSplit; ++r) peer[r] = r < split ? mapa_shared(local, (uint32_t)r) : 0u;
-  const T* bias = static_cast<const T*>(g.bias);
-  const T* residual = static_cast<const T*>(g.residual);
-  T* out = static_cast<T*>(g.out);
-  T* aux = static_cast<T*>(g.aux);
-  constexpr int kQuads = kRows / 4;   // four columns a thread
-  with_act(EPI == kEpiPlain ? MOE_ACT_NONE : g.act, [&](auto act) {
-    for (int e = rank * kDFewThreads + (int)threadIdx.x; e < tv * kQuads; e += split * kDFewThreads) {
-      const int t = e / kQuads, r = e % kQuads * 4, j = j0 + r, n = min(4, g.J - j);
-      const long long i = i0 + t, o = i * g.J + j;
-      if (n <= 0) continue;
-      const uint32_t at = (uint32_t)(t * 128 + r) * 4u;
-      float4 a[kDFewMaxSplit], b[kDFewMaxSplit];
-#pragma unroll
-      for (int c = 0; c < kDFewMaxSplit; ++c)
-        if (c < split) {
-          a[c] = ld_shared_cluster_f32x4(peer[c] + at);
-          if (EPI == kEpiGated) b[c] = ld_shared_cluster_f32x4(peer[c] + at + 256u);
-        }
-      f32x2 v[2] = {pack_f32x2(a[0].x, a[0].y), pack_f32x2(a[0].z, a[0].w)}, u[2] = {0, 0}, s[2];
-      if (EPI == kEpiGated) u[0] = pack_f32x2(b[0].x, b[0].y), u[1] = pack_f32x2(b[0].z, b[0].w);
-#pragma unroll
-      for (int c = 1; c < kDFewMaxSplit; ++c)
-        if (c < split) {
-          v[0] = add2(v[0], pack_f32x2(a[c].x, a[c].y));
-          v[1] = add2(v[1], pack_f32x2(a[c].z, a[c].w));
-          if (EPI == kEpiGated) {
-            u[0] = add2(u[0], pack_f32x2(b[c].x, b[c].y));
-            u[1] = add2(u[1], pack_f32x2(b[c].z, b[c].w));
-          }
-        }
-      if (EPI == kEpiLinear && bias) add_quad(v, bias + j, n, g.bias_vec);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) act_pair<decltype(act)::value>(v[k], v[k], s[k]);
-      if (EPI == kEpiGated) {
-        if (aux) {
-          const f32x2 f[2] = {mul2(s[0], u[0]), mul2(s[1], u[1])};
-          store_quad(f, aux + 2 * i * g.J + j, n, g.vec);
-          store_quad(v, aux + 2 * i * g.J + g.J + j, n, g.vec);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) v[k] = mul2(v[k], u[k]);
-      } else if (EPI == kEpiLinear) {
-        if (aux) store_quad(s, aux + o, n, g.vec);
-        if (residual) add_quad(v, residual + o, n, g.vec);
-      }
-      store_quad(v, out + o, n, g.vec);
-    }
-  });
+  finish_rows<T, EPI>(g, ahead, smem_u32(sums), split, i0, j0 + r, r, t0, step, tv);
   if (split > 1) cluster_sync();   // no CTA leaves while another reads its sums
 }
 

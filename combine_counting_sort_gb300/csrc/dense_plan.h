@@ -26,10 +26,12 @@ inline DensePlan dense_plan(long long I, long long J, long long K, bool gated, b
     for (int split = 1; split <= 8 && split <= KB; ++split) {
       const long long ctas = ti * tj * split;
       const int stage = 16384 + nt * 128;
-      // two CTAs an SM where the ring allows it
-      const int stages = nt <= 64 ? std::min(12, 104 * 1024 / stage) : std::min(12, 220 * 1024 / stage);
-      const int per_sm = nt <= 64 ? 2 : 1;
-      const double kb = (double)((KB + split - 1) / split);
+      // two CTAs an SM where the ring allows it and there are as many; a whole SM's ring for one
+      const int per_sm = nt <= 64 && ctas > sms ? 2 : 1;
+      const long long share = (KB + split - 1) / split;
+      // (no more stages than are filled, but room for the tile's sums)
+      const int stages = std::max((nt * 512 + stage - 1) / stage, (int)std::min<long long>(share, std::min(12, (per_sm == 2 ? 104 : 220) * 1024 / stage)));
+      const double kb = (double)share;
       const double waves = (double)((ctas + (long long)sms * per_sm - 1) / ((long long)sms * per_sm));
       const double busy = std::min<double>((double)ctas, (double)sms * per_sm) / sms;
       const double per_kb = std::max(2.0 * nt, stage / 30.0) * std::max(1.0, busy);
