@@ -8,6 +8,7 @@ is no fallback: if the library is not built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
@@ -631,30 +632,24 @@ def moe_layer_few(x: torch.Tensor, W1: torch.Tensor, W1_scale: Optional[torch.Te
 MOE_BF16, MOE_F16, MOE_F32 = range(3)
 MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = range(5)
 MOE_NORM_MAX_H, MOE_DENSE_MAX = 16384, 1 << 20
-_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
+
+_native = None
 
 
-def _dtype(t: torch.Tensor, name: str, allowed) -> int:
-    if t.dtype not in allowed:
-        raise ValueError(f"{name} must be one of {', '.join(str(d) for d in allowed)}, got {t.dtype}")
-    return _DTYPES[t.dtype]
-
-
-def _here(*tensors):
-    """Refuse tensors of another device than the current one, which the kernel
-    is launched on."""
-    dev = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"every tensor must be on the current device {dev}, got one on {t.device}")
-
-
-def _bytes(ws: Optional[torch.Tensor], name="ws"):
-    """Address and size of a workspace."""
-    return _ptr(ws, None, name), ws.numel() * ws.element_size()
-
-
-_HALF = (torch.bfloat16, torch.float16)
+def _binding():
+    """csrc/binding.cpp: checks these operators' tensors as _shape and _ptr do
+    (ValueError; also for one that is not on the current device) and calls the entry point."""
+    global _native
+    if _native is None:
+        lib()
+        path = os.path.join(os.path.dirname(LIB_PATH), "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is not built: run __graft_entry__.build() first")
+        spec = importlib.util.spec_from_file_location("_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _native = module
+    return _native
 
 
 def moe_layernorm(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor], eps: float, y: torch.Tensor,
@@ -662,16 +657,7 @@ def moe_layernorm(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optiona
     """Layer norm of each row of x [T, H] (bf16, f16 or f32) into y; weight and
     bias [H] of x's type or f32, or None; mean and rstd (f32 [T]) are written
     where given, for moe_layernorm_bwd."""
-    T, H = _dims(x, 2, "x")
-    dt = _dtype(x, "x", tuple(_DTYPES))
-    p = weight if weight is not None else bias
-    wd = x.dtype if p is None else p.dtype
-    if wd not in (x.dtype, torch.float32):
-        raise ValueError(f"weight and bias must be {x.dtype} or torch.float32, got {wd}")
-    px, pw, pb, py, pm, pr = _args((x, x.dtype, (T, H), "x"), (weight, wd, (H,), "weight"), (bias, wd, (H,), "bias"),
-                                   (y, x.dtype, (T, H), "y"), (mean, torch.float32, (T,), "mean"), (rstd, torch.float32, (T,), "rstd"))
-    _here(x, weight, bias, y, mean, rstd)
-    _check("moe_layernorm", lib().moe_layernorm(px, T, H, dt, pw, pb, _DTYPES[wd], eps, py, pm, pr, _raw_stream(stream)))
+    _check("moe_layernorm", _binding().layernorm(x, weight, bias, eps, y, mean, rstd, stream))
 
 
 def moe_layernorm_bwd_ws_bytes(T: int, H: int) -> int:
@@ -685,19 +671,7 @@ def moe_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.
     """Gradients of moe_layernorm: dx [T, H], and the sums over the rows dweight
     and dbias [H] (of weight's type; of x's or f32 where weight is None), each
     None where it is not wanted."""
-    T, H = _dims(x, 2, "x")
-    dt = _dtype(x, "x", tuple(_DTYPES))
-    p = next((t for t in (weight, dweight, dbias) if t is not None), None)
-    wd = x.dtype if p is None else p.dtype
-    if wd not in (x.dtype, torch.float32):
-        raise ValueError(f"weight, dweight and dbias must be {x.dtype} or torch.float32, got {wd}")
-    pdy, px, pw, pm, pr, pdx, pdw, pdb = _args(
-        (dy, x.dtype, (T, H), "dy"), (x, x.dtype, (T, H), "x"), (weight, wd, (H,), "weight"), (mean, torch.float32, (T,), "mean"),
-        (rstd, torch.float32, (T,), "rstd"), (dx, x.dtype, (T, H), "dx"), (dweight, wd, (H,), "dweight"), (dbias, wd, (H,), "dbias"))
-    pws, nws = _bytes(ws)
-    _here(dy, x, weight, mean, rstd, dx, dweight, dbias, ws)
-    _check("moe_layernorm_bwd", lib().moe_layernorm_bwd(pdy, px, T, H, dt, pw, _DTYPES[wd], pm, pr, pdx, pdw, pdb, pws, nws,
-                                                        _raw_stream(stream)))
+    _check("moe_layernorm_bwd", _binding().layernorm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, stream))
 
 
 def moe_linear(x: torch.Tensor, W: torch.Tensor, y: torch.Tensor, status: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -705,15 +679,7 @@ def moe_linear(x: torch.Tensor, W: torch.Tensor, y: torch.Tensor, status: torch.
     """y = act(x W^T + bias) + residual for x [T, K] and W [N, K] in bf16 or
     f16; y may be residual.  slope [T, N], written where given, is what
     moe_linear_bwd needs of the activation."""
-    T, K = _dims(x, 2, "x")
-    N = _dims(W, 2, "W")[0]
-    dt, d = _dtype(x, "x", _HALF), x.dtype
-    _status(status)
-    px, pw, py, pst, pb, pr, ps = _args((x, d, (T, K), "x"), (W, d, (N, K), "W"), (y, d, (T, N), "y"),
-                                        (status, torch.int32, status.shape, "status"), (bias, d, (N,), "bias"),
-                                        (residual, d, (T, N), "residual"), (slope, d, (T, N), "slope"))
-    _here(x, W, y, status, bias, residual, slope)
-    _check("moe_linear", lib().moe_linear(px, T, K, pw, N, dt, pb, pr, act, py, ps, pst, _raw_stream(stream)))
+    _check("moe_linear", _binding().linear(x, W, y, status, bias, residual, act, slope, stream))
 
 
 def moe_linear_bwd_ws_bytes(T: int, N: int, K: int) -> int:
@@ -728,16 +694,7 @@ def moe_linear_bwd(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, dx: Optio
     """Gradients of moe_linear: dx [T, K], dW [N, K] and dbias [N], each None
     where it is not wanted; slope as moe_linear wrote it (None: no activation).
     The residual's gradient is dy."""
-    T, K = _dims(x, 2, "x")
-    N = _dims(W, 2, "W")[0]
-    dt, d = _dtype(x, "x", _HALF), x.dtype
-    _status(status)
-    pdy, px, pw, pdx, pdw, pst, pdb, ps = _args(
-        (dy, d, (T, N), "dy"), (x, d, (T, K), "x"), (W, d, (N, K), "W"), (dx, d, (T, K), "dx"), (dW, d, (N, K), "dW"),
-        (status, torch.int32, status.shape, "status"), (dbias, d, (N,), "dbias"), (slope, d, (T, N), "slope"))
-    pws, nws = _bytes(ws)
-    _here(dy, x, W, dx, dW, ws, status, dbias, slope)
-    _check("moe_linear_bwd", lib().moe_linear_bwd(pdy, px, T, K, pw, N, dt, ps, pdx, pdw, pdb, pws, nws, pst, _raw_stream(stream)))
+    _check("moe_linear_bwd", _binding().linear_bwd(dy, x, W, dx, dW, ws, status, dbias, slope, stream))
 
 
 def moe_gated(x: torch.Tensor, W1: torch.Tensor, h: torch.Tensor, status: torch.Tensor, act: int = MOE_ACT_SILU,
@@ -745,14 +702,7 @@ def moe_gated(x: torch.Tensor, W1: torch.Tensor, h: torch.Tensor, status: torch.
     """h = act(x Wg^T) * (x Wu^T) for x [T, H] and W1 [2F, H] (gate rows, then up
     rows) in bf16 or f16.  factors [T, 2F], written where given, is what
     moe_gated_bwd multiplies dh by."""
-    T, H = _dims(x, 2, "x")
-    F = _dims(h, 2, "h")[1]
-    dt, d = _dtype(x, "x", _HALF), x.dtype
-    _status(status)
-    px, pw, ph, pst, pf = _args((x, d, (T, H), "x"), (W1, d, (2 * F, H), "W1"), (h, d, (T, F), "h"),
-                                (status, torch.int32, status.shape, "status"), (factors, d, (T, 2 * F), "factors"))
-    _here(x, W1, h, status, factors)
-    _check("moe_gated", lib().moe_gated(px, T, H, pw, F, dt, act, ph, pf, pst, _raw_stream(stream)))
+    _check("moe_gated", _binding().gated(x, W1, h, status, act, factors, stream))
 
 
 def moe_gated_bwd_ws_bytes(T: int, F: int, H: int) -> int:
@@ -765,13 +715,4 @@ def moe_gated_bwd(dh: torch.Tensor, x: torch.Tensor, W1: torch.Tensor, factors: 
                   dW1: Optional[torch.Tensor], ws: torch.Tensor, status: torch.Tensor, stream=None):
     """Gradients of moe_gated: dx [T, H] and dW1 [2F, H], each None where it is
     not wanted; factors as moe_gated wrote them."""
-    T, H = _dims(x, 2, "x")
-    F = _dims(dh, 2, "dh")[1]
-    dt, d = _dtype(x, "x", _HALF), x.dtype
-    _status(status)
-    pdh, px, pw, pf, pdx, pdw, pst = _args((dh, d, (T, F), "dh"), (x, d, (T, H), "x"), (W1, d, (2 * F, H), "W1"),
-                                           (factors, d, (T, 2 * F), "factors"), (dx, d, (T, H), "dx"), (dW1, d, (2 * F, H), "dW1"),
-                                           (status, torch.int32, status.shape, "status"))
-    pws, nws = _bytes(ws)
-    _here(dh, x, W1, factors, dx, dW1, ws, status)
-    _check("moe_gated_bwd", lib().moe_gated_bwd(pdh, px, T, H, pw, F, dt, pf, pdx, pdw, pws, nws, pst, _raw_stream(stream)))
+    _check("moe_gated_bwd", _binding().gated_bwd(dh, x, W1, factors, dx, dW1, ws, status, stream))
