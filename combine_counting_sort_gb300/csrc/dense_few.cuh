@@ -12,12 +12,11 @@
 #pragma once
 
 #include "dense.cuh"
+#include "dense_plan.h"
 
 namespace moe {
 
 constexpr int kDFewThreads = 256;
-constexpr int kDFewMaxStages = 12;
-constexpr int kDFewMaxSplit = 8;
 
 struct DFewShared {
   uint64_t full[kDFewMaxStages], empty[kDFewMaxStages], tfull;
@@ -33,16 +32,13 @@ struct DFewPlan {
   int ti;                  // tiles of i
 };
 
-MOE_DEV float4 ld_shared_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
 MOE_DEV float ld_shared_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+
+MOE_DEV void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // 16 consecutive fp32 TMEM columns of this thread's lane.
 MOE_DEV void tmem_drain16(uint32_t taddr, float (&v)[16]) {
@@ -55,93 +51,147 @@ MOE_DEV void tmem_drain16(uint32_t taddr, float (&v)[16]) {
       : "memory");
 }
 
-// Four values, n of them there, 8 bytes at a time where they lie so.
-template <typename T>
-MOE_DEV uint2 load_quad(const T* p, int n, bool vec) {
-  if (vec) return *reinterpret_cast<const uint2*>(p);
-  const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-  const uint32_t a = q[0], b = n > 1 ? q[1] : 0u, c = n > 2 ? q[2] : 0u, d = n > 3 ? q[3] : 0u;
-  return make_uint2(a | b << 16, c | d << 16);
-}
-template <typename T>
-MOE_DEV void store_quad(const f32x2* v, T* p, int n, bool vec) {
-  const T o[4] = {from_f32<T>(lo2(v[0])), from_f32<T>(hi2(v[0])), from_f32<T>(lo2(v[1])), from_f32<T>(hi2(v[1]))};
-  if (vec) {
-    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(o);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < n) p[e] = o[e];
+// A thread's four columns of a tile's row.  They lie beside one another, 8 bytes a lane, where vectors
+// fit (VEC), and where sums come from another SM, 16 bytes a lane.  Otherwise (APART) they lie as many
+// columns apart as there are lanes on a row, so that lanes are neighbours in memory.
+template <typename T, bool VEC, bool APART, int QUADS>
+struct Columns {
+  int r, n;   // the first column, and how many of the four the row has
+  MOE_DEV Columns(int left) {
+    r = (int)threadIdx.x % QUADS * (APART ? 1 : 4);
+    n = min(4, APART ? (left - r + QUADS - 1) / QUADS : left - r);
   }
-}
-
-// What finishes a tile: this thread's four columns of the rows t0, t0 + step, ..., summed over the
-// CTAs' sums in their order (one row's loads from all of them in flight).  bias and
-// the first row's residual were fetched while the products ran; the next row's is on its way while a
-// row is worked on.  Rolled up: the code runs a few times only, and then its length counts.
-template <typename T>
-struct FinishAhead {
-  uint2 bias, residual;
+  static MOE_DEV int at(int e) { return APART ? e * QUADS : e; }
+  // p: the first column's value
+  MOE_DEV uint2 load(const T* p) const {
+    if (VEC) return *reinterpret_cast<const uint2*>(p);
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = e < n ? q[at(e)] : 0u;
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+  }
+  MOE_DEV void store(const f32x2* v, T* p) const {
+    const T o[4] = {from_f32<T>(lo2(v[0])), from_f32<T>(hi2(v[0])), from_f32<T>(lo2(v[1])), from_f32<T>(hi2(v[1]))};
+    if (VEC) {
+      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < n) p[at(e)] = o[e];
+    }
+  }
+  // sums of this CTA's or (REMOTE) another one's shared memory, `from` being the first column's
+  template <bool REMOTE>
+  static MOE_DEV void sums(uint32_t from, float* f) {
+    if (!APART) {
+      if (REMOTE) asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "r"(from) : "memory");
+      else asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "r"(from) : "memory");
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (REMOTE) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f[e]) : "r"(from + 4u * at(e)) : "memory");
+        else asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[e]) : "r"(from + 4u * at(e)) : "memory");
+      }
+    }
+  }
 };
 
-template <typename T, int EPI>
-MOE_DEV void finish_rows(const DenseArgs& g, const FinishAhead<T>& ahead, uint32_t sums, int split, int i0, int j, int r, int t0, int step, int rows) {
-  const int n = min(4, g.J - j);
-  if (n <= 0) return;
-  uint32_t peer[kDFewMaxSplit];
+// What finishes a tile: this thread's columns of the rows t0, t0 + step, ... below `rows`, the sums
+// of the cluster's CTAs added up in their order.  U rows at a time, C CTAs' sums of each in flight:
+// few rows want all CTAs' at once, many rows several of their own (a load from another SM takes
+// some 300 cycles, one of global memory 600).
+template <typename T, int EPI, bool VEC, bool SPLIT, int U, int C>
+MOE_DEV void finish_rows(const DenseArgs& g, uint32_t sums, int split, int rank, int i0, int j0, int rows) {
+  constexpr int QUADS = EPI == kEpiGated ? 16 : 32;
+  const Columns<T, VEC, !VEC && !SPLIT, QUADS> cols(g.J - j0);
+  if (cols.n <= 0) return;
+  const int j = j0 + cols.r, t0 = (SPLIT ? rank * (kDFewThreads / QUADS) : 0) + (int)threadIdx.x / QUADS, step = (SPLIT ? split : 1) * (kDFewThreads / QUADS);
+  f32x2 bias[2] = {0, 0};
+  if (EPI == kEpiLinear && g.bias) {
+    const T* q = static_cast<const T*>(g.bias) + j;
+    T b[4];
 #pragma unroll
-  for (int c = 0; c < kDFewMaxSplit; ++c) peer[c] = c < split ? mapa_shared(sums + r * 4u, (uint32_t)c) : 0u;
-  uint2 next = ahead.residual;
+    for (int e = 0; e < 4; ++e) b[e] = e < cols.n ? q[cols.at(e)] : from_f32<T>(0.f);
+    bias[0] = pack_f32x2(to_f32(b[0]), to_f32(b[1]));
+    bias[1] = pack_f32x2(to_f32(b[2]), to_f32(b[3]));
+  }
+  sums += (uint32_t)cols.r * 4u;
 #pragma unroll 1
-  for (int t = t0; t < rows; t += step) {
-    const long long i = i0 + t;
-    const uint2 add = next;
-    if (EPI == kEpiLinear && g.residual && t + step < rows) next = load_quad(static_cast<const T*>(g.residual) + (i + step) * g.J + j, n, g.vec);
-    float4 a[kDFewMaxSplit], b[kDFewMaxSplit];
+  for (int t = t0; t < rows; t += U * step) {
+    uint2 add[U];
+    f32x2 v[U][2], w[U][2];
 #pragma unroll
-    for (int c = 0; c < kDFewMaxSplit; ++c)
-      if (c < split) {
-        a[c] = ld_shared_cluster_f32x4(peer[c] + (uint32_t)t * 512u);
-        if (EPI == kEpiGated) b[c] = ld_shared_cluster_f32x4(peer[c] + (uint32_t)t * 512u + 256u);
-      }
-    f32x2 v[2] = {0, 0}, w[2] = {0, 0};
-#pragma unroll
-    for (int c = 0; c < kDFewMaxSplit; ++c)
-      if (c < split) {
-        v[0] = add2(v[0], pack_f32x2(a[c].x, a[c].y));
-        v[1] = add2(v[1], pack_f32x2(a[c].z, a[c].w));
-        if (EPI == kEpiGated) {
-          w[0] = add2(w[0], pack_f32x2(b[c].x, b[c].y));
-          w[1] = add2(w[1], pack_f32x2(b[c].z, b[c].w));
-        }
-      }
-    if (EPI == kEpiLinear && g.bias) {
-      v[0] = add2(v[0], Pairs<T>::one(ahead.bias.x));
-      v[1] = add2(v[1], Pairs<T>::one(ahead.bias.y));
+    for (int u = 0; u < U; ++u) {
+      v[u][0] = v[u][1] = w[u][0] = w[u][1] = 0;
+      if (EPI == kEpiLinear && g.residual && t + u * step < rows)
+        add[u] = cols.load(static_cast<const T*>(g.residual) + (long long)(i0 + t + u * step) * g.J + j);
     }
-    f32x2 s[2];
+#pragma unroll 1
+    for (int c0 = 0; c0 < (SPLIT ? split : 1); c0 += C) {
+      float a[C][U][4], b[C][U][4];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint32_t from = SPLIT ? mapa_shared(sums, (uint32_t)min(c0 + c, split - 1)) : sums;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (t + u * step < rows && (C == 1 || c0 + c < split)) {
+            cols.template sums<SPLIT>(from + (uint32_t)(t + u * step) * 512u, a[c][u]);
+            if (EPI == kEpiGated) cols.template sums<SPLIT>(from + (uint32_t)(t + u * step) * 512u + 256u, b[c][u]);
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (t + u * step < rows && (C == 1 || c0 + c < split)) {
+            v[u][0] = add2(v[u][0], pack_f32x2(a[c][u][0], a[c][u][1]));
+            v[u][1] = add2(v[u][1], pack_f32x2(a[c][u][2], a[c][u][3]));
+            if (EPI == kEpiGated) {
+              w[u][0] = add2(w[u][0], pack_f32x2(b[c][u][0], b[c][u][1]));
+              w[u][1] = add2(w[u][1], pack_f32x2(b[c][u][2], b[c][u][3]));
+            }
+          }
+    }
     with_act(EPI == kEpiPlain ? MOE_ACT_NONE : g.act, [&](auto act) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) act_pair<decltype(act)::value>(v[k], v[k], s[k]);
-    });
-    if (EPI == kEpiGated) {
-      if (g.aux) {
-        const f32x2 f[2] = {mul2(s[0], w[0]), mul2(s[1], w[1])};
-        T* aux = static_cast<T*>(g.aux) + 2 * i * g.J + j;
-        store_quad(f, aux, n, g.vec);
-        store_quad(v, aux + g.J, n, g.vec);
-      }
+      for (int u = 0; u < U; ++u) {
+        if (t + u * step >= rows) break;
+        const long long i = i0 + t + u * step;
+        f32x2 s[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) v[k] = mul2(v[k], w[k]);
-    } else if (EPI == kEpiLinear) {
-      if (g.aux) store_quad(s, static_cast<T*>(g.aux) + i * g.J + j, n, g.vec);
-      if (g.residual) {
-        v[0] = add2(v[0], Pairs<T>::one(add.x));
-        v[1] = add2(v[1], Pairs<T>::one(add.y));
+        for (int k = 0; k < 2; ++k) {
+          if (EPI == kEpiLinear) v[u][k] = add2(v[u][k], bias[k]);
+          act_pair<decltype(act)::value>(v[u][k], v[u][k], s[k]);
+        }
+        if (EPI == kEpiGated) {
+          if (g.aux) {
+            T* aux = static_cast<T*>(g.aux) + 2 * i * g.J + j;
+            const f32x2 f[2] = {mul2(s[0], w[u][0]), mul2(s[1], w[u][1])};
+            cols.store(f, aux);
+            cols.store(v[u], aux + g.J);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) v[u][k] = mul2(v[u][k], w[u][k]);
+        } else if (EPI == kEpiLinear) {
+          if (g.aux) cols.store(s, static_cast<T*>(g.aux) + i * g.J + j);
+          if (g.residual) {
+            v[u][0] = add2(v[u][0], Pairs<T>::one(add[u].x));
+            v[u][1] = add2(v[u][1], Pairs<T>::one(add[u].y));
+          }
+        }
+        cols.store(v[u], static_cast<T*>(g.out) + i * g.J + j);
       }
-    }
-    store_quad(v, static_cast<T*>(g.out) + i * g.J + j, n, g.vec);
+    });
   }
+}
+
+template <typename T, int EPI, bool VEC>
+MOE_DEV void finish(const DenseArgs& g, uint32_t sums, int split, int rank, int i0, int j0, int rows) {
+  constexpr int G = EPI == kEpiGated ? 2 : 1;
+  if (split == 1) finish_rows<T, EPI, VEC, false, 4 / G, 1>(g, sums, split, rank, i0, j0, rows);
+  else if (rows <= split * 8 * G) finish_rows<T, EPI, VEC, true, 1, kDFewMaxSplit>(g, sums, split, rank, i0, j0, rows);
+  else finish_rows<T, EPI, VEC, true, 4 / G, 2>(g, sums, split, rank, i0, j0, rows);
 }
 
 // Q's rows j are the M operand, P's rows i the N operand.
@@ -208,15 +258,13 @@ __global__ void __launch_bounds__(kDFewThreads)
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
 
-  // what this thread finishes: four columns of the rows t0, t0 + step, ...
-  constexpr int kQuads = kRows / 4;
-  const int tv = min(plan.nt, g.I - i0), r = (int)threadIdx.x % kQuads * 4;
-  const int t0 = rank * (kDFewThreads / kQuads) + (int)threadIdx.x / kQuads, step = split * (kDFewThreads / kQuads);
-  FinishAhead<T> ahead = {};
-  if (EPI == kEpiLinear && j0 + r < g.J) {
-    const int n = min(4, g.J - j0 - r);
-    if (g.bias) ahead.bias = load_quad(static_cast<const T*>(g.bias) + j0 + r, n, g.bias_vec);
-    if (g.residual && t0 < tv) ahead.residual = load_quad(static_cast<const T*>(g.residual) + (long long)(i0 + t0) * g.J + j0 + r, n, g.vec);
+  const int tv = min(plan.nt, g.I - i0);
+  if (EPI == kEpiLinear && warp >= 2) {   // what the tile's end reads, into L2
+    const int width = min(kRows, g.J - j0) * 2, t = (int)threadIdx.x - 64;
+    if (g.bias && t * 128 < width) prefetch_l2(static_cast<const T*>(g.bias) + j0 + t * 64);
+    if (g.residual)
+      for (int e = t; e < 2 * tv; e += kDFewThreads - 64)
+        if ((e & 1) * 128 < width) prefetch_l2(static_cast<const T*>(g.residual) + (long long)(i0 + (e >> 1)) * g.J + j0 + (e & 1) * 64);
   }
 
   if (warp == 0) {
@@ -282,7 +330,8 @@ __global__ void __launch_bounds__(kDFewThreads)
     tmem_dealloc(tmem, cols);
   }
 
-  finish_rows<T, EPI>(g, ahead, smem_u32(sums), split, i0, j0 + r, r, t0, step, tv);
+  if (g.vec) finish<T, EPI, true>(g, smem_u32(sums), split, rank, i0, j0, tv);
+  else finish<T, EPI, false>(g, smem_u32(sums), split, rank, i0, j0, tv);
   if (split > 1) cluster_sync();   // no CTA leaves while another reads its sums
 }
 

@@ -27,53 +27,63 @@ bool encode_operand(CUtensorMap* map, const DenseOperand& o, int K, int box) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Clusters of two CTAs that the device holds at once; 0 where it cannot be said.
+// CTAs that the device holds at once in clusters of c; 0 where it cannot be said.
 template <typename K>
-int resident_pairs(K kernel, int nsm) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDPairSmemBytes) != cudaSuccess) return 0;
+int resident_ctas(K kernel, int threads, size_t smem, int c) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = (unsigned)c;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(2 * (nsm / 2));
-  cfg.blockDim = dim3(kDPairThreads);
-  cfg.dynamicSmemBytes = kDPairSmemBytes;
+  cfg.gridDim = dim3((unsigned)(c * 512));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n * c : 0;
+}
+
+// What the device holds, by one of the kernels (all take the same threads and shared memory).  Asked once.
+template <typename K, typename P>
+DenseDevice dense_device(K few, P pair) {
+  DenseDevice d = {};
+  d.sms = device_sm_count();
+  d.pairs = std::min(resident_ctas(pair, kDPairThreads, kDPairSmemBytes, 2), d.sms) / 2;
+  for (int c = 1; c <= kDFewMaxSplit; ++c) {
+    d.cta[0][c] = resident_ctas(few, kDFewThreads, dfew_smem_bytes(128, 6), c);
+    d.cta[1][c] = resident_ctas(few, kDFewThreads, dfew_smem_bytes(64, 4), c);
+  }
+  return d;
 }
 
 template <typename T, bool PMN, bool QMN, int EPI, bool AUX>
-int launch_pair(const CUtensorMap& tmP, const CUtensorMap& tmQ, const DenseArgs& g, int nsm, cudaStream_t st) {
+int launch_pair(const CUtensorMap& tmP, const CUtensorMap& tmQ, const DenseArgs& g, int pairs, cudaStream_t st) {
   auto kernel = dense_pair_kernel<T, PMN, QMN, EPI, AUX>;
-  static const int resident = resident_pairs(kernel, nsm);   // once: the grid is persistent
-  if (resident < 1) return MOE_ERR_CUDA;
+  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDPairSmemBytes);
+  if (attr != cudaSuccess) return MOE_ERR_CUDA;
   constexpr int kTileJ = EPI == kEpiGated ? 128 : 256;
   const long long tiles = ((long long)g.I + 255) / 256 * (((long long)g.J + kTileJ - 1) / kTileJ);
   if (tiles > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
-  return launch_next(kernel, dim3(2 * (unsigned)std::min<long long>(std::min(resident, nsm / 2), tiles)), kDPairThreads, kDPairSmemBytes, st,
-                     2, 1, tmP, tmQ, g);
+  return launch_next(kernel, dim3(2 * (unsigned)std::min<long long>(pairs, tiles)), kDPairThreads, kDPairSmemBytes, st, 2, 1, tmP, tmQ, g);
 }
 
 template <typename T, bool PMN, bool QMN, int EPI>
 int launch_dense(const DenseOperand& P, const DenseOperand& Q, DenseArgs g, cudaStream_t st) {
-  const int nsm = device_sm_count();
-  if (nsm < 2 || !device_has_tcgen05()) return MOE_ERR_UNSUPPORTED;
+  if (!device_has_tcgen05()) return MOE_ERR_UNSUPPORTED;
+  auto kernel = dense_few_kernel<T, PMN, QMN, EPI>;
+  static const DenseDevice device = dense_device(kernel, dense_pair_kernel<T, PMN, QMN, EPI, false>);
+  if (device.pairs < 1) return MOE_ERR_CUDA;
   g.timeout_ns = 2000000000ull;
-  const DensePlan plan = dense_plan(g.I, g.J, g.K, EPI == kEpiGated, PMN, nsm);
+  const DensePlan plan = dense_plan({g.I, g.J, g.K, EPI == kEpiGated, PMN, g.aux != nullptr, g.residual != nullptr, g.vec != 0}, device);
   CUtensorMap tmP, tmQ;
   if (plan.pair) {
     if (!encode_operand<T>(&tmP, P, g.K, 128) || !encode_operand<T>(&tmQ, Q, g.K, 128)) return MOE_ERR_CUDA;
-    if (EPI != kEpiPlain && g.aux) return launch_pair<T, PMN, QMN, EPI, EPI != kEpiPlain>(tmP, tmQ, g, nsm, st);
-    return launch_pair<T, PMN, QMN, EPI, false>(tmP, tmQ, g, nsm, st);
+    if (EPI != kEpiPlain && g.aux) return launch_pair<T, PMN, QMN, EPI, EPI != kEpiPlain>(tmP, tmQ, g, device.pairs, st);
+    return launch_pair<T, PMN, QMN, EPI, false>(tmP, tmQ, g, device.pairs, st);
   }
   if (!encode_operand<T>(&tmP, P, g.K, plan.nt) || !encode_operand<T>(&tmQ, Q, g.K, EPI == kEpiGated ? 64 : 128)) return MOE_ERR_CUDA;
-  auto kernel = dense_few_kernel<T, PMN, QMN, EPI>;
-  const size_t smem = dfew_smem_bytes(plan.nt, plan.stages);
-  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-  if (attr != cudaSuccess) return MOE_ERR_CUDA;
   constexpr int kRows = EPI == kEpiGated ? 64 : 128;
   DFewPlan fp;
   fp.nt = plan.nt;
@@ -82,7 +92,7 @@ int launch_dense(const DenseOperand& P, const DenseOperand& Q, DenseArgs g, cuda
   fp.ti = (int)(((long long)g.I + plan.nt - 1) / plan.nt);
   const long long ctas = (long long)fp.ti * (((long long)g.J + kRows - 1) / kRows) * plan.split;
   if (ctas > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
-  return launch_next(kernel, dim3((unsigned)ctas), kDFewThreads, smem, st, (unsigned)plan.split, 1, tmP, tmQ, g, fp);
+  return launch_next(kernel, dim3((unsigned)ctas), kDFewThreads, dfew_smem_bytes(plan.nt, plan.stages), st, (unsigned)plan.split, 1, tmP, tmQ, g, fp);
 }
 
 // The products that the operators take: x W^T (linear, gated), d W and d^T x.
