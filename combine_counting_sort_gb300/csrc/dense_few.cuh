@@ -51,6 +51,10 @@ MOE_DEV void tmem_drain16(uint32_t taddr, float (&v)[16]) {
       : "memory");
 }
 
+struct Quad {
+  uint32_t w[4];
+};
+
 // A thread's four columns of a tile's row.  They lie beside one another, 8 bytes a lane, where vectors
 // fit (VEC), and where sums come from another SM, 16 bytes a lane.  Otherwise (APART) they lie as many
 // columns apart as there are lanes on a row, so that lanes are neighbours in memory.
@@ -62,15 +66,23 @@ struct Columns {
     n = min(4, APART ? (left - r + QUADS - 1) / QUADS : left - r);
   }
   static MOE_DEV int at(int e) { return APART ? e * QUADS : e; }
-  // p: the first column's value
-  MOE_DEV uint2 load(const T* p) const {
-    if (VEC) return *reinterpret_cast<const uint2*>(p);
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-    uint32_t w[4];
+  // p: the first column's value.  As it comes, so that nothing waits for it here: two to a
+  // word (PAIRED), or one.
+  template <bool PAIRED = VEC>
+  MOE_DEV Quad load(const T* p) const {
+    Quad q;
+    if (PAIRED) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      q.w[0] = v.x;
+      q.w[1] = v.y;
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = e < n ? q[at(e)] : 0u;
-    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+      for (int e = 0; e < 4; ++e) q.w[e] = e < n ? reinterpret_cast<const uint16_t*>(p)[at(e)] : 0u;
+    }
+    return q;
   }
+  template <bool PAIRED = VEC>
+  static MOE_DEV f32x2 pair(const Quad& q, int k) { return Pairs<T>::one(PAIRED ? q.w[k] : q.w[2 * k] | q.w[2 * k + 1] << 16); }
   MOE_DEV void store(const f32x2* v, T* p) const {
     const T o[4] = {from_f32<T>(lo2(v[0])), from_f32<T>(hi2(v[0])), from_f32<T>(lo2(v[1])), from_f32<T>(hi2(v[1]))};
     if (VEC) {
@@ -97,35 +109,41 @@ struct Columns {
   }
 };
 
+// A thread's bias and its first row's residual, fetched while the products run.
+struct FinishAhead {
+  Quad bias, residual;
+};
+
+template <typename T, int EPI, bool VEC, bool SPLIT>
+MOE_DEV void fetch_ahead(FinishAhead& ahead, const DenseArgs& g, int split, int rank, int i0, int j0, int rows) {
+  const Columns<T, VEC, !VEC && !SPLIT, 32> cols(g.J - j0);
+  if (cols.n <= 0) return;
+  const int j = j0 + cols.r, t = rank * 8 + (int)threadIdx.x / 32;
+  if (g.bias) ahead.bias = cols.template load<false>(static_cast<const T*>(g.bias) + j);
+  if (g.residual && t < rows) ahead.residual = cols.load(static_cast<const T*>(g.residual) + (long long)(i0 + t) * g.J + j);
+}
+
 // What finishes a tile: this thread's columns of the rows t0, t0 + step, ... below `rows`, the sums
 // of the cluster's CTAs added up in their order.  U rows at a time, C CTAs' sums of each in flight:
 // few rows want all CTAs' at once, many rows several of their own (a load from another SM takes
 // some 300 cycles, one of global memory 600).
 template <typename T, int EPI, bool VEC, bool SPLIT, int U, int C>
-MOE_DEV void finish_rows(const DenseArgs& g, uint32_t sums, int split, int rank, int i0, int j0, int rows) {
+MOE_DEV void finish_rows(const DenseArgs& g, const FinishAhead& ahead, uint32_t sums, int split, int rank, int i0, int j0, int rows) {
   constexpr int QUADS = EPI == kEpiGated ? 16 : 32;
   const Columns<T, VEC, !VEC && !SPLIT, QUADS> cols(g.J - j0);
   if (cols.n <= 0) return;
   const int j = j0 + cols.r, t0 = (SPLIT ? rank * (kDFewThreads / QUADS) : 0) + (int)threadIdx.x / QUADS, step = (SPLIT ? split : 1) * (kDFewThreads / QUADS);
-  f32x2 bias[2] = {0, 0};
-  if (EPI == kEpiLinear && g.bias) {
-    const T* q = static_cast<const T*>(g.bias) + j;
-    T b[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) b[e] = e < cols.n ? q[cols.at(e)] : from_f32<T>(0.f);
-    bias[0] = pack_f32x2(to_f32(b[0]), to_f32(b[1]));
-    bias[1] = pack_f32x2(to_f32(b[2]), to_f32(b[3]));
-  }
   sums += (uint32_t)cols.r * 4u;
 #pragma unroll 1
   for (int t = t0; t < rows; t += U * step) {
-    uint2 add[U];
+    Quad add[U];
     f32x2 v[U][2], w[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       v[u][0] = v[u][1] = w[u][0] = w[u][1] = 0;
-      if (EPI == kEpiLinear && g.residual && t + u * step < rows)
-        add[u] = cols.load(static_cast<const T*>(g.residual) + (long long)(i0 + t + u * step) * g.J + j);
+      if (EPI != kEpiLinear || !g.residual) continue;
+      if (u == 0 && t == t0) add[u] = ahead.residual;
+      else if (t + u * step < rows) add[u] = cols.load(static_cast<const T*>(g.residual) + (long long)(i0 + t + u * step) * g.J + j);
     }
 #pragma unroll 1
     for (int c0 = 0; c0 < (SPLIT ? split : 1); c0 += C) {
@@ -161,7 +179,7 @@ MOE_DEV void finish_rows(const DenseArgs& g, uint32_t sums, int split, int rank,
         f32x2 s[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          if (EPI == kEpiLinear) v[u][k] = add2(v[u][k], bias[k]);
+          if (EPI == kEpiLinear && g.bias) v[u][k] = add2(v[u][k], cols.template pair<false>(ahead.bias, k));
           act_pair<decltype(act)::value>(v[u][k], v[u][k], s[k]);
         }
         if (EPI == kEpiGated) {
@@ -176,8 +194,8 @@ MOE_DEV void finish_rows(const DenseArgs& g, uint32_t sums, int split, int rank,
         } else if (EPI == kEpiLinear) {
           if (g.aux) cols.store(s, static_cast<T*>(g.aux) + i * g.J + j);
           if (g.residual) {
-            v[u][0] = add2(v[u][0], Pairs<T>::one(add[u].x));
-            v[u][1] = add2(v[u][1], Pairs<T>::one(add[u].y));
+            v[u][0] = add2(v[u][0], cols.template pair<VEC>(add[u], 0));
+            v[u][1] = add2(v[u][1], cols.template pair<VEC>(add[u], 1));
           }
         }
         cols.store(v[u], static_cast<T*>(g.out) + i * g.J + j);
@@ -187,16 +205,16 @@ MOE_DEV void finish_rows(const DenseArgs& g, uint32_t sums, int split, int rank,
 }
 
 template <typename T, int EPI, bool VEC>
-MOE_DEV void finish(const DenseArgs& g, uint32_t sums, int split, int rank, int i0, int j0, int rows) {
+MOE_DEV void finish(const DenseArgs& g, const FinishAhead& ahead, uint32_t sums, int split, int rank, int i0, int j0, int rows) {
   constexpr int G = EPI == kEpiGated ? 2 : 1;
-  if (split == 1) finish_rows<T, EPI, VEC, false, 4 / G, 1>(g, sums, split, rank, i0, j0, rows);
-  else if (rows <= split * 8 * G) finish_rows<T, EPI, VEC, true, 1, kDFewMaxSplit>(g, sums, split, rank, i0, j0, rows);
-  else finish_rows<T, EPI, VEC, true, 4 / G, 2>(g, sums, split, rank, i0, j0, rows);
+  if (split == 1) finish_rows<T, EPI, VEC, false, 4 / G, 1>(g, ahead, sums, split, rank, i0, j0, rows);
+  else if (rows <= split * 8 * G) finish_rows<T, EPI, VEC, true, 1, kDFewMaxSplit>(g, ahead, sums, split, rank, i0, j0, rows);
+  else finish_rows<T, EPI, VEC, true, 4 / G, 2>(g, ahead, sums, split, rank, i0, j0, rows);
 }
 
 // Q's rows j are the M operand, P's rows i the N operand.
 template <typename T, bool PMN, bool QMN, int EPI>
-__global__ void __launch_bounds__(kDFewThreads)
+__global__ void __launch_bounds__(kDFewThreads, 2)
     dense_few_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ DenseArgs g, const DFewPlan plan) {
   extern __shared__ uint8_t smem_raw[];
@@ -259,12 +277,16 @@ __global__ void __launch_bounds__(kDFewThreads)
   const uint32_t tmem = sh->tmem_base;
 
   const int tv = min(plan.nt, g.I - i0);
-  if (EPI == kEpiLinear && warp >= 2) {   // what the tile's end reads, into L2
-    const int width = min(kRows, g.J - j0) * 2, t = (int)threadIdx.x - 64;
-    if (g.bias && t * 128 < width) prefetch_l2(static_cast<const T*>(g.bias) + j0 + t * 64);
-    if (g.residual)
-      for (int e = t; e < 2 * tv; e += kDFewThreads - 64)
+  FinishAhead ahead = {};
+  if (EPI == kEpiLinear) {
+    if (g.vec) fetch_ahead<T, EPI, true, false>(ahead, g, split, rank, i0, j0, tv);
+    else if (split > 1) fetch_ahead<T, EPI, false, true>(ahead, g, split, rank, i0, j0, tv);
+    else fetch_ahead<T, EPI, false, false>(ahead, g, split, rank, i0, j0, tv);
+    if (g.residual && warp >= 2) {   // the rows behind the first into L2
+      const int width = min(kRows, g.J - j0) * 2;
+      for (int e = (int)threadIdx.x - 64 + 16; e < 2 * tv; e += kDFewThreads - 64)
         if ((e & 1) * 128 < width) prefetch_l2(static_cast<const T*>(g.residual) + (long long)(i0 + (e >> 1)) * g.J + j0 + (e & 1) * 64);
+    }
   }
 
   if (warp == 0) {
@@ -330,8 +352,8 @@ __global__ void __launch_bounds__(kDFewThreads)
     tmem_dealloc(tmem, cols);
   }
 
-  if (g.vec) finish<T, EPI, true>(g, smem_u32(sums), split, rank, i0, j0, tv);
-  else finish<T, EPI, false>(g, smem_u32(sums), split, rank, i0, j0, tv);
+  if (g.vec) finish<T, EPI, true>(g, ahead, smem_u32(sums), split, rank, i0, j0, tv);
+  else finish<T, EPI, false>(g, ahead, smem_u32(sums), split, rank, i0, j0, tv);
   if (split > 1) cluster_sync();   // no CTA leaves while another reads its sums
 }
 

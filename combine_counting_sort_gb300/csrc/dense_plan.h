@@ -2,15 +2,17 @@
 // only; no CUDA).
 //
 // Every shape that fits is given its time by a model of the two kernels, and the
-// least is taken.  The model's constants are a least-squares fit (in the logarithm, 14%
-// rms) to 2800 timings of 220 products: 1 to 4000 rows, 64 to 8000 columns, contractions of 64 to
-// 7120, every direction and epilogue.  What it picks takes 3% more than the best shape
-// timed, on average; by waves and bytes alone it was 12%.
+// least is taken.  The model's constants are fitted to 8200 timings of 460 products (1 to
+// 4000 rows, 64 to 12000 columns, contractions of 64 to 7120, every direction and
+// epilogue; operands in memory where they are larger than L2), first to the times, then for
+// what the choice costs: 2% over the best shape timed, on average, and 22% at most; by waves and
+// bytes alone it was 12%.
 #pragma once
 
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 
 namespace moe {
 
@@ -39,7 +41,7 @@ struct DenseDevice {
 };
 
 // Shared memory of the few-row kernel's ring: half an SM's for tiles of up to 64 rows where there
-// are more CTAs than SMs, otherwise all of it; no more stages than are filled, but room for the tile's sums.
+// are more CTAs than the SMs hold one each of, otherwise all of it; no more stages than are filled, but room for the tile's sums.
 inline int dfew_stages(int nt, long long share, bool half) {
   const int stage = 16384 + nt * 128, fit = std::min(kDFewMaxStages, (half ? 104 : 220) * 1024 / stage);
   return std::max((nt * 512 + stage - 1) / stage, (int)std::min<long long>(share, fit));
@@ -51,25 +53,31 @@ inline DensePlan dense_plan(const DenseShape& s, const DenseDevice& d) {
   // pairs: a tile's epilogue runs under the next tile's products, all but the last one's (ns)
   const long long tiles = (s.I + 255) / 256 * ((s.J + 2 * columns - 1) / (2 * columns));
   const double rounds = (double)((tiles + d.pairs - 1) / d.pairs);
-  const double epilogue = (2427.0 + 1637.0 * res + 1950.0 * aux) * (1.0 + 1.1 * odd);
+  const double epilogue = (2684.0 + 1614.0 * res + 1865.0 * aux) * (1.0 + 0.815 * odd);
   DensePlan best = {true, 0, 0, 0};
-  double cost = 2212.0 + std::max(rounds * KB * 286.0, (rounds - 1.0) * epilogue) + epilogue;
+  double cost = 2335.0 + std::max(rounds * KB * 355.0, (rounds - 1.0) * epilogue) + epilogue;
+  // more bytes than L2 keeps until they are used again; rows j read by two tiles of i come twice
+  const double bytes = 2.0 * (s.I * s.K + two * s.J * s.K + s.I * s.J * (1.0 + res + two * aux));
+  const bool cold = bytes > 12e6;
   for (int nt = s.p_mn ? 64 : 16; nt <= 256; nt *= 2) {
+    if (nt > (s.p_mn ? 64 : 32) && nt >= 2 * s.I) break;   // (half of its rows would be empty)
     const long long all = (s.I + nt - 1) / nt * ((s.J + columns - 1) / columns);
     for (int split = 1; split <= kDFewMaxSplit && split <= KB; ++split) {
       const long long ctas = all * split, share = (KB + split - 1) / split;
-      const bool half = nt <= 64 && ctas > d.sms;
+      const bool half = nt <= 64 && ctas > d.cta[0][split];
       const long long room = d.cta[half][split];
       if (room < split) continue;
       const double waves = (double)((ctas + room - 1) / room), at_once = (double)std::min(ctas, room);
       const double on_sm = half ? std::min(2.0, std::max(1.0, at_once / d.sms)) : 1.0;
-      // 64 of k: the products, this SM's reads, all SMs' reads
+      // 64 of k: the products, this SM's reads, all SMs' reads, this SM's reads from memory
       const double stage = 16384.0 + nt * 128.0;
-      const double per_k = std::max({1.755 * nt * on_sm, stage * on_sm / 90.0, stage * at_once / d.sms / 91.0});
-      const double rows = (double)((std::min<long long>(nt, s.I) + (long long)(8 * two) * split - 1) / ((long long)(8 * two) * split));   // a thread's
-      const double end = 798.0 + rows * (29.4 * two + 78.0 * res + 40.7 * aux * two) * (1.0 + 1.43 * odd) + 3.2 * nt * on_sm +
-                         (split > 1 ? 14.2 * std::min<long long>(nt, s.I) * on_sm : 0.0);
-      const double c = 941.0 + (split > 1 ? 655.0 : 0.0) + 107.0 * split + waves * (577.0 + share * per_k + end);
+      const double per_k = std::max({1.9 * nt * on_sm, stage * on_sm / 93.6, stage * at_once / d.sms / 76.4, cold ? 16384.0 * on_sm / 72.8 : 0.0});
+      const double memory = (bytes + (cold && nt < s.I ? 2.0 * two * s.J * s.K : 0.0)) / 5918.0;
+      const double held = (double)std::min<long long>(nt, s.I), rows = std::ceil(held / (8.0 * two * split));   // a tile's, a thread's
+      const double end = 1457.0 + rows * (13.5 * two + 92.8 * res + 61.0 * aux * two) * (1.0 + 0.553 * odd) + 2.56 * nt * on_sm +
+                         (split > 1 ? 12.06 * held * on_sm : 0.0);
+      const double alone = cold && !half && nt <= 32 ? 503.0 : 0.0;   // one small ring an SM: its start and end are not another one's work
+      const double c = 931.0 + alone + (split > 1 ? 569.0 : 0.0) + 94.3 * split + std::max(waves * (227.0 + share * per_k), memory) + waves * end;
       if (c < cost) {
         cost = c;
         best = {false, nt, dfew_stages(nt, share, half), split};
