@@ -53,7 +53,7 @@ DenseDevice dense_device(K few, P pair) {
   d.pairs = std::min(resident_ctas(pair, kDPairThreads, kDPairSmemBytes, 2), d.sms) / 2;
   for (int c = 1; c <= kDFewMaxSplit; ++c) {
     d.cta[0][c] = resident_ctas(few, kDFewThreads, dfew_smem_bytes(128, 6), c);
-    d.cta[1][c] = resident_ctas(few, kDFewThreads, dfew_smem_bytes(64, 4), c);
+    d.cta[1][c] = 2 * d.cta[0][c];   // (of kernels with tensor memory the query says one a SM whatever their size; two run)
   }
   return d;
 }
