@@ -6,70 +6,126 @@ namespace moe {
 
 // ---------------------------------------------------------------- d = dy * slope and dbias
 //
-// Memory bound: reads dy and slope, writes d.  A block of 8 warps takes 128
-// columns, a row for each half warp, four rows in flight; the blocks of a cluster
-// (gridDim.y of them) share the rows, and add up their column sums through distributed
-// shared memory in rank order.  V = 8: half-warp lane l holds columns 8 l.., in 16-byte
-// vectors; V = 1: columns l, l + 16, ...
-template <typename T, int V>
-__global__ void __launch_bounds__(256)
+// Memory bound: reads dy and slope, writes d.  A block of 256 threads takes 8 LANES columns,
+// LANES threads to a row, eight columns a thread, a few rows in flight; the blocks of a
+// cluster (gridDim.y of them) share the rows, and add up their column sums through
+// distributed shared memory in rank order.  d's rows are padded to whole vectors.  Rows of
+// dy and slope of any length (SHIFT) start anywhere: their eight values are shifted out of
+// the two vectors that hold them (857 x 5141 with the sums: 36 us value by value).
+
+// The two vectors that hold eight values from element `at` of p's `total`, as they come: by
+// predicated loads, so that nothing waits for them before they are shifted.  At the tensor's
+// ends, where a vector would reach beyond it, the values are fetched one by one then.  (One
+// vector a lane and the other from the next lane: 4.2 us against 2.0 for two rows, 15.4 against 13.4 for 857.)
+struct Unaligned {
+  uint4 lo, hi;
+  int off;   // -1: one by one
+};
+MOE_DEV void load_if(uint4& v, const uint4* p, bool there) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "l"(p), "r"((int)there));
+}
+MOE_DEV void load_unaligned(Unaligned& u, const uint16_t* p, long long at, long long total) {
+  const int off = (int)((uintptr_t)(p + at) & 15) >> 1;
+  const bool inside = at >= off && at - off + 16 <= total;
+  const uint4* v = reinterpret_cast<const uint4*>(p + at - off);
+  load_if(u.lo, v, inside);
+  load_if(u.hi, v + 1, inside);
+  u.off = inside ? off : -1;
+}
+MOE_DEV uint4 shifted(const Unaligned& u, const uint16_t* p, long long at, long long total) {
+  uint32_t w[8];
+  if (u.off < 0) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = at + k < total ? p[at + k] : 0u;
+    return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+  }
+  w[0] = u.lo.x, w[1] = u.lo.y, w[2] = u.lo.z, w[3] = u.lo.w, w[4] = u.hi.x, w[5] = u.hi.y, w[6] = u.hi.z, w[7] = u.hi.w;
+#pragma unroll
+  for (int k = 0; k < 6; ++k) w[k] = u.off & 4 ? w[k + 2] : w[k];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) w[k] = u.off & 2 ? w[k + 1] : w[k];
+  const int bits = (u.off & 1) * 16;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                    __funnelshift_r(w[3], w[4], bits));
+}
+
+template <typename T, bool SHIFT, int LANES>
+__global__ void __launch_bounds__(256, 2)
     dense_d_kernel(const T* dy, const T* slope, int I, int J, T* d, long long ldd, T* dbias) {
-  __shared__ float sums[16][128];
-  __shared__ float total[128];
-  const int lane = threadIdx.x & 15, slot = threadIdx.x >> 4, j0 = blockIdx.x * 128;
-  constexpr int NV = 8 / V, ROWS = 4;
-  float acc[8] = {};
+  constexpr int SLOTS = 256 / LANES, COLS = 8 * LANES, ROWS = SHIFT ? 2 : 4;
+  __shared__ float sums[SLOTS][COLS];
+  __shared__ float total[COLS];
+  const int lane = threadIdx.x % LANES, slot = threadIdx.x / LANES, j0 = blockIdx.x * COLS, j = j0 + 8 * lane;
+  const long long rows = I;
+  f32x2 acc[4] = {0, 0, 0, 0};
   grid_launch_next();
   grid_wait_previous();
-  const int step = 16 * gridDim.y;
-  for (long long i = blockIdx.y * 16 + slot; i < I; i += (long long)ROWS * step) {
+  const int step = SLOTS * gridDim.y;
+  const uint16_t *py = reinterpret_cast<const uint16_t*>(dy), *ps = reinterpret_cast<const uint16_t*>(slope);
+  // (columns from J on, up to whole vectors, are written with whatever is there: nothing reads them)
+  if (j < J)
+    for (long long i = blockIdx.y * SLOTS + slot; i < I; i += (long long)ROWS * step) {
+      uint4 a[ROWS], s[ROWS];
+      if (SHIFT) {
+        Unaligned ua[ROWS] = {}, us[ROWS] = {};
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      const int j = j0 + (V == 8 ? 8 * lane : 16 * c + lane);
-      if (j >= J) continue;
-      Vec<T, V> a[ROWS], s[ROWS];
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r)
-        if (i + r * step < I) {
-          a[r] = *reinterpret_cast<const Vec<T, V>*>(dy + (i + r * step) * J + j);
-          if (slope) s[r] = *reinterpret_cast<const Vec<T, V>*>(slope + (i + r * step) * J + j);
+        for (int r = 0; r < ROWS; ++r) {
+          const long long at = min(i + r * step, rows - 1) * J + j;
+          load_unaligned(ua[r], py, at, rows * J);
+          if (slope) load_unaligned(us[r], ps, at, rows * J);
         }
 #pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          const long long at = min(i + r * step, rows - 1) * J + j;
+          a[r] = shifted(ua[r], py, at, rows * J);
+          if (slope) s[r] = shifted(us[r], ps, at, rows * J);
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+          if (i + r * step < I) {
+            a[r] = *reinterpret_cast<const uint4*>(py + (i + r * step) * J + j);
+            if (slope) s[r] = *reinterpret_cast<const uint4*>(ps + (i + r * step) * J + j);
+          }
+      }
+#pragma unroll
       for (int r = 0; r < ROWS; ++r)
         if (i + r * step < I) {
-          Vec<T, V> o;
+          f32x2 f[4], g[4];
+          Pairs<T>::get(a[r], f);
+          if (slope) {
+            Pairs<T>::get(s[r], g);
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const float f = slope ? to_f32(a[r].v[v]) * to_f32(s[r].v[v]) : to_f32(a[r].v[v]);
-            acc[c * V + v] += f;
-            o.v[v] = from_f32<T>(f);
+            for (int e = 0; e < 4; ++e) f[e] = mul2(f[e], g[e]);
           }
-          if (d) *reinterpret_cast<Vec<T, V>*>(d + (i + r * step) * ldd + j) = o;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] = add2(acc[e], f[e]);
+          if (d) *reinterpret_cast<uint4*>(d + (i + r * step) * ldd + j) = Pairs<T>::put(f);
         }
     }
-  }
   if (!dbias) return;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sums[slot][V == 8 ? 8 * lane + e : 16 * e + lane] = acc[e];
+  for (int e = 0; e < 4; ++e) *reinterpret_cast<f32x2*>(&sums[slot][8 * lane + 2 * e]) = acc[e];
   __syncthreads();
-  if (threadIdx.x < 128) {
+  if (threadIdx.x < COLS) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) s += sums[w][threadIdx.x];
+    for (int w = 0; w < SLOTS; ++w) s += sums[w][threadIdx.x];
     total[threadIdx.x] = s;
   }
   cluster_sync();
-  const int j = j0 + threadIdx.x;
-  if (blockIdx.y == 0 && threadIdx.x < 128 && j < J) {
+  if (blockIdx.y == 0 && threadIdx.x < COLS && j0 + (int)threadIdx.x < J) {
     float s = 0.f;
     const uint32_t at = smem_u32(&total[threadIdx.x]);
     for (uint32_t r = 0; r < gridDim.y; ++r) s += ld_shared_cluster_f32(mapa_shared(at, r));
-    dbias[j] = from_f32<T>(s);
+    dbias[j0 + threadIdx.x] = from_f32<T>(s);
   }
   cluster_sync();
 }
 
-// d = [dh * factors[:, :F], dh * factors[:, F:]]
+// d = [dh * factors[:, :F], dh * factors[:, F:]].  (Rows of odd lengths value by value: half of d's own
+// lie across its vectors.)
 template <typename T, int V>
 __global__ void __launch_bounds__(256) gated_d_kernel(const T* dh, const T* factors, int I, int F, T* d, long long ldd) {
   const int j = (blockIdx.x * 256 + threadIdx.x) * V;
@@ -105,16 +161,24 @@ __global__ void __launch_bounds__(256) gated_d_kernel(const T* dh, const T* fact
   }
 }
 
-template <typename T>
-int launch_d(const void* dy, const void* slope, int I, int J, void* d, long long ldd, void* dbias, cudaStream_t st) {
+template <typename T, int LANES>
+int launch_d_lanes(const void* dy, const void* slope, int I, int J, void* d, long long ldd, void* dbias, cudaStream_t st) {
   const bool vec = J % 8 == 0 && aligned16(dy) && aligned16(slope);
-  const int strips = (J + 127) / 128;
-  // rows of a strip over up to 8 blocks (a cluster, where they add up their sums); without sums, over more
-  const long long want = std::max(1, 6 * 152 / strips), cap = dbias ? 8 : 1024;
-  const int ys = (int)std::min({cap, want, ((long long)I + 15) / 16});
-  auto kernel = vec ? dense_d_kernel<T, 8> : dense_d_kernel<T, 1>;
+  const int strips = (J + 8 * LANES - 1) / (8 * LANES), slots = 256 / LANES;
+  // as many blocks as run at once (two an SM, in clusters of up to 8 where they add up their sums)
+  const long long want = std::max(1, 264 / strips), cap = dbias ? 8 : 264;
+  const int ys = (int)std::min({cap, want, ((long long)I + slots - 1) / slots});
+  auto kernel = vec ? dense_d_kernel<T, false, LANES> : dense_d_kernel<T, true, LANES>;
   return launch_next(kernel, dim3((unsigned)strips, (unsigned)ys), 256, 0, st, 1, dbias ? (unsigned)ys : 1u, static_cast<const T*>(dy),
                      static_cast<const T*>(slope), I, J, static_cast<T*>(d), ldd, static_cast<T*>(dbias));
+}
+
+// Columns a block: 256 bytes of a row, or less where the clusters of so many strips would not fill the device.
+template <typename T>
+int launch_d(const void* dy, const void* slope, int I, int J, void* d, long long ldd, void* dbias, cudaStream_t st) {
+  if (!dbias || J > 18 * 128) return launch_d_lanes<T, 16>(dy, slope, I, J, d, ldd, dbias, st);
+  if (J > 18 * 64) return launch_d_lanes<T, 8>(dy, slope, I, J, d, ldd, dbias, st);
+  return launch_d_lanes<T, 4>(dy, slope, I, J, d, ldd, dbias, st);
 }
 
 template <typename T>
