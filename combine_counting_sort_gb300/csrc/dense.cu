@@ -207,16 +207,12 @@ int dense(int kind, int dtype, const DenseOperand& P, const DenseOperand& Q, con
 // dx = d W and dW = d^T x; d is [T, n] with rows of ldd
 int dense_backward(int dtype, const void* d, long long ldd, int T, int n, const void* x, int K, const void* W, void* dx, void* dW,
                    int32_t* status, cudaStream_t st) {
-  int rc = MOE_OK;
-  if (dx) {
-    DenseArgs g = {T, K, n, dx, nullptr, nullptr, nullptr, MOE_ACT_NONE, aligned16(dx), 0, status, 0};
-    rc = dense(kDenseDx, dtype, {d, false, T, ldd}, {W, true, K, K}, g, st);
-  }
-  if (rc == MOE_OK && dW) {
-    DenseArgs g = {n, K, T, dW, nullptr, nullptr, nullptr, MOE_ACT_NONE, aligned16(dW), 0, status, 0};
-    rc = dense(kDenseDw, dtype, {d, true, n, ldd}, {x, true, K, K}, g, st);
-  }
-  return rc;
+  const DenseOperand P[2] = {{d, false, T, ldd}, {d, true, n, ldd}}, Q[2] = {{W, true, K, K}, {x, true, K, K}};
+  const DenseArgs g[2] = {{T, K, n, dx, nullptr, nullptr, nullptr, MOE_ACT_NONE, aligned16(dx), 0, status, 0},
+                          {n, K, T, dW, nullptr, nullptr, nullptr, MOE_ACT_NONE, aligned16(dW), 0, status, 0}};
+  if (dx && dW) return dtype == MOE_BF16 ? dense_backward_bf16(P, Q, g, st) : dense_backward_f16(P, Q, g, st);
+  if (dx) return dense(kDenseDx, dtype, P[0], Q[0], g[0], st);
+  return dW ? dense(kDenseDw, dtype, P[1], Q[1], g[1], st) : MOE_OK;
 }
 
 }  // namespace moe

@@ -28,8 +28,9 @@ inline uint32_t dfew_stage_bytes(int nt) { return 2 * kDenseChunk + (uint32_t)nt
 inline size_t dfew_smem_bytes(int nt, int stages) { return 1024 + (size_t)stages * dfew_stage_bytes(nt) + sizeof(DFewShared); }
 
 struct DFewPlan {
-  int nt, stages, split;   // tokens a tile, ring stages, CTAs a cluster
-  int ti;                  // tiles of i
+  int nt, stages, split;   // rows a tile, ring stages, CTAs a tile
+  int cluster;             // CTAs a cluster: one tile's, or several tiles'
+  int ti, tiles;           // tiles of i, and in all
 };
 
 MOE_DEV float ld_shared_cluster_f32(uint32_t addr) {
@@ -124,11 +125,11 @@ MOE_DEV void fetch_ahead(FinishAhead& ahead, const DenseArgs& g, int split, int 
 }
 
 // What finishes a tile: this thread's columns of the rows t0, t0 + step, ... below `rows`, the sums
-// of the cluster's CTAs added up in their order.  U rows at a time, C CTAs' sums of each in flight:
+// of the tile's CTAs (from the cluster's CTA `first` on) added up in their order.  U rows at a time, C CTAs' sums of each in flight:
 // few rows want all CTAs' at once, many rows several of their own (a load from another SM takes
 // some 300 cycles, one of global memory 600).
 template <typename T, int EPI, bool VEC, bool SPLIT, int U, int C>
-MOE_DEV void finish_rows(const DenseArgs& g, const FinishAhead& ahead, uint32_t sums, int split, int rank, int i0, int j0, int rows) {
+MOE_DEV void finish_rows(const DenseArgs& g, const FinishAhead& ahead, uint32_t sums, int first, int split, int rank, int i0, int j0, int rows) {
   constexpr int QUADS = EPI == kEpiGated ? 16 : 32;
   const Columns<T, VEC, !VEC && !SPLIT, QUADS> cols(g.J - j0);
   if (cols.n <= 0) return;
@@ -150,7 +151,7 @@ MOE_DEV void finish_rows(const DenseArgs& g, const FinishAhead& ahead, uint32_t 
       float a[C][U][4], b[C][U][4];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const uint32_t from = SPLIT ? mapa_shared(sums, (uint32_t)min(c0 + c, split - 1)) : sums;
+        const uint32_t from = SPLIT ? mapa_shared(sums, (uint32_t)(first + min(c0 + c, split - 1))) : sums;
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (t + u * step < rows && (C == 1 || c0 + c < split)) {
@@ -205,25 +206,28 @@ MOE_DEV void finish_rows(const DenseArgs& g, const FinishAhead& ahead, uint32_t 
 }
 
 template <typename T, int EPI, bool VEC>
-MOE_DEV void finish(const DenseArgs& g, const FinishAhead& ahead, uint32_t sums, int split, int rank, int i0, int j0, int rows) {
+MOE_DEV void finish(const DenseArgs& g, const FinishAhead& ahead, uint32_t sums, int first, int split, int rank, int i0, int j0, int rows) {
   constexpr int G = EPI == kEpiGated ? 2 : 1;
-  if (split == 1) finish_rows<T, EPI, VEC, false, 4 / G, 1>(g, ahead, sums, split, rank, i0, j0, rows);
-  else if (rows <= split * 8 * G) finish_rows<T, EPI, VEC, true, 1, kDFewMaxSplit>(g, ahead, sums, split, rank, i0, j0, rows);
-  else finish_rows<T, EPI, VEC, true, 4 / G, 2>(g, ahead, sums, split, rank, i0, j0, rows);
+  if (split == 1) finish_rows<T, EPI, VEC, false, 4 / G, 1>(g, ahead, sums, first, split, rank, i0, j0, rows);
+  else if (rows <= split * 8 * G) finish_rows<T, EPI, VEC, true, 1, kDFewMaxSplit>(g, ahead, sums, first, split, rank, i0, j0, rows);
+  else finish_rows<T, EPI, VEC, true, 4 / G, 2>(g, ahead, sums, first, split, rank, i0, j0, rows);
 }
 
-// Q's rows j are the M operand, P's rows i the N operand.
+// CTA `cta` of a product: Q's rows j are the M operand, P's rows i the N operand.
 template <typename T, bool PMN, bool QMN, int EPI>
-__global__ void __launch_bounds__(kDFewThreads, 2)
-    dense_few_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                     const __grid_constant__ DenseArgs g, const DFewPlan plan) {
+MOE_DEV void dense_few_cta(const CUtensorMap& tmP, const CUtensorMap& tmQ, const DenseArgs& g, const DFewPlan& plan, int cta) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t stage_bytes = 2 * kDenseChunk + (uint32_t)plan.nt * 128;
   DFewShared* sh = reinterpret_cast<DFewShared*>(ring + (size_t)plan.stages * stage_bytes);
   const int warp = threadIdx.x >> 5;
-  const int split = plan.split, rank = split > 1 ? (int)cluster_ctarank() : 0;
-  const int tile = (int)blockIdx.x / split;
+  const int split = plan.split, in_cluster = plan.cluster > 1 ? (int)cluster_ctarank() : 0, rank = in_cluster % split;
+  const int tile = cta / split;
+  if (tile >= plan.tiles) {   // fills up a cluster
+    cluster_sync();
+    cluster_sync();
+    return;
+  }
   constexpr int kRows = EPI == kEpiGated ? 64 : 128;   // columns of out a tile
   const int i0 = tile % plan.ti * plan.nt, j0 = tile / plan.ti * kRows;
   const int KB = (g.K + kDenseBK - 1) / kDenseBK;
@@ -345,16 +349,37 @@ __global__ void __launch_bounds__(kDFewThreads, 2)
     }
   }
   tc_fence_before();
-  if (split > 1) cluster_sync();
+  if (plan.cluster > 1) cluster_sync();
   else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, cols);
   }
 
-  if (g.vec) finish<T, EPI, true>(g, ahead, smem_u32(sums), split, rank, i0, j0, tv);
-  else finish<T, EPI, false>(g, ahead, smem_u32(sums), split, rank, i0, j0, tv);
-  if (split > 1) cluster_sync();   // no CTA leaves while another reads its sums
+  if (g.vec) finish<T, EPI, true>(g, ahead, smem_u32(sums), in_cluster - rank, split, rank, i0, j0, tv);
+  else finish<T, EPI, false>(g, ahead, smem_u32(sums), in_cluster - rank, split, rank, i0, j0, tv);
+  if (plan.cluster > 1) cluster_sync();   // no CTA leaves while another reads its sums
+}
+
+template <typename T, bool PMN, bool QMN, int EPI>
+__global__ void __launch_bounds__(kDFewThreads, 2)
+    dense_few_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                     const __grid_constant__ DenseArgs g, const __grid_constant__ DFewPlan plan) {
+  dense_few_cta<T, PMN, QMN, EPI>(tmP, tmQ, g, plan, (int)blockIdx.x);
+}
+
+// dx = d W (the first `first` CTAs) and dW = d^T x in one launch
+struct DBoth {
+  CUtensorMap P[2], Q[2];
+  DenseArgs g[2];
+  DFewPlan plan[2];
+  int first;
+};
+template <typename T>
+__global__ void __launch_bounds__(kDFewThreads, 2) dense_both_kernel(const __grid_constant__ DBoth b) {
+  const int cta = (int)blockIdx.x;
+  if (cta < b.first) dense_few_cta<T, false, true, kEpiPlain>(b.P[0], b.Q[0], b.g[0], b.plan[0], cta);
+  else dense_few_cta<T, true, true, kEpiPlain>(b.P[1], b.Q[1], b.g[1], b.plan[1], cta - b.first);
 }
 
 }  // namespace moe

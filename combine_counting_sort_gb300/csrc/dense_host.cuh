@@ -8,6 +8,8 @@
 
 namespace moe {
 
+constexpr uint64_t kDenseTimeoutNs = 2000000000ull;
+
 // One operand: `rows` of i (or j) by g.K of k; ld is the length of its rows in memory.
 struct DenseOperand {
   const void* p;
@@ -69,14 +71,50 @@ int launch_pair(const CUtensorMap& tmP, const CUtensorMap& tmQ, const DenseArgs&
   return launch_next(kernel, dim3(2 * (unsigned)std::min<long long>(pairs, tiles)), kDPairThreads, kDPairSmemBytes, st, 2, 1, tmP, tmQ, g);
 }
 
+inline DenseShape shape_of(const DenseArgs& g, bool gated, bool p_mn) {
+  return {g.I, g.J, g.K, gated, p_mn, g.aux != nullptr, g.residual != nullptr, g.vec != 0};
+}
+
+// The plans of the shapes that a thread asked for last (a plan takes longer than a launch).
+struct DensePlans {
+  DenseShape shape[2];
+  DensePlan plan[2];
+  bool both;
+};
+inline bool same_shape(const DenseShape& a, const DenseShape& b) {
+  return a.I == b.I && a.J == b.J && a.K == b.K && a.gated == b.gated && a.p_mn == b.p_mn && a.aux == b.aux && a.residual == b.residual && a.vec == b.vec;
+}
+inline DensePlans& plans_at(DensePlans (&kept)[64], const DenseShape& s) {
+  return kept[(unsigned long long)((s.I * 1000003 + s.J) * 1000003 + s.K + s.aux * 7 + s.residual * 13 + s.vec * 29) * 0x9E3779B97F4A7C15ull >> 58];
+}
+
+// The kernel's form of a plan; the CTAs that it takes, in whole clusters.
+inline long long few_ctas(const DenseArgs& g, const DensePlan& plan, int rows, int cluster, DFewPlan* fp) {
+  fp->nt = plan.nt;
+  fp->stages = plan.stages;
+  fp->split = plan.split;
+  fp->cluster = cluster;
+  fp->ti = (int)(((long long)g.I + plan.nt - 1) / plan.nt);
+  const long long tiles = (long long)fp->ti * (((long long)g.J + rows - 1) / rows);
+  fp->tiles = (int)std::min<long long>(tiles, 0x7FFFFFFF);
+  return (tiles * plan.split + cluster - 1) / cluster * cluster;
+}
+
 template <typename T, bool PMN, bool QMN, int EPI>
 int launch_dense(const DenseOperand& P, const DenseOperand& Q, DenseArgs g, cudaStream_t st) {
   if (!device_has_tcgen05()) return MOE_ERR_UNSUPPORTED;
   auto kernel = dense_few_kernel<T, PMN, QMN, EPI>;
   static const DenseDevice device = dense_device(kernel, dense_pair_kernel<T, PMN, QMN, EPI, false>);
   if (device.pairs < 1) return MOE_ERR_CUDA;
-  g.timeout_ns = 2000000000ull;
-  const DensePlan plan = dense_plan({g.I, g.J, g.K, EPI == kEpiGated, PMN, g.aux != nullptr, g.residual != nullptr, g.vec != 0}, device);
+  g.timeout_ns = kDenseTimeoutNs;
+  const DenseShape shape = shape_of(g, EPI == kEpiGated, PMN);
+  static thread_local DensePlans kept[64] = {};
+  DensePlans& at = plans_at(kept, shape);
+  if (!same_shape(at.shape[0], shape)) {
+    at.plan[0] = dense_plan(shape, device);
+    at.shape[0] = shape;
+  }
+  const DensePlan plan = at.plan[0];
   CUtensorMap tmP, tmQ;
   if (plan.pair) {
     if (!encode_operand<T>(&tmP, P, g.K, 128) || !encode_operand<T>(&tmQ, Q, g.K, 128)) return MOE_ERR_CUDA;
@@ -84,15 +122,45 @@ int launch_dense(const DenseOperand& P, const DenseOperand& Q, DenseArgs g, cuda
     return launch_pair<T, PMN, QMN, EPI, false>(tmP, tmQ, g, device.pairs, st);
   }
   if (!encode_operand<T>(&tmP, P, g.K, plan.nt) || !encode_operand<T>(&tmQ, Q, g.K, EPI == kEpiGated ? 64 : 128)) return MOE_ERR_CUDA;
-  constexpr int kRows = EPI == kEpiGated ? 64 : 128;
   DFewPlan fp;
-  fp.nt = plan.nt;
-  fp.stages = plan.stages;
-  fp.split = plan.split;
-  fp.ti = (int)(((long long)g.I + plan.nt - 1) / plan.nt);
-  const long long ctas = (long long)fp.ti * (((long long)g.J + kRows - 1) / kRows) * plan.split;
+  const long long ctas = few_ctas(g, plan, EPI == kEpiGated ? 64 : 128, plan.split, &fp);
   if (ctas > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
   return launch_next(kernel, dim3((unsigned)ctas), kDFewThreads, dfew_smem_bytes(plan.nt, plan.stages), st, (unsigned)plan.split, 1, tmP, tmQ, g, fp);
+}
+
+// dx = d W and dW = d^T x, in one launch where that is quicker
+template <typename T>
+int launch_backward(const DenseOperand (&P)[2], const DenseOperand (&Q)[2], const DenseArgs (&g)[2], cudaStream_t st) {
+  if (!device_has_tcgen05()) return MOE_ERR_UNSUPPORTED;
+  auto kernel = dense_both_kernel<T>;
+  static const DenseDevice device = dense_device(kernel, dense_pair_kernel<T, false, true, kEpiPlain, false>);
+  if (device.pairs < 1) return MOE_ERR_CUDA;
+  const DenseShape s[2] = {shape_of(g[0], false, false), shape_of(g[1], false, true)};
+  static thread_local DensePlans kept[64] = {};
+  DensePlans& at = plans_at(kept, s[0]);
+  if (!same_shape(at.shape[0], s[0]) || !same_shape(at.shape[1], s[1])) {
+    at.both = dense_plan_both(s, device, at.plan);
+    at.shape[0] = s[0];
+    at.shape[1] = s[1];
+  }
+  const DensePlan(&plan)[2] = at.plan;
+  if (!at.both) {
+    const int rc = launch_dense<T, false, true, kEpiPlain>(P[0], Q[0], g[0], st);
+    return rc ? rc : launch_dense<T, true, true, kEpiPlain>(P[1], Q[1], g[1], st);
+  }
+  const int cluster = std::max(plan[0].split, plan[1].split);
+  DBoth b;
+  long long ctas[2];
+  for (int i = 0; i < 2; ++i) {
+    if (!encode_operand<T>(&b.P[i], P[i], g[i].K, plan[i].nt) || !encode_operand<T>(&b.Q[i], Q[i], g[i].K, 128)) return MOE_ERR_CUDA;
+    b.g[i] = g[i];
+    b.g[i].timeout_ns = kDenseTimeoutNs;
+    ctas[i] = few_ctas(g[i], plan[i], 128, cluster, &b.plan[i]);
+  }
+  if (ctas[0] + ctas[1] > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+  b.first = (int)ctas[0];
+  const size_t smem = std::max(dfew_smem_bytes(plan[0].nt, plan[0].stages), dfew_smem_bytes(plan[1].nt, plan[1].stages));
+  return launch_next(kernel, dim3((unsigned)(ctas[0] + ctas[1])), kDFewThreads, smem, st, (unsigned)cluster, 1, b);
 }
 
 // The products that the operators take: x W^T (linear, gated), d W and d^T x.
@@ -110,5 +178,7 @@ int dense_product(int kind, const DenseOperand& P, const DenseOperand& Q, const 
 
 int dense_product_bf16(int kind, const DenseOperand& P, const DenseOperand& Q, const DenseArgs& g, cudaStream_t st);
 int dense_product_f16(int kind, const DenseOperand& P, const DenseOperand& Q, const DenseArgs& g, cudaStream_t st);
+int dense_backward_bf16(const DenseOperand (&P)[2], const DenseOperand (&Q)[2], const DenseArgs (&g)[2], cudaStream_t st);
+int dense_backward_f16(const DenseOperand (&P)[2], const DenseOperand (&Q)[2], const DenseArgs (&g)[2], cudaStream_t st);
 
 }  // namespace moe
