@@ -21,10 +21,6 @@ struct Unaligned {
   uint4 lo, hi;
   int off;   // -1: one by one
 };
-MOE_DEV void load_if(uint4& v, const uint4* p, bool there) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "l"(p), "r"((int)there));
-}
 MOE_DEV void load_unaligned(Unaligned& u, const uint16_t* p, long long at, long long total) {
   const int off = (int)((uintptr_t)(p + at) & 15) >> 1;
   const bool inside = at >= off && at - off + 16 <= total;
@@ -34,20 +30,13 @@ MOE_DEV void load_unaligned(Unaligned& u, const uint16_t* p, long long at, long 
   u.off = inside ? off : -1;
 }
 MOE_DEV uint4 shifted(const Unaligned& u, const uint16_t* p, long long at, long long total) {
-  uint32_t w[8];
   if (u.off < 0) {
+    uint32_t w[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) w[k] = at + k < total ? p[at + k] : 0u;
     return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
   }
-  w[0] = u.lo.x, w[1] = u.lo.y, w[2] = u.lo.z, w[3] = u.lo.w, w[4] = u.hi.x, w[5] = u.hi.y, w[6] = u.hi.z, w[7] = u.hi.w;
-#pragma unroll
-  for (int k = 0; k < 6; ++k) w[k] = u.off & 4 ? w[k + 2] : w[k];
-#pragma unroll
-  for (int k = 0; k < 5; ++k) w[k] = u.off & 2 ? w[k + 1] : w[k];
-  const int bits = (u.off & 1) * 16;
-  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
-                    __funnelshift_r(w[3], w[4], bits));
+  return shifted8(u.lo, u.hi, u.off);
 }
 
 template <typename T, bool SHIFT, int LANES>

@@ -36,6 +36,24 @@ struct alignas(V == 1 ? sizeof(T) : 16) Vec {
 template <typename T>
 constexpr int kVec16 = 16 / (int)sizeof(T);
 
+// 16 bytes by a predicated load: no branch, so nothing waits for it here.
+MOE_DEV void load_if(uint4& v, const void* p, bool there) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "l"(p), "r"((int)there));
+}
+
+// Eight 16-bit values from value `off` (0 to 7) of two vectors on.
+MOE_DEV uint4 shifted8(const uint4& lo, const uint4& hi, int off) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int k = 0; k < 6; ++k) w[k] = off & 4 ? w[k + 2] : w[k];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) w[k] = off & 2 ? w[k + 1] : w[k];
+  const int bits = (off & 1) * 16;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                    __funnelshift_r(w[3], w[4], bits));
+}
+
 // ---------------------------------------------------------------- pairs of fp32 (.f32x2 instructions)
 
 using f32x2 = unsigned long long;

@@ -135,40 +135,55 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdPerSm<T, NV, MASK>) norm_fwd_
   cp_async_wait<0>();
 }
 
-// Few rows: a block a row, everything loaded at once straight into registers (one
-// vector a thread), since the latency of one row is the time.
-template <typename T, typename W, int BLOCK, bool MASK>
-__global__ void __launch_bounds__(BLOCK) norm_fwd_few_kernel(const NormArgs p) {
-  constexpr int V = kVec16<T>, P = V / 2, WARPS = BLOCK / 32;
-  __shared__ float2 stats[WARPS];
-  __shared__ float counts[WARPS];
-  const long long row = blockIdx.x;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const RowPart<T, BLOCK, 1, MASK> part(p.H, row);
+// Few rows: all of them at once, everything loaded straight into registers (one vector
+// a thread, TPR threads a row), since the latency of one row is the time.
+// What is held between the passes stays packed, so that an SM holds 1536 threads and more.
+template <typename T, typename W, int TPR, bool MASK>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, (TPR <= 64 ? 4 : TPR <= 256 ? 6 : TPR == 512 ? 3 : 2)) norm_fwd_few_kernel(const NormArgs p) {
+  constexpr int V = kVec16<T>, P = V / 2, WARPS = TPR / 32, BLOCK = TPR < 256 ? 256 : TPR;
+  __shared__ float2 stats[BLOCK / 32];
+  __shared__ float counts[BLOCK / 32];
+  const int grp = (int)threadIdx.x / TPR, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long row = (long long)blockIdx.x * (BLOCK / TPR) + grp;
+  const RowPart<T, TPR, 1, MASK> part(p.H, row);
   const T* src = static_cast<const T*>(p.x) + row * p.H + part.first;
-  f32x2 v[P], w[P], b[P];
+  uint4 raw = make_uint4(0, 0, 0, 0);
+  ParamVec<T, W> w, b;
   grid_launch_next();
   grid_wait_previous();
+  if (row >= p.T) return;   // (a whole group)
+  if (MASK) {
+    // a row's first and last vectors have its neighbours' values too, but none behind the last row
+    uint4 wr[2] = {}, br[2] = {};
+    const bool there = part.any(0), inside = row < p.T - 1 || part.col(0) + V <= p.H;
+    load_if(raw, src, there && inside);
+    part.template params_begin<W>(p.weight, 0, wr);
+    part.template params_begin<W>(p.bias, 0, br);
+    if (there) {
+      if (!inside) {
+        f32x2 v[P];
 #pragma unroll
-  for (int e = 0; e < P; ++e) v[e] = w[e] = b[e] = 0;
-  if (part.any(0)) {
-    if (part.whole(0)) {
-      Pairs<T>::get(*reinterpret_cast<const uint4*>(src), v);
-    } else {
-#pragma unroll
-      for (int e = 0; e < P; ++e)
-        v[e] = pack_f32x2(2 * e >= part.lo(0) && 2 * e < part.hi(0) ? to_f32(src[2 * e]) : 0.f,
-                          2 * e + 1 >= part.lo(0) && 2 * e + 1 < part.hi(0) ? to_f32(src[2 * e + 1]) : 0.f);
+        for (int e = 0; e < P; ++e)
+          v[e] = pack_f32x2(2 * e >= part.lo(0) && 2 * e < part.hi(0) ? to_f32(src[2 * e]) : 0.f,
+                            2 * e + 1 >= part.lo(0) && 2 * e + 1 < part.hi(0) ? to_f32(src[2 * e + 1]) : 0.f);
+        raw = Pairs<T>::put(v);
+      }
+      w = part.template params_end<W>(p.weight, 1.f, 0, wr);
+      b = part.template params_end<W>(p.bias, 0.f, 0, br);
     }
-    if (!MASK && p.weight) reinterpret_cast<const ParamVec<T, W>*>(static_cast<const W*>(p.weight) + part.col(0))->get(w);
-    else part.template params<W>(p.weight, 1.f, 0).get(w);
-    if (!MASK && p.bias) reinterpret_cast<const ParamVec<T, W>*>(static_cast<const W*>(p.bias) + part.col(0))->get(b);
-    else part.template params<W>(p.bias, 0.f, 0).get(b);
+  } else if (part.any(0)) {
+    raw = *reinterpret_cast<const uint4*>(src);
+    if (p.weight) w = *reinterpret_cast<const ParamVec<T, W>*>(static_cast<const W*>(p.weight) + part.col(0));
+    else w = part.template params<W>(p.weight, 1.f, 0);
+    if (p.bias) b = *reinterpret_cast<const ParamVec<T, W>*>(static_cast<const W*>(p.bias) + part.col(0));
+    else b = part.template params<W>(p.bias, 0.f, 0);
   }
   const float n = warp_sum((float)max(0, part.hi(0) - part.lo(0))), inv_h = 1.f / (float)p.H;
-  f32x2 s = v[0];
+  f32x2 v[P], s = 0;
+  Pairs<T>::get(raw, v);
+  if (part.any(0)) part.mask(0, v);
 #pragma unroll
-  for (int e = 1; e < P; ++e) s = add2(s, v[e]);
+  for (int e = 0; e < P; ++e) s = add2(s, v[e]);
   const float warp_s = warp_sum(sum2(s)), m = n > 0.f ? warp_s / n : 0.f;
   f32x2 d[P], q = 0;
 #pragma unroll
@@ -179,22 +194,32 @@ __global__ void __launch_bounds__(BLOCK) norm_fwd_few_kernel(const NormArgs p) {
     for (int e = 0; e < P; ++e) q = fma2(d[e], d[e], q);
   }
   const float warp_q = warp_sum(sum2(q));
-  if (lane == 0) {
-    stats[warp] = make_float2(warp_s, warp_q);
-    counts[warp] = n;
+  float mean = m, var = warp_q * inv_h;
+  if (WARPS > 1) {
+    if (lane == 0) {
+      stats[warp] = make_float2(warp_s, warp_q);
+      counts[warp] = n;
+    }
+    group_sync<TPR, BLOCK>();
+    const int peer = grp * WARPS + lane;
+    const float2 o = lane < WARPS ? stats[peer] : make_float2(0.f, 0.f);
+    const float on = lane < WARPS ? counts[peer] : 0.f;
+    mean = warp_sum(o.x) * inv_h;
+    const float off = on > 0.f ? o.x / on - mean : 0.f;
+    var = warp_sum(fmaf(on * off, off, o.y)) * inv_h;
   }
-  __syncthreads();
-  const float2 o = lane < WARPS ? stats[lane] : make_float2(0.f, 0.f);
-  const float on = lane < WARPS ? counts[lane] : 0.f, mean = warp_sum(o.x) * inv_h;
-  const float off = on > 0.f ? o.x / on - mean : 0.f;
-  const float rstd = 1.f / sqrtf(warp_sum(fmaf(on * off, off, o.y)) * inv_h + p.eps);
-  if (threadIdx.x == 0) {
+  const float rstd = 1.f / sqrtf(var + p.eps);
+  if (part.tid == 0) {
     if (p.mean) p.mean[row] = mean;
     if (p.rstd) p.rstd[row] = rstd;
   }
   if (part.any(0)) {
+    f32x2 wp[P], bp[P];
+    Pairs<T>::get(raw, v);
+    w.get(wp);
+    b.get(bp);
 #pragma unroll
-    for (int e = 0; e < P; ++e) v[e] = fma2(fma2(v[e], both(rstd), both(-mean * rstd)), w[e], b[e]);
+    for (int e = 0; e < P; ++e) v[e] = fma2(fma2(v[e], both(rstd), both(-mean * rstd)), wp[e], bp[e]);
     part.store(static_cast<T*>(p.y) + row * p.H + part.first, 0, Pairs<T>::put(v));
   }
 }
@@ -241,12 +266,23 @@ int launch_fwd_any(const NormArgs& p, cudaStream_t st) {
   return launch_next(norm_fwd_any_kernel<T, W>, dim3(p.T), 512, 0, st, 1, 1, p);
 }
 
+template <typename T, typename W, int TPR, bool MASK>
+int launch_fwd_few(const NormArgs& p, cudaStream_t st) {
+  constexpr int BLOCK = TPR < 256 ? 256 : TPR, ROWS = BLOCK / TPR;
+  return launch_next(norm_fwd_few_kernel<T, W, TPR, MASK>, dim3((p.T + ROWS - 1) / ROWS), BLOCK, 0, st, 1, 1, p);
+}
+
 template <typename T, typename W, bool MASK>
 int norm_fwd(const NormArgs& p, cudaStream_t st) {
   constexpr int V = kVec16<T>;
-  if (p.T <= 304 && norm_tpr(p.H, V, V) <= 1024) {
-    if (norm_tpr(p.H, V, V) <= 256) return launch_next(norm_fwd_few_kernel<T, W, 256, MASK>, dim3(p.T), 256, 0, st, 1, 1, p);
-    return launch_next(norm_fwd_few_kernel<T, W, 1024, MASK>, dim3(p.T), 1024, 0, st, 1, 1, p);
+  switch (norm_tpr(p.H, V, V)) {
+    case 32: if (few_rows(p.T, 32)) return launch_fwd_few<T, W, 32, MASK>(p, st); break;
+    case 64: if (few_rows(p.T, 64)) return launch_fwd_few<T, W, 64, MASK>(p, st); break;
+    case 128: if (few_rows(p.T, 128)) return launch_fwd_few<T, W, 128, MASK>(p, st); break;
+    case 256: if (few_rows(p.T, 256)) return launch_fwd_few<T, W, 256, MASK>(p, st); break;
+    case 512: if (few_rows(p.T, 512)) return launch_fwd_few<T, W, 512, MASK>(p, st); break;
+    case 1024: if (few_rows(p.T, 1024)) return launch_fwd_few<T, W, 1024, MASK>(p, st); break;
+    default: break;
   }
   // Values a thread: as many as leave two blocks an SM room in registers and shared memory.
   // (One block of 1024 threads with a turn more in its ring: 50.8 us against 46.9 at 8192 x 7168.)

@@ -13,6 +13,10 @@
 // and stored value by value.
 #pragma once
 
+#include <string.h>
+
+#include <type_traits>
+
 #include "dtype.cuh"
 #include "host_util.h"
 
@@ -108,9 +112,28 @@ struct RowPart {
     for (int e = 0; e < V / 2; ++e)
       v[e] = pack_f32x2(2 * e >= a && 2 * e < b ? lo2(v[e]) : 0.f, 2 * e + 1 >= a && 2 * e + 1 < b ? hi2(v[e]) : 0.f);
   }
-  // this thread's weights (or biases) of vector i, for registers; zeros outside the row
+  // This thread's weights (or biases) of vector i, for registers; unspecified outside the row.  16-bit
+  // ones come out of the two vectors that hold them, which `begin` loads and `end` waits for.
   template <typename W>
-  MOE_DEV ParamVec<T, W> params(const void* src, float none, int i) const {
+  MOE_DEV bool params_packed(const void* src, int i) const {
+    const int c = col(i), off = c & 7;
+    return sizeof(W) == 2 && src && c >= off && c - off + 16 <= H;
+  }
+  template <typename W>
+  MOE_DEV void params_begin(const void* src, int i, uint4 (&raw)[2]) const {
+    const bool there = params_packed<W>(src, i);
+    const W* p = static_cast<const W*>(src) + (col(i) & ~7);
+    load_if(raw[0], p, there);
+    load_if(raw[1], p + 8, there);
+  }
+  template <typename W>
+  MOE_DEV ParamVec<T, W> params_end(const void* src, float none, int i, const uint4 (&raw)[2]) const {
+    ParamVec<T, W> r;
+    if (params_packed<W>(src, i)) {
+      const uint4 packed = shifted8(raw[0], raw[1], col(i) & 7);
+      memcpy(&r, &packed, sizeof(uint4));
+      return r;
+    }
     const W* p = static_cast<const W*>(src);
     f32x2 v[V / 2];
 #pragma unroll
@@ -120,9 +143,14 @@ struct RowPart {
       const float b = j + 1 >= 0 && j + 1 < H ? (p ? to_f32(p[j + 1]) : none) : 0.f;
       v[e / 2] = pack_f32x2(a, b);
     }
-    ParamVec<T, W> r;
     r.set(v);
     return r;
+  }
+  template <typename W>
+  MOE_DEV ParamVec<T, W> params(const void* src, float none, int i) const {
+    uint4 raw[2] = {};
+    params_begin<W>(src, i, raw);
+    return params_end<W>(src, none, i, raw);
   }
 };
 
@@ -146,10 +174,14 @@ MOE_DEV float block_sum(float v, float* scratch) {
 template <typename W>
 MOE_DEV float param(const void* p, int j, float none) { return p ? to_f32(static_cast<const W*>(p)[j]) : none; }
 
-// [H] weights (or biases) into shared memory
+// [H] weights (or biases) into shared memory, H of them being whole vectors
 template <int BLOCK, typename W>
 MOE_DEV void copy_params(W* dst, const void* src, float none, int H) {
-  for (int j = threadIdx.x; j < H; j += BLOCK) dst[j] = src ? static_cast<const W*>(src)[j] : from_f32<W>(none);
+  if (src) {
+    for (int j = threadIdx.x; j < H / kVec16<W>; j += BLOCK) reinterpret_cast<uint4*>(dst)[j] = static_cast<const uint4*>(src)[j];
+  } else {
+    for (int j = threadIdx.x; j < H; j += BLOCK) dst[j] = from_f32<W>(none);
+  }
 }
 
 // All threads of this thread's group.  Barriers 1 to 15, and the block's own for the last of 16
@@ -170,6 +202,12 @@ inline int norm_tpr(int H, int vec, int values) {
   while (tpr * values < norm_span(H, vec)) tpr *= 2;
   return tpr;
 }
+
+// Rows few enough to be taken all at once: up to two and a half times the threads that run at once (four times: 17.1 us against 11.0 at 9728 x 1024, 16.3
+// against 14.2 at 4864 x 1111; once: 4.1 against 8.7 at 304 x 7168).
+inline bool few_rows(int T, int tpr) { return 2LL * T * tpr <= 5 * 2048LL * device_sm_count(); }
+
+int norm_bwd_few(int dtype, int wdtype, const NormArgs& p, void* dweight, void* dbias, cudaStream_t st);
 
 inline size_t elem_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 inline bool norm_shape_ok(int T, int H) { return T >= 0 && H >= 1 && H <= MOE_NORM_MAX_H; }
