@@ -1,8 +1,9 @@
 """A small decoder of MoE blocks, one CUDA graph replay per step.
 
 Each block adds to a token's state what its routed experts give it
-(moe_layer_few, FP8 or 4-bit expert weights) and what a shared expert does
-(moe_matvec_w4 twice); a 4-bit vocabulary projection picks the next token.
+(moe_layer_few, FP8 or 4-bit expert weights) and what a shared expert does: 4-bit
+(moe_matvec_w4 twice) or in bf16 (moe_gated, and moe_linear onto the routed output); a
+4-bit vocabulary projection picks the next token.
 There is no attention: the example shows the decoding calls together, with
 random weights.
 
@@ -36,7 +37,7 @@ def quantise_fp8(W):
 
 
 class Block:
-    def __init__(self, gen, T, H, F, E, k, weights, group, status):
+    def __init__(self, gen, T, H, F, E, k, weights, shared, group, status):
         def rand(*shape):
             return (torch.randn(*shape, generator=gen, device="cuda") * shape[-1] ** -0.5).to(torch.bfloat16)
 
@@ -47,7 +48,10 @@ class Block:
         else:
             self.W1, self.W2, self.s1, self.s2 = quantise_w4(rand(E, 2 * F, H), group), quantise_w4(rand(E, H, F), group), None, None
         self.layer_group = 0 if weights == "fp8" else group
-        self.shared_up, self.shared_down = quantise_w4(rand(1, 2 * F, H), group)[0], quantise_w4(rand(1, H, F), group)[0]
+        self.shared = shared
+        up, down = rand(1, 2 * F, H), rand(1, H, F)
+        self.shared_up, self.shared_down = (up[0], down[0]) if shared == "bf16" else (quantise_w4(up, group)[0], quantise_w4(down, group)[0])
+        self.act = torch.empty(T, F, dtype=torch.bfloat16, device="cuda")
         # what a call writes, and its workspace: made once
         self.ids = torch.empty(T, k, dtype=torch.int32, device="cuda")
         self.w = torch.empty(T, k, device="cuda")
@@ -60,6 +64,10 @@ class Block:
         h = torch.nn.functional.rms_norm(x.float(), x.shape[-1:]).to(torch.bfloat16)
         moe.moe_layer_few(h, self.W1, self.s1, self.W2, self.s2, self.ids, self.w, self.routed, self.ws, self.status,
                           router=self.router, group=self.layer_group)
+        if self.shared == "bf16":
+            moe.moe_gated(h, self.shared_up, self.act, self.status)
+            moe.moe_linear(self.act, self.shared_down, self.down, self.status, residual=self.routed)
+            return x + self.down
         moe.moe_matvec_w4(h, self.shared_up, self.group, self.up, self.status)
         gate, up = self.up.float().chunk(2, -1)
         moe.moe_matvec_w4((torch.nn.functional.silu(gate) * up).to(torch.bfloat16), self.shared_down, self.group, self.down, self.status)
@@ -72,6 +80,7 @@ def main():
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--blocks", type=int, default=2)
     ap.add_argument("--weights", choices=("fp8", "w4"), default="w4")
+    ap.add_argument("--shared", choices=("w4", "bf16"), default="w4", help="the shared expert's weights")
     ap.add_argument("--hidden", type=int, default=2048)
     ap.add_argument("--ffn", type=int, default=1024)
     ap.add_argument("--experts", type=int, default=64)
@@ -80,7 +89,7 @@ def main():
     a = ap.parse_args()
     gen = torch.Generator(device="cuda").manual_seed(0)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    blocks = [Block(gen, a.tokens, a.hidden, a.ffn, a.experts, a.topk, a.weights, 128, status) for _ in range(a.blocks)]
+    blocks = [Block(gen, a.tokens, a.hidden, a.ffn, a.experts, a.topk, a.weights, a.shared, 128, status) for _ in range(a.blocks)]
     embedding = torch.randn(a.vocab, a.hidden, generator=gen, device="cuda").to(torch.bfloat16)
     vocabulary = quantise_w4((torch.randn(1, a.vocab, a.hidden, generator=gen, device="cuda") * a.hidden ** -0.5).to(torch.bfloat16))[0]
     logits = torch.empty(a.tokens, a.vocab, dtype=torch.bfloat16, device="cuda")
