@@ -32,6 +32,10 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdPerSm<T, NV, MASK>) norm_fwd_
   const long long stride = groups * p.H;
   const T* src = static_cast<const T*>(p.x) + g * p.H + part.first;   // vector 0 of the next row to fetch
   T* dst = static_cast<T*>(p.y) + g * p.H + part.first;
+  // (4000 x 8001: 37.8 us with branches, 32.8 without; rows of whole vectors 45.3 against 49.2)
+  if (MASK)
+#pragma unroll
+    for (int d = 0; d < D; ++d) part.clear_absent(mine + d * SLOT, STEP);
 #pragma unroll
   for (int d = 0; d < D - 1; ++d, src += stride) {
     if (g + d * groups < p.T) part.fetch(src, g + d * groups == p.T - 1, mine_at + d * SLOT, STEP);
@@ -66,13 +70,13 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdPerSm<T, NV, MASK>) norm_fwd_
     f32x2 v[NV][P];
     f32x2 s = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (part.any(i)) {
-        Pairs<T>::get(*reinterpret_cast<const uint4*>(mine + slot * SLOT + i * STEP), v[i]);
-        part.mask(i, v[i]);
+    for (int i = 0; i < NV; ++i) {
+      if (!MASK && !part.any(i)) continue;
+      Pairs<T>::get(*reinterpret_cast<const uint4*>(mine + slot * SLOT + i * STEP), v[i]);
+      part.mask(i, v[i]);
 #pragma unroll
-        for (int e = 0; e < P; ++e) s = add2(s, v[i][e]);
-      }
+      for (int e = 0; e < P; ++e) s = add2(s, v[i][e]);
+    }
     const int next = slot == 0 ? D - 1 : slot - 1;   // the slot read a row ago
     const long long ahead = row + (D - 1) * groups;
     if (ahead < p.T) part.fetch(src, ahead == p.T - 1, mine_at + next * SLOT, STEP);
@@ -83,15 +87,15 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdPerSm<T, NV, MASK>) norm_fwd_
     const float warp_s = warp_sum(sum2(s)), m = warp_s * warp_inv;
     f32x2 q = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (part.any(i)) {
-        f32x2 d[P];
+    for (int i = 0; i < NV; ++i) {
+      if (!MASK && !part.any(i)) continue;
+      f32x2 d[P];
 #pragma unroll
-        for (int e = 0; e < P; ++e) d[e] = add2(v[i][e], both(-m));
-        part.mask(i, d);
+      for (int e = 0; e < P; ++e) d[e] = add2(v[i][e], both(-m));
+      part.mask(i, d);
 #pragma unroll
-        for (int e = 0; e < P; ++e) q = fma2(d[e], d[e], q);
-      }
+      for (int e = 0; e < P; ++e) q = fma2(d[e], d[e], q);
+    }
     const float warp_q = warp_sum(sum2(q));
     float mean = m, var = warp_q * inv_h;
     if (WARPS > 1) {
@@ -116,20 +120,20 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdPerSm<T, NV, MASK>) norm_fwd_
       if (p.rstd) p.rstd[row] = rstd;
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (part.any(i)) {
-        f32x2 wp[P], bp[P], o[P];
-        if (MASK) {
-          w[i].get(wp);
-          b[i].get(bp);
-        } else {
-          reinterpret_cast<const ParamVec<T, W>*>(ws + part.col(i))->get(wp);
-          reinterpret_cast<const ParamVec<T, W>*>(bs + part.col(i))->get(bp);
-        }
-#pragma unroll
-        for (int e = 0; e < P; ++e) o[e] = fma2(fma2(v[i][e], both(rstd), off), wp[e], bp[e]);
-        part.store(dst, i, Pairs<T>::put(o));
+    for (int i = 0; i < NV; ++i) {
+      if (!MASK && !part.any(i)) continue;
+      f32x2 wp[P], bp[P], o[P];
+      if (MASK) {
+        w[i].get(wp);
+        b[i].get(bp);
+      } else {
+        reinterpret_cast<const ParamVec<T, W>*>(ws + part.col(i))->get(wp);
+        reinterpret_cast<const ParamVec<T, W>*>(bs + part.col(i))->get(bp);
       }
+#pragma unroll
+      for (int e = 0; e < P; ++e) o[e] = fma2(fma2(v[i][e], both(rstd), off), wp[e], bp[e]);
+      if (part.any(i)) part.store(dst, i, Pairs<T>::put(o));
+    }
     dst += stride;
   }
   cp_async_wait<0>();

@@ -88,6 +88,12 @@ struct RowPart {
     for (int i = 0; i < NV; ++i)
       if (any(i)) cp_async16(slot + i * step, src + i * TPR * V, MASK && last_row ? (uint32_t)(hi(i) * sizeof(T)) : 16u);
   }
+  // zeros into the slots of vectors that the rows do not have: work on masked rows then needs no branches
+  MOE_DEV void clear_absent(uint8_t* slot, uint32_t step) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (!any(i)) *reinterpret_cast<uint4*>(slot + i * step) = make_uint4(0, 0, 0, 0);
+  }
   // store vector i of the row whose vector 0 is at `dst`
   MOE_DEV void store(T* dst, int i, const uint4& v) const {
     T* p = dst + i * TPR * V;
