@@ -12,6 +12,10 @@
 // Roles per CTA (384 threads): warp 0 streams stages of both operands, warp 1 of
 // the even CTA issues the products, warps 4-11 of both CTAs hold the epilogue (two
 // warps a quarter of the rows, each half the columns).
+//
+// Bound by the tensor cores (8192 x 2048 x 7168 gated: 247 us, 1.95 PFLOP/s; with factors
+// 262) until an epilogue takes longer than a tile's products: 4096 x 7168 x 2048 65 us, with
+// gelu_tanh 72, slope 79 and residual 82 (tensor pipe 75% of the active cycles).
 #pragma once
 
 #include "dense.cuh"

@@ -549,7 +549,8 @@ int moe_linear(const void* x, int T, int K, const void* W, int N, int dtype, con
                const void* residual, int act, void* y, void* slope, int32_t* status, moe_stream_t stream);
 
 /* moe_linear_bwd: with d = dy * slope (slope NULL: d = dy, no activation) rounded to dtype for the
- * products,
+ * products (the tensor core takes 16-bit operands; slope in 32 bits would save the other rounding and
+ * cost half as much again to read),
  *   dx = d W,  dW = d^T x,  dbias = sum_t dy * slope (fp32, from the unrounded d);
  * the residual's gradient is dy itself.
  *   dx device dtype [T, K], dW device dtype [N, K], dbias device dtype [N]; each NULL where
