@@ -13,32 +13,6 @@ namespace moe {
 // dy and slope of any length (SHIFT) start anywhere: their eight values are shifted out of
 // the two vectors that hold them (857 x 5141 with the sums: 36 us value by value).
 
-// The two vectors that hold eight values from element `at` of p's `total`, as they come: by
-// predicated loads, so that nothing waits for them before they are shifted.  At the tensor's
-// ends, where a vector would reach beyond it, the values are fetched one by one then.  (One
-// vector a lane and the other from the next lane: 4.2 us against 2.0 for two rows, 15.4 against 13.4 for 857.)
-struct Unaligned {
-  uint4 lo, hi;
-  int off;   // -1: one by one
-};
-MOE_DEV void load_unaligned(Unaligned& u, const uint16_t* p, long long at, long long total) {
-  const int off = (int)((uintptr_t)(p + at) & 15) >> 1;
-  const bool inside = at >= off && at - off + 16 <= total;
-  const uint4* v = reinterpret_cast<const uint4*>(p + at - off);
-  load_if(u.lo, v, inside);
-  load_if(u.hi, v + 1, inside);
-  u.off = inside ? off : -1;
-}
-MOE_DEV uint4 shifted(const Unaligned& u, const uint16_t* p, long long at, long long total) {
-  if (u.off < 0) {
-    uint32_t w[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = at + k < total ? p[at + k] : 0u;
-    return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-  }
-  return shifted8(u.lo, u.hi, u.off);
-}
-
 template <typename T, bool SHIFT, int LANES>
 __global__ void __launch_bounds__(256, 2)
     dense_d_kernel(const T* dy, const T* slope, int I, int J, T* d, long long ldd, T* dbias) {

@@ -152,6 +152,8 @@ MOE_DEV void with_act(int act, F&& f) {
   }
 }
 
+MOE_DEV void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // ---------------------------------------------------------------- 32 x 32 blocks between registers and rows
 //
 // A warp holds its accumulators with lane l having 32 columns of row i0 + l, and works
@@ -192,6 +194,34 @@ MOE_DEV void store_block(const f32x2 (&v)[16], T* out, long long ld, int i0, int
       if (i0 + r < I && j0 + 8 * c < J)
         *reinterpret_cast<uint4*>(out + (long long)(i0 + r) * ld + j0 + 8 * c) = *reinterpret_cast<const uint4*>(stage + block_at(r, c));
     }
+  } else if (j0 + 32 <= J) {
+    // Rows that start anywhere: 16-byte stores between their first and last boundary, the values of each
+    // out of the two vectors of the stage that hold them; the eight values beside them one by one.
+    // (12 stores instead of the 32 of a value a lane, which take some 6 cycles each.)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = 8 * k + (lane >> 2), c = lane & 3;
+      T* row = out + (long long)(i0 + r) * ld + j0;
+      const int head = (8 - vector_offset(row)) & 7;
+      if (i0 + r < I && (head == 0 || c < 3)) {
+        const uint4 lo = *reinterpret_cast<const uint4*>(stage + block_at(r, c)), hi = *reinterpret_cast<const uint4*>(stage + block_at(r, (c + 1) & 3));
+        *reinterpret_cast<uint4*>(row + head + 8 * c) = shifted8(lo, hi, head);
+      }
+    }
+    T edge[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = 4 * k + (lane >> 3), q = lane & 7;
+      const int head = (8 - vector_offset(out + (long long)(i0 + r) * ld + j0)) & 7, col = q < head ? q : 24 + q;
+      edge[k] = *reinterpret_cast<const T*>(stage + block_at(r, col >> 3) + (col & 7) * 2);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = 4 * k + (lane >> 3), q = lane & 7;
+      T* row = out + (long long)(i0 + r) * ld + j0;
+      const int head = (8 - vector_offset(row)) & 7;
+      if (i0 + r < I && head) row[q < head ? q : 24 + q] = edge[k];
+    }
   } else if (j0 + lane < J) {
 #pragma unroll
     for (int k = 0; k < 32; k += 8) {   // eight rows read before they are written: the compiler may not swap the two
@@ -205,29 +235,27 @@ MOE_DEV void store_block(const f32x2 (&v)[16], T* out, long long ld, int i0, int
   }
 }
 
-// A block's residual as its rows lie, fetched ahead of its use: with vectors 16 bytes of rows
-// 8 k + lane / 4, otherwise a column's 32 values, two rows a word.
-struct alignas(16) ResidualAhead {
-  uint32_t v[16];
+// A block's residual as its rows lie: 16 bytes of rows 8 k + lane / 4, fetched ahead of its use.  Rows
+// that start anywhere are asked for in L2 then, and loaded where they are used.
+struct ResidualAhead {
+  uint4 v[4];
 };
 
 template <typename T>
 MOE_DEV void fetch_residual(ResidualAhead& a, const DenseArgs& g, int i0, int j0) {
-  const int lane = threadIdx.x & 31, j = j0 + (g.vec ? 8 * (lane & 3) : lane);
-  if (!g.residual || j >= g.J) return;
-  const uint16_t* p = static_cast<const uint16_t*>(g.residual) + (long long)i0 * g.J + j;
+  const int lane = threadIdx.x & 31;
+  if (!g.residual || j0 >= g.J) return;
+  const T* p = static_cast<const T*>(g.residual) + (long long)i0 * g.J + j0;
   if (g.vec) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int r = 8 * k + (lane >> 2);
-      if (i0 + r < g.I) *reinterpret_cast<uint4*>(a.v + 4 * k) = *reinterpret_cast<const uint4*>(p + (long long)r * g.J);
+      const int r = 8 * k + (lane >> 2), c = 8 * (lane & 3);
+      if (i0 + r < g.I && j0 + c < g.J) a.v[k] = *reinterpret_cast<const uint4*>(p + (long long)r * g.J + c);
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const uint32_t lo = i0 + 2 * k < g.I ? p[(long long)(2 * k) * g.J] : 0u, hi = i0 + 2 * k + 1 < g.I ? p[(long long)(2 * k + 1) * g.J] : 0u;
-      a.v[k] = lo | hi << 16;
-    }
+  } else if (i0 + lane < g.I) {
+    const T* row = p + (long long)lane * g.J;
+    prefetch_l2(row);
+    prefetch_l2(row + min(32, g.J - j0) - 1);
   }
 }
 
@@ -260,18 +288,21 @@ MOE_DEV void drain_biased(uint32_t taddr, f32x2 (&v)[16], const DenseArgs& g, in
 }
 
 // The residual's block into shared memory, and from there to the lanes of its rows.
-MOE_DEV void put_residual(const ResidualAhead& a, bool vec, uint8_t* stage) {
-  const int lane = threadIdx.x & 31;
-  if (vec) {
+MOE_DEV void put_residual(const ResidualAhead& a, const DenseArgs& g, int i0, int j0, uint8_t* stage) {
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  if (g.vec) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(stage + block_at(8 * k + (lane >> 2), c)) = a.v[k];
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(g.residual);
+    const long long total = (long long)g.I * g.J, at = (long long)(i0 + (lane >> 2)) * g.J + j0 + 8 * c;
+    const auto there = [&](int k) { return i0 + 8 * k + (lane >> 2) < g.I && j0 + 8 * c < g.J; };
+    Unaligned u[4] = {};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) load_unaligned(u[k], p, at + 8LL * k * g.J, total, there(k));
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      *reinterpret_cast<uint4*>(stage + block_at(8 * k + (lane >> 2), lane & 3)) = *reinterpret_cast<const uint4*>(a.v + 4 * k);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      *reinterpret_cast<uint16_t*>(stage + block_at(2 * k, lane >> 3) + (lane & 7) * 2) = (uint16_t)a.v[k];
-      *reinterpret_cast<uint16_t*>(stage + block_at(2 * k + 1, lane >> 3) + (lane & 7) * 2) = (uint16_t)(a.v[k] >> 16);
-    }
+      if (there(k)) *reinterpret_cast<uint4*>(stage + block_at(8 * k + (lane >> 2), c)) = shifted(u[k], p, at + 8LL * k * g.J, total);
   }
 }
 

@@ -44,8 +44,6 @@ MOE_DEV float ld_shared_cluster_f32(uint32_t addr) {
   return v;
 }
 
-MOE_DEV void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
 // 16 consecutive fp32 TMEM columns of this thread's lane.
 MOE_DEV void tmem_drain16(uint32_t taddr, float (&v)[16]) {
   asm volatile(

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kDPairThreads, 1)
           }
           store_block(u, out, g.J, i0, j0, g.I, g.J, g.vec, stage);
         } else if (EPI == kEpiLinear) {
-          if (g.residual) put_residual(ahead, g.vec, stage + kBlockBytes);
+          if (g.residual) put_residual(ahead, g, i0, j0, stage + kBlockBytes);
           if (c + 1 < kChunks) fetch_residual<T>(ahead, g, i0, j0 + 32);
           if (AUX) {
             f32x2 f[16];

@@ -2,10 +2,10 @@
 // only; no CUDA).
 //
 // Every shape that fits is given its time by a model of the two kernels, and the
-// least is taken.  The model's constants are fitted to 8200 timings of 460 products (1 to
+// least is taken.  The model's constants are fitted to 9500 timings of 550 products (1 to
 // 4000 rows, 64 to 12000 columns, contractions of 64 to 7120, every direction and
 // epilogue; operands in memory where they are larger than L2), first to the times, then for
-// what the choice costs: 2% over the best shape timed, on average, and 22% at most; by waves and
+// what the choice costs: 3% over the best shape timed, on average, and 33% at most; by waves and
 // bytes alone it was 12%.
 #pragma once
 
@@ -67,13 +67,13 @@ inline double dfew_cost(const DenseShape& s, const DenseDevice& d, int nt, int s
   const double on_sm = half ? std::min(2.0, std::max(1.0, at_once / d.sms)) : 1.0;
   // 64 of k: the products, this SM's reads, all SMs' reads, this SM's reads from memory
   const double stage = 16384.0 + nt * 128.0;
-  const double per_k = std::max({1.9 * nt * on_sm, stage * on_sm / 93.6, stage * at_once / d.sms / 76.4, cold ? 16384.0 * on_sm / 72.8 : 0.0});
-  const double memory = (bytes + (cold && nt < s.I ? 2.0 * two * s.J * s.K : 0.0)) / 5918.0;
+  const double per_k = std::max({1.9 * nt * on_sm, stage * on_sm / 94.4, stage * at_once / d.sms / 78.6, cold ? 16384.0 * on_sm / 72.0 : 0.0});
+  const double memory = (bytes + (cold && nt < s.I ? 2.0 * two * s.J * s.K : 0.0)) / 6200.0;
   const double held = (double)std::min<long long>(nt, s.I), rows = std::ceil(held / (8.0 * two * split));   // a tile's, a thread's
-  const double end = 1457.0 + rows * (13.5 * two + 92.8 * res + 61.0 * aux * two) * (1.0 + 0.553 * odd) + 2.56 * nt * on_sm +
-                     (split > 1 ? 12.06 * held * on_sm : 0.0);
-  const double alone = cold && !half && nt <= 32 ? 503.0 : 0.0;   // one small ring an SM: its start and end are not another one's work
-  return 931.0 + alone + (split > 1 ? 569.0 : 0.0) + 94.3 * split + std::max(waves * (227.0 + share * per_k), memory) + waves * end;
+  const double end = 1228.0 + rows * (14.7 * two + 120.0 * res + 70.5 * aux * two) * (1.0 + 0.414 * odd) + 3.38 * nt * on_sm +
+                     (split > 1 ? 13.8 * held * on_sm : 0.0);
+  const double alone = cold && !half && nt <= 32 ? 566.0 : 0.0;   // one small ring an SM: its start and end are not another one's work
+  return 827.0 + alone + (split > 1 ? 407.0 : 0.0) + 130.3 * split + std::max(waves * (484.0 + share * per_k), memory) + end + (waves - 1.0) * 0.92 * end;
 }
 
 inline double dpair_cost(const DenseShape& s, const DenseDevice& d) {
@@ -82,8 +82,8 @@ inline double dpair_cost(const DenseShape& s, const DenseDevice& d) {
   // a tile's epilogue runs under the next tile's products, all but the last one's
   const long long tiles = (s.I + 255) / 256 * ((s.J + columns - 1) / columns);
   const double rounds = (double)((tiles + d.pairs - 1) / d.pairs);
-  const double epilogue = (2684.0 + 1614.0 * res + 1865.0 * aux) * (1.0 + 0.815 * odd);
-  return 2335.0 + std::max(rounds * KB * 355.0, (rounds - 1.0) * epilogue) + epilogue;
+  const double epilogue = (2944.0 + 1134.0 * res + 3255.0 * aux) * (1.0 + 0.434 * odd) + 4016.0 * res * odd;
+  return 1010.0 + std::max(rounds * KB * 362.6, (rounds - 1.0) * epilogue) + epilogue;
 }
 
 // f(nt) for the rows a tile may have

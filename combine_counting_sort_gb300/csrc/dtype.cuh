@@ -42,6 +42,9 @@ MOE_DEV void load_if(uint4& v, const void* p, bool there) {
                : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "l"(p), "r"((int)there));
 }
 
+// 16-bit values from the vector boundary at or before p
+MOE_DEV int vector_offset(const void* p) { return (int)((uintptr_t)p & 15) >> 1; }
+
 // Eight 16-bit values from value `off` (0 to 7) of two vectors on.
 MOE_DEV uint4 shifted8(const uint4& lo, const uint4& hi, int off) {
   uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -52,6 +55,32 @@ MOE_DEV uint4 shifted8(const uint4& lo, const uint4& hi, int off) {
   const int bits = (off & 1) * 16;
   return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
                     __funnelshift_r(w[3], w[4], bits));
+}
+
+// The two vectors that hold eight values from element `at` of p's `total`, as they come: by
+// predicated loads, so that nothing waits for them before they are shifted.  At the tensor's
+// ends, where a vector would reach beyond it, the values are fetched one by one then.  (One
+// vector a lane and the other from the next lane: 4.2 us against 2.0 for two rows, 15.4 against 13.4 for 857.)
+struct Unaligned {
+  uint4 lo, hi;
+  int off;   // -1: one by one
+};
+MOE_DEV void load_unaligned(Unaligned& u, const uint16_t* p, long long at, long long total, bool wanted = true) {
+  const int off = (int)((uintptr_t)(p + at) & 15) >> 1;
+  const bool inside = at >= off && at - off + 16 <= total;
+  const uint4* v = reinterpret_cast<const uint4*>(p + at - off);
+  load_if(u.lo, v, inside && wanted);
+  load_if(u.hi, v + 1, inside && wanted);
+  u.off = inside ? off : -1;
+}
+MOE_DEV uint4 shifted(const Unaligned& u, const uint16_t* p, long long at, long long total) {
+  if (u.off < 0) {
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = at + k < total ? p[at + k] : 0u;
+    return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+  }
+  return shifted8(u.lo, u.hi, u.off);
 }
 
 // ---------------------------------------------------------------- pairs of fp32 (.f32x2 instructions)
