@@ -229,7 +229,7 @@ def test_gated_on_unaligned_views(T, F, H, status):
 
 
 @pytest.mark.parametrize("dtype", [BF, F16, F32])
-@pytest.mark.parametrize("T,H", [(1, 33), (7, 1000), (400, 1111), (900, 4096), (5000, 200), (40, 8200)])
+@pytest.mark.parametrize("T,H", [(1, 33), (7, 1000), (400, 1111), (900, 4096), (5000, 200), (40, 8200), (700, 7168), (2500, 1112), (1200, 1999)])
 def test_norm_on_unaligned_views_and_in_place(T, H, dtype):
     """The same values on a view, in place, and aligned: the results agree to the roundings of two orders
     of summation, (H / 16 + 32) 2^-22 of the terms, and one rounding to the type."""
@@ -380,3 +380,35 @@ def test_repeats_bit_for_bit(status):
         s.step()
         for k, v in s.outputs().items():
             assert torch.equal(v, want[k]), k
+
+
+# ---------------------------------------------------------------- in the decoding example, and a short workspace
+
+def test_decoding_with_a_shared_expert_in_bf16():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "decode_moe.py"), "--shared", "bf16", "--tokens", "3", "--steps", "4",
+                        "--hidden", "256", "--ffn", "128", "--experts", "16", "--topk", "4", "--vocab", "512"], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert "3 sequences x 4 steps" in r.stdout
+
+
+def test_refused_on_the_gpu(status):
+    x, W, y = ints(gen(1), 40, 64), ints(gen(2), 24, 64), torch.empty(40, 24, dtype=BF, device="cuda")
+    ws = ws_of(moe.moe_linear_bwd_ws_bytes(40, 24, 64))
+    with pytest.raises(ValueError, match="contiguous"):
+        moe.moe_linear(x.t().contiguous().t(), W, y, status)
+    with pytest.raises(ValueError, match="status must be torch.int32"):
+        moe.moe_linear(x, W, y, status.float())
+    with pytest.raises(ValueError, match="bias must be torch.bfloat16"):
+        moe.moe_linear(x, W, y, status, bias=torch.zeros(24, device="cuda"))
+    with pytest.raises(ValueError, match="ws must be a CUDA tensor"):
+        moe.moe_linear_bwd(y, x, W, None, None, torch.empty(1 << 16, dtype=torch.uint8), status)
+    with pytest.raises(moe.MoEError, match="INVALID_ARG"):
+        moe.moe_linear_bwd(y, x, W, torch.empty_like(x), None, ws[:-256].clone()[:256], status, slope=y)
+    with pytest.raises(moe.MoEError, match="INVALID_ARG"):   # operands of a product start on 16 bytes
+        moe.moe_linear(shifted(x)[0], W, y, status)
+    with pytest.raises(moe.MoEError, match="INVALID_ARG"):   # and a contraction is a multiple of 8
+        moe.moe_linear(x[:, :63].contiguous(), W[:, :63].contiguous(), y, status)
