@@ -67,13 +67,14 @@ inline double dfew_cost(const DenseShape& s, const DenseDevice& d, int nt, int s
   const double on_sm = half ? std::min(2.0, std::max(1.0, at_once / d.sms)) : 1.0;
   // 64 of k: the products, this SM's reads, all SMs' reads, this SM's reads from memory
   const double stage = 16384.0 + nt * 128.0;
-  const double per_k = std::max({1.9 * nt * on_sm, stage * on_sm / 94.4, stage * at_once / d.sms / 78.6, cold ? 16384.0 * on_sm / 72.0 : 0.0});
-  const double memory = (bytes + (cold && nt < s.I ? 2.0 * two * s.J * s.K : 0.0)) / 6200.0;
+  const double per_k = std::max({1.9 * nt * on_sm, stage * on_sm / 94.4, stage * at_once / d.sms / 78.6, cold ? 16384.0 * on_sm / 76.3 : 0.0});
+  // memory, which wants some 256 CTAs of small tiles to keep it busy
+  const double memory = (bytes + (cold && nt < s.I ? 2.0 * two * s.J * s.K : 0.0)) / 6200.0 * (1.0 + (nt <= 32 ? 0.173 : 0.0) * std::max(0.0, 1.0 - at_once / 256.0));
   const double held = (double)std::min<long long>(nt, s.I), rows = std::ceil(held / (8.0 * two * split));   // a tile's, a thread's
-  const double end = 1228.0 + rows * (14.7 * two + 120.0 * res + 70.5 * aux * two) * (1.0 + 0.414 * odd) + 3.38 * nt * on_sm +
+  const double end = 1249.0 + rows * (12.7 * two + 158.0 * res + 66.8 * aux * two) * (1.0 + 0.367 * odd) + 3.42 * nt * on_sm +
                      (split > 1 ? 13.8 * held * on_sm : 0.0);
-  const double alone = cold && !half && nt <= 32 ? 566.0 : 0.0;   // one small ring an SM: its start and end are not another one's work
-  return 827.0 + alone + (split > 1 ? 407.0 : 0.0) + 130.3 * split + std::max(waves * (484.0 + share * per_k), memory) + end + (waves - 1.0) * 0.92 * end;
+  const double alone = cold && !half && nt <= 32 ? 836.0 : 0.0;   // one small ring an SM: its start and end are not another one's work
+  return 785.0 + alone + (split > 1 ? 495.0 : 0.0) + 126.5 * split + std::max(waves * (434.0 + share * per_k), memory) + end + (waves - 1.0) * 0.944 * end;
 }
 
 inline double dpair_cost(const DenseShape& s, const DenseDevice& d) {
@@ -82,8 +83,8 @@ inline double dpair_cost(const DenseShape& s, const DenseDevice& d) {
   // a tile's epilogue runs under the next tile's products, all but the last one's
   const long long tiles = (s.I + 255) / 256 * ((s.J + columns - 1) / columns);
   const double rounds = (double)((tiles + d.pairs - 1) / d.pairs);
-  const double epilogue = (2944.0 + 1134.0 * res + 3255.0 * aux) * (1.0 + 0.434 * odd) + 4016.0 * res * odd;
-  return 1010.0 + std::max(rounds * KB * 362.6, (rounds - 1.0) * epilogue) + epilogue;
+  const double epilogue = (2944.0 + 1022.0 * res + 3042.0 * aux) * (1.0 + 0.411 * odd) + 4937.0 * res * odd;
+  return 960.0 + std::max(rounds * KB * 389.4, (rounds - 1.0) * epilogue) + epilogue;
 }
 
 // f(nt) for the rows a tile may have
