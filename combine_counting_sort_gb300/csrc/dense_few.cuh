@@ -10,9 +10,9 @@
 // cluster, in the CTAs' order, and finishes it.  No atomics, no workspace, one
 // launch; results do not change from run to run.
 //
-// Two blocks an SM stream weights at 6.3 TB/s where there are enough of them (48 x 32768 x 7168
-// 75 us); a call's fixed cost is launch 2 us, set-up 0.5, the first copy 1, the end 1 to 2.  One row
-// of 7168 x 2048 takes 8.2 us (4.3 of them the weights' bytes).  The sums come by loads from the other
+// Two blocks an SM stream weights at 6.4 TB/s where there are enough of them (48 x 32768 x 7168
+// 73.5 us); a call's fixed cost is launch 2 us, set-up 0.5, the first copy 1, the end 1 to 2.  One row
+// of 7168 x 2048 takes 8.3 us (4.3 of them the weights' bytes).  The sums come by loads from the other
 // SMs, 16 bytes a cycle; bulk copies between the SMs were no faster (11.5 us against 10.4 for 64 rows).
 #pragma once
 

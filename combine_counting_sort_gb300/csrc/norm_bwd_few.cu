@@ -4,7 +4,7 @@
 // take rows, all at once with a vector a thread, and others take strips of
 // columns over all rows, which they read a second time (out of L2).  Against each
 // block's sums in a workspace and a second kernel, whose bytes are a row's of
-// fp32 for each block: 300 x 7168 13.0 us, one row 7.2.
+// fp32 for each block: 300 x 7168 13.0 us against 7.3 here, one row 7.2 against 2.0.
 //
 // A strip is 8 vectors wide; the blocks of a cluster share its rows and add up
 // their sums through distributed shared memory in rank order.
