@@ -29,10 +29,9 @@ bool encode_operand(CUtensorMap* map, const DenseOperand& o, int K, int box) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// CTAs that the device holds at once in clusters of c; 0 where it cannot be said.
+// CTAs that the device holds at once in clusters of c; below 0 where it cannot be said.
 template <typename K>
 int resident_ctas(K kernel, int threads, size_t smem, int c) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -44,27 +43,50 @@ int resident_ctas(K kernel, int threads, size_t smem, int c) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n * c : 0;
+  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n * c : -1;
 }
 
-// What the device holds, by one of the kernels (all take the same threads and shared memory).  Asked once.
+// What the current device holds, by one of the kernels (all take the same threads and shared memory),
+// whose limits of shared memory are set there.
 template <typename K, typename P>
-DenseDevice dense_device(K few, P pair) {
-  DenseDevice d = {};
-  d.sms = device_sm_count();
-  d.pairs = std::min(resident_ctas(pair, kDPairThreads, kDPairSmemBytes, 2), d.sms) / 2;
+bool ask_device(K few, P pair, DenseDevice* d) {
+  if (cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
+      cudaFuncSetAttribute(pair, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
+    return false;
+  d->sms = device_sm_count();
+  d->pairs = std::min(resident_ctas(pair, kDPairThreads, kDPairSmemBytes, 2), d->sms) / 2;
+  if (d->pairs < 1) return false;
   for (int c = 1; c <= kDFewMaxSplit; ++c) {
-    d.cta[0][c] = resident_ctas(few, kDFewThreads, dfew_smem_bytes(128, 6), c);
-    d.cta[1][c] = 2 * d.cta[0][c];   // (of kernels with tensor memory the query says one a SM whatever their size; two run)
+    const int n = resident_ctas(few, kDFewThreads, dfew_smem_bytes(128, 6), c);
+    if (n < 0) return false;
+    d->cta[0][c] = n;
+    d->cta[1][c] = 2 * n;   // (of kernels with tensor memory the query says one a SM whatever their size; two run)
   }
-  return d;
+  return true;
 }
+
+// Asked once on each device.
+class DenseDevices {
+ public:
+  template <typename K, typename P>
+  bool get(int dev, K few, P pair, DenseDevice* d) {
+    if (dev >= 64) return ask_device(few, pair, d);
+    if (!once_(dev, [&] { return ask_device(few, pair, &kept_[dev]); })) return false;
+    *d = kept_[dev];
+    return true;
+  }
+
+ private:
+  OncePerDevice once_;
+  DenseDevice kept_[64];
+};
 
 template <typename T, bool PMN, bool QMN, int EPI, bool AUX>
 int launch_pair(const CUtensorMap& tmP, const CUtensorMap& tmQ, const DenseArgs& g, int pairs, cudaStream_t st) {
   auto kernel = dense_pair_kernel<T, PMN, QMN, EPI, AUX>;
-  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDPairSmemBytes);
-  if (attr != cudaSuccess) return MOE_ERR_CUDA;
+  static OncePerDevice limit;
+  if (!limit(current_device(), [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDPairSmemBytes) == cudaSuccess; }))
+    return MOE_ERR_CUDA;
   constexpr int kTileJ = EPI == kEpiGated ? 128 : 256;
   const long long tiles = ((long long)g.I + 255) / 256 * (((long long)g.J + kTileJ - 1) / kTileJ);
   if (tiles > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
@@ -75,8 +97,9 @@ inline DenseShape shape_of(const DenseArgs& g, bool gated, bool p_mn) {
   return {g.I, g.J, g.K, gated, p_mn, g.aux != nullptr, g.residual != nullptr, g.vec != 0};
 }
 
-// The plans of the shapes that a thread asked for last (a plan takes longer than a launch).
+// The plans of the shapes that a thread asked for last (a plan takes longer than a launch), each for its device.
 struct DensePlans {
+  int device;
   DenseShape shape[2];
   DensePlan plan[2];
   bool both;
@@ -104,14 +127,17 @@ template <typename T, bool PMN, bool QMN, int EPI>
 int launch_dense(const DenseOperand& P, const DenseOperand& Q, DenseArgs g, cudaStream_t st) {
   if (!device_has_tcgen05()) return MOE_ERR_UNSUPPORTED;
   auto kernel = dense_few_kernel<T, PMN, QMN, EPI>;
-  static const DenseDevice device = dense_device(kernel, dense_pair_kernel<T, PMN, QMN, EPI, false>);
-  if (device.pairs < 1) return MOE_ERR_CUDA;
+  static DenseDevices devices;
+  const int dev = current_device();
+  DenseDevice device;
+  if (!devices.get(dev, kernel, dense_pair_kernel<T, PMN, QMN, EPI, false>, &device)) return MOE_ERR_CUDA;
   g.timeout_ns = kDenseTimeoutNs;
   const DenseShape shape = shape_of(g, EPI == kEpiGated, PMN);
   static thread_local DensePlans kept[64] = {};
   DensePlans& at = plans_at(kept, shape);
-  if (!same_shape(at.shape[0], shape)) {
+  if (at.device != dev || !same_shape(at.shape[0], shape)) {
     at.plan[0] = dense_plan(shape, device);
+    at.device = dev;
     at.shape[0] = shape;
   }
   const DensePlan plan = at.plan[0];
@@ -133,13 +159,16 @@ template <typename T>
 int launch_backward(const DenseOperand (&P)[2], const DenseOperand (&Q)[2], const DenseArgs (&g)[2], cudaStream_t st) {
   if (!device_has_tcgen05()) return MOE_ERR_UNSUPPORTED;
   auto kernel = dense_both_kernel<T>;
-  static const DenseDevice device = dense_device(kernel, dense_pair_kernel<T, false, true, kEpiPlain, false>);
-  if (device.pairs < 1) return MOE_ERR_CUDA;
+  static DenseDevices devices;
+  const int dev = current_device();
+  DenseDevice device;
+  if (!devices.get(dev, kernel, dense_pair_kernel<T, false, true, kEpiPlain, false>, &device)) return MOE_ERR_CUDA;
   const DenseShape s[2] = {shape_of(g[0], false, false), shape_of(g[1], false, true)};
   static thread_local DensePlans kept[64] = {};
   DensePlans& at = plans_at(kept, s[0]);
-  if (!same_shape(at.shape[0], s[0]) || !same_shape(at.shape[1], s[1])) {
+  if (at.device != dev || !same_shape(at.shape[0], s[0]) || !same_shape(at.shape[1], s[1])) {
     at.both = dense_plan_both(s, device, at.plan);
+    at.device = dev;
     at.shape[0] = s[0];
     at.shape[1] = s[1];
   }

@@ -8,6 +8,8 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
+#include <mutex>
 
 #include "../../include/moe.h"
 
@@ -56,6 +58,33 @@ inline int device_sm_count() {
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
   return n;
 }
+
+inline int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
+// What a process sets or asks once on each of its devices (a kernel's shared-memory limit, how many
+// blocks are resident): `f` says whether it could, and a failure is not kept.  Devices from 64 on
+// have no bit here and do it at each call.
+class OncePerDevice {
+ public:
+  template <typename F>
+  bool operator()(int dev, F&& f) {
+    if (dev < 0) return false;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done_.load(std::memory_order_acquire) & bit) return true;
+    std::lock_guard<std::mutex> lock(mutex_);
+    if (done_.load(std::memory_order_relaxed) & bit) return true;
+    if (!f()) return false;
+    done_.fetch_or(bit, std::memory_order_release);
+    return true;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+  std::mutex mutex_;
+};
 
 // sm_100-class (tcgen05) device?
 inline bool device_has_tcgen05() {

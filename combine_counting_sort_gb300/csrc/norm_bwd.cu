@@ -247,8 +247,9 @@ int launch_bwd(const NormArgs& p, void* dweight, void* dbias, cudaStream_t st) {
   static_assert(ring >= (size_t)2 * BLOCK * NV * kVec16<T> * 4, "the groups' sums fit the ring");
   const size_t smem = ring + (MASK ? 0 : (size_t)p.H * sizeof(W));
   auto kernel = norm_bwd_kernel<T, W, TPR, BLOCK, NV, D, MASK>;
-  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024);
-  if (attr != cudaSuccess) return MOE_ERR_CUDA;
+  static OncePerDevice limit;
+  if (!limit(current_device(), [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024) == cudaSuccess; }))
+    return MOE_ERR_CUDA;
   const int blocks = norm_blocks(p.T, BLOCK / TPR, BLOCK == 256 && smem <= 112 * 1024 ? 2 : 1, device_sm_count());
   const int rc = launch_next(kernel, dim3(blocks), BLOCK, smem, st, 1, 1, p);
   return rc ? rc : launch_sums<W>(p, blocks, dweight, dbias, st);
