@@ -205,8 +205,8 @@ extern "C" int moe_linear_bwd(const void* dy, const void* x, int T, int K, const
   if (!aligned2(dx) || !aligned2(dW) || !aligned2(dbias)) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   if (T == 0) {   // sums over no rows
-    if (dW && cudaMemsetAsync(dW, 0, (size_t)N * K * 2, st) != cudaSuccess) return MOE_ERR_CUDA;
-    if (dbias && cudaMemsetAsync(dbias, 0, (size_t)N * 2, st) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dW && !cuda_ok(cudaMemsetAsync(dW, 0, (size_t)N * K * 2, st))) return MOE_ERR_CUDA;
+    if (dbias && !cuda_ok(cudaMemsetAsync(dbias, 0, (size_t)N * 2, st))) return MOE_ERR_CUDA;
     return MOE_OK;
   }
   size_t need = 0;
@@ -247,7 +247,7 @@ extern "C" int moe_gated_bwd(const void* dh, const void* x, int T, int H, const 
   if (!aligned2(dx) || !aligned2(dW1)) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   if (T == 0) {   // sums over no rows
-    if (dW1 && cudaMemsetAsync(dW1, 0, (size_t)2 * F * H * 2, st) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dW1 && !cuda_ok(cudaMemsetAsync(dW1, 0, (size_t)2 * F * H * 2, st))) return MOE_ERR_CUDA;
     return MOE_OK;
   }
   size_t need = 0;

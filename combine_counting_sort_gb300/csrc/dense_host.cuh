@@ -43,15 +43,15 @@ int resident_ctas(K kernel, int threads, size_t smem, int c) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n * c : -1;
+  return cuda_ok(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) ? n * c : -1;
 }
 
 // What the current device holds, by one of the kernels (all take the same threads and shared memory),
 // whose limits of shared memory are set there.
 template <typename K, typename P>
 bool ask_device(K few, P pair, DenseDevice* d) {
-  if (cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
-      cudaFuncSetAttribute(pair, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
+  if (!cuda_ok(cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024)) ||
+      !cuda_ok(cudaFuncSetAttribute(pair, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024)))
     return false;
   d->sms = device_sm_count();
   d->pairs = std::min(resident_ctas(pair, kDPairThreads, kDPairSmemBytes, 2), d->sms) / 2;
@@ -85,7 +85,7 @@ template <typename T, bool PMN, bool QMN, int EPI, bool AUX>
 int launch_pair(const CUtensorMap& tmP, const CUtensorMap& tmQ, const DenseArgs& g, int pairs, cudaStream_t st) {
   auto kernel = dense_pair_kernel<T, PMN, QMN, EPI, AUX>;
   static OncePerDevice limit;
-  if (!limit(current_device(), [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDPairSmemBytes) == cudaSuccess; }))
+  if (!limit(current_device(), [&] { return cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDPairSmemBytes)); }))
     return MOE_ERR_CUDA;
   constexpr int kTileJ = EPI == kEpiGated ? 128 : 256;
   const long long tiles = ((long long)g.I + 255) / 256 * (((long long)g.J + kTileJ - 1) / kTileJ);

@@ -59,6 +59,13 @@ inline int device_sm_count() {
   return n;
 }
 
+// A call reports its own failures: none is left behind for a later one's cudaGetLastError.
+inline bool cuda_ok(cudaError_t e) {
+  if (e == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
 inline int current_device() {
   int dev = 0;
   return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
@@ -145,7 +152,7 @@ int launch_next(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cu
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = cx * cy > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, kernel, args...)) ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace moe

@@ -260,7 +260,7 @@ int launch_fwd(const NormArgs& p, cudaStream_t st) {
   const size_t smem = (size_t)D * NV * kFwdThreads * 16 + (MASK ? 0 : 2 * (size_t)p.H * sizeof(W));
   auto kernel = norm_fwd_kernel<T, W, TPR, NV, D, MASK>;
   static OncePerDevice limit;
-  if (!limit(current_device(), [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024) == cudaSuccess; }))
+  if (!limit(current_device(), [&] { return cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024)); }))
     return MOE_ERR_CUDA;
   const int per_sm = smem <= 112 * 1024 ? kFwdPerSm<T, NV, MASK> : 1;
   return launch_next(kernel, dim3(norm_blocks(p.T, kFwdThreads / TPR, per_sm, device_sm_count())), kFwdThreads, smem, st, 1, 1, p);

@@ -248,7 +248,7 @@ int launch_bwd(const NormArgs& p, void* dweight, void* dbias, cudaStream_t st) {
   const size_t smem = ring + (MASK ? 0 : (size_t)p.H * sizeof(W));
   auto kernel = norm_bwd_kernel<T, W, TPR, BLOCK, NV, D, MASK>;
   static OncePerDevice limit;
-  if (!limit(current_device(), [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024) == cudaSuccess; }))
+  if (!limit(current_device(), [&] { return cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024)); }))
     return MOE_ERR_CUDA;
   const int blocks = norm_blocks(p.T, BLOCK / TPR, BLOCK == 256 && smem <= 112 * 1024 ? 2 : 1, device_sm_count());
   const int rc = launch_next(kernel, dim3(blocks), BLOCK, smem, st, 1, 1, p);
@@ -306,8 +306,8 @@ extern "C" int moe_layernorm_bwd(const void* dy, const void* x, int T, int H, in
   if (!elem_aligned(weight, wdtype) || !elem_aligned(dweight, wdtype) || !elem_aligned(dbias, wdtype)) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   if (T == 0) {   // sums over no rows
-    if (dweight && cudaMemsetAsync(dweight, 0, H * elem_bytes(wdtype), st) != cudaSuccess) return MOE_ERR_CUDA;
-    if (dbias && cudaMemsetAsync(dbias, 0, H * elem_bytes(wdtype), st) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dweight && !cuda_ok(cudaMemsetAsync(dweight, 0, H * elem_bytes(wdtype), st))) return MOE_ERR_CUDA;
+    if (dbias && !cuda_ok(cudaMemsetAsync(dbias, 0, H * elem_bytes(wdtype), st))) return MOE_ERR_CUDA;
     return MOE_OK;
   }
   size_t need = 0;

@@ -76,6 +76,26 @@ int main() {
 }
 """
 
+LEFT_BEHIND = CALLS + r"""
+int main() {
+  // after a call that failed, wherever it did, a later cudaGetLastError finds nothing
+  int dev = 0;
+  for (int which = 0; which < 3; ++which, ++dev) {
+    fake().device = dev;
+    for (auto call : calls) {
+      int& fail = which == 0 ? fake().fail_attribute : which == 1 ? fake().fail_occupancy : fake().fail_launch;
+      fail = 1;
+      const int rc = call();
+      EXPECT(rc == MOE_ERR_CUDA || (rc == MOE_OK && fail == 1));   // (a limit that is set already is not set again)
+      fail = 0;
+      EXPECT(fake().last == cudaSuccess);
+      EXPECT(call() == MOE_OK);
+    }
+  }
+  printf("ok\n");
+}
+"""
+
 
 def run(source, tmp_path):
     from combine_counting_sort_gb300 import _build
@@ -95,6 +115,10 @@ def run(source, tmp_path):
 
 def test_every_device_has_its_own(tmp_path):
     run(DEVICES, tmp_path)
+
+
+def test_a_failure_leaves_no_error_behind(tmp_path):
+    run(LEFT_BEHIND, tmp_path)
 
 
 def test_a_failure_is_not_kept(tmp_path):
