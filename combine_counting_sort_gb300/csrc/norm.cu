@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdPerSm<T, NV, MASK>) norm_fwd_
     for (int d = 0; d < D; ++d) part.clear_absent(mine + d * SLOT, STEP);
 #pragma unroll
   for (int d = 0; d < D - 1; ++d, src += stride) {
-    if (g + d * groups < p.T) part.fetch(src, g + d * groups == p.T - 1, mine_at + d * SLOT, STEP);
+    if (g + d * groups < p.T) part.fetch(src, g + d * groups >= p.tail, mine_at + d * SLOT, STEP);
     cp_async_commit();
   }
   W* const ws = reinterpret_cast<W*>(ring + D * SLOT);
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdPerSm<T, NV, MASK>) norm_fwd_
     }
     const int next = slot == 0 ? D - 1 : slot - 1;   // the slot read a row ago
     const long long ahead = row + (D - 1) * groups;
-    if (ahead < p.T) part.fetch(src, ahead == p.T - 1, mine_at + next * SLOT, STEP);
+    if (ahead < p.T) part.fetch(src, ahead >= p.tail, mine_at + next * SLOT, STEP);
     cp_async_commit();
     src += stride;
     slot = slot == D - 1 ? 0 : slot + 1;
@@ -157,9 +157,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, (TPR <= 64 ? 4 : TPR <=
   grid_wait_previous();
   if (row >= p.T) return;   // (a whole group)
   if (MASK) {
-    // a row's first and last vectors have its neighbours' values too, but none behind the last row
+    // a row's first and last vectors have its neighbours' values too, but none behind the tensor
     uint4 wr[2] = {}, br[2] = {};
-    const bool there = part.any(0), inside = row < p.T - 1 || part.col(0) + V <= p.H;
+    const bool there = part.any(0), inside = part.readable(0, row >= p.tail) == V;
     load_if(raw, src, there && inside);
     part.template params_begin<W>(p.weight, 0, wr);
     part.template params_begin<W>(p.bias, 0, br);
@@ -323,7 +323,7 @@ extern "C" int moe_layernorm(const void* x, int T, int H, int dtype, const void*
   if (!elem_aligned(x, dtype) || !elem_aligned(y, dtype) || !elem_aligned(weight, wdtype) || !elem_aligned(bias, wdtype) ||
       !elem_aligned(mean, MOE_F32) || !elem_aligned(rstd, MOE_F32))
     return MOE_ERR_INVALID_ARG;
-  const NormArgs p = {x, nullptr, weight, bias, T, H, eps, y, mean, rstd, nullptr};
+  const NormArgs p = {x, nullptr, weight, bias, T, H, eps, y, mean, rstd, nullptr, norm_tail(T, H, dtype)};
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == MOE_F32) return norm_fwd<float, float>(p, st);
   if (dtype == MOE_BF16) return wdtype == MOE_F32 ? norm_fwd<__nv_bfloat16, float>(p, st) : norm_fwd<__nv_bfloat16, __nv_bfloat16>(p, st);

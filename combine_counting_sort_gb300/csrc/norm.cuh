@@ -35,7 +35,16 @@ struct NormArgs {
   float* mean;
   float* rstd;
   float* part;  // backward: [blocks][2][H] sums of each block's rows
+  int tail;     // norm_tail
 };
+
+// A row's last vector reaches up to V - 1 values into the rows behind it, but not past the tensor's end: from
+// this row on, where fewer are left (the last row; more of them where rows are shorter than a vector), it
+// is read up to its row's end.
+inline int norm_tail(int T, int H, int dtype) {
+  const int V = dtype == MOE_F32 ? 4 : 8;
+  return T - (V - 1 + H - 1) / H;
+}
 
 // A vector's worth of weights: W's own 16 bytes where W is the rows' type, else fp32.
 // Rows of whole vectors read them from a copy in shared memory; those of MASK, whose
@@ -66,6 +75,8 @@ MOE_DEV void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes) : "memory");
 }
 
+#define MOE_BOTH __host__ __device__ __forceinline__
+
 // MASK: rows of no whole number of vectors, whose first and last vectors are shared
 // with the rows beside them.
 template <typename T, int TPR, int NV, bool MASK>
@@ -73,20 +84,23 @@ struct RowPart {
   static constexpr int V = kVec16<T>;
   int H, tid, first;   // first: column of this thread's vector 0
 
-  MOE_DEV RowPart(int H_, long long first_row) : H(H_), tid((int)threadIdx.x % TPR), first(tid * V - (MASK ? (int)(first_row * H_ % V) : 0)) {}
+  MOE_BOTH RowPart(int H_, long long first_row, int tid_) : H(H_), tid(tid_), first(tid_ * V - (MASK ? (int)(first_row * H_ % V) : 0)) {}
+  MOE_DEV RowPart(int H_, long long first_row) : RowPart(H_, first_row, (int)threadIdx.x % TPR) {}
   // first column of vector i, and the part [lo, hi) of it that is this row's
-  MOE_DEV int col(int i) const { return first + i * TPR * V; }
-  MOE_DEV int lo(int i) const { return max(0, -col(i)); }
-  MOE_DEV int hi(int i) const { return min(V, H - col(i)); }
-  MOE_DEV bool any(int i) const { return col(i) < H; }
-  MOE_DEV bool whole(int i) const { return !MASK || (col(i) >= 0 && col(i) + V <= H); }
+  MOE_BOTH int col(int i) const { return first + i * TPR * V; }
+  MOE_BOTH int lo(int i) const { return max(0, -col(i)); }
+  MOE_BOTH int hi(int i) const { return min(V, H - col(i)); }
+  MOE_BOTH bool any(int i) const { return col(i) < H; }
+  MOE_BOTH bool whole(int i) const { return !MASK || (col(i) >= 0 && col(i) + V <= H); }
 
-  // Start copying this thread's vectors of a row into its slots, `step` bytes apart; `src` is
-  // vector 0.  A vector reaches into the rows beside it, but not past the last row.
-  MOE_DEV void fetch(const T* src, bool last_row, uint32_t slot, uint32_t step) const {
+  // values of vector i that are read, from the vector's start on, in a row that is one of the tail's (norm_tail) or not
+  MOE_BOTH int readable(int i, bool tail) const { return MASK && tail ? hi(i) : V; }
+
+  // Start copying this thread's vectors of a row into its slots, `step` bytes apart; `src` is vector 0.
+  MOE_DEV void fetch(const T* src, bool tail, uint32_t slot, uint32_t step) const {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (any(i)) cp_async16(slot + i * step, src + i * TPR * V, MASK && last_row ? (uint32_t)(hi(i) * sizeof(T)) : 16u);
+      if (any(i)) cp_async16(slot + i * step, src + i * TPR * V, (uint32_t)(readable(i, tail) * sizeof(T)));
   }
   // zeros into the slots of vectors that the rows do not have: work on masked rows then needs no branches
   MOE_DEV void clear_absent(uint8_t* slot, uint32_t step) const {

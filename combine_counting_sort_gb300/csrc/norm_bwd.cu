@@ -36,8 +36,8 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) norm_bwd_kernel(const Norm
   for (int d = 0; d < D - 1; ++d, at += stride) {
     const long long row = g + (long long)d * groups;
     if (row < p.T) {
-      part.fetch(x + at, row == p.T - 1, mine_at + d * SLOT, STEP);
-      part.fetch(dy + at, row == p.T - 1, mine_at + d * SLOT + HALF, STEP);
+      part.fetch(x + at, row >= p.tail, mine_at + d * SLOT, STEP);
+      part.fetch(dy + at, row >= p.tail, mine_at + d * SLOT + HALF, STEP);
     }
     cp_async_commit();
   }
@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) norm_bwd_kernel(const Norm
     const long long ahead = row + (long long)(D - 1) * groups;
     const int next = slot == 0 ? D - 1 : slot - 1;   // the slot read a row ago
     if (ahead < p.T) {
-      part.fetch(x + at, ahead == p.T - 1, mine_at + next * SLOT, STEP);
-      part.fetch(dy + at, ahead == p.T - 1, mine_at + next * SLOT + HALF, STEP);
+      part.fetch(x + at, ahead >= p.tail, mine_at + next * SLOT, STEP);
+      part.fetch(dy + at, ahead >= p.tail, mine_at + next * SLOT + HALF, STEP);
     }
     cp_async_commit();
     at += stride;
@@ -317,7 +317,7 @@ extern "C" int moe_layernorm_bwd(const void* dy, const void* x, int T, int H, in
       !elem_aligned(rstd, MOE_F32) || !aligned16(ws))
     return MOE_ERR_INVALID_ARG;
   if (2 * device_sm_count() > kNormMaxBlocks) return MOE_ERR_UNSUPPORTED;
-  const NormArgs p = {x, dy, weight, nullptr, T, H, 0.f, dx, const_cast<float*>(mean), const_cast<float*>(rstd), static_cast<float*>(ws)};
+  const NormArgs p = {x, dy, weight, nullptr, T, H, 0.f, dx, const_cast<float*>(mean), const_cast<float*>(rstd), static_cast<float*>(ws), norm_tail(T, H, dtype)};
   // Few rows, and no more than 12 of them to a thread of a strip (22: 14.3 us against 9.8 at 5719 x 143; 10: 7.0 against
   // 11.6 at 1200 x 2048).  dx over x or dy would change what the strips' blocks read.
   const int vec = dtype == MOE_F32 ? 4 : 8, tpr = norm_tpr(H, vec, vec);

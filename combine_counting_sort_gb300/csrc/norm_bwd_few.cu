@@ -133,8 +133,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 4 : 1024 /
   if (row >= p.T) return;   // (a whole group)
   const RowPart<T, TPR, 1, MASK> part(p.H, row);
   const long long at = row * p.H + part.first;
-  // a row's first and last vectors have its neighbours' values too, but none behind the last row
-  const bool there = part.any(0), inside = !MASK || row < p.T - 1 || part.col(0) + V <= p.H;
+  // a row's first and last vectors have its neighbours' values too, but none behind the tensor
+  const bool there = part.any(0), inside = part.readable(0, row >= p.tail) == V;
   uint4 xr = make_uint4(0, 0, 0, 0), dr = xr, wr[2] = {};
   ParamVec<T, W> w;
   load_if(xr, x + at, there && inside);

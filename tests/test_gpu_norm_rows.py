@@ -1,0 +1,69 @@
+"""Layer norm on rows where it can go wrong: shorter than a vector beside what is not the tensor's.
+Bounds as in test_gpu_norm.py."""
+import pytest
+import torch
+
+import combine_counting_sort_gb300 as moe
+from tests import gpu_util
+from tests.test_gpu_norm import E, TYPES, data, forward_bounds, rounding, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    gpu_util.build()
+
+
+def framed(t, by):
+    """t's values between NaN, `by` of them in front: a whole number of vectors, or none."""
+    n = t.numel()
+    buf = torch.full((by + n + 16,), float("nan"), dtype=t.dtype, device="cuda")
+    v = buf[by:by + n].view(t.shape)
+    v.copy_(t)
+    return v, buf, by
+
+
+def frame_kept(buf, by, n):
+    return bool(buf[:by].isnan().all() and buf[by + n:].isnan().all())
+
+
+def check_against_formula(x, dy, w, b, eps, y, mean, rstd, dx, dw, db):
+    """Every output of a forward and a backward call against 64 bits, by test_gpu_norm.py's bounds."""
+    T, H = x.shape
+    dtype = x.dtype
+    _, r64, n, en, er = forward_bounds(x, H, eps)
+    w64, dy64 = w.double(), dy.double()
+    want = n * w64 + b.double()
+    within(y, want, rounding(want, dtype) + (en * w64.abs() + 2 * E * (n * w64).abs() + E * want.abs()) * 1.01, "y")
+    within(rstd[:, None], r64, er, "rstd")
+    g = dy64 * w64
+    m1, m2 = g.mean(1, keepdim=True), (g * n).mean(1, keepdim=True)
+    want = r64 * (g - m1 - n * m2)
+    s = H / 64 + 16
+    e1, e2 = s * E * g.abs().mean(1, keepdim=True), s * E * (g * n).abs().mean(1, keepdim=True) + (g.abs() * en).mean(1, keepdim=True)
+    size = g.abs() + m1.abs() + (n * m2).abs()
+    e = r64 * (e1 + en * m2.abs() + n.abs() * e2 + en * e2 + 5 * E * size) + er * (size + e1 + n.abs() * e2)
+    within(dx, want, rounding(want, dtype) + e * 1.05, "dx")
+    want = (dy64 * n).sum(0)
+    within(dw, want, rounding(want, dtype) + (T + 8) * E * (dy64 * n).abs().sum(0) + (dy64.abs() * en).sum(0) * 1.01, "dweight")
+    within(db, dy64.sum(0), rounding(dy64.sum(0), dtype) + (T + 8) * E * dy64.abs().sum(0), "dbias")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H", [1, 2, 3, 4, 5, 6, 7, 8, 9, 15])
+def test_short_rows_beside_other_values(H, dtype):
+    """Rows shorter than a vector, whose loads meet several rows and the tensor's ends: what lies around the
+    tensor stays out of the results and as it was, for few rows and for many."""
+    for T in (1, 2, 3, 5, 8, 9, 70001):
+        x, dy, w, b = data(T, H, dtype, 100 * T + H)
+        for by in (8, 3):
+            (xv, _, _), (dv, _, _), (wv, _, _), (bv, _, _) = (framed(t, by) for t in (x, dy, w, b))
+            (yv, yb, _), (gv, gb, _) = framed(torch.zeros_like(x), by), framed(torch.zeros_like(x), by)
+            (sv, sb, _), (tv, tb, _) = framed(torch.zeros_like(w), by), framed(torch.zeros_like(w), by)
+            mean, rstd = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+            moe.moe_layernorm(xv, wv, bv, 1e-2, yv, mean=mean, rstd=rstd)
+            ws = torch.empty(moe.moe_layernorm_bwd_ws_bytes(T, H), dtype=torch.uint8, device="cuda")
+            moe.moe_layernorm_bwd(dv, xv, wv, mean, rstd, gv, sv, tv, ws)
+            check_against_formula(x, dy, w, b, 1e-2, yv, mean, rstd, gv, sv, tv)
+            assert all(frame_kept(*f) for f in ((yb, by, T * H), (gb, by, T * H), (sb, by, H), (tb, by, H)))
