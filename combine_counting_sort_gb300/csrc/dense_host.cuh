@@ -47,33 +47,35 @@ int resident_ctas(K kernel, int threads, size_t smem, int c) {
 }
 
 // What the current device holds, by one of the kernels (all take the same threads and shared memory),
-// whose limits of shared memory are set there.
+// whose limits of shared memory are set there; its status.
 template <typename K, typename P>
-bool ask_device(K few, P pair, DenseDevice* d) {
+int ask_device(K few, P pair, DenseDevice* d) {
+  if (!device_has_tcgen05()) return MOE_ERR_UNSUPPORTED;
   if (!cuda_ok(cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024)) ||
       !cuda_ok(cudaFuncSetAttribute(pair, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024)))
-    return false;
+    return MOE_ERR_CUDA;
   d->sms = device_sm_count();
   d->pairs = std::min(resident_ctas(pair, kDPairThreads, kDPairSmemBytes, 2), d->sms) / 2;
-  if (d->pairs < 1) return false;
+  if (d->pairs < 1) return MOE_ERR_CUDA;
   for (int c = 1; c <= kDFewMaxSplit; ++c) {
     const int n = resident_ctas(few, kDFewThreads, dfew_smem_bytes(128, 6), c);
-    if (n < 0) return false;
+    if (n < 0) return MOE_ERR_CUDA;
     d->cta[0][c] = n;
     d->cta[1][c] = 2 * n;   // (of kernels with tensor memory the query says one a SM whatever their size; two run)
   }
-  return true;
+  return MOE_OK;
 }
 
 // Asked once on each device.
 class DenseDevices {
  public:
   template <typename K, typename P>
-  bool get(int dev, K few, P pair, DenseDevice* d) {
+  int get(int dev, K few, P pair, DenseDevice* d) {
     if (dev >= 64) return ask_device(few, pair, d);
-    if (!once_(dev, [&] { return ask_device(few, pair, &kept_[dev]); })) return false;
+    int rc = MOE_ERR_CUDA;
+    if (!once_(dev, [&] { return (rc = ask_device(few, pair, &kept_[dev])) == MOE_OK; })) return rc;
     *d = kept_[dev];
-    return true;
+    return MOE_OK;
   }
 
  private:
@@ -125,12 +127,11 @@ inline long long few_ctas(const DenseArgs& g, const DensePlan& plan, int rows, i
 
 template <typename T, bool PMN, bool QMN, int EPI>
 int launch_dense(const DenseOperand& P, const DenseOperand& Q, DenseArgs g, cudaStream_t st) {
-  if (!device_has_tcgen05()) return MOE_ERR_UNSUPPORTED;
   auto kernel = dense_few_kernel<T, PMN, QMN, EPI>;
   static DenseDevices devices;
   const int dev = current_device();
   DenseDevice device;
-  if (!devices.get(dev, kernel, dense_pair_kernel<T, PMN, QMN, EPI, false>, &device)) return MOE_ERR_CUDA;
+  if (const int rc = devices.get(dev, kernel, dense_pair_kernel<T, PMN, QMN, EPI, false>, &device)) return rc;
   g.timeout_ns = kDenseTimeoutNs;
   const DenseShape shape = shape_of(g, EPI == kEpiGated, PMN);
   static thread_local DensePlans kept[64] = {};
@@ -157,12 +158,11 @@ int launch_dense(const DenseOperand& P, const DenseOperand& Q, DenseArgs g, cuda
 // dx = d W and dW = d^T x, in one launch where that is quicker
 template <typename T>
 int launch_backward(const DenseOperand (&P)[2], const DenseOperand (&Q)[2], const DenseArgs (&g)[2], cudaStream_t st) {
-  if (!device_has_tcgen05()) return MOE_ERR_UNSUPPORTED;
   auto kernel = dense_both_kernel<T>;
   static DenseDevices devices;
   const int dev = current_device();
   DenseDevice device;
-  if (!devices.get(dev, kernel, dense_pair_kernel<T, false, true, kEpiPlain, false>, &device)) return MOE_ERR_CUDA;
+  if (const int rc = devices.get(dev, kernel, dense_pair_kernel<T, false, true, kEpiPlain, false>, &device)) return rc;
   const DenseShape s[2] = {shape_of(g[0], false, false), shape_of(g[1], false, true)};
   static thread_local DensePlans kept[64] = {};
   DensePlans& at = plans_at(kept, s[0]);
