@@ -4,8 +4,10 @@
 //
 // Memory bound: reads x and writes y once.  Mean and variance come from one
 // exchange between a row's warps: each takes its own mean, then its squares about
-// that mean, and the warps' sums and squares are joined about the row's mean, so
-// nothing cancels for rows far from zero.  Sums are fp32 in a fixed order.
+// that mean, and the warps' means and squares are joined about the row's mean, so
+// nothing cancels for rows far from zero: their means are right to the last bit (warp_stats), and
+// n is made of deviations, for x * rstd - mean * rstd would round at the size of mean * rstd.  A row of
+// equal values has n = 0.  Sums are fp32 in a fixed order.
 #include "norm.cuh"
 
 namespace moe {
@@ -14,6 +16,19 @@ constexpr int kFwdThreads = 512;
 // Blocks an SM: two, unless registers hold weights and biases too.
 template <typename T, int NV, bool MASK>
 constexpr int kFwdPerSm = !MASK && NV * kVec16<T> <= 32 ? 2 : 1;
+
+// A warp's mean and squares about it.  `mean` is off by the roundings of a sum of n values; further than four
+// deviations from zero they are not small beside a deviation, and the sum of the thread's deviations, which
+// `deviations` gives, moves it.  (Taken for every row: 90.3 us against 87.7 at
+// 8192 x 7168 fp32.)
+template <typename F>
+MOE_DEV float2 warp_stats(float mean, float squares, float inv_n, F&& deviations) {
+  if (mean * mean > 16.f * inv_n * squares) {
+    const float r = warp_sum(deviations()), move = r * inv_n, q = fmaf(-move, r, squares);
+    return make_float2(mean + move, q < 0.f ? 0.f : q);
+  }
+  return make_float2(mean, squares);
+}
 
 template <typename T, typename W, int TPR, int NV, int D, bool MASK>
 __global__ void __launch_bounds__(kFwdThreads, kFwdPerSm<T, NV, MASK>) norm_fwd_kernel(const NormArgs p) {
@@ -62,7 +77,7 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdPerSm<T, NV, MASK>) norm_fwd_
   if (lane == 0) counts[warp] = warp_n;
   __syncthreads();
   const int peer = grp * WARPS + lane % WARPS;   // the warp whose sums this lane joins
-  const float peer_n = counts[peer], peer_inv = peer_n > 0.f ? 1.f / peer_n : 0.f, inv_h = 1.f / (float)p.H;
+  const float peer_n = counts[peer], inv_h = 1.f / (float)p.H;
 
   int slot = 0, turn = 0;
   for (long long row = g; row < p.T; row += groups, turn ^= 1) {
@@ -84,37 +99,46 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdPerSm<T, NV, MASK>) norm_fwd_
     src += stride;
     slot = slot == D - 1 ? 0 : slot + 1;
 
-    const float warp_s = warp_sum(sum2(s)), m = warp_s * warp_inv;
+    const float m = warp_sum(sum2(s)) * warp_inv;
     f32x2 q = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!MASK && !part.any(i)) continue;
-      f32x2 d[P];
 #pragma unroll
-      for (int e = 0; e < P; ++e) d[e] = add2(v[i][e], both(-m));
-      part.mask(i, d);
+      for (int e = 0; e < P; ++e) v[i][e] = add2(v[i][e], both(-m));
+      part.mask(i, v[i]);
 #pragma unroll
-      for (int e = 0; e < P; ++e) q = fma2(d[e], d[e], q);
+      for (int e = 0; e < P; ++e) q = fma2(v[i][e], v[i][e], q);
     }
-    const float warp_q = warp_sum(sum2(q));
-    float mean = m, var = warp_q * inv_h;
+    const float2 own = warp_stats(m, warp_sum(sum2(q)), warp_inv, [&] {
+      f32x2 r = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!MASK && !part.any(i)) continue;
+#pragma unroll
+        for (int e = 0; e < P; ++e) r = add2(r, v[i][e]);
+      }
+      return sum2(r);
+    });
+    float mean = own.x, var = own.y * inv_h;
     if (WARPS > 1) {
-      if (lane == 0) stats[turn][warp] = make_float2(warp_s, warp_q);
+      if (lane == 0) stats[turn][warp] = own;
       group_sync<TPR, BLOCK>();
       const float2 o = stats[turn][peer];
-      float t = o.x;
+      const float from = stats[turn][grp * WARPS].x;   // the first warp's mean
+      float t = peer_n * (o.x - from);
 #pragma unroll
       for (int k = WARPS / 2; k > 0; k >>= 1) t += __shfl_xor_sync(0xffffffffu, t, k);
-      mean = t * inv_h;
-      const float off = o.x * peer_inv - mean;
+      mean = fmaf(t, inv_h, from);
+      const float off = o.x - mean;
       t = fmaf(peer_n * off, off, o.y);
 #pragma unroll
       for (int k = WARPS / 2; k > 0; k >>= 1) t += __shfl_xor_sync(0xffffffffu, t, k);
       var = t * inv_h;
     }
     const float rstd = 1.f / sqrtf(var + p.eps);
-    // n = x * rstd - mean * rstd: its rounding is that of the mean itself, 2^-24 |mean| rstd
-    const f32x2 off = both(-mean * rstd);
+    // from the deviations about the warp's mean: their distance to the row's is of their own size
+    const f32x2 r2 = both(rstd), off = both((m - mean) * rstd);
     if (part.tid == 0) {
       if (p.mean) p.mean[row] = mean;
       if (p.rstd) p.rstd[row] = rstd;
@@ -131,7 +155,7 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdPerSm<T, NV, MASK>) norm_fwd_
         reinterpret_cast<const ParamVec<T, W>*>(bs + part.col(i))->get(bp);
       }
 #pragma unroll
-      for (int e = 0; e < P; ++e) o[e] = fma2(fma2(v[i][e], both(rstd), off), wp[e], bp[e]);
+      for (int e = 0; e < P; ++e) o[e] = fma2(fma2(v[i][e], r2, off), wp[e], bp[e]);
       if (part.any(i)) part.store(dst, i, Pairs<T>::put(o));
     }
     dst += stride;
@@ -182,34 +206,38 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, (TPR <= 64 ? 4 : TPR <=
     if (p.bias) b = *reinterpret_cast<const ParamVec<T, W>*>(static_cast<const W*>(p.bias) + part.col(0));
     else b = part.template params<W>(p.bias, 0.f, 0);
   }
-  const float n = warp_sum((float)max(0, part.hi(0) - part.lo(0))), inv_h = 1.f / (float)p.H;
+  const float n = warp_sum((float)max(0, part.hi(0) - part.lo(0))), inv_n = n > 0.f ? 1.f / n : 0.f, inv_h = 1.f / (float)p.H;
   f32x2 v[P], s = 0;
   Pairs<T>::get(raw, v);
   if (part.any(0)) part.mask(0, v);
 #pragma unroll
   for (int e = 0; e < P; ++e) s = add2(s, v[e]);
-  const float warp_s = warp_sum(sum2(s)), m = n > 0.f ? warp_s / n : 0.f;
-  f32x2 d[P], q = 0;
+  const float m = warp_sum(sum2(s)) * inv_n;
+  f32x2 d[P], q = 0, r = 0;
 #pragma unroll
   for (int e = 0; e < P; ++e) d[e] = add2(v[e], both(-m));
   if (part.any(0)) {
     part.mask(0, d);
 #pragma unroll
-    for (int e = 0; e < P; ++e) q = fma2(d[e], d[e], q);
+    for (int e = 0; e < P; ++e) {
+      q = fma2(d[e], d[e], q);
+      r = add2(r, d[e]);
+    }
   }
-  const float warp_q = warp_sum(sum2(q));
-  float mean = m, var = warp_q * inv_h;
+  const float2 own = warp_stats(m, warp_sum(sum2(q)), inv_n, [&] { return sum2(r); });
+  float mean = own.x, var = own.y * inv_h;
   if (WARPS > 1) {
     if (lane == 0) {
-      stats[warp] = make_float2(warp_s, warp_q);
+      stats[warp] = own;
       counts[warp] = n;
     }
     group_sync<TPR, BLOCK>();
     const int peer = grp * WARPS + lane;
     const float2 o = lane < WARPS ? stats[peer] : make_float2(0.f, 0.f);
     const float on = lane < WARPS ? counts[peer] : 0.f;
-    mean = warp_sum(o.x) * inv_h;
-    const float off = on > 0.f ? o.x / on - mean : 0.f;
+    const float from = __shfl_sync(0xffffffffu, o.x, 0);   // the first warp's mean
+    mean = fmaf(warp_sum(on * (o.x - from)), inv_h, from);
+    const float off = o.x - mean;
     var = warp_sum(fmaf(on * off, off, o.y)) * inv_h;
   }
   const float rstd = 1.f / sqrtf(var + p.eps);
@@ -223,7 +251,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, (TPR <= 64 ? 4 : TPR <=
     w.get(wp);
     b.get(bp);
 #pragma unroll
-    for (int e = 0; e < P; ++e) v[e] = fma2(fma2(v[e], both(rstd), both(-mean * rstd)), wp[e], bp[e]);
+    for (int e = 0; e < P; ++e) v[e] = fma2(mul2(add2(v[e], both(-mean)), both(rstd)), wp[e], bp[e]);
     part.store(static_cast<T*>(p.y) + row * p.H + part.first, 0, Pairs<T>::put(v));
   }
 }
@@ -240,13 +268,16 @@ __global__ void __launch_bounds__(512) norm_fwd_any_kernel(const NormArgs p) {
   grid_launch_next();
   grid_wait_previous();
   for (int j = threadIdx.x; j < p.H; j += 512) s += to_f32(x[j]);
-  const float mean = block_sum<512>(s, scratch) / (float)p.H;
+  const float m = block_sum<512>(s, scratch) / (float)p.H;
+  float r = 0.f;
   s = 0.f;
   for (int j = threadIdx.x; j < p.H; j += 512) {
-    const float d = to_f32(x[j]) - mean;
+    const float d = to_f32(x[j]) - m;
     s = fmaf(d, d, s);
+    r += d;
   }
-  const float rstd = 1.f / sqrtf(block_sum<512>(s, scratch) / (float)p.H + p.eps);
+  r = block_sum<512>(r, scratch) / (float)p.H;
+  const float mean = m + r, rstd = 1.f / sqrtf(fmaxf(fmaf(-r, r, block_sum<512>(s, scratch) / (float)p.H), 0.f) + p.eps);
   if (threadIdx.x == 0) {
     if (p.mean) p.mean[row] = mean;
     if (p.rstd) p.rstd[row] = rstd;

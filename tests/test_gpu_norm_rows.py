@@ -1,5 +1,5 @@
-"""Layer norm on rows where it can go wrong: shorter than a vector beside what is not the tensor's.
-Bounds as in test_gpu_norm.py."""
+"""Layer norm on rows where it can go wrong: shorter than a vector beside what is not the tensor's, of
+equal values, and far from zero.  Bounds as in test_gpu_norm.py where nothing else is said."""
 import pytest
 import torch
 
@@ -67,3 +67,62 @@ def test_short_rows_beside_other_values(H, dtype):
             moe.moe_layernorm_bwd(dv, xv, wv, mean, rstd, gv, sv, tv, ws)
             check_against_formula(x, dy, w, b, 1e-2, yv, mean, rstd, gv, sv, tv)
             assert all(frame_kept(*f) for f in ((yb, by, T * H), (gb, by, T * H), (sb, by, H), (tb, by, H)))
+
+
+def forms(H, dtype):
+    """Rows and the alignment of x that take each of the forward kernels: few rows, many rows, rows that start anywhere."""
+    many = 1 + 8_000_000 // max(H, 256)
+    return ((3, 0), (many, 0), (5, 1))
+
+
+def at_offset(x, by):
+    buf = torch.empty(x.numel() + by, dtype=x.dtype, device="cuda")
+    v = buf[by:].view(x.shape)
+    v.copy_(x)
+    return v
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H", [1, 2, 7, 33, 64, 100, 777, 1000, 1111, 4096, 7168, 8191, 12288, 16383, 16384])
+def test_rows_of_equal_values(H, dtype):
+    """Their mean is the value, n is 0 and y the bias, bit for bit, however far from zero and at every alignment; so
+    is dweight 0.  (f16 rows of more than 8192 values: 2^13 times 11 bits fill fp32.)"""
+    values = torch.tensor([0.0, 1.0, 100.0, -3.25, 50000.0, 0.1, 1000.123, -7.7e-3, 12345.678], device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(H)
+    w, b = (torch.randn(H, generator=g, device="cuda").to(dtype) for _ in range(2))
+    for T, by in forms(H, dtype):
+        c = values.repeat(T // 9 + 1)[:T].to(dtype)
+        x = at_offset(c[:, None].expand(T, H), by)
+        y, mean, rstd = torch.full_like(x, float("nan")), torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        moe.moe_layernorm(x, w, b, 1e-5, y, mean=mean, rstd=rstd)
+        assert torch.equal(mean, c.float()), (T, by)
+        assert torch.equal(y, b[None].expand(T, H)), (T, by, float((y.double() - b.double()).abs().max()))
+        dy, dx, dw, db = torch.randn(T, H, generator=g, device="cuda").to(dtype), torch.empty_like(x), torch.empty_like(w), torch.empty_like(w)
+        ws = torch.empty(moe.moe_layernorm_bwd_ws_bytes(T, H), dtype=torch.uint8, device="cuda")
+        moe.moe_layernorm_bwd(dy, x, w, mean, rstd, dx, dw, db, ws)
+        assert torch.equal(dw, torch.zeros_like(dw)), (T, by)
+
+
+@pytest.mark.parametrize("far", [1e3, -1e5])
+@pytest.mark.parametrize("H", [33, 100, 1000, 1111, 4096, 7168, 12288, 16384])
+def test_f32_rows_far_from_zero(H, far):
+    """Rows whose mean is 10^3 and 10^5 times their deviation.  A warp's mean and the row's are each rounded once, by
+    half a step of |mean|, the deviations from the first are exact, and their sum is off by (H / 64 + 14) e of their
+    size: no rounding of a sum of H such values is left, which would be (H / 64 + 12) e |mean|."""
+    eps = 1e-5
+    for T, by in forms(H, torch.float32):
+        g = torch.Generator(device="cuda").manual_seed(T + H)
+        x = at_offset(torch.randn(T, H, generator=g, device="cuda") + far, by)
+        y, mean, rstd = torch.full_like(x, float("nan")), torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        moe.moe_layernorm(x, None, None, eps, y, mean=mean, rstd=rstd)
+        x64 = x.double()
+        m64 = x64.mean(1, keepdim=True)
+        d = x64 - m64
+        var = d.square().mean(1, keepdim=True)
+        r64 = (var + eps).rsqrt()
+        em = 1.05 * E * m64.abs() + (H / 64 + 14) * E * d.abs().mean(1, keepdim=True)
+        ed = em + E * d.abs()
+        er = r64 * (0.55 * ((2 * d.abs() * ed + ed.square()).mean(1, keepdim=True) + (H / 64 + 14) * E * var) / (var + eps) + 4 * E)
+        within(mean[:, None], m64, em, "mean")
+        within(rstd[:, None], r64, er, "rstd")
+        within(y, d * r64, ed * r64 + (d.abs() + ed) * er + 3 * E * (d * r64).abs(), "y")
