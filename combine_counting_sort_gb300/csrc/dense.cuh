@@ -113,7 +113,9 @@ MOE_DEV void act_pair(f32x2 a, f32x2& y, f32x2& slope) {
     const f32x2 a2 = mul2(a, a);
     const f32x2 s = rcp_pair(add2(ex2_pair(mul2(a, fma2(a2, both(-d * kLog2e), both(-c * kLog2e)))), one));
     y = mul2(a, s);
-    slope = fma2(mul2(y, fma2(s, both(-1.f), one)), fma2(a2, both(3.f * d), both(c)), s);
+    // (a^2 kept finite: where it overflows, 1 - s is 0 long since, and 0 times infinity is no slope)
+    const f32x2 b2 = pack_f32x2(fminf(lo2(a2), 1e30f), fminf(hi2(a2), 1e30f));
+    slope = fma2(mul2(y, fma2(s, both(-1.f), one)), fma2(b2, both(3.f * d), both(c)), s);
   } else if (ACT == MOE_ACT_GELU) {
     const f32x2 b = pack_f32x2(fabsf(lo2(a)), fabsf(hi2(a)));
     const f32x2 e = ex2_pair(mul2(mul2(a, a), both(-0.5f * kLog2e)));
