@@ -33,18 +33,20 @@ def nvcc() -> str:
 
 
 def _inputs():
+    """The library's sources, what they depend on, and what the binding does."""
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    deps = srcs + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        [os.path.join(ROOT, "include", "moe.h"), __file__]
-    return srcs, deps
+    both = [os.path.join(ROOT, "include", "moe.h"), __file__]
+    return srcs, srcs + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + both, \
+        [os.path.join(CSRC, "binding.cpp"), *both]
+
+
+def _current(target: str, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    _, deps = _inputs()
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(d) <= t for d in deps)
+    _, lib_deps, binding_deps = _inputs()
+    return _current(LIB, lib_deps) and _current(BINDING, binding_deps)
 
 
 def _binding_command(src: str, obj: str):
@@ -62,45 +64,48 @@ def _link_binding(obj: str):
     import torch
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + ".tmp"
-    r = subprocess.run([shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", LIB_DIR, "-l:libmoe.so", "-L", libs, "-ltorch_python",
-                        "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", LIB_DIR, "-l:libmoe.so", "-L", libs, "-ltorch_python", "-ltorch_cpu",
+          "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs], "link failed")
     os.replace(tmp, BINDING)
 
 
+def _run(cmd, what: str) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+    return r.stdout + r.stderr
+
+
 def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) -> str:
-    if not force and up_to_date():
+    """Builds what is out of date.  The library needs nvcc alone: where the binding cannot be built (no torch, no
+    Python headers) that is raised, with the library in place."""
+    srcs, lib_deps, binding_deps = _inputs()
+    need_lib, need_binding = force or not _current(LIB, lib_deps), force or not _current(BINDING, binding_deps)
+    if not need_lib and not need_binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
-    srcs, _ = _inputs()
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".o")
         cmd = _binding_command(src, obj) if src.endswith(".cpp") else [cc, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{os.path.basename(cmd[0])} failed on {src}:\n{r.stdout}\n{r.stderr}")
-        return obj, r.stdout + r.stderr
+        return obj, _run(cmd, f"{os.path.basename(cmd[0])} failed on {src}")
 
-    binding = os.path.join(CSRC, "binding.cpp")
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        results = list(ex.map(compile_one, [binding, *srcs]))
+        binding = ex.submit(compile_one, os.path.join(CSRC, "binding.cpp")) if need_binding else None
+        results = list(ex.map(compile_one, srcs)) if need_lib else []
     if verbose or ptxas_info:
         for obj, log in results:
             if log.strip():
                 print(f"== {os.path.basename(obj)}\n{log}")
-    binding_obj, *objs = [o for o, _ in results]
-    tmp = LIB + ".tmp"
-    cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+    if need_lib:
+        tmp = LIB + ".tmp"
+        _run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *(o for o, _ in results)], "link failed")
+        os.replace(tmp, LIB)
+    if need_binding:
+        _link_binding(binding.result()[0])
     return LIB
 
 
