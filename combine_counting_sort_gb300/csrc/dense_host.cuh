@@ -106,12 +106,6 @@ struct DensePlans {
   DensePlan plan[2];
   bool both;
 };
-inline bool same_shape(const DenseShape& a, const DenseShape& b) {
-  return a.I == b.I && a.J == b.J && a.K == b.K && a.gated == b.gated && a.p_mn == b.p_mn && a.aux == b.aux && a.residual == b.residual && a.vec == b.vec;
-}
-inline DensePlans& plans_at(DensePlans (&kept)[64], const DenseShape& s) {
-  return kept[(unsigned long long)((s.I * 1000003 + s.J) * 1000003 + s.K + s.aux * 7 + s.residual * 13 + s.vec * 29) * 0x9E3779B97F4A7C15ull >> 58];
-}
 
 // The kernel's form of a plan; the CTAs that it takes, in whole clusters.
 inline long long few_ctas(const DenseArgs& g, const DensePlan& plan, int rows, int cluster, DFewPlan* fp) {
@@ -134,8 +128,8 @@ int launch_dense(const DenseOperand& P, const DenseOperand& Q, DenseArgs g, cuda
   if (const int rc = devices.get(dev, kernel, dense_pair_kernel<T, PMN, QMN, EPI, false>, &device)) return rc;
   g.timeout_ns = kDenseTimeoutNs;
   const DenseShape shape = shape_of(g, EPI == kEpiGated, PMN);
-  static thread_local DensePlans kept[64] = {};
-  DensePlans& at = plans_at(kept, shape);
+  static thread_local DensePlans kept[kPlanSlots] = {};
+  DensePlans& at = kept[plan_slot(shape)];
   if (at.device != dev || !same_shape(at.shape[0], shape)) {
     at.plan[0] = dense_plan(shape, device);
     at.device = dev;
@@ -164,8 +158,8 @@ int launch_backward(const DenseOperand (&P)[2], const DenseOperand (&Q)[2], cons
   DenseDevice device;
   if (const int rc = devices.get(dev, kernel, dense_pair_kernel<T, false, true, kEpiPlain, false>, &device)) return rc;
   const DenseShape s[2] = {shape_of(g[0], false, false), shape_of(g[1], false, true)};
-  static thread_local DensePlans kept[64] = {};
-  DensePlans& at = plans_at(kept, s[0]);
+  static thread_local DensePlans kept[kPlanSlots] = {};
+  DensePlans& at = kept[plan_slot(s[0])];
   if (at.device != dev || !same_shape(at.shape[0], s[0]) || !same_shape(at.shape[1], s[1])) {
     at.both = dense_plan_both(s, device, at.plan);
     at.device = dev;

@@ -33,6 +33,17 @@ struct DenseShape {
   bool aux, residual, vec;   // of the epilogue: a second output, a third input, 16-byte vectors
 };
 
+inline bool same_shape(const DenseShape& a, const DenseShape& b) {
+  return a.I == b.I && a.J == b.J && a.K == b.K && a.gated == b.gated && a.p_mn == b.p_mn && a.aux == b.aux && a.residual == b.residual && a.vec == b.vec;
+}
+
+// Where a shape's plan is kept.
+constexpr int kPlanSlots = 64;
+inline int plan_slot(const DenseShape& s) {
+  const uint64_t h = ((uint64_t)s.I * 1000003u + (uint64_t)s.J) * 1000003u + (uint64_t)s.K + s.aux * 7u + s.residual * 13u + s.vec * 29u;
+  return (int)(h * 0x9E3779B97F4A7C15ull >> 58);
+}
+
 // What the device holds at once: CTAs in clusters of c that fill an SM (cta[0][c]) or
 // half of one (cta[1][c]), and pairs.
 struct DenseDevice {
