@@ -96,6 +96,32 @@ int main() {
 }
 """
 
+GRIDS = CALLS + r"""
+static int blocks(int (*call)(int rows), int rows, int dev) {
+  fake().device = dev;
+  fake().launches.clear();
+  EXPECT(call(rows) == MOE_OK);
+  const dim3 g = fake().launches[0].grid;
+  return (int)(g.x * g.y);
+}
+static int sums(int T) { return moe_linear_bwd(A, A, T, 512, A, 4096, MOE_BF16, A, 0, 0, A, A, big, S, 0); }
+static int slopes(int T) { return moe_linear_bwd(A, A, T, 512, A, 4096, MOE_BF16, A, A, 0, 0, A, big, S, 0); }
+static int factors(int T) { return moe_gated_bwd(A, A, T, 512, A, 4096, MOE_BF16, A, A, 0, A, big, S, 0); }
+int main() {
+  // the elementwise kernels in front of the backward products, with more rows than any device takes at once:
+  // as many blocks as the device runs, whichever it is (32 strips of 128 columns; the gated one's of 2048)
+  fake().sms[1] = 76;
+  for (int dev : {0, 1}) {
+    const int sms = fake().sms[dev];
+    EXPECT(blocks(slopes, 1 << 20, dev) > 2 * sms - 32 && blocks(slopes, 1 << 20, dev) <= 2 * sms);
+    EXPECT(blocks(sums, 1 << 20, dev) > sms && blocks(sums, 1 << 20, dev) <= 2 * sms);
+    EXPECT(blocks(factors, 1 << 20, dev) == 16 * sms);
+  }
+  EXPECT(blocks(slopes, 1, 0) == 32 && blocks(factors, 1, 0) == 2);
+  printf("ok\n");
+}
+"""
+
 
 def run(source, tmp_path):
     from combine_counting_sort_gb300 import _build
@@ -115,6 +141,10 @@ def run(source, tmp_path):
 
 def test_every_device_has_its_own(tmp_path):
     run(DEVICES, tmp_path)
+
+
+def test_grids_are_the_devices(tmp_path):
+    run(GRIDS, tmp_path)
 
 
 def test_a_failure_leaves_no_error_behind(tmp_path):
