@@ -126,3 +126,39 @@ def test_f32_rows_far_from_zero(H, far):
         within(mean[:, None], m64, em, "mean")
         within(rstd[:, None], r64, er, "rstd")
         within(y, d * r64, ed * r64 + (d.abs() + ed) * er + 3 * E * (d * r64).abs(), "y")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,H", [(1, 33), (7, 1000), (400, 1111), (900, 4096), (5000, 200), (40, 8200), (700, 7168), (2500, 1112), (1200, 1999), (6, 16383)])
+def test_in_place_and_on_views_against_the_formula(T, H, dtype):
+    """y over x, dx over dy, dx over x, and tensors that start anywhere: each within the bounds of test_gpu_norm.py
+    of the formula, as separate aligned tensors are."""
+    x, dy, w, b = data(T, H, dtype, 7 * T + H)
+    eps = 1e-5
+    ws = torch.empty(moe.moe_layernorm_bwd_ws_bytes(T, H), dtype=torch.uint8, device="cuda")
+
+    def run(xf, y, dyb, xb, dx, w, b, new):
+        mean, rstd, dw, db = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), new(w), new(b)
+        moe.moe_layernorm(xf, w, b, eps, y, mean=mean, rstd=rstd)
+        out = y.clone()   # (y may be what the backward call writes into)
+        ws.fill_(0xFF)
+        moe.moe_layernorm_bwd(dyb, xb, w, mean, rstd, dx, dw, db, ws)
+        check_against_formula(x, dy, w, b, eps, out, mean, rstd, dx, dw, db)
+
+    def copy(t):
+        return t.clone()
+
+    def view(t):
+        return at_offset(t, 1)
+
+    xi, di = copy(x), copy(dy)
+    run(xi, xi, di, x, di, w, b, copy)            # y over x, dx over dy
+    xb = copy(x)
+    run(x, copy(x), dy, xb, xb, w, b, copy)       # dx over x
+    wv, bv = view(w), view(b)
+    run(view(x), view(x), view(dy), view(x), view(x), wv, bv, view)
+    xi, di = view(x), view(dy)
+    run(xi, xi, di, view(x), di, wv, bv, view)    # the same on views
+    xb = view(x)
+    run(view(x), view(x), view(dy), xb, xb, wv, bv, view)
+    run(x, copy(x), view(dy), x, copy(x), w, bv, copy)   # one tensor alone starts anywhere
