@@ -13,9 +13,10 @@
 // the even CTA issues the products, warps 4-11 of both CTAs hold the epilogue (two
 // warps a quarter of the rows, each half the columns).
 //
-// Bound by the tensor cores (8192 x 2048 x 7168 gated: 247 us, 1.95 PFLOP/s; with factors
-// 262) until an epilogue takes longer than a tile's products: 4096 x 7168 x 2048 65 us, with
-// gelu_tanh 72, slope 79 and residual 82 (tensor pipe 75% of the active cycles).
+// Bound by the tensor cores (8192 x 2048 x 7168 gated: 247 us, 1.95 PFLOP/s, in a graph; one call after
+// another, under the power cap, 286; with factors 260) until an epilogue takes longer than a tile's
+// products: 4096 x 7168 x 2048 65 us, with gelu_tanh 68, slope 74 and residual 83 (tensor pipe 77%
+// of the active cycles); 4096 x 7168 x 512 32, the floor 15.5.
 #pragma once
 
 #include "dense.cuh"

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdPerSm<T, NV, MASK>) norm_fwd_
   const long long stride = groups * p.H;
   const T* src = static_cast<const T*>(p.x) + g * p.H + part.first;   // vector 0 of the next row to fetch
   T* dst = static_cast<T*>(p.y) + g * p.H + part.first;
-  // (4000 x 8001: 37.8 us with branches, 32.8 without; rows of whole vectors 45.3 against 49.2)
+  // (4000 x 8001: 37.8 us with branches, 32.4 without; rows of whole vectors are slower without, 49 against 45)
   if (MASK)
 #pragma unroll
     for (int d = 0; d < D; ++d) part.clear_absent(mine + d * SLOT, STEP);

@@ -223,8 +223,8 @@ inline int norm_tpr(int H, int vec, int values) {
   return tpr;
 }
 
-// Rows few enough to be taken all at once: up to two and a half times the threads that run at once (four times: 17.1 us against 11.0 at 9728 x 1024, 16.3
-// against 14.2 at 4864 x 1111; once: 4.1 against 8.7 at 304 x 7168).
+// Rows few enough to be taken all at once: up to two and a half times the threads that run at once (four times: 16.7 us against 9.2 at 9728 x 1024, 18.0
+// against 12.9 at 4864 x 1111; never: 5.7 against 4.0 at 304 x 7168).
 inline bool few_rows(int T, int tpr) { return 2LL * T * tpr <= 5 * 2048LL * device_sm_count(); }
 
 int norm_bwd_few(int dtype, int wdtype, const NormArgs& p, void* dweight, void* dbias, cudaStream_t st);

@@ -497,7 +497,8 @@ int moe_layer_few(const uint16_t* x, int T, int H, const uint16_t* router, int E
 /* ---------------------------------------------------------------------------
  * Dense operators beside the experts, for serving and for training: the norm
  * before a router, a shared expert's gated block, projections that end in the
- * residual stream.  Tensors are contiguous.  Sums are fp32 and taken in a fixed
+ * residual stream.  Tensors are contiguous, and on the current device, which a call
+ * launches on; a process may use several.  Sums are fp32 and taken in a fixed
  * order: a call's results do not change from run to run.
  *
  * Types: MOE_BF16 or MOE_F16 for every tensor of a call (layer norm also takes
@@ -516,7 +517,8 @@ typedef enum moe_act {
 /* moe_layernorm: each row of x [T, H] to
  *   y = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps)
  * with the mean and the variance (over H, not H - 1) of that row in fp32, one
- * rounding at the end.
+ * rounding at the end.  A mean further than four deviations from zero is right to its last bit; a row of
+ * equal values gives the bias.
  *   weight, bias  device wdtype [H] (dtype or MOE_F32), each NULL where there is none.
  *   y             device dtype [T, H]; may be x.
  *   mean, rstd    device f32 [T], written where given: the backward pass reads them.
@@ -550,7 +552,7 @@ int moe_linear(const void* x, int T, int K, const void* W, int N, int dtype, con
 
 /* moe_linear_bwd: with d = dy * slope (slope NULL: d = dy, no activation) rounded to dtype for the
  * products (the tensor core takes 16-bit operands; slope in 32 bits would save the other rounding and
- * cost half as much again to read),
+ * cost half as much again to read; in MOE_F16 a d below 2^-25 becomes 0, so gradients want a loss scale),
  *   dx = d W,  dW = d^T x,  dbias = sum_t dy * slope (fp32, from the unrounded d);
  * the residual's gradient is dy itself.
  *   dx device dtype [T, K], dW device dtype [N, K], dbias device dtype [N]; each NULL where
@@ -572,7 +574,7 @@ int moe_gated(const void* x, int T, int H, const void* W1, int F, int dtype, int
               void* factors, int32_t* status, moe_stream_t stream);
 
 /* moe_gated_bwd: with d = [dh * factors[:, :F], dh * factors[:, F:]] rounded to
- * dtype for the products,  dx = d W1,  dW1 = d^T x.
+ * dtype for the products (as moe_linear_bwd's),  dx = d W1,  dW1 = d^T x.
  *   dx device dtype [T, H], dW1 device dtype [2F, H]; each NULL where it is not wanted
  *   (W1, or x, is then not read and may be NULL).
  *   ws device workspace of moe_gated_bwd_ws_bytes, 256-byte aligned; any contents. */
