@@ -102,8 +102,9 @@ MOE_DEV void act_pair(f32x2 a, f32x2& y, f32x2& slope) {
   const f32x2 one = both(1.f);
   if (ACT == MOE_ACT_RELU) {
     const float l = lo2(a), h = hi2(a);
-    y = pack_f32x2(l < 0.f ? 0.f : l, h < 0.f ? 0.f : h);   // (a NaN stays)
-    slope = pack_f32x2(l > 0.f ? 1.f : 0.f, h > 0.f ? 1.f : 0.f);
+    const float yl = l < 0.f ? 0.f : l, yh = h < 0.f ? 0.f : h;   // (a NaN stays, in the slope too)
+    y = pack_f32x2(yl, yh);
+    slope = pack_f32x2(l > 0.f ? 1.f : yl, h > 0.f ? 1.f : yh);
   } else if (ACT == MOE_ACT_SILU) {
     const f32x2 s = rcp_pair(add2(ex2_pair(mul2(a, both(-kLog2e))), one));
     y = mul2(a, s);

@@ -1,5 +1,5 @@
-"""The dense operators' activations on values as large as bf16 holds: what an outlier in the sums leaves of
-the output and of the slope."""
+"""The dense operators' activations on values as large as bf16 holds, and on NaN: what an outlier in the sums
+leaves of the output and of the slope."""
 import pytest
 import torch
 
@@ -47,3 +47,20 @@ def test_outliers(T, N, act, status):
     moe.moe_gated(x, W1, h, status, act=ACTS[act], factors=factors)
     assert torch.equal(h, (a * on)[:, None].expand(T, N))
     assert torch.equal(factors, torch.cat((on[:, None].expand(T, N), (a * on)[:, None].expand(T, N)), 1))
+
+
+@pytest.mark.parametrize("act", [a for a in ACTS if a != "none"])
+@pytest.mark.parametrize("T", [12, 4096])
+def test_nan_is_in_the_slope_too(T, act, status):
+    """The slope at a sum that is NaN is NaN, as the output is, so that the gradients say so; the rows beside it are untouched."""
+    x, W = torch.ones(T, 8, dtype=BF, device="cuda"), torch.ones(2048, 8, dtype=BF, device="cuda")
+    x[5, 3] = float("nan")
+    rows = [t for t in range(T) if t != 5]
+    y, slope = nan_like(T, 2048, dtype=BF), nan_like(T, 2048, dtype=BF)
+    moe.moe_linear(x, W, y, status, act=ACTS[act], slope=slope)
+    assert y[5].isnan().all() and slope[5].isnan().all()
+    assert torch.isfinite(y[rows].float()).all() and torch.isfinite(slope[rows].float()).all()
+    h, factors = nan_like(T, 1024, dtype=BF), nan_like(T, 2048, dtype=BF)
+    moe.moe_gated(x, W, h, status, act=ACTS[act], factors=factors)
+    assert h[5].isnan().all() and factors[5].isnan().all()
+    assert torch.isfinite(h[rows].float()).all() and torch.isfinite(factors[rows].float()).all()
